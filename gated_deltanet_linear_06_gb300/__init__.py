@@ -47,6 +47,29 @@ class Dims(ctypes.Structure):
                 ("l2_eps", ctypes.c_float), ("rms_eps", ctypes.c_float)]
 
 
+class AttnDims(ctypes.Structure):
+    """gdn_attn_dims."""
+    _fields_ = [("h_q", ctypes.c_int), ("h_kv", ctypes.c_int), ("d", ctypes.c_int),
+                ("rot", ctypes.c_int), ("n_axes", ctypes.c_int), ("rope_pairs", ctypes.c_int),
+                ("norm_eps", ctypes.c_float), ("scale", ctypes.c_float)]
+
+
+def make_attn_dims(h_q=16, h_kv=2, d=256, rot=64, n_axes=1, rope_pairs=0, norm_eps=1e-6,
+                   scale=0.0) -> AttnDims:
+    return AttnDims(h_q, h_kv, d, rot, n_axes, rope_pairs, norm_eps, scale)
+
+
+class MoeDims(ctypes.Structure):
+    """gdn_moe_dims."""
+    _fields_ = [("hidden", ctypes.c_int), ("inter", ctypes.c_int), ("experts", ctypes.c_int),
+                ("top_k", ctypes.c_int), ("shared_inter", ctypes.c_int), ("renorm", ctypes.c_int)]
+
+
+def make_moe_dims(hidden=2048, inter=512, experts=256, top_k=8, shared_inter=0,
+                  renorm=1) -> MoeDims:
+    return MoeDims(hidden, inter, experts, top_k, shared_inter, renorm)
+
+
 def make_dims(h_k=16, h_v=32, d_k=128, d_v=128, conv_w=4, chunk=64, l2_eps=1e-6,
               rms_eps=1e-6) -> Dims:
     return Dims(h_k, h_v, d_k, d_v, conv_w, chunk, l2_eps, rms_eps)
@@ -126,6 +149,20 @@ def lib() -> ctypes.CDLL:
             L.gdn_in_proj.argtypes = [DP, ctypes.c_int, ctypes.c_longlong] + [_P] * 8
             L.gdn_out_proj.restype = ctypes.c_int
             L.gdn_out_proj.argtypes = [DP, ctypes.c_int, ctypes.c_longlong] + [_P] * 5
+            AP, MP = ctypes.POINTER(AttnDims), ctypes.POINTER(MoeDims)
+            ll = ctypes.c_longlong
+            L.gdn_attn_prep.restype = ctypes.c_int
+            L.gdn_attn_prep.argtypes = [AP, ll] + [_P, ll, ll] * 3 + [_P] * 6 + [ll] + [_P] * 5
+            L.gdn_attn_decode_shared_workspace_bytes.restype = ctypes.c_size_t
+            L.gdn_attn_decode_shared_workspace_bytes.argtypes = [AP, ctypes.c_int, ctypes.c_int]
+            L.gdn_attn_decode_shared.restype = ctypes.c_int
+            L.gdn_attn_decode_shared.argtypes = [AP, ctypes.c_int, ll, ctypes.c_int, ctypes.c_int] + \
+                [_P] * 4 + [ll, _P, ctypes.c_int, _P, _P, ll, ll, _P, _P, ctypes.c_size_t, _P, _P]
+            L.gdn_moe_step_workspace_bytes.restype = ctypes.c_size_t
+            L.gdn_moe_step_workspace_bytes.argtypes = [MP, ctypes.c_int]
+            L.gdn_moe_step.restype = ctypes.c_int
+            L.gdn_moe_step.argtypes = [MP, ctypes.c_int] + [_P] * 8 + [ctypes.c_int] + [_P] * 3 + \
+                [ctypes.c_size_t, _P, _P]
             L.gdn_read_device_status.restype = ctypes.c_int
             L.gdn_read_device_status.argtypes = [_P, _P, ctypes.POINTER(ctypes.c_int32)]
             _lib = L
@@ -510,6 +547,105 @@ def gdn_out_proj(dims: Dims, hidden: int, o, w_out, y, device_status=None, strea
         _ptr(y, bf, "y", T * H), _ptr(device_status, torch.int32, "device_status", 1),
         _stream(stream))
     _check(st, "gdn_out_proj")
+
+
+def _view(t, name, tokens, heads, d):
+    """Address and (token, head) element strides of a bf16 CUDA view whose last
+    two dimensions are [heads][d] and whose leading ones are tokens evenly apart."""
+    if t is None:
+        return None, 0, 0
+    sh, st = t.shape, t.stride()
+    if not t.is_cuda or t.dtype != torch.bfloat16 or len(sh) < 3 or sh[-2] != heads or sh[-1] != d \
+            or (d > 1 and st[-1] != 1) or t.numel() != tokens * heads * d:
+        raise ValueError(f"{name}: want a CUDA bfloat16 tensor of [{tokens}, {heads}, {d}] with its "
+                         f"last dimension contiguous, got {t.dtype} {tuple(sh)} strides {st}")
+    for i in range(len(sh) - 3):
+        if sh[i] > 1 and st[i] != st[i + 1] * sh[i + 1]:
+            raise ValueError(f"{name}: tokens are not evenly apart (strides {st})")
+    return t.data_ptr(), st[-3], st[-2]
+
+
+def gdn_attn_prep(dims: AttnDims, q, k, v, q_norm_w, k_norm_w, inv_freq, freq_axis, pos, q_out,
+                  k_cache, v_cache, slot=None, device_status=None, stream=None):
+    """q and k norms, rotary positions and the cache write in one pass.  q, k
+    and v are [T, heads, d] views (None leaves one out); the caches are
+    [pages, page, h_kv, d] or [rows, h_kv, d]; slot [T] int32 names each token's row."""
+    f32, i32 = torch.float32, torch.int32
+    d, rot = dims.d, dims.rot
+    lead = next((x for x in (q, k, v) if x is not None), None)
+    T = int(lead.shape[0]) if lead is not None else 0
+    vq, vk, vv = (_view(q, "q", T, dims.h_q, d), _view(k, "k", T, dims.h_kv, d),
+                  _view(v, "v", T, dims.h_kv, d))
+    rows = 0
+    for cache, x in ((k_cache, k), (v_cache, v)):
+        if x is not None:
+            n = cache.numel() // (dims.h_kv * d)
+            if n * dims.h_kv * d != cache.numel() or (rows and n != rows):
+                raise ValueError("k_cache, v_cache: want the same whole number of [h_kv, d] rows")
+            rows = n
+    axes = None if dims.n_axes <= 1 or freq_axis is None else _ptr(freq_axis, i32, "freq_axis", rot // 2)
+    st = lib().gdn_attn_prep(
+        ctypes.byref(dims), T, *vq, *vk, *vv, _ptr(q_norm_w, f32, "q_norm_w", d),
+        _ptr(k_norm_w, f32, "k_norm_w", d), _ptr(inv_freq, torch.float64, "inv_freq", rot // 2), axes,
+        _ptr(pos, i32, "pos", max(dims.n_axes, 1) * T), _ptr(slot, i32, "slot", T), rows,
+        _ptr(q_out, torch.bfloat16, "q_out", T * dims.h_q * d) if q is not None else None,
+        _ptr(k_cache, torch.bfloat16, "k_cache") if k is not None else None,
+        _ptr(v_cache, torch.bfloat16, "v_cache") if v is not None else None,
+        _ptr(device_status, i32, "device_status", 1), _stream(stream))
+    _check(st, "gdn_attn_prep")
+
+
+def gdn_attn_decode_shared_workspace_bytes(dims: AttnDims, batch: int, steps: int = 1) -> int:
+    return lib().gdn_attn_decode_shared_workspace_bytes(ctypes.byref(dims), int(batch), int(steps))
+
+
+def gdn_attn_decode_shared(dims: AttnDims, q, k_cache, v_cache, prefix_pages, prefix_len, tail_pages,
+                           tail_len, out, workspace, gate=None, device_status=None, stream=None):
+    """Attention of q [B, steps, h_q, d] over a prefix that all sequences share
+    (its pages, prefix_len tokens) and each sequence's own tail (tail_pages
+    [B, width], tail_len [B]); the caches are [pages, page, h_kv, d]."""
+    bf, i32 = torch.bfloat16, torch.int32
+    B, S = int(q.shape[0]), int(q.shape[1])
+    n, L = B * S * dims.h_q * dims.d, int(prefix_len)
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.shape[2] != dims.h_kv or \
+            k_cache.shape[3] != dims.d:
+        raise ValueError("k_cache, v_cache: want [pages, page, h_kv, d], both alike")
+    pages, page = int(k_cache.shape[0]), int(k_cache.shape[1])
+    if L > 0 and (prefix_pages is None or prefix_pages.numel() < -(-L // page)):
+        raise ValueError("prefix_pages: fewer pages than the prefix has")
+    width = 0 if tail_pages is None else int(tail_pages.shape[-1])
+    g, g_st, g_sh = _view(gate, "gate", B * S, dims.h_q, dims.d)
+    st = lib().gdn_attn_decode_shared(
+        ctypes.byref(dims), page, pages, B, S, _ptr(q, bf, "q", n), _ptr(k_cache, bf, "k_cache"),
+        _ptr(v_cache, bf, "v_cache"), _ptr(prefix_pages, i32, "prefix_pages"), L,
+        _ptr(tail_pages, i32, "tail_pages", B * width), width, _ptr(tail_len, i32, "tail_len", B),
+        g, g_st, g_sh, _ptr(out, bf, "out", n), _ptr(workspace, torch.uint8, "workspace"),
+        workspace.numel(), _ptr(device_status, i32, "device_status", 1), _stream(stream))
+    _check(st, "gdn_attn_decode_shared")
+
+
+def gdn_moe_step_workspace_bytes(dims: MoeDims, tokens: int) -> int:
+    return lib().gdn_moe_step_workspace_bytes(ctypes.byref(dims), int(tokens))
+
+
+def gdn_moe_step(dims: MoeDims, x, w_router, w_gate_up, w_down, y, workspace, w_shared_gate_up=None,
+                 w_shared_down=None, w_shared_gate=None, topk_id=None, topk_w=None,
+                 device_status=None, stream=None):
+    """A whole mixture-of-experts layer: x [T, hidden] -> y [T, hidden] (bf16 or fp32)."""
+    bf, f32, i32 = torch.bfloat16, torch.float32, torch.int32
+    T, H, I, E, Is = int(x.shape[0]), dims.hidden, dims.inter, dims.experts, dims.shared_inter
+    if y.dtype not in (bf, f32):
+        raise ValueError("y: want bfloat16 or float32")
+    st = lib().gdn_moe_step(
+        ctypes.byref(dims), T, _ptr(x, bf, "x", T * H), _ptr(w_router, bf, "w_router", E * H),
+        _ptr(w_gate_up, bf, "w_gate_up", E * 2 * I * H), _ptr(w_down, bf, "w_down", E * H * I),
+        _ptr(w_shared_gate_up, bf, "w_shared_gate_up", 2 * Is * H),
+        _ptr(w_shared_down, bf, "w_shared_down", H * Is), _ptr(w_shared_gate, bf, "w_shared_gate", H),
+        _ptr(y, y.dtype, "y", T * H), GDN_DTYPE_F32 if y.dtype == f32 else GDN_DTYPE_BF16,
+        _ptr(topk_id, i32, "topk_id", T * dims.top_k), _ptr(topk_w, f32, "topk_w", T * dims.top_k),
+        _ptr(workspace, torch.uint8, "workspace"), workspace.numel(),
+        _ptr(device_status, i32, "device_status", 1), _stream(stream))
+    _check(st, "gdn_moe_step")
 
 
 def gdn_read_device_status(status_word, stream=None) -> int:

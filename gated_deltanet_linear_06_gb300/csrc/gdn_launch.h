@@ -131,4 +131,45 @@ size_t prefill_scratch_bytes_unsplit(int n_seqs);
 // SMs, or 0 when it does not split (a whole number of chunks, >= 1024 tokens).
 long long prefill_segment_tokens(int n_seqs, int h_v, long long total_tokens, int sms);
 
+// gdn_attn_prep: element strides; null q, k or v leaves that part out.
+struct AttnPrepArgs {
+  const uint16_t *q, *k, *v;
+  long long q_st, q_sh, k_st, k_sh, v_st, v_sh;
+  const float *q_w, *k_w;
+  const double* inv_freq;
+  const int32_t *freq_axis, *pos, *slot;
+  uint16_t *q_out, *k_cache, *v_cache;
+  int32_t* status;
+  long long tokens, cache_rows;
+  int h_q, h_kv, d, rot, n_axes, pairs;
+  float eps;
+};
+cudaError_t launch_attn_prep(const AttnPrepArgs& p, cudaStream_t stream);
+
+struct AttnSharedArgs {
+  const uint16_t *q, *k_cache, *v_cache, *gate;
+  const int32_t *prefix_pages, *tail_pages, *tail_len;
+  long long prefix_len, n_pages, gate_st, gate_sh;
+  uint16_t* out;
+  void* scratch;
+  int32_t* status;
+  int batch, steps, h_q, h_kv, d, page, tail_width;
+  float scale;
+};
+cudaError_t launch_attn_shared(const AttnSharedArgs& p, cudaStream_t stream);
+size_t attn_shared_scratch_bytes(int batch, int steps, int h_q, int h_kv, int d);
+
+struct MoeArgs {
+  const uint16_t *x, *w_router, *w_gate_up, *w_down, *s_gate_up, *s_down, *s_gate;
+  void* y;
+  int32_t* topk_id;
+  float* topk_w;
+  void* scratch;
+  int32_t* status;
+  int tokens, hidden, inter, experts, top_k, shared_inter;
+  bool renorm, out_f32;
+};
+cudaError_t launch_moe(const MoeArgs& p, cudaStream_t stream);
+size_t moe_scratch_bytes(int tokens, int hidden, int inter, int experts, int top_k, int shared_inter);
+
 }  // namespace gdn

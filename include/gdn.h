@@ -464,6 +464,159 @@ gdn_status gdn_in_proj(const gdn_dims* dims, int hidden, long long tokens, const
 gdn_status gdn_out_proj(const gdn_dims* dims, int hidden, long long tokens, const void* o,
                         const void* w_out, void* y, int32_t* device_status, void* stream);
 
+/*
+ * The other two blocks of a hybrid model's decode step.  In the models the
+ * pages run, every fourth layer is a gated-attention layer with a growing KV
+ * cache in place of the recurrent state, and every layer is followed by a
+ * mixture-of-experts block (llmxabe README, architecture paragraph).  Three
+ * calls cover what lies between their dense projections:
+ *   gdn_attn_prep            q and k norms, rotary positions, cache write
+ *   gdn_attn_decode_shared   attention of a batch that shares a long prefix
+ *   gdn_moe_step             a whole mixture-of-experts layer, few tokens
+ *
+ * Attention dimensions.  h_q query heads read h_kv key/value heads (query head
+ * h reads h / (h_q / h_kv)); d: head size, 64, 128 or 256; rot: rotated
+ * dimensions, the first rot of d, a multiple of 16, 0 for none; n_axes: position
+ * axes (1 .. GDN_ATTN_MAX_AXES; time, height and width of pictures and video
+ * are three); rope_pairs: 0 turns dimension i with i + rot/2, 1 turns 2i with
+ * 2i + 1; norm_eps: of the RMS norms; scale: of the scores, 0 for 1/sqrt(d).
+ *
+ * Cache.  k_cache and v_cache are bf16 [pages][page][h_kv][d], dense: row
+ * r = page_index * page + offset holds one token.
+ */
+typedef struct gdn_attn_dims {
+  int h_q;
+  int h_kv;
+  int d;
+  int rot;
+  int n_axes;
+  int rope_pairs;
+  float norm_eps;
+  float scale;
+} gdn_attn_dims;
+
+#define GDN_ATTN_MAX_AXES 4
+#define GDN_ATTN_MAX_STEPS 8    /* most tokens per sequence of gdn_attn_decode_shared */
+#define GDN_ATTN_MAX_BATCH 1024 /* most sequences of gdn_attn_decode_shared */
+#define GDN_ATTN_MAX_ROWS 128   /* most steps * (h_q / h_kv) */
+
+/*
+ * q and k norms, rotary positions and the cache write, in one pass over a
+ * token's heads.  Per head x of q and k:
+ *   y   = x / sqrt(mean(x^2) + norm_eps) * w
+ *   phi = pos[axis(i)][t] * inv_freq[i],  i = 0 .. rot/2 - 1
+ *   (y_a, y_b) <- (y_a cos phi - y_b sin phi, y_b cos phi + y_a sin phi)
+ * all in fp32, rounded once to bf16.  The angle is reduced to a fraction of a
+ * turn in 64-bit fixed point, so far positions lose nothing.
+ *
+ *   q, k, v    bf16, element strides (token, head) each, both multiples of 8, the
+ *              d elements of a head contiguous: dense arrays or views of a
+ *              projection's output.  A null q, k or v leaves that part out.
+ *   q_norm_w, k_norm_w  fp32 [d], or null for no norm
+ *   inv_freq   fp64 [rot / 2], radians per position (null when rot is 0)
+ *   freq_axis  int32 [rot / 2], the axis of each frequency; null when n_axes is 1
+ *   pos        int32 [n_axes][tokens] (null when rot is 0)
+ *   slot       int32 [tokens]: the cache row of each token; negative: not stored.
+ *              Null: token t goes to row t.
+ *   cache_rows rows of the caches (pages * page); a slot or an axis outside its
+ *              range sets GDN_ERR_DEVICE_BOUNDS and the row is not stored (an
+ *              axis out of range reads as axis 0)
+ *   q_out      bf16 [tokens][h_q][d]; it may be q itself when q is dense
+ *   k_cache, v_cache  bf16 [cache_rows][h_kv][d]
+ * Two tokens with the same slot leave one of their rows there.
+ */
+gdn_status gdn_attn_prep(const gdn_attn_dims* dims, long long tokens, const void* q,
+                         long long q_token_stride, long long q_head_stride, const void* k,
+                         long long k_token_stride, long long k_head_stride, const void* v,
+                         long long v_token_stride, long long v_head_stride,
+                         const float* q_norm_w, const float* k_norm_w, const double* inv_freq,
+                         const int32_t* freq_axis, const int32_t* pos, const int32_t* slot,
+                         long long cache_rows, void* q_out, void* k_cache, void* v_cache,
+                         int32_t* device_status, void* stream);
+
+/*
+ * Attention of a batch of sequences that share one prefix.  Sequence b has
+ * `steps` query tokens (1 in plain decode, more when drafted tokens are
+ * verified) and attends to the prefix's prefix_len tokens and then to its own
+ * tail of tail_len[b] tokens, the last `steps` of which are the query tokens
+ * themselves: query i sees the tail's tokens 0 .. tail_len[b] - steps + i.
+ *   out = softmax(scale q [K_prefix; K_tail]^T) [V_prefix; V_tail] * sigmoid(gate)
+ * The prefix is read once for the whole batch.  A query that sees no token at
+ * all gives zeros.
+ *
+ *   page          tokens per page: 16, 32, 64, 128 or 256
+ *   n_pages       pages of the caches
+ *   q             bf16 [batch][steps][h_q][d]
+ *   prefix_pages  int32 [ceil(prefix_len / page)]; null when prefix_len is 0
+ *   prefix_len    tokens of the prefix, on the host (a step's launches do not
+ *                 depend on the tails' lengths, so a captured step stays valid
+ *                 while they grow)
+ *   tail_pages    int32 [batch][tail_width], entries past a tail's end unread;
+ *                 null when tail_width is 0 (no tails)
+ *   tail_len      int32 [batch], device; null when tail_width is 0
+ *   gate          null, or bf16 with element strides (token, head), multiples of
+ *                 8, token = b * steps + i
+ *   out           bf16 [batch][steps][h_q][d]
+ *   workspace     >= gdn_attn_decode_shared_workspace_bytes, 256-byte aligned
+ * A page index outside [0, n_pages) or a tail length outside
+ * [0, tail_width * page] sets GDN_ERR_DEVICE_BOUNDS; the sequences that reach it
+ * have unspecified outputs (nothing outside the caches is read).
+ * The order of a row's sums depends on the batch, the lengths and the GPU's SM
+ * count, and on nothing else: equal calls give equal bits, but a sequence's last
+ * bits may differ between batches.
+ */
+size_t gdn_attn_decode_shared_workspace_bytes(const gdn_attn_dims* dims, int batch, int steps);
+gdn_status gdn_attn_decode_shared(const gdn_attn_dims* dims, int page, long long n_pages,
+                                  int batch, int steps, const void* q, const void* k_cache,
+                                  const void* v_cache, const int32_t* prefix_pages,
+                                  long long prefix_len, const int32_t* tail_pages,
+                                  int tail_width, const int32_t* tail_len, const void* gate,
+                                  long long gate_token_stride, long long gate_head_stride,
+                                  void* out, void* workspace, size_t workspace_bytes,
+                                  int32_t* device_status, void* stream);
+
+/*
+ * A whole mixture-of-experts layer for a few tokens.  Per token x:
+ *   p   = softmax(W_router x) over the experts
+ *   top = the top_k largest (ties to the lowest index), weights p, divided by
+ *         their sum when renorm is set
+ *   y   = sum over top of weight_e W_down,e (silu(W_gate,e x) * (W_up,e x))
+ *         + sigmoid(w_shared_gate . x) W_down,s (silu(W_gate,s x) * (W_up,s x))
+ * the last line when shared_inter > 0 (without w_shared_gate its factor is 1).
+ *
+ *   x            bf16 [tokens][hidden], tokens 0 .. GDN_MOE_MAX_TOKENS
+ *   w_router     bf16 [experts][hidden]
+ *   w_gate_up    bf16 [experts][2 inter][hidden], the inter gate rows first
+ *   w_down       bf16 [experts][hidden][inter]
+ *   w_shared_gate_up [2 shared_inter][hidden], w_shared_down [hidden][shared_inter],
+ *   w_shared_gate [hidden]: bf16; null when shared_inter is 0
+ *   y            [tokens][hidden], bf16 or fp32 (out_dtype)
+ *   topk_id      null or int32 [tokens][top_k];  topk_w null or fp32 [tokens][top_k]
+ *   workspace    >= gdn_moe_step_workspace_bytes, 256-byte aligned
+ * hidden, inter and shared_inter are multiples of 8, at most 16384; experts at
+ * most 1024; top_k at most 32.  Router logits are summed so that they are exact
+ * to about 48 bits; everything else is summed in fp32, the activations between
+ * the two products are carried as pairs of bf16 (16 bits of significand).  A
+ * token's result does not depend on the other tokens of the call, bit for bit.
+ */
+typedef struct gdn_moe_dims {
+  int hidden;
+  int inter;
+  int experts;
+  int top_k;
+  int shared_inter;
+  int renorm;
+} gdn_moe_dims;
+
+#define GDN_MOE_MAX_TOKENS 64
+
+size_t gdn_moe_step_workspace_bytes(const gdn_moe_dims* dims, int tokens);
+gdn_status gdn_moe_step(const gdn_moe_dims* dims, int tokens, const void* x, const void* w_router,
+                        const void* w_gate_up, const void* w_down, const void* w_shared_gate_up,
+                        const void* w_shared_down, const void* w_shared_gate, void* y,
+                        int out_dtype, int32_t* topk_id, float* topk_w, void* workspace,
+                        size_t workspace_bytes, int32_t* device_status, void* stream);
+
 /* Waits for the stream, then reads a device status word (the first 4 bytes
  * of a prefill workspace, or a decode device_status word) into *code:
  * GDN_OK or the first device-side error recorded.  Returns GDN_ERR_CUDA if
