@@ -1,81 +1,919 @@
-// gdn_attn_shared.cu -- attention of a batch of sequences that share a prefix.
+// gdn_attn_shared.cu -- attention of a batch of sequences that share a long
+// prefix, each with a paged tail of its own (tcgen05 tensor cores).
 //
-// One CTA per (query row, head), four warps that take every fourth key: the
-// running maximum, sum and output of the softmax per warp, joined at the end.
+// Mathematics.  Row r = (sequence, step, query head) wants
+//   o = sum_j e^{s_j - m} v_j / sum_j e^{s_j - m},  s_j = scale q.k_j,
+// over the prefix's keys and then its tail's.  Any partition of the keys into
+// ranges can be summed apart: a range leaves (m, l = sum e^{s - m}, O = sum
+// e^{s - m} v), and ranges join as sum 2^{m_i - M} O_i / sum 2^{m_i - M} l_i.
+//
+// Jobs.  The rows of one key head meet the prefix together: 128 rows (whole
+// tokens of h_q / h_kv heads) by the prefix's keys is one job, a dense product
+// that reads the prefix once per 128 rows instead of once per row.  A
+// sequence's tail by its own steps * h_q / h_kv rows is another, bound by its
+// bytes.  Both are rows x keys x d products and run through the same pipeline;
+// a tail's unused rows of the 128 cost tensor time that its loads hide.
+//
+// Split.  All jobs' tiles of 128 keys are laid end to end, weighted by what a
+// tile costs, and every CTA (one per SM) takes an equal share, so a single
+// long prefix fills the GPU as well as many short tails do.  A share ends
+// where it ends, inside a job if need be: a job's ranges are joined by a
+// second launch.  The shares follow from the lengths alone, so equal calls add
+// in equal order.  Each CTA sums the tails' costs itself from tail_len on the
+// device; the host needs no lengths, and a captured step stays valid.
+//
+// Pipeline per CTA, over its tiles without a pause between jobs:
+//   warp 0     TMA: q tiles, K and V in a ring of stages (128-byte swizzle); a
+//              lane per box, a box per page piece of up to 64 rows and 64
+//              dimensions
+//   warp 1     S = Q K^T of tile i + 1, then O += P V of tile i, so that the
+//              tensor cores work through the softmax of the next tile
+//   warps 2-9  softmax: a thread holds half a row's 128 scores; P goes back to
+//              tensor memory as bf16 over the scores it came from and is read
+//              from there as the A operand
+// TMEM: O (d columns) and two score tiles (2 x 128).  O is rescaled only when a
+// row's maximum has grown by more than 8 binary orders (P <= 2^8 fits bf16 as
+// well as P <= 1 does, and the sums are fp32), so almost never.
+//
+// Rounding: weights P to bf16 (half a step, 2^-8 of each weight), because the
+// tensor cores take both operands in one 16-bit type; scores, maxima, sums and
+// outputs stay fp32 until the one rounding of the result.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include "../../include/gdn.h"
 #include "gdn_common.cuh"
 #include "gdn_launch.h"
+#include "gdn_prefill.cuh"
+#include "gdn_tc.cuh"
 
 namespace gdn {
 namespace {
 
+constexpr int kTile = 128;            // keys per tile
+constexpr int kMaxCtas = 160;         // shares the workspace has room for
+constexpr int kThreads = 320;
+constexpr int kSoftWarps = 8;
+constexpr int kMaxStages = 13;
+constexpr uint32_t kCtrlBytes = 3072;
+
+// What a tile costs, in quarters of a prefix tile's products: a tail tile is
+// bound by its loads; each job has a fixed part (its rows in and out).
+constexpr int kCostPrefix = 4, kCostTail = 6, kCostJob = 3;
+
+// Shape of one call, the same for both launches.
+struct Plan {
+  int ntok, h_kv, G, R;        // query tokens, key heads, group, rows of a tail job
+  int tpb, nmb;                // tokens per prefix job, prefix jobs per key head
+  int np, ncta;                // prefix jobs, shares
+  long long ptiles;            // prefix tiles
+  long long wp;                // cost of all prefix jobs
+};
+
+struct SharedParams {
+  AttnSharedArgs a;
+  Plan pl;
+  long long* tail_cost;        // [batch + 1] running cost of the tails (relative to wp)
+  float4* ml;                  // (m, l half 0, l half 1, -) per slot row
+  float* opart;                // per slot: [d / 4][rows][4]
+};
+
 template <int D>
-__global__ void __launch_bounds__(128) attn_shared_simple(const AttnSharedArgs p) {
-  constexpr int E = D / 32;
-  const int tok = blockIdx.x, h = blockIdx.y, b = tok / p.steps, step = tok % p.steps;
-  const int hk = h / (p.h_q / p.h_kv);
+struct Cfg {
+  static constexpr int KD = D < 128 ? D : 128;          // dimensions of a K stage (128 keys)
+  static constexpr int NKS = D / KD;                    // K stages per tile
+  static constexpr int VR = D == 256 ? 64 : 128;        // keys of a V stage (all dimensions)
+  static constexpr int NVS = kTile / VR;
+  static constexpr uint32_t STAGE = kTile * KD * 2;     // = VR * D * 2
+  static constexpr int NST = D == 256 ? 5 : (D == 128 ? 6 : 12);
+  static constexpr uint32_t QBYTES = 128 * D * 2;
+  static constexpr uint32_t SMEM = kCtrlBytes + QBYTES + NST * STAGE;
+  static constexpr uint32_t IDESC_QK = tc::idesc_bf16(128, kTile, 0, 0);
+  static constexpr uint32_t IDESC_PV = tc::idesc_bf16(128, D, 0, 1);
+  static constexpr uint64_t DESC_K = tc::sdesc_sw128(16, 1024);
+  static constexpr uint64_t DESC_V = tc::sdesc_sw128(VR * 128, 1024);
+  static constexpr uint32_t T_S = 256;                  // TMEM column of the score tiles
+  static_assert(STAGE == (uint32_t)VR * D * 2, "one ring for K and V");
+  static_assert(SMEM <= 227 * 1024, "shared memory");
+  static_assert(NST <= kMaxStages, "barriers");
+};
+
+struct Ctrl {
+  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t q_full[2], q_done[2], s_full[2], p_ready[2];
+  uint64_t pv_done;            // each tile's O product
+  uint64_t seg_done;           // a segment's last
+  uint64_t pair[4];            // the two warps of a row quarter
+  uint32_t tmem;
+  int job0;
+  long long x0, x1, pos0;
+  float red[2][2][128];        // row maxima of a half tile, by tile parity
+};
+static_assert(sizeof(Ctrl) <= kCtrlBytes, "control block");
+
+__device__ __forceinline__ void arrive(uint64_t* mbar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(tc::smem_u32(mbar)) : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* tm, int x, int y, int z, uint64_t* mbar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+      "[%5];" ::"r"(tc::smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(tc::smem_u32(mbar))
+      : "memory");
+}
+
+// D[tmem] (+)= A[tmem] * B[smem], one K = 16 step.
+__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate));
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ long long share_start(const Plan& pl, long long total, int c) {
+  return total * c / pl.ncta;
+}
+__device__ __forceinline__ int tail_tiles(int len) { return (len + kTile - 1) / kTile; }
+__device__ __forceinline__ long long tail_cost_of(int len) {
+  return len > 0 ? (long long)tail_tiles(len) * kCostTail + kCostJob : 0;
+}
+// Tiles of a job that starts at `pos` which lie before x.
+__device__ __forceinline__ long long tiles_before(long long x, long long pos, int per_tile, long long n) {
+  const long long t = (x - pos - kCostJob) / per_tile;
+  return x - pos - kCostJob <= 0 ? 0 : (t < n ? t : n);
+}
+// A tail's length, clamped into its table.
+__device__ __forceinline__ int tail_length(const AttnSharedArgs& a, int b) {
+  if (a.tail_width == 0) return 0;
+  const int n = a.tail_len[b], top = a.tail_width * a.page;
+  return n < 0 ? 0 : (n > top ? top : n);
+}
+
+// Walks the tiles of one share, job by job.  Every role keeps its own.
+struct Cursor {
+  long long pos;       // cost position of the job `job`
+  long long x0, x1;
+  int job;             // next job to look at
+  int len;             // of the current sequence's tail (jobs of one sequence are adjacent)
+  int seg;             // segments begun, minus one
+  // the current segment
+  bool prefix, valid, first, last;
+  int hk, mb;          // key head; block of rows (prefix) or sequence (tail)
+  int slot_job;        // prefix job, or tail job
+  long long t, t1, keys;
+
+  __device__ __forceinline__ void init(const SharedParams& p, const Ctrl* c) {
+    pos = c->pos0;
+    x0 = c->x0;
+    x1 = c->x1;
+    job = c->job0;
+    len = -1;
+    seg = -1;
+    valid = true;
+    find(p);
+  }
+  __device__ __forceinline__ void find(const SharedParams& p) {
+    const Plan& pl = p.pl;
+    const int njobs = pl.np + p.a.batch * pl.h_kv;
+    while (true) {
+      if (job >= njobs || pos >= x1) {
+        valid = false;
+        return;
+      }
+      long long n, cost;
+      int per;
+      prefix = job < pl.np;
+      if (prefix) {
+        hk = job / pl.nmb;
+        mb = job - hk * pl.nmb;
+        slot_job = job;
+        n = pl.ptiles;
+        per = kCostPrefix;
+        keys = p.a.prefix_len;
+        cost = n * kCostPrefix + kCostJob;
+      } else {
+        slot_job = job - pl.np;
+        mb = slot_job / pl.h_kv;
+        hk = slot_job - mb * pl.h_kv;
+        if (hk == 0 || len < 0) len = tail_length(p.a, mb);
+        n = tail_tiles(len);
+        per = kCostTail;
+        keys = len;
+        cost = tail_cost_of(len);
+      }
+      const long long a = tiles_before(x0, pos, per, n), b = tiles_before(x1, pos, per, n);
+      pos += cost;
+      ++job;
+      if (a < b) {
+        t = a;
+        t1 = b;
+        first = true;
+        last = a + 1 == b;
+        ++seg;
+        return;
+      }
+    }
+  }
+  __device__ __forceinline__ void next(const SharedParams& p) {
+    if (++t < t1) {
+      first = false;
+      last = t + 1 == t1;
+    } else {
+      find(p);
+    }
+  }
+  // keys of the current tile
+  __device__ __forceinline__ int count() const {
+    const long long r = keys - t * kTile;
+    return r < kTile ? (int)r : kTile;
+  }
+};
+
+template <int D>
+struct Ring {
+  int s = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void step() {
+    if (++s == Cfg<D>::NST) {
+      s = 0;
+      ph ^= 1u;
+    }
+  }
+};
+
+// One wait of a role: false (and the status word) when it gave up.
+__device__ __forceinline__ bool wait_for(const AttnSharedArgs& a, uint64_t* mbar, uint32_t parity) {
+  if (tc::mbar_wait(mbar, parity, kWaitBudget)) return true;
+  record_status(a.status, GDN_ERR_DEVICE_TIMEOUT);
+  return false;
+}
+
+// 64 scores of this thread's row: both loads in flight, one wait.
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, float (&v)[64]) {
+  uint32_t r[64];
+#define GDN_LD32(o, at)                                                                                          \
+  asm volatile(                                                                                                  \
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%"  \
+      "18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"                                          \
+      : "=r"(r[o + 0]), "=r"(r[o + 1]), "=r"(r[o + 2]), "=r"(r[o + 3]), "=r"(r[o + 4]), "=r"(r[o + 5]),          \
+        "=r"(r[o + 6]), "=r"(r[o + 7]), "=r"(r[o + 8]), "=r"(r[o + 9]), "=r"(r[o + 10]), "=r"(r[o + 11]),        \
+        "=r"(r[o + 12]), "=r"(r[o + 13]), "=r"(r[o + 14]), "=r"(r[o + 15]), "=r"(r[o + 16]), "=r"(r[o + 17]),    \
+        "=r"(r[o + 18]), "=r"(r[o + 19]), "=r"(r[o + 20]), "=r"(r[o + 21]), "=r"(r[o + 22]), "=r"(r[o + 23]),    \
+        "=r"(r[o + 24]), "=r"(r[o + 25]), "=r"(r[o + 26]), "=r"(r[o + 27]), "=r"(r[o + 28]), "=r"(r[o + 29]),    \
+        "=r"(r[o + 30]), "=r"(r[o + 31])                                                                         \
+      : "r"(at))
+  GDN_LD32(0, taddr);
+  GDN_LD32(32, taddr + 32);
+#undef GDN_LD32
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                       const __grid_constant__ CUtensorMap tm_qp, const __grid_constant__ CUtensorMap tm_qt,
+                       const __grid_constant__ SharedParams p) {
+  using C = Cfg<D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Ctrl* ctl = reinterpret_cast<Ctrl*>(smem);
+  const AttnSharedArgs& a = p.a;
+  const Plan& pl = p.pl;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  __shared__ float so[4][D], sm[4], sl[4];
-  float q[E], o[E], m = -INFINITY, den = 0.0f;
-  for (int e = 0; e < E; ++e) {
-    q[e] = bf16_to_f32(p.q[((size_t)tok * p.h_q + h) * D + e * 32 + lane]) * p.scale;
-    o[e] = 0.0f;
+  const uint32_t base = tc::smem_u32(smem);
+  uint8_t* const qs = smem + kCtrlBytes;
+  uint8_t* const ring = qs + C::QBYTES;
+  if (base & 1023u) {   // the swizzle atoms need it; shared memory starts there
+    record_status(a.status, GDN_ERR_CUDA);
+    return;
   }
-  long long tail = p.tail_width > 0 ? p.tail_len[b] : 0;
-  if (tail < 0 || tail > (long long)p.tail_width * p.page) {
-    record_status(p.status, GDN_ERR_DEVICE_BOUNDS);
-    tail = 0;
-  }
-  const long long seen = max(0LL, tail - p.steps + 1 + step);
-  for (long long j = warp; j < p.prefix_len + seen; j += 4) {
-    const bool pre = j < p.prefix_len;
-    const long long jj = pre ? j : j - p.prefix_len;
-    const long long pg = pre ? p.prefix_pages[jj / p.page] : p.tail_pages[(size_t)b * p.tail_width + jj / p.page];
-    if (pg < 0 || pg >= p.n_pages) {
-      record_status(p.status, GDN_ERR_DEVICE_BOUNDS);
-      continue;
+
+  // ---- this CTA's share: the running cost of the tails, then a search ----
+  long long* scan = reinterpret_cast<long long*>(ring);   // [batch + 1] and warp totals, before the ring is used
+  long long* wsum = scan + GDN_ATTN_MAX_BATCH + 8;
+  {
+    constexpr int PER = 4;
+    static_assert(kThreads * PER >= GDN_ATTN_MAX_BATCH, "one pass");
+    long long v[PER], sum = 0;
+    for (int i = 0; i < PER; ++i) {
+      const int b = threadIdx.x * PER + i;
+      v[i] = 0;
+      if (b < a.batch && a.tail_width > 0) {
+        const int n = a.tail_len[b];
+        if ((n < 0 || (long long)n > (long long)a.tail_width * a.page) && blockIdx.x == 0)
+          record_status(a.status, GDN_ERR_DEVICE_BOUNDS);
+        v[i] = tail_cost_of(tail_length(a, b)) * pl.h_kv;
+      }
+      sum += v[i];
     }
-    const size_t row = ((size_t)(pg * p.page + jj % p.page) * p.h_kv + hk) * D;
-    float s = 0.0f;
-    for (int e = 0; e < E; ++e) s = fmaf(q[e], bf16_to_f32(p.k_cache[row + e * 32 + lane]), s);
-    s = warp_sum(s);
-    const float mn = fmaxf(m, s);
-    if (mn == -INFINITY) continue;
-    const float c = __expf(m - mn), w = __expf(s - mn);
-    den = den * c + w;
-    for (int e = 0; e < E; ++e) o[e] = o[e] * c + w * bf16_to_f32(p.v_cache[row + e * 32 + lane]);
-    m = mn;
+    long long inc = sum;
+    for (int m = 1; m < 32; m <<= 1) {
+      const long long o = __shfl_up_sync(0xffffffffu, inc, m);
+      if (lane >= m) inc += o;
+    }
+    if (lane == 31) wsum[warp] = inc;
+    __syncthreads();
+    long long run = inc - sum;
+    for (int w = 0; w < warp; ++w) run += wsum[w];
+    for (int i = 0; i < PER; ++i) {
+      const int b = threadIdx.x * PER + i;
+      if (b <= a.batch) {
+        scan[b] = run;
+        if (blockIdx.x == 0) p.tail_cost[b] = run;
+      }
+      run += v[i];
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      const long long total = pl.wp + scan[a.batch];
+      ctl->x0 = share_start(pl, total, blockIdx.x);
+      ctl->x1 = share_start(pl, total, blockIdx.x + 1);
+      if (ctl->x0 < pl.wp) {
+        const long long cost = pl.ptiles * kCostPrefix + kCostJob;
+        const long long j = ctl->x0 / cost;
+        ctl->job0 = (int)j;
+        ctl->pos0 = j * cost;
+      } else {
+        const long long x = ctl->x0 - pl.wp;
+        int lo = 0, hi = a.batch;      // the last b with scan[b] <= x
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (scan[mid] <= x) lo = mid; else hi = mid;
+        }
+        ctl->job0 = pl.np + lo * pl.h_kv;
+        ctl->pos0 = pl.wp + scan[lo];
+      }
+      for (int s = 0; s < C::NST; ++s) {
+        tc::mbar_init(&ctl->full[s], 1);
+        tc::mbar_init(&ctl->empty[s], 1);
+      }
+      for (int i = 0; i < 2; ++i) {
+        tc::mbar_init(&ctl->q_full[i], 1);
+        tc::mbar_init(&ctl->q_done[i], 1);
+        tc::mbar_init(&ctl->s_full[i], 1);
+        tc::mbar_init(&ctl->p_ready[i], kSoftWarps);
+      }
+      tc::mbar_init(&ctl->pv_done, 1);
+      tc::mbar_init(&ctl->seg_done, 1);
+      for (int i = 0; i < 4; ++i) tc::mbar_init(&ctl->pair[i], 2);
+      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
   }
-  for (int e = 0; e < E; ++e) so[warp][e * 32 + lane] = o[e];
-  if (lane == 0) { sm[warp] = m; sl[warp] = den; }
+  if (warp == 1) tc::tmem_alloc(&ctl->tmem, 512);
+  tc::fence_proxy_async();   // the scan's writes before the ring's copies
+  tc::fence_before_sync();
   __syncthreads();
-  const float mt = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
-  for (int i = threadIdx.x; i < D; i += 128) {
-    float a = 0.0f, l = 0.0f;
-    for (int w = 0; w < 4; ++w) {
-      const float c = sm[w] == -INFINITY ? 0.0f : __expf(sm[w] - mt);
-      a += c * so[w][i];
-      l += c * sl[w];
+  tc::fence_after_sync();
+  const uint32_t tmem = ctl->tmem;
+  // the q region holds two tail jobs' rows when they are few, else one
+  const bool halves = pl.R <= 64;
+
+  if (warp == 0) {
+    // ---- loads ----
+    Cursor ck, cv;
+    ck.init(p, ctl);
+    cv.init(p, ctl);
+    Ring<D> r;
+    const int rpb = a.page < 64 ? a.page : 64;           // rows per box
+    const int shift = 31 - __clz(a.page);
+    bool ok = true, prev_whole = true;
+    long long issued = 0;
+    // `n` rows from `key` on, `db` blocks of 64 dimensions from block d0 on: lane = box
+    auto load_rows = [&](const CUtensorMap* tm, const Cursor& c, long long key, int n, int stage_rows, int db,
+                         int d0) {
+      ok = wait_for(a, &ctl->empty[r.s], r.ph ^ 1u);
+      if (!ok) return;
+      const int nb = (n + rpb - 1) / rpb;
+      if (lane == 0) mbar_expect_tx(&ctl->full[r.s], (uint32_t)(nb * rpb * 128 * db));
+      __syncwarp();
+      if (lane < nb * db) {
+        const int j = lane / db, d = lane - j * db;
+        const long long row = key + j * rpb;
+        const int32_t* table = c.prefix ? a.prefix_pages : a.tail_pages + (size_t)c.mb * a.tail_width;
+        int pg = table[row >> shift];
+        if (pg < 0 || pg >= a.n_pages) {
+          record_status(a.status, GDN_ERR_DEVICE_BOUNDS);
+          pg = 0;
+        }
+        tma_load_2d(ring + r.s * C::STAGE + d * (stage_rows * 128) + j * (rpb * 128), tm, c.hk * D + (d0 + d) * 64,
+                    (int)(((long long)pg << shift) + (row & (a.page - 1))), &ctl->full[r.s]);
+      }
+      __syncwarp();
+      ++issued;
+      r.step();
+    };
+    auto load_k = [&]() {
+      if (ck.first) {
+        const int s = ck.seg, h = s & 1;
+        const bool whole = ck.prefix || !halves;
+        if (s >= 2) ok = wait_for(a, &ctl->q_done[h], (uint32_t)((s >> 1) - 1) & 1u);
+        if (ok && s >= 1 && (whole || prev_whole))
+          ok = wait_for(a, &ctl->q_done[h ^ 1], (uint32_t)((s - 1) >> 1) & 1u);
+        if (!ok) return;
+        prev_whole = whole;
+        const uint32_t bytes = (uint32_t)(ck.prefix ? pl.tpb * pl.G : pl.R) * 128;
+        if (lane == 0) mbar_expect_tx(&ctl->q_full[h], bytes * (D / 64));
+        __syncwarp();
+        if (lane < D / 64)
+          tma_load_3d(qs + lane * 16384 + (whole ? 0 : h * 8192), ck.prefix ? &tm_qp : &tm_qt, lane * 64,
+                      ck.hk * pl.G, ck.mb * (ck.prefix ? pl.tpb : a.steps), &ctl->q_full[h]);
+        __syncwarp();
+      }
+      const int n = ck.count();
+      for (int i = 0; i < C::NKS && ok; ++i) load_rows(&tm_k, ck, ck.t * kTile, n, kTile, C::KD / 64, i * (C::KD / 64));
+    };
+    if (ck.valid) {
+      load_k();
+      if (ok) ck.next(p);
+      while (ok && cv.valid) {
+        if (ck.valid) {
+          load_k();
+          if (!ok) break;
+          ck.next(p);
+        }
+        const int n = cv.count();
+        for (int i = 0; i < C::NVS && ok; ++i)
+          if (n > i * C::VR)
+            load_rows(&tm_v, cv, cv.t * kTile + i * C::VR, min(n - i * C::VR, C::VR), C::VR, D / 64, 0);
+        cv.next(p);
+      }
+      // take every used stage once more: the products' releases have landed before the CTA ends
+      for (int i = 0; i < C::NST && i < issued && ok; ++i) {
+        // step back over the newest stages
+        const int s = (r.s + C::NST - 1 - i) % C::NST;
+        const uint32_t ph = r.s - 1 - i >= 0 ? r.ph : r.ph ^ 1u;
+        ok = wait_for(a, &ctl->empty[s], ph);
+      }
     }
-    float r = l > 0.0f ? a / l : (l == 0.0f ? 0.0f : l);
-    if (p.gate) r *= sigmoid(bf16_to_f32(p.gate[(size_t)tok * p.gate_st + (size_t)h * p.gate_sh + i]));
-    p.out[((size_t)tok * p.h_q + h) * D + i] = f32_to_bf16(r);
+  } else if (warp == 1) {
+    // ---- products ----
+    Cursor cq, cp;
+    cq.init(p, ctl);
+    cp.init(p, ctl);
+    Ring<D> r;
+    bool ok = true;
+    uint32_t iq = 0, ip = 0;
+    const uint32_t qa = base + kCtrlBytes, ra = qa + C::QBYTES;
+    auto issue_qk = [&]() {
+      const int h = cq.seg & 1;
+      if (cq.first) {
+        ok = wait_for(a, &ctl->q_full[h], (uint32_t)(cq.seg >> 1) & 1u);
+        if (!ok) return;
+      }
+      const uint32_t q0 = qa + ((cq.prefix || !halves) ? 0 : h * 8192);
+      const uint32_t d = tmem + C::T_S + (iq & 1u) * kTile;
+      for (int i = 0; i < C::NKS; ++i) {
+        ok = wait_for(a, &ctl->full[r.s], r.ph);
+        if (!ok) return;
+        tc::fence_after_sync();
+        if (lane == 0) {
+          const uint32_t k0 = ra + r.s * C::STAGE;
+#pragma unroll
+          for (int k = 0; k < C::KD / 16; ++k) {
+            const int db = k >> 2, kk = k & 3;
+            tc::mma_bf16(d, tc::sdesc_at(C::DESC_K, q0 + (i * (C::KD / 64) + db) * 16384 + kk * 32),
+                         tc::sdesc_at(C::DESC_K, k0 + db * 16384 + kk * 32), C::IDESC_QK, (i | k) != 0);
+          }
+          tc::mma_commit(&ctl->empty[r.s]);
+        }
+        __syncwarp();
+        r.step();
+      }
+      if (lane == 0) {
+        tc::mma_commit(&ctl->s_full[iq & 1u]);
+        if (cq.last) tc::mma_commit(&ctl->q_done[h]);
+      }
+      __syncwarp();
+      ++iq;
+    };
+    auto issue_pv = [&]() {
+      ok = wait_for(a, &ctl->p_ready[ip & 1u], (ip >> 1) & 1u);
+      if (!ok) return;
+      const uint32_t pa = tmem + C::T_S + (ip & 1u) * kTile;
+      const int n = cp.count();
+      for (int i = 0; i < C::NVS; ++i) {
+        const int ni = min(n - i * C::VR, C::VR);
+        if (ni <= 0) break;
+        ok = wait_for(a, &ctl->full[r.s], r.ph);
+        if (!ok) return;
+        const int steps = (ni + 15) >> 4;
+        // a masked key has weight zero, but zero times a stale NaN is NaN: its
+        // values in the last 16 rows become zeros
+        if (ni & 15) {
+          uint8_t* v = ring + r.s * C::STAGE;
+          const int z = 16 - (ni & 15), words = z * (D / 8);   // 16-byte pieces
+          for (int w = lane; w < words; w += 32) {
+            const int row = ni + w / (D / 8), c = w % (D / 8);
+            *reinterpret_cast<uint4*>(v + (c >> 3) * (C::VR * 128) + row * 128 + ((c & 7) << 4)) =
+                make_uint4(0, 0, 0, 0);
+          }
+          tc::fence_proxy_async();
+          __syncwarp();
+        }
+        tc::fence_after_sync();
+        if (lane == 0) {
+          const uint32_t v0 = ra + r.s * C::STAGE;
+          for (int k = 0; k < steps; ++k) {
+            const int key = i * C::VR + k * 16;   // keys 64 .. 127 lie 64 columns on
+            mma_bf16_ts(tmem, pa + (key >> 6) * 64 + ((key & 63) >> 1), tc::sdesc_at(C::DESC_V, v0 + k * 2048),
+                        C::IDESC_PV, !(cp.first && i == 0 && k == 0));
+          }
+          tc::mma_commit(&ctl->empty[r.s]);
+        }
+        __syncwarp();
+        r.step();
+      }
+      if (lane == 0) {
+        tc::mma_commit(&ctl->pv_done);
+        if (cp.last) tc::mma_commit(&ctl->seg_done);
+      }
+      __syncwarp();
+      ++ip;
+    };
+    if (cq.valid) {
+      issue_qk();
+      if (ok) cq.next(p);
+      while (ok && cp.valid) {
+        if (cq.valid) {
+          issue_qk();
+          if (!ok) break;
+          cq.next(p);
+        }
+        issue_pv();
+        if (ok) cp.next(p);
+      }
+    }
+  } else {
+    // ---- softmax and the share's partial results ----
+    Cursor c;
+    c.init(p, ctl);
+    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    const int row = quarter * 32 + lane;
+    const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+    const float sc = a.scale * 1.44269504088896340736f;   // scores in binary orders
+    uint32_t it = 0, met = 0;
+    float m = -INFINITY, l = 0.0f;
+    bool ok = true;
+    while (ok && c.valid) {
+      const int rows = c.prefix ? min(pl.tpb, pl.ntok - c.mb * pl.tpb) * pl.G : pl.R;
+      const bool active = quarter * 32 < rows;
+      ok = wait_for(a, &ctl->s_full[it & 1u], (it >> 1) & 1u);
+      if (!ok) break;
+      if (active) {
+        tc::fence_after_sync();
+        const uint32_t ts = tmem + lanes + C::T_S + (it & 1u) * kTile + half * 64;
+        float s[64];
+        tmem_ld64(ts, s);
+        // keys this row sees in its half of the tile
+        long long see = c.keys - c.t * kTile;
+        if (!c.prefix) see -= a.steps - 1 - row / pl.G;
+        int nv = row < rows ? (int)min(see, (long long)kTile) - half * 64 : 0;
+        if (!__all_sync(0xffffffffu, nv >= 64)) {
+#pragma unroll
+          for (int j = 0; j < 64; ++j) s[j] = j < nv ? s[j] : -INFINITY;
+        }
+        float mx = s[0];
+#pragma unroll
+        for (int j = 1; j < 64; ++j) mx = fmaxf(mx, s[j]);
+        ctl->red[it & 1u][half][row] = mx;
+        __syncwarp();
+        if (lane == 0) arrive(&ctl->pair[quarter]);
+        ok = wait_for(a, &ctl->pair[quarter], met);
+        if (!ok) break;
+        met ^= 1u;
+        mx = fmaxf(mx, ctl->red[it & 1u][half ^ 1][row]) * sc;
+        if (c.first) {
+          m = mx;
+          l = 0.0f;
+        } else {
+          const bool grow = mx > m + 8.0f;
+          if (__any_sync(0xffffffffu, grow)) {
+            // O is behind by 2^8 or more in some row: bring it to the new maximum.
+            // (This tile's scores came after the products of tile it - 2, so the
+            // wait can only be for those of tile it - 1.)
+            ok = wait_for(a, &ctl->pv_done, (it - 1) & 1u);
+            if (!ok) break;
+            tc::fence_after_sync();
+            const float f = grow ? ex2(m - mx) : 1.0f;
+            if (grow) {
+              m = mx;
+              l *= f;
+            }
+#pragma unroll 1
+            for (int o = 0; o < D / 2; o += 32) {
+              float v[32];
+              const uint32_t at = tmem + lanes + half * (D / 2) + o;
+              tc::tmem_ld32(at, v);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] *= f;
+              tc::tmem_st32(at, v);
+            }
+          }
+        }
+        const float mu = m == -INFINITY ? 0.0f : m;
+        float pk[32];
+        float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          const float e0 = ex2(fmaf(s[2 * j], sc, -mu)), e1 = ex2(fmaf(s[2 * j + 1], sc, -mu));
+          s0 += e0;
+          s1 += e1;
+          pk[j] = __uint_as_float(pack_bf16x2(e0, e1));
+        }
+        l += s0 + s1;
+        tc::tmem_st32(ts, pk);
+      }
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) arrive(&ctl->p_ready[it & 1u]);
+      if (c.last) {
+        ok = wait_for(a, &ctl->seg_done, (uint32_t)c.seg & 1u);
+        if (!ok) break;
+        if (active) {
+          tc::fence_after_sync();
+          const int stride = c.prefix ? 128 : pl.R;
+          const long long slot = c.slot_job + (long long)blockIdx.x;
+          const long long row0 = c.prefix ? slot * 128 : (long long)(pl.np + (pl.np ? pl.ncta : 0)) * 128 + slot * pl.R;
+          if (row < rows) {
+            float* w = reinterpret_cast<float*>(p.ml + row0 + row);
+            if (half == 0) *reinterpret_cast<float2*>(w) = make_float2(m, l);
+            else w[2] = l;
+          }
+          float4* o4 = reinterpret_cast<float4*>(p.opart) + row0 * (D / 4) + row;
+#pragma unroll 1
+          for (int o = 0; o < D / 2; o += 32) {
+            float v[32];
+            tc::tmem_ld32(tmem + lanes + half * (D / 2) + o, v);
+            if (row < rows) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                o4[(long long)(half * (D / 8) + o / 4 + j) * stride] =
+                    make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+            }
+          }
+          tc::fence_before_sync();
+        }
+        __syncwarp();
+      }
+      ++it;
+      c.next(p);
+    }
   }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  if (warp == 1) tc::tmem_dealloc(tmem, 512);
+}
+
+// Joins a token's ranges: a CTA takes one query token, one key head and 64 of
+// its dimensions; a thread one group head and four dimensions of a share of the
+// ranges, the shares meeting in shared memory in a fixed order.
+constexpr int kJoinThreads = 256;
+
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) attn_shared_join(const __grid_constant__ SharedParams p) {
+  __shared__ float4 acc[kJoinThreads];
+  __shared__ float2 stat[kJoinThreads];
+  __shared__ long long list[2 * kMaxCtas];   // first slot row of each range
+  __shared__ int count[2][kJoinThreads / 32];
+  static_assert(kMaxCtas <= kJoinThreads, "a thread per share");
+  const AttnSharedArgs& a = p.a;
+  const Plan& pl = p.pl;
+  const int tok = blockIdx.x, hk = blockIdx.y, d0 = blockIdx.z * 16;   // in groups of 4 dimensions
+  const int b = tok / a.steps, step = tok - b * a.steps;
+  const long long t_lo = p.tail_cost[b], t_hi = p.tail_cost[b + 1];
+  const long long total = pl.wp + p.tail_cost[a.batch];
+  int n_prefix = 0, n_ranges = 0;
+
+  // the shares that hold ranges of this token's two jobs (its prefix block, its
+  // tail) for this key head
+  const int mb = tok / pl.tpb;
+  const int job[2] = {hk * pl.nmb + mb, b * pl.h_kv + hk};
+  const long long cost_tail = (t_hi - t_lo) / pl.h_kv;
+  const int stride[2] = {128, pl.R};                       // rows of a slot
+  const int in[2] = {(tok - mb * pl.tpb) * pl.G, step * pl.G};
+  const long long region[2] = {0, (long long)(pl.np ? pl.np + pl.ncta : 0) * 128};
+  {
+    bool has[2] = {false, false};
+    if (threadIdx.x < pl.ncta) {
+      const long long x0 = share_start(pl, total, threadIdx.x), x1 = share_start(pl, total, threadIdx.x + 1);
+      if (pl.np) {
+        const long long pos = job[0] * (pl.ptiles * kCostPrefix + kCostJob);
+        has[0] = tiles_before(x0, pos, kCostPrefix, pl.ptiles) < tiles_before(x1, pos, kCostPrefix, pl.ptiles);
+      }
+      if (cost_tail > 0) {
+        const long long pos = pl.wp + t_lo + hk * cost_tail, n = (cost_tail - kCostJob) / kCostTail;
+        has[1] = tiles_before(x0, pos, kCostTail, n) < tiles_before(x1, pos, kCostTail, n);
+      }
+    }
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    unsigned bal[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      bal[k] = __ballot_sync(0xffffffffu, has[k]);
+      if (lane == 0) count[k][warp] = __popc(bal[k]);
+    }
+    __syncthreads();
+    // prefix ranges first, then the tail's, each in the order of the shares
+    int at = 0;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      int mine = at;
+      for (int w = 0; w < kJoinThreads / 32; ++w) {
+        if (w < warp) mine += count[k][w];
+        at += count[k][w];
+      }
+      if (has[k])
+        list[mine + __popc(bal[k] & ((1u << lane) - 1))] = region[k] + (long long)(job[k] + threadIdx.x) * stride[k];
+      if (k == 0) n_prefix = at;
+    }
+    n_ranges = at;
+    __syncthreads();
+  }
+
+  const int items = pl.G * 16;
+  for (int i0 = 0; i0 < items; i0 += kJoinThreads) {
+    const int width = min(items - i0, kJoinThreads), groups = kJoinThreads / width;
+    const int grp = threadIdx.x / width, item = i0 + threadIdx.x % width;
+    const int c4 = d0 + item / pl.G, g = item % pl.G;
+    float M = -INFINITY, L = 0.0f;
+    float4 o = make_float4(0, 0, 0, 0);
+    if (grp < groups) {
+#pragma unroll 4
+      for (int i = grp; i < n_ranges; i += groups) {
+        const int k = i >= n_prefix;
+        const long long origin = list[i];
+        const int r = (k ? in[1] : in[0]) + g;
+        const float4 ml = p.ml[origin + r];
+        const float4 v = reinterpret_cast<const float4*>(p.opart)[origin * (D / 4) + (long long)c4 * (k ? stride[1] : stride[0]) + r];
+        const float mn = fmaxf(M, ml.x);
+        const float f = mn == -INFINITY ? 1.0f : ex2(M - mn), w = mn == -INFINITY ? 0.0f : ex2(ml.x - mn);
+        L = L * f + (ml.y + ml.z) * w;
+        o.x = o.x * f + v.x * w;
+        o.y = o.y * f + v.y * w;
+        o.z = o.z * f + v.z * w;
+        o.w = o.w * f + v.w * w;
+        M = mn;
+      }
+    }
+    acc[threadIdx.x] = o;
+    stat[threadIdx.x] = make_float2(M, L);
+    __syncthreads();
+    if (threadIdx.x < width) {
+      for (int q = 1; q < groups; ++q) {
+        const float2 st = stat[q * width + threadIdx.x];
+        const float4 v = acc[q * width + threadIdx.x];
+        const float mn = fmaxf(M, st.x);
+        if (mn == -INFINITY) continue;
+        const float f = ex2(M - mn), w = ex2(st.x - mn);
+        L = L * f + st.y * w;
+        o.x = o.x * f + v.x * w;
+        o.y = o.y * f + v.y * w;
+        o.z = o.z * f + v.z * w;
+        o.w = o.w * f + v.w * w;
+        M = mn;
+      }
+      // no key seen: zeros.  (A NaN sum stays NaN.)
+      const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+      float r[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
+      const int h = hk * pl.G + g;
+      if (a.gate) {
+        const uint2 gt = *reinterpret_cast<const uint2*>(a.gate + tok * a.gate_st + h * a.gate_sh + 4 * c4);
+        r[0] *= sigmoid(__uint_as_float(gt.x << 16));
+        r[1] *= sigmoid(__uint_as_float(gt.x & 0xffff0000u));
+        r[2] *= sigmoid(__uint_as_float(gt.y << 16));
+        r[3] *= sigmoid(__uint_as_float(gt.y & 0xffff0000u));
+      }
+      uint2 w;
+      w.x = pack_bf16x2(r[0], r[1]);
+      w.y = pack_bf16x2(r[2], r[3]);
+      *reinterpret_cast<uint2*>(a.out + ((long long)tok * a.h_q + h) * D + 4 * c4) = w;
+    }
+    __syncthreads();
+  }
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) !=
+            cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  }();
+  return fn;
+}
+
+bool encode(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+            const cuuint32_t* box) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = map_encoder();
+  if (!enc) return false;
+  const cuuint32_t one[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides, box, one,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The cache as a matrix of rows (token) by h_kv * d: boxes of 64 dimensions by a page piece.
+bool cache_map(CUtensorMap* m, const AttnSharedArgs& p, const void* base) {
+  const cuuint64_t dims[2] = {(cuuint64_t)p.h_kv * p.d, (cuuint64_t)p.n_pages * p.page};
+  const cuuint64_t strides[1] = {(cuuint64_t)p.h_kv * p.d * 2};
+  const cuuint32_t box[2] = {64, (cuuint32_t)(p.page < 64 ? p.page : 64)};
+  return encode(m, base, 2, dims, strides, box);
+}
+
+// q as [token][head][d]: boxes of 64 dimensions by a group's heads by `tokens` tokens.
+bool q_map(CUtensorMap* m, const AttnSharedArgs& p, int G, int tokens) {
+  const cuuint64_t dims[3] = {(cuuint64_t)p.d, (cuuint64_t)p.h_q, (cuuint64_t)p.batch * p.steps};
+  const cuuint64_t strides[2] = {(cuuint64_t)p.d * 2, (cuuint64_t)p.h_q * p.d * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)tokens};
+  return encode(m, p.q, 3, dims, strides, box);
+}
+
+size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
+
+Plan make_plan(int batch, int steps, int h_q, int h_kv, long long prefix_len, int ncta) {
+  Plan pl;
+  pl.h_kv = h_kv;
+  pl.G = h_q / h_kv;
+  pl.R = steps * pl.G;
+  pl.ntok = batch * steps;
+  pl.tpb = 128 / pl.G;
+  pl.nmb = (pl.ntok + pl.tpb - 1) / pl.tpb;
+  pl.ptiles = (prefix_len + kTile - 1) / kTile;
+  pl.np = pl.ptiles > 0 ? h_kv * pl.nmb : 0;
+  pl.ncta = ncta;
+  pl.wp = pl.np * (pl.ptiles * kCostPrefix + kCostJob);
+  return pl;
+}
+
+// Slot rows: a job's range in share c has slot job + c (each step to the next
+// range moves to the next job, the next share or both).
+size_t slot_rows(const Plan& pl, int batch, int ncta) {
+  return (size_t)(pl.np ? pl.np + ncta : 0) * 128 + ((size_t)batch * pl.h_kv + ncta) * pl.R;
+}
+
+template <int D>
+cudaError_t launch_d(const AttnSharedArgs& a, cudaStream_t stream, int sms) {
+  using C = Cfg<D>;
+  SharedParams p;
+  p.a = a;
+  p.pl = make_plan(a.batch, a.steps, a.h_q, a.h_kv, a.prefix_len, sms < kMaxCtas ? sms : kMaxCtas);
+  char* ws = static_cast<char*>(a.scratch);
+  p.tail_cost = reinterpret_cast<long long*>(ws);
+  ws += up256((size_t)(a.batch + 1) * 8);
+  const size_t rows = slot_rows(p.pl, a.batch, p.pl.ncta);
+  p.ml = reinterpret_cast<float4*>(ws);
+  ws += up256(rows * sizeof(float4));
+  p.opart = reinterpret_cast<float*>(ws);
+
+  CUtensorMap tk, tv, tqp, tqt;
+  const bool cached = a.prefix_len > 0 || a.tail_width > 0;
+  // without a cache no tile is loaded; q stands in for the unused maps
+  if (!q_map(&tqp, a, p.pl.G, p.pl.tpb) || !q_map(&tqt, a, p.pl.G, a.steps)) return cudaErrorInvalidValue;
+  tk = tv = tqp;
+  if (cached && (!cache_map(&tk, a, a.k_cache) || !cache_map(&tv, a, a.v_cache))) return cudaErrorInvalidValue;
+  cudaError_t e;
+  if ((e = cudaFuncSetAttribute(attn_shared_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)C::SMEM)) != cudaSuccess)
+    return e;
+  attn_shared_kernel<D><<<p.pl.ncta, kThreads, C::SMEM, stream>>>(tk, tv, tqp, tqt, p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  attn_shared_join<D><<<dim3(p.pl.ntok, p.pl.h_kv, D / 64), kJoinThreads, 0, stream>>>(p);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
-size_t attn_shared_scratch_bytes(int, int, int, int, int) { return 256; }
+size_t attn_shared_scratch_bytes(int batch, int steps, int h_q, int h_kv, int d) {
+  const Plan pl = make_plan(batch > 0 ? batch : 1, steps, h_q, h_kv, 1, kMaxCtas);
+  const size_t rows = slot_rows(pl, batch, kMaxCtas);
+  return up256((size_t)(batch + 1) * 8) + up256(rows * sizeof(float4)) + up256(rows * d * 4);
+}
 
 cudaError_t launch_attn_shared(const AttnSharedArgs& p, cudaStream_t stream) {
-  const dim3 grid(p.batch * p.steps, p.h_q);
+  int dev = 0, sms = 0;
+  cudaError_t e;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+  if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
   switch (p.d) {
-    case 64: attn_shared_simple<64><<<grid, 128, 0, stream>>>(p); break;
-    case 128: attn_shared_simple<128><<<grid, 128, 0, stream>>>(p); break;
-    case 256: attn_shared_simple<256><<<grid, 128, 0, stream>>>(p); break;
-    default: return cudaErrorInvalidValue;
+    case 64: return launch_d<64>(p, stream, sms);
+    case 128: return launch_d<128>(p, stream, sms);
+    case 256: return launch_d<256>(p, stream, sms);
   }
-  return cudaGetLastError();
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace gdn

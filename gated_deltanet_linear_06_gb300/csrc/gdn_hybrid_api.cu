@@ -127,10 +127,10 @@ gdn_status gdn_attn_decode_shared(const gdn_attn_dims* dims, int page, long long
   gdn::TraceRange trace_range("gdn_attn_decode_shared");
   const gdn_status st = check_shared(dims, batch, steps);
   if (st != GDN_OK) return st;
-  if (page <= 0 || n_pages < 0 || prefix_len < 0 || tail_width < 0 || !aligned(device_status, 4))
+  if (page <= 0 || n_pages < 0 || n_pages > (1LL << 40) || prefix_len < 0 || tail_width < 0 || !aligned(device_status, 4))
     return GDN_ERR_INVALID_ARG;
   if (page != 16 && page != 32 && page != 64 && page != 128 && page != 256) return GDN_ERR_UNSUPPORTED;
-  if (prefix_len > 0x7fffffffLL || n_pages > 0x7fffffffLL || (long long)tail_width * page > 0x7fffffffLL)
+  if (prefix_len > 0x7fffffffLL || n_pages * page > 0x7fffffffLL || (long long)tail_width * page > 0x7fffffffLL)
     return GDN_ERR_UNSUPPORTED;
   if (batch == 0) return GDN_OK;
   if (!need16(q) || !need16(out) || !maybe16(gate) || !maybe16(prefix_pages) || !maybe16(tail_pages) ||
