@@ -7,27 +7,34 @@
 // ranges can be summed apart: a range leaves (m, l = sum e^{s - m}, O = sum
 // e^{s - m} v), and ranges join as sum 2^{m_i - M} O_i / sum 2^{m_i - M} l_i.
 //
-// Jobs.  The rows of one key head meet the prefix together: 128 rows (whole
+// Jobs.  The rows of one key head meet the prefix together: 256 rows (whole
 // tokens of h_q / h_kv heads) by the prefix's keys is one job, a dense product
-// that reads the prefix once per 128 rows instead of once per row.  A
+// that reads the prefix once per 256 rows instead of once per row.  A
 // sequence's tail by its own steps * h_q / h_kv rows is another, bound by its
 // bytes.  Both are rows x keys x d products and run through the same pipeline;
-// a tail's unused rows of the 128 cost tensor time that its loads hide.
+// a tail's unused rows of the 256 cost tensor time that its loads hide.
 //
 // Split.  All jobs' tiles of 128 keys are laid end to end, weighted by what a
-// tile costs, and every CTA (one per SM) takes an equal share, so a single
+// tile costs, and every pair of CTAs (one per SM) takes an equal share, so a single
 // long prefix fills the GPU as well as many short tails do.  A share ends
 // where it ends, inside a job if need be: a job's ranges are joined by a
 // second launch.  The shares follow from the lengths alone, so equal calls add
-// in equal order.  Each CTA sums the tails' costs itself from tail_len on the
+// in equal order.  Each pair sums the tails' costs itself from tail_len on the
 // device; the host needs no lengths, and a captured step stays valid.
 //
-// Pipeline per CTA, over its tiles without a pause between jobs:
-//   warp 0     TMA: q tiles, K and V in a ring of stages (128-byte swizzle); a
-//              lane per box, a box per page piece of up to 64 rows and 64
-//              dimensions
-//   warp 1     S = Q K^T of tile i + 1, then O += P V of tile i, so that the
-//              tensor cores work through the softmax of the next tile
+// Pair.  The two CTAs of a cluster hold 128 rows each and run one product
+// (cta_group::2): each brings half of the keys of K and half of the dimensions
+// of V, so a tile costs an SM half the shared memory and half the L2 traffic it
+// would cost alone.  (With one CTA per job of 128 rows at d = 256, the five
+// stages that fit beside q held 1.25 tiles, and a tile took 4600 clocks for
+// 2048 of products.)
+//
+// Pipeline per pair, over its tiles without a pause between jobs:
+//   warp 0     TMA, each CTA its half: q tiles, K and V in a ring of stages, all
+//              reported to the first CTA
+//   warp 1     of the first CTA: S = Q K^T of tile i + 1, then O += P V of tile
+//              i, so that the tensor cores work through the softmax of the next
+//              tile
 //   warps 2-9  softmax: a thread holds half a row's 128 scores; P goes back to
 //              tensor memory as bf16 over the scores it came from and is read
 //              from there as the A operand
@@ -51,21 +58,21 @@ namespace gdn {
 namespace {
 
 constexpr int kTile = 128;            // keys per tile
-constexpr int kMaxCtas = 160;         // shares the workspace has room for
+constexpr int kMaxShares = 80;        // CTA pairs the workspace has room for
 constexpr int kThreads = 320;
 constexpr int kSoftWarps = 8;
-constexpr int kMaxStages = 13;
+constexpr int kMaxStages = 16;
 constexpr uint32_t kCtrlBytes = 3072;
 
 // What a tile costs, in quarters of a prefix tile's products: a tail tile is
 // bound by its loads; each job has a fixed part (its rows in and out).
-constexpr int kCostPrefix = 4, kCostTail = 6, kCostJob = 3;
+constexpr int kCostPrefix = 4, kCostTail = 4, kCostJob = 2;
 
 // Shape of one call, the same for both launches.
 struct Plan {
   int ntok, h_kv, G, R;        // query tokens, key heads, group, rows of a tail job
-  int tpb, nmb;                // tokens per prefix job, prefix jobs per key head
-  int np, ncta;                // prefix jobs, shares
+  int tpb, nmb;                // tokens per CTA of a prefix job, prefix jobs per key head
+  int np, shares;              // prefix jobs, shares (CTA pairs)
   long long ptiles;            // prefix tiles
   long long wp;                // cost of all prefix jobs
 };
@@ -80,23 +87,28 @@ struct SharedParams {
 
 template <int D>
 struct Cfg {
-  static constexpr int KD = D < 128 ? D : 128;          // dimensions of a K stage (128 keys)
-  static constexpr int NKS = D / KD;                    // K stages per tile
-  static constexpr int VR = D == 256 ? 64 : 128;        // keys of a V stage (all dimensions)
-  static constexpr int NVS = kTile / VR;
-  static constexpr uint32_t STAGE = kTile * KD * 2;     // = VR * D * 2
-  static constexpr int NST = D == 256 ? 5 : (D == 128 ? 6 : 12);
+  static constexpr uint32_t STAGE = 128 * D;            // 64 keys of K, or 128 keys of half of V's dimensions
+  static constexpr int NST = D == 256 ? 5 : (D == 128 ? 12 : 16);
   static constexpr uint32_t QBYTES = 128 * D * 2;
   static constexpr uint32_t SMEM = kCtrlBytes + QBYTES + NST * STAGE;
-  static constexpr uint32_t IDESC_QK = tc::idesc_bf16(128, kTile, 0, 0);
-  static constexpr uint32_t IDESC_PV = tc::idesc_bf16(128, D, 0, 1);
+  static constexpr uint32_t IDESC_QK = tc::idesc_bf16(256, kTile, 0, 0);
+  static constexpr uint32_t IDESC_PV = tc::idesc_bf16(256, D, 0, 1);
   static constexpr uint64_t DESC_K = tc::sdesc_sw128(16, 1024);
-  static constexpr uint64_t DESC_V = tc::sdesc_sw128(VR * 128, 1024);
+  // V: rows of VROW bytes, half of the dimensions in blocks of up to 64; at d = 64
+  // a half is 32 dimensions and the swizzle spans 64 bytes
+  static constexpr int VROW = D == 64 ? 64 : 128, VBLK = D == 64 ? 1 : D / 128;
   static constexpr uint32_t T_S = 256;                  // TMEM column of the score tiles
-  static_assert(STAGE == (uint32_t)VR * D * 2, "one ring for K and V");
   static_assert(SMEM <= 227 * 1024, "shared memory");
   static_assert(NST <= kMaxStages, "barriers");
 };
+
+// Descriptor of V read MN-major; blocks of dimensions are `lbo` bytes apart.
+template <int D>
+__device__ __forceinline__ uint64_t desc_v(uint32_t lbo) {
+  const uint64_t sw = D == 64 ? 4 : 2;   // 64- or 128-byte swizzle
+  return (static_cast<uint64_t>((lbo >> 4) & 0x3FFF) << 16) |
+         (static_cast<uint64_t>((8 * Cfg<D>::VROW) >> 4) << 32) | (static_cast<uint64_t>(1) << 46) | (sw << 61);
+}
 
 struct Ctrl {
   uint64_t full[kMaxStages], empty[kMaxStages];
@@ -114,23 +126,54 @@ static_assert(sizeof(Ctrl) <= kCtrlBytes, "control block");
 __device__ __forceinline__ void arrive(uint64_t* mbar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(tc::smem_u32(mbar)) : "memory");
 }
+// Address of the pair's CTA `rank`'s copy of a shared variable.
+__device__ __forceinline__ uint32_t peer(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void arrive_at(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 
-__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* tm, int x, int y, int z, uint64_t* mbar) {
+// Boxes into this CTA's shared memory, reported to `mbar` of either CTA of the pair.
+__device__ __forceinline__ void tma_pair(void* dst, const CUtensorMap* tm, int x, int y, int z, uint32_t mbar) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
-      "[%5];" ::"r"(tc::smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(tc::smem_u32(mbar))
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+      "[%1, {%2, %3, %4}], [%5];" ::"r"(tc::smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(mbar)
       : "memory");
 }
 
-// D[tmem] (+)= A[tmem] * B[smem], one K = 16 step.
-__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+// D[tmem] (+)= A B^T over the pair, one K = 16 step: A in shared memory, or in
+// tensor memory (_ts).
+__device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                         uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate));
+}
+__device__ __forceinline__ void mma_pair_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
                                             uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate));
+}
+// Both CTAs' copies of the mbarrier arrive once the products issued so far are done.
+__device__ __forceinline__ void commit_pair(uint64_t* mbar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          tc::smem_u32(mbar)),
+      "h"((uint16_t)3)
+      : "memory");
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -140,7 +183,7 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 __device__ __forceinline__ long long share_start(const Plan& pl, long long total, int c) {
-  return total * c / pl.ncta;
+  return total * c / pl.shares;
 }
 __device__ __forceinline__ int tail_tiles(int len) { return (len + kTile - 1) / kTile; }
 __device__ __forceinline__ long long tail_cost_of(int len) {
@@ -178,6 +221,7 @@ struct Cursor {
     job = c->job0;
     len = -1;
     seg = -1;
+    t = t1 = 0;
     valid = true;
     find(p);
   }
@@ -257,6 +301,13 @@ __device__ __forceinline__ bool wait_for(const AttnSharedArgs& a, uint64_t* mbar
   return false;
 }
 
+// The same for a barrier that the other CTA's threads arrive at.
+__device__ __forceinline__ bool wait_for_pair(const AttnSharedArgs& a, uint64_t* mbar, uint32_t parity) {
+  const bool ok = wait_for(a, mbar, parity);
+  asm volatile("fence.acq_rel.cluster;" ::: "memory");
+  return ok;
+}
+
 // 64 scores of this thread's row: both loads in flight, one wait.
 __device__ __forceinline__ void tmem_ld64(uint32_t taddr, float (&v)[64]) {
   uint32_t r[64];
@@ -280,7 +331,7 @@ __device__ __forceinline__ void tmem_ld64(uint32_t taddr, float (&v)[64]) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                        const __grid_constant__ CUtensorMap tm_qp, const __grid_constant__ CUtensorMap tm_qt,
                        const __grid_constant__ SharedParams p) {
@@ -293,7 +344,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t base = tc::smem_u32(smem);
   uint8_t* const qs = smem + kCtrlBytes;
   uint8_t* const ring = qs + C::QBYTES;
-  if (base & 1023u) {   // the swizzle atoms need it; shared memory starts there
+  const uint32_t rank = blockIdx.x & 1u;
+  const int share = blockIdx.x >> 1;
+  if (base & 1023u) {   // the swizzle atoms need it; shared memory starts there (in both CTAs alike)
     record_status(a.status, GDN_ERR_CUDA);
     return;
   }
@@ -336,8 +389,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     if (threadIdx.x == 0) {
       const long long total = pl.wp + scan[a.batch];
-      ctl->x0 = share_start(pl, total, blockIdx.x);
-      ctl->x1 = share_start(pl, total, blockIdx.x + 1);
+      ctl->x0 = share_start(pl, total, share);
+      ctl->x1 = share_start(pl, total, share + 1);
       if (ctl->x0 < pl.wp) {
         const long long cost = pl.ptiles * kCostPrefix + kCostJob;
         const long long j = ctl->x0 / cost;
@@ -361,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::mbar_init(&ctl->q_full[i], 1);
         tc::mbar_init(&ctl->q_done[i], 1);
         tc::mbar_init(&ctl->s_full[i], 1);
-        tc::mbar_init(&ctl->p_ready[i], kSoftWarps);
+        tc::mbar_init(&ctl->p_ready[i], 2 * kSoftWarps);
       }
       tc::mbar_init(&ctl->pv_done, 1);
       tc::mbar_init(&ctl->seg_done, 1);
@@ -369,10 +422,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
   }
-  if (warp == 1) tc::tmem_alloc(&ctl->tmem, 512);
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(tc::smem_u32(&ctl->tmem)));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+  }
   tc::fence_proxy_async();   // the scan's writes before the ring's copies
   tc::fence_before_sync();
   __syncthreads();
+  cluster_sync();            // the other CTA's barriers are set up
   tc::fence_after_sync();
   const uint32_t tmem = ctl->tmem;
   // the q region holds two tail jobs' rows when they are few, else one
@@ -380,37 +437,39 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // ---- loads ----
-    Cursor ck, cv;
-    ck.init(p, ctl);
-    cv.init(p, ctl);
+    // A page table entry is a trip to L2: lane j reads the entry of piece j of the
+    // tile after next while this one's loads are issued (K and then V of a tile
+    // use the same pieces).
+    Cursor cn, ck, cv;
+    cn.init(p, ctl);
+    ck = cn;
+    cv = cn;
     Ring<D> r;
     const int rpb = a.page < 64 ? a.page : 64;           // rows per box
-    const int shift = 31 - __clz(a.page);
+    const int rsh = 31 - __clz(rpb), shift = 31 - __clz(a.page);
     bool ok = true, prev_whole = true;
     long long issued = 0;
-    // `n` rows from `key` on, `db` blocks of 64 dimensions from block d0 on: lane = box
-    auto load_rows = [&](const CUtensorMap* tm, const Cursor& c, long long key, int n, int stage_rows, int db,
-                         int d0) {
-      ok = wait_for(a, &ctl->empty[r.s], r.ph ^ 1u);
-      if (!ok) return;
-      const int nb = (n + rpb - 1) / rpb;
-      if (lane == 0) mbar_expect_tx(&ctl->full[r.s], (uint32_t)(nb * rpb * 128 * db));
-      __syncwarp();
-      if (lane < nb * db) {
-        const int j = lane / db, d = lane - j * db;
-        const long long row = key + j * rpb;
-        const int32_t* table = c.prefix ? a.prefix_pages : a.tail_pages + (size_t)c.mb * a.tail_width;
-        int pg = table[row >> shift];
-        if (pg < 0 || pg >= a.n_pages) {
-          record_status(a.status, GDN_ERR_DEVICE_BOUNDS);
-          pg = 0;
-        }
-        tma_load_2d(ring + r.s * C::STAGE + d * (stage_rows * 128) + j * (rpb * 128), tm, c.hk * D + (d0 + d) * 64,
-                    (int)(((long long)pg << shift) + (row & (a.page - 1))), &ctl->full[r.s]);
+    // row of the cache where piece `lane` of c's tile begins
+    auto piece = [&](const Cursor& c) -> int {
+      const long long row = c.t * kTile + (lane << rsh);
+      if (!c.valid || (lane << rsh) >= c.count()) return 0;
+      const int32_t* table = c.prefix ? a.prefix_pages : a.tail_pages + (size_t)c.mb * a.tail_width;
+      int pg = __ldg(table + (row >> shift));
+      if (pg < 0 || pg >= a.n_pages) {
+        record_status(a.status, GDN_ERR_DEVICE_BOUNDS);
+        pg = 0;
       }
+      return (int)(((long long)pg << shift) + (row & (a.page - 1)));
+    };
+    int rows_n = piece(cn), rows_k = 0, rows_v = 0;
+    // The next stage, for a tile of n keys: both CTAs' boxes report to the first
+    // CTA, which expects the bytes of all.
+    auto open_stage = [&](int n) -> uint32_t {
+      ok = wait_for(a, &ctl->empty[r.s], r.ph ^ 1u);
+      if (ok && rank == 0 && lane == 0)
+        mbar_expect_tx(&ctl->full[r.s], (uint32_t)(((n + rpb - 1) >> rsh) << rsh) * (D * 2));
       __syncwarp();
-      ++issued;
-      r.step();
+      return peer(tc::smem_u32(&ctl->full[r.s]), 0);
     };
     auto load_k = [&]() {
       if (ck.first) {
@@ -421,31 +480,63 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = wait_for(a, &ctl->q_done[h ^ 1], (uint32_t)((s - 1) >> 1) & 1u);
         if (!ok) return;
         prev_whole = whole;
-        const uint32_t bytes = (uint32_t)(ck.prefix ? pl.tpb * pl.G : pl.R) * 128;
-        if (lane == 0) mbar_expect_tx(&ctl->q_full[h], bytes * (D / 64));
+        // a prefix job has rows in both CTAs, a tail in the first
+        const uint32_t bytes = (uint32_t)(ck.prefix ? 2 * pl.tpb * pl.G : pl.R) * D * 2;
+        const uint32_t mbar = peer(tc::smem_u32(&ctl->q_full[h]), 0);
+        if (rank == 0 && lane == 0) mbar_expect_tx(&ctl->q_full[h], bytes);
         __syncwarp();
-        if (lane < D / 64)
-          tma_load_3d(qs + lane * 16384 + (whole ? 0 : h * 8192), ck.prefix ? &tm_qp : &tm_qt, lane * 64,
-                      ck.hk * pl.G, ck.mb * (ck.prefix ? pl.tpb : a.steps), &ctl->q_full[h]);
+        if (lane < D / 64 && (ck.prefix || rank == 0))
+          tma_pair(qs + lane * 16384 + (whole ? 0 : h * 8192), ck.prefix ? &tm_qp : &tm_qt, lane * 64, ck.hk * pl.G,
+                   ck.prefix ? (2 * ck.mb + (int)rank) * pl.tpb : ck.mb * a.steps, mbar);
         __syncwarp();
       }
       const int n = ck.count();
-      for (int i = 0; i < C::NKS && ok; ++i) load_rows(&tm_k, ck, ck.t * kTile, n, kTile, C::KD / 64, i * (C::KD / 64));
+      const uint32_t mbar = open_stage(n);
+      if (!ok) return;
+      // this CTA's 64 keys: [block of 64 dimensions][64 keys][128 bytes]; pieces of
+      // 64 keys come with all their blocks in one box
+      const int mine = min(max(n - 64 * (int)rank, 0), 64), nb = (mine + rpb - 1) >> rsh;
+      const int per = rpb == 64 ? 1 : D / 64;      // boxes per piece
+      const int j = lane / per, d = lane - j * per;
+      const int row = __shfl_sync(0xffffffffu, rows_k, (((int)rank * 64 >> rsh) + j) & 31);
+      if (lane < nb * per)
+        tma_pair(ring + r.s * C::STAGE + d * 8192 + ((j * 128) << rsh), &tm_k, 0, row, ck.hk * (D / 64) + d, mbar);
+      __syncwarp();
+      ++issued;
+      r.step();
+    };
+    auto load_v = [&]() {
+      const int n = cv.count();
+      const uint32_t mbar = open_stage(n);
+      if (!ok) return;
+      // all keys of half of the dimensions: [piece][block of dimensions][keys][VROW bytes]
+      const int nb = (n + rpb - 1) >> rsh;
+      if (lane < nb)
+        tma_pair(ring + r.s * C::STAGE + ((lane * D) << rsh), &tm_v, D == 64 ? 32 * (int)rank : 0, rows_v,
+                 D == 64 ? cv.hk : cv.hk * (D / 64) + (int)rank * C::VBLK, mbar);
+      __syncwarp();
+      ++issued;
+      r.step();
+    };
+    // ck steps to the tile cn has looked up, cn to the one after
+    auto advance = [&]() {
+      rows_v = rows_k;
+      rows_k = rows_n;
+      ck = cn;
+      cn.next(p);
+      rows_n = piece(cn);
     };
     if (ck.valid) {
+      rows_k = rows_n;
+      cn.next(p);
+      rows_n = piece(cn);
       load_k();
-      if (ok) ck.next(p);
       while (ok && cv.valid) {
-        if (ck.valid) {
-          load_k();
-          if (!ok) break;
-          ck.next(p);
-        }
-        const int n = cv.count();
-        for (int i = 0; i < C::NVS && ok; ++i)
-          if (n > i * C::VR)
-            load_rows(&tm_v, cv, cv.t * kTile + i * C::VR, min(n - i * C::VR, C::VR), C::VR, D / 64, 0);
-        cv.next(p);
+        advance();
+        if (ck.valid) load_k();
+        if (!ok) break;
+        load_v();
+        cv = ck;
       }
       // take every used stage once more: the products' releases have landed before the CTA ends
       for (int i = 0; i < C::NST && i < issued && ok; ++i) {
@@ -456,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == 1) {
-    // ---- products ----
+    // ---- products, by the first CTA for both ----
     Cursor cq, cp;
     cq.init(p, ctl);
     cp.init(p, ctl);
@@ -464,6 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     uint32_t iq = 0, ip = 0;
     const uint32_t qa = base + kCtrlBytes, ra = qa + C::QBYTES;
+    const int rpb = a.page < 64 ? a.page : 64, rsh = 31 - __clz(rpb);
     auto issue_qk = [&]() {
       const int h = cq.seg & 1;
       if (cq.first) {
@@ -472,75 +564,71 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const uint32_t q0 = qa + ((cq.prefix || !halves) ? 0 : h * 8192);
       const uint32_t d = tmem + C::T_S + (iq & 1u) * kTile;
-      for (int i = 0; i < C::NKS; ++i) {
-        ok = wait_for(a, &ctl->full[r.s], r.ph);
-        if (!ok) return;
-        tc::fence_after_sync();
-        if (lane == 0) {
-          const uint32_t k0 = ra + r.s * C::STAGE;
-#pragma unroll
-          for (int k = 0; k < C::KD / 16; ++k) {
-            const int db = k >> 2, kk = k & 3;
-            tc::mma_bf16(d, tc::sdesc_at(C::DESC_K, q0 + (i * (C::KD / 64) + db) * 16384 + kk * 32),
-                         tc::sdesc_at(C::DESC_K, k0 + db * 16384 + kk * 32), C::IDESC_QK, (i | k) != 0);
-          }
-          tc::mma_commit(&ctl->empty[r.s]);
-        }
-        __syncwarp();
-        r.step();
-      }
+      ok = wait_for(a, &ctl->full[r.s], r.ph);
+      if (!ok) return;
+      tc::fence_after_sync();
       if (lane == 0) {
-        tc::mma_commit(&ctl->s_full[iq & 1u]);
-        if (cq.last) tc::mma_commit(&ctl->q_done[h]);
+        const uint32_t k0 = ra + r.s * C::STAGE;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+          mma_pair(d, tc::sdesc_at(C::DESC_K, q0 + (k >> 2) * 16384 + (k & 3) * 32),
+                   tc::sdesc_at(C::DESC_K, k0 + (k >> 2) * 8192 + (k & 3) * 32), C::IDESC_QK, k != 0);
+        commit_pair(&ctl->empty[r.s]);
+      }
+      __syncwarp();
+      r.step();
+      if (lane == 0) {
+        commit_pair(&ctl->s_full[iq & 1u]);
+        if (cq.last) commit_pair(&ctl->q_done[h]);
       }
       __syncwarp();
       ++iq;
     };
     auto issue_pv = [&]() {
-      ok = wait_for(a, &ctl->p_ready[ip & 1u], (ip >> 1) & 1u);
+      ok = wait_for_pair(a, &ctl->p_ready[ip & 1u], (ip >> 1) & 1u);
       if (!ok) return;
       const uint32_t pa = tmem + C::T_S + (ip & 1u) * kTile;
-      const int n = cp.count();
-      for (int i = 0; i < C::NVS; ++i) {
-        const int ni = min(n - i * C::VR, C::VR);
-        if (ni <= 0) break;
-        ok = wait_for(a, &ctl->full[r.s], r.ph);
-        if (!ok) return;
-        const int steps = (ni + 15) >> 4;
-        // a masked key has weight zero, but zero times a stale NaN is NaN: its
-        // values in the last 16 rows become zeros
-        if (ni & 15) {
-          uint8_t* v = ring + r.s * C::STAGE;
-          const int z = 16 - (ni & 15), words = z * (D / 8);   // 16-byte pieces
-          for (int w = lane; w < words; w += 32) {
-            const int row = ni + w / (D / 8), c = w % (D / 8);
-            *reinterpret_cast<uint4*>(v + (c >> 3) * (C::VR * 128) + row * 128 + ((c & 7) << 4)) =
-                make_uint4(0, 0, 0, 0);
-          }
-          tc::fence_proxy_async();
-          __syncwarp();
+      const int n = cp.count(), steps = (n + 15) >> 4;
+      ok = wait_for(a, &ctl->full[r.s], r.ph);
+      if (!ok) return;
+      // a masked key has weight zero, but zero times a stale NaN is NaN: its
+      // values in the last 16 rows become zeros, in both CTAs
+      if (n & 15) {
+        const int z = 16 - (n & 15), chunks = C::VROW / 16 * C::VBLK;   // 16-byte pieces of a row
+        const uint32_t v = ra + r.s * C::STAGE + (((n >> rsh) * D) << rsh);
+        const uint32_t v0 = peer(v, 0), v1 = peer(v, 1);
+        for (int w = lane; w < z * chunks; w += 32) {
+          const int row = (n & (rpb - 1)) + w / chunks, c = w % chunks;
+          const uint32_t off = (c / (C::VROW / 16)) * (rpb * C::VROW) + row * C::VROW + (c % (C::VROW / 16)) * 16;
+          asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(v0 + off), "r"(0) : "memory");
+          asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(v1 + off), "r"(0) : "memory");
         }
-        tc::fence_after_sync();
-        if (lane == 0) {
-          const uint32_t v0 = ra + r.s * C::STAGE;
-          for (int k = 0; k < steps; ++k) {
-            const int key = i * C::VR + k * 16;   // keys 64 .. 127 lie 64 columns on
-            mma_bf16_ts(tmem, pa + (key >> 6) * 64 + ((key & 63) >> 1), tc::sdesc_at(C::DESC_V, v0 + k * 2048),
-                        C::IDESC_PV, !(cp.first && i == 0 && k == 0));
-          }
-          tc::mma_commit(&ctl->empty[r.s]);
-        }
+        asm volatile("fence.acq_rel.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async;" ::: "memory");
         __syncwarp();
-        r.step();
       }
+      tc::fence_after_sync();
       if (lane == 0) {
-        tc::mma_commit(&ctl->pv_done);
-        if (cp.last) tc::mma_commit(&ctl->seg_done);
+        const uint32_t v0 = ra + r.s * C::STAGE;
+        const uint64_t dv = desc_v<D>(rpb * C::VROW);
+        for (int k = 0; k < steps; ++k) {
+          const int key = k * 16;   // keys 64 .. 127 of P lie 64 columns on
+          mma_pair_ts(tmem, pa + (key >> 6) * 64 + ((key & 63) >> 1),
+                      tc::sdesc_at(dv, v0 + (((key >> rsh) * D) << rsh) + (key & (rpb - 1)) * C::VROW), C::IDESC_PV,
+                      !(cp.first && k == 0));
+        }
+        commit_pair(&ctl->empty[r.s]);
+      }
+      __syncwarp();
+      r.step();
+      if (lane == 0) {
+        commit_pair(&ctl->pv_done);
+        if (cp.last) commit_pair(&ctl->seg_done);
       }
       __syncwarp();
       ++ip;
     };
-    if (cq.valid) {
+    if (rank == 0 && cq.valid) {
       issue_qk();
       if (ok) cq.next(p);
       while (ok && cp.valid) {
@@ -565,7 +653,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     float m = -INFINITY, l = 0.0f;
     bool ok = true;
     while (ok && c.valid) {
-      const int rows = c.prefix ? min(pl.tpb, pl.ntok - c.mb * pl.tpb) * pl.G : pl.R;
+      // this CTA's rows of the job
+      const int rows = c.prefix ? min(max(pl.ntok - (2 * c.mb + (int)rank) * pl.tpb, 0), pl.tpb) * pl.G
+                                : (rank == 0 ? pl.R : 0);
       const bool active = quarter * 32 < rows;
       ok = wait_for(a, &ctl->s_full[it & 1u], (it >> 1) & 1u);
       if (!ok) break;
@@ -635,15 +725,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) arrive(&ctl->p_ready[it & 1u]);
+      if (lane == 0) arrive_at(peer(tc::smem_u32(&ctl->p_ready[it & 1u]), 0));
       if (c.last) {
         ok = wait_for(a, &ctl->seg_done, (uint32_t)c.seg & 1u);
         if (!ok) break;
         if (active) {
           tc::fence_after_sync();
           const int stride = c.prefix ? 128 : pl.R;
-          const long long slot = c.slot_job + (long long)blockIdx.x;
-          const long long row0 = c.prefix ? slot * 128 : (long long)(pl.np + (pl.np ? pl.ncta : 0)) * 128 + slot * pl.R;
+          const long long slot = c.slot_job + share;
+          const long long row0 = c.prefix ? slot * 256 + rank * 128
+                                          : (long long)(pl.np ? pl.np + pl.shares : 0) * 256 + slot * pl.R;
           if (row < rows) {
             float* w = reinterpret_cast<float*>(p.ml + row0 + row);
             if (half == 0) *reinterpret_cast<float2*>(w) = make_float2(m, l);
@@ -672,7 +763,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  if (warp == 1) tc::tmem_dealloc(tmem, 512);
+  cluster_sync();   // no product, report or arrival of the other CTA is on its way here any more
+  if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
 // Joins a token's ranges: a CTA takes one query token, one key head and 64 of
@@ -684,9 +776,9 @@ template <int D>
 __global__ void __launch_bounds__(kJoinThreads) attn_shared_join(const __grid_constant__ SharedParams p) {
   __shared__ float4 acc[kJoinThreads];
   __shared__ float2 stat[kJoinThreads];
-  __shared__ long long list[2 * kMaxCtas];   // first slot row of each range
+  __shared__ long long list[2 * kMaxShares];   // first slot row of each range
   __shared__ int count[2][kJoinThreads / 32];
-  static_assert(kMaxCtas <= kJoinThreads, "a thread per share");
+  static_assert(kMaxShares <= kJoinThreads, "a thread per share");
   const AttnSharedArgs& a = p.a;
   const Plan& pl = p.pl;
   const int tok = blockIdx.x, hk = blockIdx.y, d0 = blockIdx.z * 16;   // in groups of 4 dimensions
@@ -697,15 +789,15 @@ __global__ void __launch_bounds__(kJoinThreads) attn_shared_join(const __grid_co
 
   // the shares that hold ranges of this token's two jobs (its prefix block, its
   // tail) for this key head
-  const int mb = tok / pl.tpb;
-  const int job[2] = {hk * pl.nmb + mb, b * pl.h_kv + hk};
+  const int blk = tok / pl.tpb;                            // block of a CTA's rows
+  const int job[2] = {hk * pl.nmb + (blk >> 1), b * pl.h_kv + hk};
   const long long cost_tail = (t_hi - t_lo) / pl.h_kv;
-  const int stride[2] = {128, pl.R};                       // rows of a slot
-  const int in[2] = {(tok - mb * pl.tpb) * pl.G, step * pl.G};
-  const long long region[2] = {0, (long long)(pl.np ? pl.np + pl.ncta : 0) * 128};
+  const int stride[2] = {128, pl.R};                       // rows of a CTA's part of a slot
+  const int in[2] = {(tok - blk * pl.tpb) * pl.G, step * pl.G};
+  const long long region[2] = {(blk & 1) * 128, (long long)(pl.np ? pl.np + pl.shares : 0) * 256};
   {
     bool has[2] = {false, false};
-    if (threadIdx.x < pl.ncta) {
+    if (threadIdx.x < pl.shares) {
       const long long x0 = share_start(pl, total, threadIdx.x), x1 = share_start(pl, total, threadIdx.x + 1);
       if (pl.np) {
         const long long pos = job[0] * (pl.ptiles * kCostPrefix + kCostJob);
@@ -734,7 +826,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_shared_join(const __grid_co
         at += count[k][w];
       }
       if (has[k])
-        list[mine + __popc(bal[k] & ((1u << lane) - 1))] = region[k] + (long long)(job[k] + threadIdx.x) * stride[k];
+        list[mine + __popc(bal[k] & ((1u << lane) - 1))] = region[k] + (long long)(job[k] + threadIdx.x) * (k ? pl.R : 256);
       if (k == 0) n_prefix = at;
     }
     n_ranges = at;
@@ -816,22 +908,26 @@ PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
   return fn;
 }
 
-bool encode(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
-            const cuuint32_t* box) {
+bool encode(CUtensorMap* m, const void* base, const cuuint64_t* dims, const cuuint64_t* strides,
+            const cuuint32_t* box, CUtensorMapSwizzle swizzle) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = map_encoder();
   if (!enc) return false;
   const cuuint32_t one[3] = {1, 1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides, box, one,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, one,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The cache as a matrix of rows (token) by h_kv * d: boxes of 64 dimensions by a page piece.
-bool cache_map(CUtensorMap* m, const AttnSharedArgs& p, const void* base) {
-  const cuuint64_t dims[2] = {(cuuint64_t)p.h_kv * p.d, (cuuint64_t)p.n_pages * p.page};
-  const cuuint64_t strides[1] = {(cuuint64_t)p.h_kv * p.d * 2};
-  const cuuint32_t box[2] = {64, (cuuint32_t)(p.page < 64 ? p.page : 64)};
-  return encode(m, base, 2, dims, strides, box);
+// The cache as [block of 64 dimensions][token row][64 dimensions].  K: boxes of a
+// page piece with all of a head's blocks when the piece is 64 rows, else with one
+// block.  V: boxes of a page piece with half of a head's dimensions.
+bool cache_map(CUtensorMap* m, const AttnSharedArgs& p, const void* base, bool v) {
+  const cuuint32_t rpb = p.page < 64 ? p.page : 64;
+  const cuuint64_t dims[3] = {64, (cuuint64_t)p.n_pages * p.page, (cuuint64_t)p.h_kv * p.d / 64};
+  const cuuint64_t strides[2] = {(cuuint64_t)p.h_kv * p.d * 2, 128};
+  const cuuint32_t blocks = v ? (p.d == 64 ? 1 : p.d / 128) : (rpb == 64 ? p.d / 64 : 1);
+  const cuuint32_t box[3] = {v && p.d == 64 ? 32u : 64u, rpb, blocks};
+  return encode(m, base, dims, strides, box, v && p.d == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 // q as [token][head][d]: boxes of 64 dimensions by a group's heads by `tokens` tokens.
@@ -839,30 +935,30 @@ bool q_map(CUtensorMap* m, const AttnSharedArgs& p, int G, int tokens) {
   const cuuint64_t dims[3] = {(cuuint64_t)p.d, (cuuint64_t)p.h_q, (cuuint64_t)p.batch * p.steps};
   const cuuint64_t strides[2] = {(cuuint64_t)p.d * 2, (cuuint64_t)p.h_q * p.d * 2};
   const cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)tokens};
-  return encode(m, p.q, 3, dims, strides, box);
+  return encode(m, p.q, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 
-Plan make_plan(int batch, int steps, int h_q, int h_kv, long long prefix_len, int ncta) {
+Plan make_plan(int batch, int steps, int h_q, int h_kv, long long prefix_len, int shares) {
   Plan pl;
   pl.h_kv = h_kv;
   pl.G = h_q / h_kv;
   pl.R = steps * pl.G;
   pl.ntok = batch * steps;
   pl.tpb = 128 / pl.G;
-  pl.nmb = (pl.ntok + pl.tpb - 1) / pl.tpb;
+  pl.nmb = (pl.ntok + 2 * pl.tpb - 1) / (2 * pl.tpb);
   pl.ptiles = (prefix_len + kTile - 1) / kTile;
   pl.np = pl.ptiles > 0 ? h_kv * pl.nmb : 0;
-  pl.ncta = ncta;
+  pl.shares = shares;
   pl.wp = pl.np * (pl.ptiles * kCostPrefix + kCostJob);
   return pl;
 }
 
 // Slot rows: a job's range in share c has slot job + c (each step to the next
 // range moves to the next job, the next share or both).
-size_t slot_rows(const Plan& pl, int batch, int ncta) {
-  return (size_t)(pl.np ? pl.np + ncta : 0) * 128 + ((size_t)batch * pl.h_kv + ncta) * pl.R;
+size_t slot_rows(const Plan& pl, int batch) {
+  return (size_t)(pl.np ? pl.np + pl.shares : 0) * 256 + ((size_t)batch * pl.h_kv + pl.shares) * pl.R;
 }
 
 template <int D>
@@ -870,11 +966,12 @@ cudaError_t launch_d(const AttnSharedArgs& a, cudaStream_t stream, int sms) {
   using C = Cfg<D>;
   SharedParams p;
   p.a = a;
-  p.pl = make_plan(a.batch, a.steps, a.h_q, a.h_kv, a.prefix_len, sms < kMaxCtas ? sms : kMaxCtas);
+  p.pl = make_plan(a.batch, a.steps, a.h_q, a.h_kv, a.prefix_len,
+                   sms < 2 ? 1 : (sms / 2 < kMaxShares ? sms / 2 : kMaxShares));
   char* ws = static_cast<char*>(a.scratch);
   p.tail_cost = reinterpret_cast<long long*>(ws);
   ws += up256((size_t)(a.batch + 1) * 8);
-  const size_t rows = slot_rows(p.pl, a.batch, p.pl.ncta);
+  const size_t rows = slot_rows(p.pl, a.batch);
   p.ml = reinterpret_cast<float4*>(ws);
   ws += up256(rows * sizeof(float4));
   p.opart = reinterpret_cast<float*>(ws);
@@ -884,12 +981,12 @@ cudaError_t launch_d(const AttnSharedArgs& a, cudaStream_t stream, int sms) {
   // without a cache no tile is loaded; q stands in for the unused maps
   if (!q_map(&tqp, a, p.pl.G, p.pl.tpb) || !q_map(&tqt, a, p.pl.G, a.steps)) return cudaErrorInvalidValue;
   tk = tv = tqp;
-  if (cached && (!cache_map(&tk, a, a.k_cache) || !cache_map(&tv, a, a.v_cache))) return cudaErrorInvalidValue;
+  if (cached && (!cache_map(&tk, a, a.k_cache, false) || !cache_map(&tv, a, a.v_cache, true))) return cudaErrorInvalidValue;
   cudaError_t e;
   if ((e = cudaFuncSetAttribute(attn_shared_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 (int)C::SMEM)) != cudaSuccess)
     return e;
-  attn_shared_kernel<D><<<p.pl.ncta, kThreads, C::SMEM, stream>>>(tk, tv, tqp, tqt, p);
+  attn_shared_kernel<D><<<2 * p.pl.shares, kThreads, C::SMEM, stream>>>(tk, tv, tqp, tqt, p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   attn_shared_join<D><<<dim3(p.pl.ntok, p.pl.h_kv, D / 64), kJoinThreads, 0, stream>>>(p);
   return cudaGetLastError();
@@ -898,8 +995,8 @@ cudaError_t launch_d(const AttnSharedArgs& a, cudaStream_t stream, int sms) {
 }  // namespace
 
 size_t attn_shared_scratch_bytes(int batch, int steps, int h_q, int h_kv, int d) {
-  const Plan pl = make_plan(batch > 0 ? batch : 1, steps, h_q, h_kv, 1, kMaxCtas);
-  const size_t rows = slot_rows(pl, batch, kMaxCtas);
+  const Plan pl = make_plan(batch > 0 ? batch : 1, steps, h_q, h_kv, 1, kMaxShares);
+  const size_t rows = slot_rows(pl, batch);
   return up256((size_t)(batch + 1) * 8) + up256(rows * sizeof(float4)) + up256(rows * d * 4);
 }
 

@@ -8,7 +8,7 @@ import pytest
 import gated_deltanet_linear_06_gb300 as gdn
 from gated_deltanet_linear_06_gb300 import build as gbuild
 
-TILE, COST_PREFIX, COST_TAIL, COST_JOB = 128, 4, 6, 3     # as in csrc/gdn_attn_shared.cu
+TILE, COST_PREFIX, COST_TAIL, COST_JOB = 128, 4, 4, 2     # as in csrc/gdn_attn_shared.cu
 
 
 def tiles_before(x, pos, per, n):
@@ -36,10 +36,10 @@ def test_shares_cover_every_tile_once_and_the_join_finds_them(seed):
     batch, steps = rng.choice([1, 2, 7, 40, 200]), rng.choice([1, 1, 3, 8])
     hkv, G = rng.choice([1, 2, 5]), rng.choice([1, 2, 6, 8, 16])
     prefix = rng.choice([0, 1, 100, 128, 700, 5000, 33000])
-    ncta = rng.choice([152, 160, 20])
+    ncta = rng.choice([76, 80, 10])      # pairs of CTAs
     tails = [rng.choice([0, 1, rng.randrange(2000)]) for _ in range(batch)]
     ntok, R, tpb = batch * steps, steps * G, 128 // G
-    nmb, pt = -(-ntok // tpb), -(-prefix // TILE)
+    nmb, pt = -(-ntok // (2 * tpb)), -(-prefix // TILE)
     np_ = hkv * nmb if pt else 0
     jobs = [(COST_PREFIX, pt, pt * COST_PREFIX + COST_JOB)] * np_
     scan = [0]
@@ -55,7 +55,7 @@ def test_shares_cover_every_tile_once_and_the_join_finds_them(seed):
 
     done = [0] * len(jobs)
     slots, ranges = set(), {}
-    prefix_rows = (np_ + ncta) * 128 if np_ else 0
+    prefix_rows = (np_ + ncta) * 256 if np_ else 0
     all_rows = prefix_rows + (batch * hkv + ncta) * R
     for c in range(ncta):
         if start[c] < wp:
@@ -67,8 +67,8 @@ def test_shares_cover_every_tile_once_and_the_join_finds_them(seed):
         for j, a, b in walk(job0, pos0, start[c], start[c + 1], jobs):
             assert a == done[j]
             done[j] = b
-            rows = 128 if j < np_ else R
-            row0 = (j + c) * 128 if j < np_ else prefix_rows + (j - np_ + c) * R
+            rows = 256 if j < np_ else R
+            row0 = (j + c) * 256 if j < np_ else prefix_rows + (j - np_ + c) * R
             assert row0 not in slots and 0 <= row0 and row0 + rows <= all_rows
             slots.add(row0)
             ranges.setdefault(j, []).append((c, row0))
@@ -81,16 +81,16 @@ def test_shares_cover_every_tile_once_and_the_join_finds_them(seed):
             found = {0: [], 1: []}
             for c in range(ncta):
                 if np_:
-                    j = hk * nmb + tok // tpb
+                    j = hk * nmb + tok // (2 * tpb)
                     pos = j * (pt * COST_PREFIX + COST_JOB)
                     if tiles_before(start[c], pos, COST_PREFIX, pt) < tiles_before(start[c + 1], pos, COST_PREFIX, pt):
-                        found[0].append((c, (j + c) * 128))
+                        found[0].append((c, (j + c) * 256))
                 one = (scan[b + 1] - scan[b]) // hkv
                 if one:
                     pos, n = wp + scan[b] + hk * one, (one - COST_JOB) // COST_TAIL
                     if tiles_before(start[c], pos, COST_TAIL, n) < tiles_before(start[c + 1], pos, COST_TAIL, n):
                         found[1].append((c, prefix_rows + (b * hkv + hk + c) * R))
-            assert found[0] == ranges.get(hk * nmb + tok // tpb if np_ else -1, [])
+            assert found[0] == ranges.get(hk * nmb + tok // (2 * tpb) if np_ else -1, [])
             assert found[1] == ranges.get(np_ + b * hkv + hk, [])
 
     # the workspace holds the costs, the statistics and the outputs of all slots
