@@ -133,7 +133,7 @@ __device__ __forceinline__ uint32_t peer(uint32_t addr, uint32_t rank) {
   return r;
 }
 __device__ __forceinline__ void arrive_at(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
@@ -296,16 +296,18 @@ struct Ring {
 
 // One wait of a role: false (and the status word) when it gave up.
 __device__ __forceinline__ bool wait_for(const AttnSharedArgs& a, uint64_t* mbar, uint32_t parity) {
-  if (tc::mbar_wait(mbar, parity, kWaitBudget)) return true;
+  // the usual case, without the clock
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred P1;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 P1, [%1], %2;\n\t"
+      "selp.b32 %0, 1, 0, P1;\n\t}\n"
+      : "=r"(done)
+      : "r"(tc::smem_u32(mbar)), "r"(parity)
+      : "memory");
+  if (done || tc::mbar_wait(mbar, parity, kWaitBudget)) return true;
   record_status(a.status, GDN_ERR_DEVICE_TIMEOUT);
   return false;
-}
-
-// The same for a barrier that the other CTA's threads arrive at.
-__device__ __forceinline__ bool wait_for_pair(const AttnSharedArgs& a, uint64_t* mbar, uint32_t parity) {
-  const bool ok = wait_for(a, mbar, parity);
-  asm volatile("fence.acq_rel.cluster;" ::: "memory");
-  return ok;
 }
 
 // 64 scores of this thread's row: both loads in flight, one wait.
@@ -585,7 +587,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       ++iq;
     };
     auto issue_pv = [&]() {
-      ok = wait_for_pair(a, &ctl->p_ready[ip & 1u], (ip >> 1) & 1u);
+      ok = wait_for(a, &ctl->p_ready[ip & 1u], (ip >> 1) & 1u);
       if (!ok) return;
       const uint32_t pa = tmem + C::T_S + (ip & 1u) * kTile;
       const int n = cp.count(), steps = (n + 15) >> 4;
@@ -611,12 +613,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (lane == 0) {
         const uint32_t v0 = ra + r.s * C::STAGE;
         const uint64_t dv = desc_v<D>(rpb * C::VROW);
-        for (int k = 0; k < steps; ++k) {
-          const int key = k * 16;   // keys 64 .. 127 of P lie 64 columns on
-          mma_pair_ts(tmem, pa + (key >> 6) * 64 + ((key & 63) >> 1),
-                      tc::sdesc_at(dv, v0 + (((key >> rsh) * D) << rsh) + (key & (rpb - 1)) * C::VROW), C::IDESC_PV,
-                      !(cp.first && k == 0));
-        }
+        // keys 16 k ..: pieces of rpb keys with all their blocks, one after the other;
+        // keys 64 .. 127 of P lie 64 columns on.  (Unrolled: the addresses of a step
+        // computed in a loop took longer than its product.)
+#pragma unroll
+        for (int k = 0; k < kTile / 16; ++k)
+          if (k < steps)
+            mma_pair_ts(tmem, pa + (k >> 2) * 64 + (k & 3) * 8,
+                        tc::sdesc_at(dv, v0 + k * 16 * C::VROW + (((k * 16) >> rsh) << rsh) * (D - C::VROW)),
+                        C::IDESC_PV, k == 0 ? !cp.first : 1u);
         commit_pair(&ctl->empty[r.s]);
       }
       __syncwarp();
@@ -672,9 +677,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int j = 0; j < 64; ++j) s[j] = j < nv ? s[j] : -INFINITY;
         }
-        float mx = s[0];
+        float mq[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-        for (int j = 1; j < 64; ++j) mx = fmaxf(mx, s[j]);
+        for (int j = 4; j < 64; ++j) mq[j & 3] = fmaxf(mq[j & 3], s[j]);
+        float mx = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
         ctl->red[it & 1u][half][row] = mx;
         __syncwarp();
         if (lane == 0) arrive(&ctl->pair[quarter]);
