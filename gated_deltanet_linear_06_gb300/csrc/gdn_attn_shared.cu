@@ -61,7 +61,7 @@ constexpr int kTile = 128;            // keys per tile
 constexpr int kMaxShares = 80;        // CTA pairs the workspace has room for
 constexpr int kThreads = 320;
 constexpr int kSoftWarps = 8;
-constexpr int kMaxStages = 16;
+constexpr int kMaxStages = 8;
 constexpr uint32_t kCtrlBytes = 3072;
 
 // What a tile costs, in quarters of a prefix tile's products: a tail tile is
@@ -88,9 +88,9 @@ struct SharedParams {
 template <int D>
 struct Cfg {
   static constexpr uint32_t STAGE = 128 * D;            // 64 keys of K, or 128 keys of half of V's dimensions
-  static constexpr int NST = D == 256 ? 5 : (D == 128 ? 12 : 16);
+  static constexpr int NK = D == 256 ? 3 : (D == 128 ? 6 : 8), NV = D == 256 ? 2 : NK;   // stages
   static constexpr uint32_t QBYTES = 128 * D * 2;
-  static constexpr uint32_t SMEM = kCtrlBytes + QBYTES + NST * STAGE;
+  static constexpr uint32_t SMEM = kCtrlBytes + QBYTES + (NK + NV) * STAGE;
   static constexpr uint32_t IDESC_QK = tc::idesc_bf16(256, kTile, 0, 0);
   static constexpr uint32_t IDESC_PV = tc::idesc_bf16(256, D, 0, 1);
   static constexpr uint64_t DESC_K = tc::sdesc_sw128(16, 1024);
@@ -99,7 +99,7 @@ struct Cfg {
   static constexpr int VROW = D == 64 ? 64 : 128, VBLK = D == 64 ? 1 : D / 128;
   static constexpr uint32_t T_S = 256;                  // TMEM column of the score tiles
   static_assert(SMEM <= 227 * 1024, "shared memory");
-  static_assert(NST <= kMaxStages, "barriers");
+  static_assert(NK <= kMaxStages && NV <= kMaxStages && NK >= 2, "barriers");
 };
 
 // Descriptor of V read MN-major; blocks of dimensions are `lbo` bytes apart.
@@ -111,10 +111,11 @@ __device__ __forceinline__ uint64_t desc_v(uint32_t lbo) {
 }
 
 struct Ctrl {
-  uint64_t full[kMaxStages], empty[kMaxStages];
-  uint64_t q_full[2], q_done[2], s_full[2], p_ready[2];
-  uint64_t pv_done;            // each tile's O product
-  uint64_t seg_done;           // a segment's last
+  uint64_t k_full[kMaxStages], v_full[kMaxStages];
+  uint64_t s_full[kMaxStages];    // a tile's scores are done, and so is its K stage
+  uint64_t pv_done[kMaxStages];   // a tile's O product is done, and so is its V stage
+  uint64_t q_full[2], q_done[2], p_ready[2];
+  uint64_t seg_done;              // a segment's last O product
   uint64_t pair[4];            // the two warps of a row quarter
   uint32_t tmem;
   int job0;
@@ -195,10 +196,12 @@ __device__ __forceinline__ long long tiles_before(long long x, long long pos, in
   return x - pos - kCostJob <= 0 ? 0 : (t < n ? t : n);
 }
 // A tail's length, clamped into its table.
-__device__ __forceinline__ int tail_length(const AttnSharedArgs& a, int b) {
-  if (a.tail_width == 0) return 0;
-  const int n = a.tail_len[b], top = a.tail_width * a.page;
+__device__ __forceinline__ int clamp_tail(const AttnSharedArgs& a, int n) {
+  const int top = a.tail_width * a.page;
   return n < 0 ? 0 : (n > top ? top : n);
+}
+__device__ __forceinline__ int tail_length(const AttnSharedArgs& a, int b) {
+  return a.tail_width == 0 ? 0 : clamp_tail(a, a.tail_len[b]);
 }
 
 // Walks the tiles of one share, job by job.  Every role keeps its own.
@@ -207,19 +210,20 @@ struct Cursor {
   long long x0, x1;
   int job;             // next job to look at
   int len;             // of the current sequence's tail (jobs of one sequence are adjacent)
+  int ahead;           // tail_len of the next sequence, on its way
   int seg;             // segments begun, minus one
   // the current segment
   bool prefix, valid, first, last;
   int hk, mb;          // key head; block of rows (prefix) or sequence (tail)
   int slot_job;        // prefix job, or tail job
-  long long t, t1, keys;
+  int t, t1, keys;
 
   __device__ __forceinline__ void init(const SharedParams& p, const Ctrl* c) {
     pos = c->pos0;
     x0 = c->x0;
     x1 = c->x1;
     job = c->job0;
-    len = -1;
+    len = ahead = -1;
     seg = -1;
     t = t1 = 0;
     valid = true;
@@ -233,28 +237,31 @@ struct Cursor {
         valid = false;
         return;
       }
-      long long n, cost;
-      int per;
+      long long cost;
+      int n, per;
       prefix = job < pl.np;
       if (prefix) {
         hk = job / pl.nmb;
         mb = job - hk * pl.nmb;
         slot_job = job;
-        n = pl.ptiles;
+        n = (int)pl.ptiles;
         per = kCostPrefix;
-        keys = p.a.prefix_len;
-        cost = n * kCostPrefix + kCostJob;
+        keys = (int)p.a.prefix_len;
+        cost = pl.ptiles * kCostPrefix + kCostJob;
       } else {
         slot_job = job - pl.np;
         mb = slot_job / pl.h_kv;
         hk = slot_job - mb * pl.h_kv;
-        if (hk == 0 || len < 0) len = tail_length(p.a, mb);
+        if (hk == 0 || len < 0) {
+          len = len < 0 ? tail_length(p.a, mb) : clamp_tail(p.a, ahead);
+          if (p.a.tail_width > 0 && mb + 1 < p.a.batch) ahead = p.a.tail_len[mb + 1];
+        }
         n = tail_tiles(len);
         per = kCostTail;
         keys = len;
         cost = tail_cost_of(len);
       }
-      const long long a = tiles_before(x0, pos, per, n), b = tiles_before(x1, pos, per, n);
+      const int a = (int)tiles_before(x0, pos, per, n), b = (int)tiles_before(x1, pos, per, n);
       pos += cost;
       ++job;
       if (a < b) {
@@ -277,17 +284,17 @@ struct Cursor {
   }
   // keys of the current tile
   __device__ __forceinline__ int count() const {
-    const long long r = keys - t * kTile;
-    return r < kTile ? (int)r : kTile;
+    return min(keys - t * kTile, kTile);
   }
 };
 
-template <int D>
+// Position in a ring of N stages.
+template <int N>
 struct Ring {
   int s = 0;
   uint32_t ph = 0;
   __device__ __forceinline__ void step() {
-    if (++s == Cfg<D>::NST) {
+    if (++s == N) {
       s = 0;
       ph ^= 1u;
     }
@@ -345,7 +352,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t base = tc::smem_u32(smem);
   uint8_t* const qs = smem + kCtrlBytes;
-  uint8_t* const ring = qs + C::QBYTES;
+  uint8_t* const ring = qs + C::QBYTES;           // K stages, then V stages
   const uint32_t rank = blockIdx.x & 1u;
   const int share = blockIdx.x >> 1;
   if (base & 1023u) {   // the swizzle atoms need it; shared memory starts there (in both CTAs alike)
@@ -408,17 +415,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ctl->job0 = pl.np + lo * pl.h_kv;
         ctl->pos0 = pl.wp + scan[lo];
       }
-      for (int s = 0; s < C::NST; ++s) {
-        tc::mbar_init(&ctl->full[s], 1);
-        tc::mbar_init(&ctl->empty[s], 1);
+      for (int s = 0; s < kMaxStages; ++s) {
+        tc::mbar_init(&ctl->k_full[s], 1);
+        tc::mbar_init(&ctl->v_full[s], 1);
+        tc::mbar_init(&ctl->s_full[s], 1);
+        tc::mbar_init(&ctl->pv_done[s], 1);
       }
       for (int i = 0; i < 2; ++i) {
         tc::mbar_init(&ctl->q_full[i], 1);
         tc::mbar_init(&ctl->q_done[i], 1);
-        tc::mbar_init(&ctl->s_full[i], 1);
         tc::mbar_init(&ctl->p_ready[i], 2 * kSoftWarps);
       }
-      tc::mbar_init(&ctl->pv_done, 1);
       tc::mbar_init(&ctl->seg_done, 1);
       for (int i = 0; i < 4; ++i) tc::mbar_init(&ctl->pair[i], 2);
       asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -446,14 +453,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     cn.init(p, ctl);
     ck = cn;
     cv = cn;
-    Ring<D> r;
+    Ring<C::NK> rk;
+    Ring<C::NV> rv;
     const int rpb = a.page < 64 ? a.page : 64;           // rows per box
     const int rsh = 31 - __clz(rpb), shift = 31 - __clz(a.page);
     bool ok = true, prev_whole = true;
-    long long issued = 0;
+    uint32_t loaded = 0, segs = 0;
     // row of the cache where piece `lane` of c's tile begins
     auto piece = [&](const Cursor& c) -> int {
-      const long long row = c.t * kTile + (lane << rsh);
+      const int row = c.t * kTile + (lane << rsh);
       if (!c.valid || (lane << rsh) >= c.count()) return 0;
       const int32_t* table = c.prefix ? a.prefix_pages : a.tail_pages + (size_t)c.mb * a.tail_width;
       int pg = __ldg(table + (row >> shift));
@@ -464,14 +472,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       return (int)(((long long)pg << shift) + (row & (a.page - 1)));
     };
     int rows_n = piece(cn), rows_k = 0, rows_v = 0;
-    // The next stage, for a tile of n keys: both CTAs' boxes report to the first
-    // CTA, which expects the bytes of all.
-    auto open_stage = [&](int n) -> uint32_t {
-      ok = wait_for(a, &ctl->empty[r.s], r.ph ^ 1u);
+    // Opens a stage for a tile of n keys: both CTAs' boxes report to the first CTA,
+    // which expects the bytes of all.
+    auto open_stage = [&](uint64_t* full, uint64_t* used, uint32_t ph, int n) -> uint32_t {
+      ok = wait_for(a, used, ph ^ 1u);
       if (ok && rank == 0 && lane == 0)
-        mbar_expect_tx(&ctl->full[r.s], (uint32_t)(((n + rpb - 1) >> rsh) << rsh) * (D * 2));
+        mbar_expect_tx(full, (uint32_t)(((n + rpb - 1) >> rsh) << rsh) * (D * 2));
       __syncwarp();
-      return peer(tc::smem_u32(&ctl->full[r.s]), 0);
+      return peer(tc::smem_u32(full), 0);
     };
     auto load_k = [&]() {
       if (ck.first) {
@@ -482,6 +490,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           ok = wait_for(a, &ctl->q_done[h ^ 1], (uint32_t)((s - 1) >> 1) & 1u);
         if (!ok) return;
         prev_whole = whole;
+        ++segs;
         // a prefix job has rows in both CTAs, a tail in the first
         const uint32_t bytes = (uint32_t)(ck.prefix ? 2 * pl.tpb * pl.G : pl.R) * D * 2;
         const uint32_t mbar = peer(tc::smem_u32(&ctl->q_full[h]), 0);
@@ -493,7 +502,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         __syncwarp();
       }
       const int n = ck.count();
-      const uint32_t mbar = open_stage(n);
+      const uint32_t mbar = open_stage(&ctl->k_full[rk.s], &ctl->s_full[rk.s], rk.ph, n);
       if (!ok) return;
       // this CTA's 64 keys: [block of 64 dimensions][64 keys][128 bytes]; pieces of
       // 64 keys come with all their blocks in one box
@@ -502,23 +511,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int j = lane / per, d = lane - j * per;
       const int row = __shfl_sync(0xffffffffu, rows_k, (((int)rank * 64 >> rsh) + j) & 31);
       if (lane < nb * per)
-        tma_pair(ring + r.s * C::STAGE + d * 8192 + ((j * 128) << rsh), &tm_k, 0, row, ck.hk * (D / 64) + d, mbar);
+        tma_pair(ring + rk.s * C::STAGE + d * 8192 + ((j * 128) << rsh), &tm_k, 0, row, ck.hk * (D / 64) + d, mbar);
       __syncwarp();
-      ++issued;
-      r.step();
+      rk.step();
     };
     auto load_v = [&]() {
       const int n = cv.count();
-      const uint32_t mbar = open_stage(n);
+      const uint32_t mbar = open_stage(&ctl->v_full[rv.s], &ctl->pv_done[rv.s], rv.ph, n);
       if (!ok) return;
       // all keys of half of the dimensions: [piece][block of dimensions][keys][VROW bytes]
       const int nb = (n + rpb - 1) >> rsh;
       if (lane < nb)
-        tma_pair(ring + r.s * C::STAGE + ((lane * D) << rsh), &tm_v, D == 64 ? 32 * (int)rank : 0, rows_v,
+        tma_pair(ring + (C::NK + rv.s) * C::STAGE + ((lane * D) << rsh), &tm_v, D == 64 ? 32 * (int)rank : 0, rows_v,
                  D == 64 ? cv.hk : cv.hk * (D / 64) + (int)rank * C::VBLK, mbar);
       __syncwarp();
-      ++issued;
-      r.step();
+      ++loaded;
+      rv.step();
     };
     // ck steps to the tile cn has looked up, cn to the one after
     auto advance = [&]() {
@@ -540,20 +548,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         load_v();
         cv = ck;
       }
-      // take every used stage once more: the products' releases have landed before the CTA ends
-      for (int i = 0; i < C::NST && i < issued && ok; ++i) {
-        // step back over the newest stages
-        const int s = (r.s + C::NST - 1 - i) % C::NST;
-        const uint32_t ph = r.s - 1 - i >= 0 ? r.ph : r.ph ^ 1u;
-        ok = wait_for(a, &ctl->empty[s], ph);
-      }
+      // the products' last reports have landed before the CTA ends
+      for (uint32_t i = 1; i <= (uint32_t)C::NV && i <= loaded && ok; ++i)
+        ok = wait_for(a, &ctl->pv_done[(loaded - i) % C::NV], ((loaded - i) / C::NV) & 1u);
+      if (ok) ok = wait_for(a, &ctl->q_done[(segs - 1) & 1u], ((segs - 1) >> 1) & 1u);
     }
   } else if (warp == 1) {
     // ---- products, by the first CTA for both ----
     Cursor cq, cp;
     cq.init(p, ctl);
     cp.init(p, ctl);
-    Ring<D> r;
+    Ring<C::NK> rk;
+    Ring<C::NV> rv;
     bool ok = true;
     uint32_t iq = 0, ip = 0;
     const uint32_t qa = base + kCtrlBytes, ra = qa + C::QBYTES;
@@ -566,24 +572,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       const uint32_t q0 = qa + ((cq.prefix || !halves) ? 0 : h * 8192);
       const uint32_t d = tmem + C::T_S + (iq & 1u) * kTile;
-      ok = wait_for(a, &ctl->full[r.s], r.ph);
+      ok = wait_for(a, &ctl->k_full[rk.s], rk.ph);
       if (!ok) return;
       tc::fence_after_sync();
       if (lane == 0) {
-        const uint32_t k0 = ra + r.s * C::STAGE;
+        const uint32_t k0 = ra + rk.s * C::STAGE;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
           mma_pair(d, tc::sdesc_at(C::DESC_K, q0 + (k >> 2) * 16384 + (k & 3) * 32),
                    tc::sdesc_at(C::DESC_K, k0 + (k >> 2) * 8192 + (k & 3) * 32), C::IDESC_QK, k != 0);
-        commit_pair(&ctl->empty[r.s]);
-      }
-      __syncwarp();
-      r.step();
-      if (lane == 0) {
-        commit_pair(&ctl->s_full[iq & 1u]);
+        commit_pair(&ctl->s_full[rk.s]);
         if (cq.last) commit_pair(&ctl->q_done[h]);
       }
       __syncwarp();
+      rk.step();
       ++iq;
     };
     auto issue_pv = [&]() {
@@ -591,13 +593,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (!ok) return;
       const uint32_t pa = tmem + C::T_S + (ip & 1u) * kTile;
       const int n = cp.count(), steps = (n + 15) >> 4;
-      ok = wait_for(a, &ctl->full[r.s], r.ph);
+      ok = wait_for(a, &ctl->v_full[rv.s], rv.ph);
       if (!ok) return;
+      const uint32_t vs = ra + (C::NK + rv.s) * C::STAGE;
       // a masked key has weight zero, but zero times a stale NaN is NaN: its
       // values in the last 16 rows become zeros, in both CTAs
       if (n & 15) {
         const int z = 16 - (n & 15), chunks = C::VROW / 16 * C::VBLK;   // 16-byte pieces of a row
-        const uint32_t v = ra + r.s * C::STAGE + (((n >> rsh) * D) << rsh);
+        const uint32_t v = vs + (((n >> rsh) * D) << rsh);
         const uint32_t v0 = peer(v, 0), v1 = peer(v, 1);
         for (int w = lane; w < z * chunks; w += 32) {
           const int row = (n & (rpb - 1)) + w / chunks, c = w % chunks;
@@ -611,7 +614,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       tc::fence_after_sync();
       if (lane == 0) {
-        const uint32_t v0 = ra + r.s * C::STAGE;
         const uint64_t dv = desc_v<D>(rpb * C::VROW);
         // keys 16 k ..: pieces of rpb keys with all their blocks, one after the other;
         // keys 64 .. 127 of P lie 64 columns on.  (Unrolled: the addresses of a step
@@ -620,17 +622,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int k = 0; k < kTile / 16; ++k)
           if (k < steps)
             mma_pair_ts(tmem, pa + (k >> 2) * 64 + (k & 3) * 8,
-                        tc::sdesc_at(dv, v0 + k * 16 * C::VROW + (((k * 16) >> rsh) << rsh) * (D - C::VROW)),
+                        tc::sdesc_at(dv, vs + k * 16 * C::VROW + (((k * 16) >> rsh) << rsh) * (D - C::VROW)),
                         C::IDESC_PV, k == 0 ? !cp.first : 1u);
-        commit_pair(&ctl->empty[r.s]);
-      }
-      __syncwarp();
-      r.step();
-      if (lane == 0) {
-        commit_pair(&ctl->pv_done);
+        commit_pair(&ctl->pv_done[rv.s]);
         if (cp.last) commit_pair(&ctl->seg_done);
       }
       __syncwarp();
+      rv.step();
       ++ip;
     };
     if (rank == 0 && cq.valid) {
@@ -654,15 +652,52 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int row = quarter * 32 + lane;
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     const float sc = a.scale * 1.44269504088896340736f;   // scores in binary orders
+    const int step = row / pl.G;                          // of a tail's row
     uint32_t it = 0, met = 0;
+    Ring<C::NK> rs;       // tile it's scores
+    Ring<C::NV> ro;       // tile it - 1's O product
     float m = -INFINITY, l = 0.0f;
     bool ok = true;
+    // A finished segment is written out in the next one's first tile, after that
+    // tile's weights: its last product runs meanwhile, and the next segment's first
+    // product, which overwrites O, waits for the weights' arrival.
+    struct {
+      bool pending = false;
+      uint32_t seg;
+      int rows, stride;
+      long long row0;
+      float m, l;
+    } done;
+    auto write_out = [&]() {
+      done.pending = false;
+      ok = wait_for(a, &ctl->seg_done, done.seg & 1u);
+      if (!ok || quarter * 32 >= done.rows) return;
+      tc::fence_after_sync();
+      const bool mine = row < done.rows;
+      if (mine) {
+        float* w = reinterpret_cast<float*>(p.ml + done.row0 + row);
+        if (half == 0) *reinterpret_cast<float2*>(w) = make_float2(done.m, done.l);
+        else w[2] = done.l;
+      }
+      float4* o4 = reinterpret_cast<float4*>(p.opart) + done.row0 * (D / 4) + (long long)(half * (D / 8)) * done.stride + row;
+#pragma unroll 1
+      for (int o = 0; o < D / 2; o += 32) {
+        float v[32];
+        tc::tmem_ld32(tmem + lanes + half * (D / 2) + o, v);
+        if (mine) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            o4[(long long)j * done.stride] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+        }
+        o4 += 8 * (long long)done.stride;
+      }
+    };
     while (ok && c.valid) {
       // this CTA's rows of the job
       const int rows = c.prefix ? min(max(pl.ntok - (2 * c.mb + (int)rank) * pl.tpb, 0), pl.tpb) * pl.G
                                 : (rank == 0 ? pl.R : 0);
       const bool active = quarter * 32 < rows;
-      ok = wait_for(a, &ctl->s_full[it & 1u], (it >> 1) & 1u);
+      ok = wait_for(a, &ctl->s_full[rs.s], rs.ph);
       if (!ok) break;
       if (active) {
         tc::fence_after_sync();
@@ -670,9 +705,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         float s[64];
         tmem_ld64(ts, s);
         // keys this row sees in its half of the tile
-        long long see = c.keys - c.t * kTile;
-        if (!c.prefix) see -= a.steps - 1 - row / pl.G;
-        int nv = row < rows ? (int)min(see, (long long)kTile) - half * 64 : 0;
+        int see = c.keys - c.t * kTile;
+        if (!c.prefix) see -= a.steps - 1 - step;
+        const int nv = row < rows ? see - half * 64 : 0;
         if (!__all_sync(0xffffffffu, nv >= 64)) {
 #pragma unroll
           for (int j = 0; j < 64; ++j) s[j] = j < nv ? s[j] : -INFINITY;
@@ -695,9 +730,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const bool grow = mx > m + 8.0f;
           if (__any_sync(0xffffffffu, grow)) {
             // O is behind by 2^8 or more in some row: bring it to the new maximum.
-            // (This tile's scores came after the products of tile it - 2, so the
-            // wait can only be for those of tile it - 1.)
-            ok = wait_for(a, &ctl->pv_done, (it - 1) & 1u);
+            ok = wait_for(a, &ctl->pv_done[ro.s], ro.ph);
             if (!ok) break;
             tc::fence_after_sync();
             const float f = grow ? ex2(m - mx) : 1.0f;
@@ -729,42 +762,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         l += s0 + s1;
         tc::tmem_st32(ts, pk);
       }
+      if (done.pending) {
+        write_out();
+        if (!ok) break;
+      }
       tc::fence_before_sync();
       __syncwarp();
       if (lane == 0) arrive_at(peer(tc::smem_u32(&ctl->p_ready[it & 1u]), 0));
       if (c.last) {
-        ok = wait_for(a, &ctl->seg_done, (uint32_t)c.seg & 1u);
-        if (!ok) break;
-        if (active) {
-          tc::fence_after_sync();
-          const int stride = c.prefix ? 128 : pl.R;
-          const long long slot = c.slot_job + share;
-          const long long row0 = c.prefix ? slot * 256 + rank * 128
-                                          : (long long)(pl.np ? pl.np + pl.shares : 0) * 256 + slot * pl.R;
-          if (row < rows) {
-            float* w = reinterpret_cast<float*>(p.ml + row0 + row);
-            if (half == 0) *reinterpret_cast<float2*>(w) = make_float2(m, l);
-            else w[2] = l;
-          }
-          float4* o4 = reinterpret_cast<float4*>(p.opart) + row0 * (D / 4) + row;
-#pragma unroll 1
-          for (int o = 0; o < D / 2; o += 32) {
-            float v[32];
-            tc::tmem_ld32(tmem + lanes + half * (D / 2) + o, v);
-            if (row < rows) {
-#pragma unroll
-              for (int j = 0; j < 8; ++j)
-                o4[(long long)(half * (D / 8) + o / 4 + j) * stride] =
-                    make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-            }
-          }
-          tc::fence_before_sync();
-        }
-        __syncwarp();
+        const long long slot = c.slot_job + share;
+        done.pending = true;
+        done.seg = (uint32_t)c.seg;
+        done.rows = rows;
+        done.stride = c.prefix ? 128 : pl.R;
+        done.row0 = c.prefix ? slot * 256 + rank * 128
+                             : (long long)(pl.np ? pl.np + pl.shares : 0) * 256 + slot * pl.R;
+        done.m = m;
+        done.l = l;
       }
+      if (it > 0) ro.step();
+      rs.step();
       ++it;
       c.next(p);
     }
+    if (ok && done.pending) write_out();
   }
   tc::fence_before_sync();
   __syncthreads();
