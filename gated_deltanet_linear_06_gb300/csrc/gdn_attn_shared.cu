@@ -32,9 +32,11 @@
 // Pipeline per pair, over its tiles without a pause between jobs:
 //   warp 0     TMA, each CTA its half: q tiles, K and V in a ring of stages, all
 //              reported to the first CTA
-//   warp 1     of the first CTA: S = Q K^T of tile i + 1, then O += P V of tile
-//              i, so that the tensor cores work through the softmax of the next
-//              tile
+//   warp 1     of the first CTA, for both: S = Q K^T
+//   warp 10    likewise: O += P V.  (One warp for both products left the tensor
+//              cores idle for some 500 clocks at each change between them, 1000
+//              of a tile's 3400; now one's barriers pass under the other's
+//              products.)
 //   warps 2-9  softmax: a thread holds half a row's 128 scores; P goes back to
 //              tensor memory as bf16 over the scores it came from and is read
 //              from there as the A operand
@@ -59,8 +61,9 @@ namespace {
 
 constexpr int kTile = 128;            // keys per tile
 constexpr int kMaxShares = 80;        // CTA pairs the workspace has room for
-constexpr int kThreads = 320;
+constexpr int kThreads = 352;
 constexpr int kSoftWarps = 8;
+constexpr int kPvWarp = 2 + kSoftWarps;
 constexpr int kMaxStages = 8;
 constexpr uint32_t kCtrlBytes = 3072;
 
@@ -554,26 +557,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (ok) ok = wait_for(a, &ctl->q_done[(segs - 1) & 1u], ((segs - 1) >> 1) & 1u);
     }
   } else if (warp == 1) {
-    // ---- products, by the first CTA for both ----
-    Cursor cq, cp;
-    cq.init(p, ctl);
-    cp.init(p, ctl);
+    // ---- scores, by the first CTA for both ----
+    Cursor c;
+    c.init(p, ctl);
     Ring<C::NK> rk;
-    Ring<C::NV> rv;
-    bool ok = true;
-    uint32_t iq = 0, ip = 0;
+    Ring<C::NV> ro;       // the O product of tile it - 2, whose weights lie where these scores go
+    bool ok = rank == 0;
     const uint32_t qa = base + kCtrlBytes, ra = qa + C::QBYTES;
-    const int rpb = a.page < 64 ? a.page : 64, rsh = 31 - __clz(rpb);
-    auto issue_qk = [&]() {
-      const int h = cq.seg & 1;
-      if (cq.first) {
-        ok = wait_for(a, &ctl->q_full[h], (uint32_t)(cq.seg >> 1) & 1u);
-        if (!ok) return;
+    for (uint32_t it = 0; ok && c.valid; ++it) {
+      const int h = c.seg & 1;
+      if (it >= 2) {
+        ok = wait_for(a, &ctl->pv_done[ro.s], ro.ph);
+        ro.step();
       }
-      const uint32_t q0 = qa + ((cq.prefix || !halves) ? 0 : h * 8192);
-      const uint32_t d = tmem + C::T_S + (iq & 1u) * kTile;
-      ok = wait_for(a, &ctl->k_full[rk.s], rk.ph);
-      if (!ok) return;
+      if (ok && c.first) ok = wait_for(a, &ctl->q_full[h], (uint32_t)(c.seg >> 1) & 1u);
+      if (ok) ok = wait_for(a, &ctl->k_full[rk.s], rk.ph);
+      if (!ok) break;
+      const uint32_t q0 = qa + ((c.prefix || !halves) ? 0 : h * 8192);
+      const uint32_t d = tmem + C::T_S + (it & 1u) * kTile;
       tc::fence_after_sync();
       if (lane == 0) {
         const uint32_t k0 = ra + rk.s * C::STAGE;
@@ -582,20 +583,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           mma_pair(d, tc::sdesc_at(C::DESC_K, q0 + (k >> 2) * 16384 + (k & 3) * 32),
                    tc::sdesc_at(C::DESC_K, k0 + (k >> 2) * 8192 + (k & 3) * 32), C::IDESC_QK, k != 0);
         commit_pair(&ctl->s_full[rk.s]);
-        if (cq.last) commit_pair(&ctl->q_done[h]);
+        if (c.last) commit_pair(&ctl->q_done[h]);
       }
       __syncwarp();
       rk.step();
-      ++iq;
-    };
-    auto issue_pv = [&]() {
-      ok = wait_for(a, &ctl->p_ready[ip & 1u], (ip >> 1) & 1u);
-      if (!ok) return;
-      const uint32_t pa = tmem + C::T_S + (ip & 1u) * kTile;
-      const int n = cp.count(), steps = (n + 15) >> 4;
+      c.next(p);
+    }
+  } else if (warp == kPvWarp) {
+    // ---- outputs, by the first CTA for both ----
+    Cursor c;
+    c.init(p, ctl);
+    Ring<C::NV> rv;
+    bool ok = rank == 0;
+    const uint32_t ra = base + kCtrlBytes + C::QBYTES + C::NK * C::STAGE;
+    const int rpb = a.page < 64 ? a.page : 64, rsh = 31 - __clz(rpb);
+    for (uint32_t it = 0; ok && c.valid; ++it) {
+      const uint32_t pa = tmem + C::T_S + (it & 1u) * kTile, vs = ra + rv.s * C::STAGE;
+      const int n = c.count(), steps = (n + 15) >> 4;
       ok = wait_for(a, &ctl->v_full[rv.s], rv.ph);
-      if (!ok) return;
-      const uint32_t vs = ra + (C::NK + rv.s) * C::STAGE;
+      if (!ok) break;
       // a masked key has weight zero, but zero times a stale NaN is NaN: its
       // values in the last 16 rows become zeros, in both CTAs
       if (n & 15) {
@@ -603,8 +609,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t v = vs + (((n >> rsh) * D) << rsh);
         const uint32_t v0 = peer(v, 0), v1 = peer(v, 1);
         for (int w = lane; w < z * chunks; w += 32) {
-          const int row = (n & (rpb - 1)) + w / chunks, c = w % chunks;
-          const uint32_t off = (c / (C::VROW / 16)) * (rpb * C::VROW) + row * C::VROW + (c % (C::VROW / 16)) * 16;
+          const int row = (n & (rpb - 1)) + w / chunks, c16 = w % chunks;
+          const uint32_t off = (c16 / (C::VROW / 16)) * (rpb * C::VROW) + row * C::VROW + (c16 % (C::VROW / 16)) * 16;
           asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(v0 + off), "r"(0) : "memory");
           asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(v1 + off), "r"(0) : "memory");
         }
@@ -612,6 +618,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         asm volatile("fence.proxy.async;" ::: "memory");
         __syncwarp();
       }
+      ok = wait_for(a, &ctl->p_ready[it & 1u], (it >> 1) & 1u);
+      if (!ok) break;
       tc::fence_after_sync();
       if (lane == 0) {
         const uint64_t dv = desc_v<D>(rpb * C::VROW);
@@ -623,26 +631,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (k < steps)
             mma_pair_ts(tmem, pa + (k >> 2) * 64 + (k & 3) * 8,
                         tc::sdesc_at(dv, vs + k * 16 * C::VROW + (((k * 16) >> rsh) << rsh) * (D - C::VROW)),
-                        C::IDESC_PV, k == 0 ? !cp.first : 1u);
+                        C::IDESC_PV, k == 0 ? !c.first : 1u);
         commit_pair(&ctl->pv_done[rv.s]);
-        if (cp.last) commit_pair(&ctl->seg_done);
+        if (c.last) commit_pair(&ctl->seg_done);
       }
       __syncwarp();
       rv.step();
-      ++ip;
-    };
-    if (rank == 0 && cq.valid) {
-      issue_qk();
-      if (ok) cq.next(p);
-      while (ok && cp.valid) {
-        if (cq.valid) {
-          issue_qk();
-          if (!ok) break;
-          cq.next(p);
-        }
-        issue_pv();
-        if (ok) cp.next(p);
-      }
+      c.next(p);
     }
   } else {
     // ---- softmax and the share's partial results ----
