@@ -38,11 +38,14 @@
 //              of a tile's 3400; now one's barriers pass under the other's
 //              products.)
 //   warps 2-9  softmax: a thread holds half a row's 128 scores; P goes back to
-//              tensor memory as bf16 over the scores it came from and is read
-//              from there as the A operand
-// TMEM: O (d columns) and two score tiles (2 x 128).  O is rescaled only when a
-// row's maximum has grown by more than 8 binary orders (P <= 2^8 fits bf16 as
-// well as P <= 1 does, and the sums are fp32), so almost never.
+//              tensor memory as bf16 and is read from there as the A operand
+// TMEM: O (d columns), one score tile (128), two weight tiles (64 each).  The
+// scores' place is free again as soon as they are in registers, so the next
+// tile's scores are computed under this one's exponentials and O product (with
+// two score tiles and the weights written over them, each score product waited
+// for the O product two tiles back: 2880 clocks a tile).  O is rescaled only
+// when a row's maximum has grown by more than 8 binary orders (P <= 2^8 fits
+// bf16 as well as P <= 1 does, and the sums are fp32), so almost never.
 //
 // Rounding: weights P to bf16 (half a step, 2^-8 of each weight), because the
 // tensor cores take both operands in one 16-bit type; scores, maxima, sums and
@@ -100,7 +103,7 @@ struct Cfg {
   // V: rows of VROW bytes, half of the dimensions in blocks of up to 64; at d = 64
   // a half is 32 dimensions and the swizzle spans 64 bytes
   static constexpr int VROW = D == 64 ? 64 : 128, VBLK = D == 64 ? 1 : D / 128;
-  static constexpr uint32_t T_S = 256;                  // TMEM column of the score tiles
+  static constexpr uint32_t T_S = 256, T_P = 384;       // TMEM columns of the scores, the weights
   static_assert(SMEM <= 227 * 1024, "shared memory");
   static_assert(NK <= kMaxStages && NV <= kMaxStages && NK >= 2, "barriers");
 };
@@ -118,6 +121,7 @@ struct Ctrl {
   uint64_t s_full[kMaxStages];    // a tile's scores are done, and so is its K stage
   uint64_t pv_done[kMaxStages];   // a tile's O product is done, and so is its V stage
   uint64_t q_full[2], q_done[2], p_ready[2];
+  uint64_t s_free;                // the scores are in registers
   uint64_t seg_done;              // a segment's last O product
   uint64_t pair[4];            // the two warps of a row quarter
   uint32_t tmem;
@@ -430,6 +434,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tc::mbar_init(&ctl->p_ready[i], 2 * kSoftWarps);
       }
       tc::mbar_init(&ctl->seg_done, 1);
+      tc::mbar_init(&ctl->s_free, 2 * kSoftWarps);
       for (int i = 0; i < 4; ++i) tc::mbar_init(&ctl->pair[i], 2);
       asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -561,20 +566,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     Cursor c;
     c.init(p, ctl);
     Ring<C::NK> rk;
-    Ring<C::NV> ro;       // the O product of tile it - 2, whose weights lie where these scores go
     bool ok = rank == 0;
     const uint32_t qa = base + kCtrlBytes, ra = qa + C::QBYTES;
     for (uint32_t it = 0; ok && c.valid; ++it) {
       const int h = c.seg & 1;
-      if (it >= 2) {
-        ok = wait_for(a, &ctl->pv_done[ro.s], ro.ph);
-        ro.step();
-      }
+      if (it >= 1) ok = wait_for(a, &ctl->s_free, (it - 1) & 1u);
       if (ok && c.first) ok = wait_for(a, &ctl->q_full[h], (uint32_t)(c.seg >> 1) & 1u);
       if (ok) ok = wait_for(a, &ctl->k_full[rk.s], rk.ph);
       if (!ok) break;
       const uint32_t q0 = qa + ((c.prefix || !halves) ? 0 : h * 8192);
-      const uint32_t d = tmem + C::T_S + (it & 1u) * kTile;
+      const uint32_t d = tmem + C::T_S;
       tc::fence_after_sync();
       if (lane == 0) {
         const uint32_t k0 = ra + rk.s * C::STAGE;
@@ -598,7 +599,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t ra = base + kCtrlBytes + C::QBYTES + C::NK * C::STAGE;
     const int rpb = a.page < 64 ? a.page : 64, rsh = 31 - __clz(rpb);
     for (uint32_t it = 0; ok && c.valid; ++it) {
-      const uint32_t pa = tmem + C::T_S + (it & 1u) * kTile, vs = ra + rv.s * C::STAGE;
+      const uint32_t pa = tmem + C::T_P + (it & 1u) * 64, vs = ra + rv.s * C::STAGE;
       const int n = c.count(), steps = (n + 15) >> 4;
       ok = wait_for(a, &ctl->v_full[rv.s], rv.ph);
       if (!ok) break;
@@ -623,13 +624,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       tc::fence_after_sync();
       if (lane == 0) {
         const uint64_t dv = desc_v<D>(rpb * C::VROW);
-        // keys 16 k ..: pieces of rpb keys with all their blocks, one after the other;
-        // keys 64 .. 127 of P lie 64 columns on.  (Unrolled: the addresses of a step
-        // computed in a loop took longer than its product.)
+        // keys 16 k ..: pieces of rpb keys with all their blocks, one after the other.
+        // (Unrolled: the addresses of a step computed in a loop took longer than its
+        // product.)
 #pragma unroll
         for (int k = 0; k < kTile / 16; ++k)
           if (k < steps)
-            mma_pair_ts(tmem, pa + (k >> 2) * 64 + (k & 3) * 8,
+            mma_pair_ts(tmem, pa + k * 8,
                         tc::sdesc_at(dv, vs + k * 16 * C::VROW + (((k * 16) >> rsh) << rsh) * (D - C::VROW)),
                         C::IDESC_PV, k == 0 ? !c.first : 1u);
         commit_pair(&ctl->pv_done[rv.s]);
@@ -650,7 +651,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int step = row / pl.G;                          // of a tail's row
     uint32_t it = 0, met = 0;
     Ring<C::NK> rs;       // tile it's scores
-    Ring<C::NV> ro;       // tile it - 1's O product
+    Ring<C::NV> ro, rp;   // the O products of tiles it - 1 and it - 2
     float m = -INFINITY, l = 0.0f;
     bool ok = true;
     // A finished segment is written out in the next one's first tile, after that
@@ -694,11 +695,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const bool active = quarter * 32 < rows;
       ok = wait_for(a, &ctl->s_full[rs.s], rs.ph);
       if (!ok) break;
-      if (active) {
+      tc::fence_after_sync();
+      float s[64];
+      if (active) tmem_ld64(tmem + lanes + C::T_S + half * 64, s);
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) arrive_at(peer(tc::smem_u32(&ctl->s_free), 0));
+      // the weights go where those of tile it - 2 were
+      if (it >= 2) {
+        ok = wait_for(a, &ctl->pv_done[rp.s], rp.ph);
+        if (!ok) break;
         tc::fence_after_sync();
-        const uint32_t ts = tmem + lanes + C::T_S + (it & 1u) * kTile + half * 64;
-        float s[64];
-        tmem_ld64(ts, s);
+        rp.step();
+      }
+      if (active) {
         // keys this row sees in its half of the tile
         int see = c.keys - c.t * kTile;
         if (!c.prefix) see -= a.steps - 1 - step;
@@ -755,7 +765,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           pk[j] = __uint_as_float(pack_bf16x2(e0, e1));
         }
         l += s0 + s1;
-        tc::tmem_st32(ts, pk);
+        tc::tmem_st32(tmem + lanes + C::T_P + (it & 1u) * 64 + half * 32, pk);
       }
       if (done.pending) {
         write_out();
