@@ -37,6 +37,7 @@
 //              cores idle for some 500 clocks at each change between them, 1000
 //              of a tile's 3400; now one's barriers pass under the other's
 //              products.)
+//   warp 11    a tail's last V tile: zeros in the rows past its end
 //   warps 2-9  softmax: a thread holds half a row's 128 scores; P goes back to
 //              tensor memory as bf16 and is read from there as the A operand
 // TMEM: O (d columns), one score tile (128), two weight tiles (64 each).  The
@@ -64,9 +65,9 @@ namespace {
 
 constexpr int kTile = 128;            // keys per tile
 constexpr int kMaxShares = 80;        // CTA pairs the workspace has room for
-constexpr int kThreads = 352;
+constexpr int kThreads = 384;
 constexpr int kSoftWarps = 8;
-constexpr int kPvWarp = 2 + kSoftWarps;
+constexpr int kPvWarp = 2 + kSoftWarps, kCleanWarp = kPvWarp + 1;
 constexpr int kMaxStages = 8;
 constexpr uint32_t kCtrlBytes = 3072;
 
@@ -122,6 +123,7 @@ struct Ctrl {
   uint64_t pv_done[kMaxStages];   // a tile's O product is done, and so is its V stage
   uint64_t q_full[2], q_done[2], p_ready[2];
   uint64_t s_free;                // the scores are in registers
+  uint64_t landed[kMaxStages];    // this CTA's half of a V tile that ends inside 16 keys, by its stage
   uint64_t seg_done;              // a segment's last O product
   uint64_t pair[4];            // the two warps of a row quarter
   uint32_t tmem;
@@ -424,7 +426,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       for (int s = 0; s < kMaxStages; ++s) {
         tc::mbar_init(&ctl->k_full[s], 1);
-        tc::mbar_init(&ctl->v_full[s], 1);
+        tc::mbar_init(&ctl->v_full[s], 2);
+        tc::mbar_init(&ctl->landed[s], 1);
         tc::mbar_init(&ctl->s_full[s], 1);
         tc::mbar_init(&ctl->pv_done[s], 1);
       }
@@ -449,6 +452,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   cluster_sync();            // the other CTA's barriers are set up
   tc::fence_after_sync();
   const uint32_t tmem = ctl->tmem;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // the q region holds two tail jobs' rows when they are few, else one
   const bool halves = pl.R <= 64;
 
@@ -480,15 +484,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       return (int)(((long long)pg << shift) + (row & (a.page - 1)));
     };
     int rows_n = piece(cn), rows_k = 0, rows_v = 0;
-    // Opens a stage for a tile of n keys: both CTAs' boxes report to the first CTA,
-    // which expects the bytes of all.
-    auto open_stage = [&](uint64_t* full, uint64_t* used, uint32_t ph, int n) -> uint32_t {
-      ok = wait_for(a, used, ph ^ 1u);
-      if (ok && rank == 0 && lane == 0)
-        mbar_expect_tx(full, (uint32_t)(((n + rpb - 1) >> rsh) << rsh) * (D * 2));
-      __syncwarp();
-      return peer(tc::smem_u32(full), 0);
-    };
+    const auto tile_rows = [&](int n) { return ((n + rpb - 1) >> rsh) << rsh; };   // rows of its boxes
     auto load_k = [&]() {
       if (ck.first) {
         const int s = ck.seg, h = s & 1;
@@ -510,8 +506,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         __syncwarp();
       }
       const int n = ck.count();
-      const uint32_t mbar = open_stage(&ctl->k_full[rk.s], &ctl->s_full[rk.s], rk.ph, n);
+      ok = wait_for(a, &ctl->s_full[rk.s], rk.ph ^ 1u);
       if (!ok) return;
+      // both CTAs' boxes report to the first, which expects the bytes of all
+      const uint32_t mbar = peer(tc::smem_u32(&ctl->k_full[rk.s]), 0);
+      if (rank == 0 && lane == 0) mbar_expect_tx(&ctl->k_full[rk.s], (uint32_t)tile_rows(n) * (D * 2));
+      __syncwarp();
       // this CTA's 64 keys: [block of 64 dimensions][64 keys][128 bytes]; pieces of
       // 64 keys come with all their blocks in one box
       const int mine = min(max(n - 64 * (int)rank, 0), 64), nb = (mine + rpb - 1) >> rsh;
@@ -525,8 +525,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     };
     auto load_v = [&]() {
       const int n = cv.count();
-      const uint32_t mbar = open_stage(&ctl->v_full[rv.s], &ctl->pv_done[rv.s], rv.ph, n);
+      ok = wait_for(a, &ctl->pv_done[rv.s], rv.ph ^ 1u);
       if (!ok) return;
+      // as for K, with an arrival of each CTA; a tile that ends inside 16 keys reports
+      // to its own CTA, whose cleaning warp then arrives
+      uint32_t mbar = peer(tc::smem_u32(&ctl->v_full[rv.s]), 0);
+      if (n & 15) {
+        mbar = peer(tc::smem_u32(&ctl->landed[rv.s]), rank);
+        if (lane == 0) mbar_expect_tx(&ctl->landed[rv.s], (uint32_t)tile_rows(n) * D);
+      } else if (lane == 0) {
+        if (rank == 0) mbar_expect_tx(&ctl->v_full[rv.s], (uint32_t)tile_rows(n) * (D * 2));
+        else arrive_at(mbar);
+      }
+      __syncwarp();
       // all keys of half of the dimensions: [piece][block of dimensions][keys][VROW bytes]
       const int nb = (n + rpb - 1) >> rsh;
       if (lane < nb)
@@ -603,22 +614,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int n = c.count(), steps = (n + 15) >> 4;
       ok = wait_for(a, &ctl->v_full[rv.s], rv.ph);
       if (!ok) break;
-      // a masked key has weight zero, but zero times a stale NaN is NaN: its
-      // values in the last 16 rows become zeros, in both CTAs
-      if (n & 15) {
-        const int z = 16 - (n & 15), chunks = C::VROW / 16 * C::VBLK;   // 16-byte pieces of a row
-        const uint32_t v = vs + (((n >> rsh) * D) << rsh);
-        const uint32_t v0 = peer(v, 0), v1 = peer(v, 1);
-        for (int w = lane; w < z * chunks; w += 32) {
-          const int row = (n & (rpb - 1)) + w / chunks, c16 = w % chunks;
-          const uint32_t off = (c16 / (C::VROW / 16)) * (rpb * C::VROW) + row * C::VROW + (c16 % (C::VROW / 16)) * 16;
-          asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(v0 + off), "r"(0) : "memory");
-          asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(v1 + off), "r"(0) : "memory");
-        }
-        asm volatile("fence.acq_rel.cluster;" ::: "memory");
-        asm volatile("fence.proxy.async;" ::: "memory");
-        __syncwarp();
-      }
       ok = wait_for(a, &ctl->p_ready[it & 1u], (it >> 1) & 1u);
       if (!ok) break;
       tc::fence_after_sync();
@@ -639,6 +634,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       __syncwarp();
       rv.step();
       c.next(p);
+    }
+  } else if (warp == kCleanWarp) {
+    // ---- the rows past a tail's end ----
+    // A masked key has weight zero, but zero times a stale NaN is NaN: its values in
+    // the last 16 rows that the product reads become zeros.
+    Cursor c;
+    c.init(p, ctl);
+    Ring<C::NV> rv;
+    uint32_t phases = 0;      // one bit per stage: its use of `landed` that comes next
+    bool ok = true;
+    const int rpb = a.page < 64 ? a.page : 64, rsh = 31 - __clz(rpb);
+    for (; c.valid; c.next(p), rv.step()) {
+      const int n = c.count();
+      if ((n & 15) == 0) continue;
+      ok = wait_for(a, &ctl->landed[rv.s], (phases >> rv.s) & 1u);
+      if (!ok) break;
+      phases ^= 1u << rv.s;
+      uint8_t* v = ring + (C::NK + rv.s) * C::STAGE + (((n >> rsh) * D) << rsh);
+      constexpr int per = C::VROW / 16, chunks = per * C::VBLK;   // 16-byte pieces of a row
+      for (int w = lane; w < (16 - (n & 15)) * chunks; w += 32) {
+        const int row = (n & (rpb - 1)) + w / chunks, c16 = w % chunks;
+        *reinterpret_cast<uint4*>(v + (c16 / per) * (rpb * C::VROW) + row * C::VROW + (c16 % per) * 16) =
+            make_uint4(0, 0, 0, 0);
+      }
+      tc::fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) arrive_at(peer(tc::smem_u32(&ctl->v_full[rv.s]), 0));
     }
   } else {
     // ---- softmax and the share's partial results ----
@@ -799,7 +821,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
-// Joins a token's ranges: a CTA takes one query token, one key head and 64 of
+// Joins a token's ranges: a CTA takes one query token, one key head and 32 of
 // its dimensions; a thread one group head and four dimensions of a share of the
 // ranges, the shares meeting in shared memory in a fixed order.
 constexpr int kJoinThreads = 256;
@@ -813,8 +835,10 @@ __global__ void __launch_bounds__(kJoinThreads) attn_shared_join(const __grid_co
   static_assert(kMaxShares <= kJoinThreads, "a thread per share");
   const AttnSharedArgs& a = p.a;
   const Plan& pl = p.pl;
-  const int tok = blockIdx.x, hk = blockIdx.y, d0 = blockIdx.z * 16;   // in groups of 4 dimensions
+  const int tok = blockIdx.x, hk = blockIdx.y, d0 = blockIdx.z * 8;   // in groups of 4 dimensions
   const int b = tok / a.steps, step = tok - b * a.steps;
+  // launched while the first kernel runs; its results are there from here on
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const long long t_lo = p.tail_cost[b], t_hi = p.tail_cost[b + 1];
   const long long total = pl.wp + p.tail_cost[a.batch];
   int n_prefix = 0, n_ranges = 0;
@@ -865,7 +889,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_shared_join(const __grid_co
     __syncthreads();
   }
 
-  const int items = pl.G * 16;
+  const int items = pl.G * 8;
   for (int i0 = 0; i0 < items; i0 += kJoinThreads) {
     const int width = min(items - i0, kJoinThreads), groups = kJoinThreads / width;
     const int grp = threadIdx.x / width, item = i0 + threadIdx.x % width;
@@ -1020,8 +1044,17 @@ cudaError_t launch_d(const AttnSharedArgs& a, cudaStream_t stream, int sms) {
     return e;
   attn_shared_kernel<D><<<2 * p.pl.shares, kThreads, C::SMEM, stream>>>(tk, tv, tqp, tqt, p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  attn_shared_join<D><<<dim3(p.pl.ntok, p.pl.h_kv, D / 64), kJoinThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  // the join's launch passes under the first kernel
+  cudaLaunchAttribute overlap;
+  overlap.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  overlap.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.pl.ntok, p.pl.h_kv, D / 32);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = stream;
+  cfg.attrs = &overlap;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attn_shared_join<D>, p);
 }
 
 }  // namespace
