@@ -88,6 +88,7 @@ struct SharedParams {
   AttnSharedArgs a;
   Plan pl;
   long long* tail_cost;        // [batch + 1] running cost of the tails (relative to wp)
+  long long* starts;           // [shares + 1] where each share begins
   float4* ml;                  // (m, l half 0, l half 1, -) per slot row
   float* opart;                // per slot: [d / 4][rows][4]
 };
@@ -405,6 +406,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       run += v[i];
     }
     __syncthreads();
+    if (blockIdx.x == 0 && threadIdx.x <= pl.shares)
+      p.starts[threadIdx.x] = share_start(pl, pl.wp + scan[a.batch], threadIdx.x);
     if (threadIdx.x == 0) {
       const long long total = pl.wp + scan[a.batch];
       ctl->x0 = share_start(pl, total, share);
@@ -821,9 +824,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
-// Joins a token's ranges: a CTA takes one query token, one key head and 32 of
-// its dimensions; a thread one group head and four dimensions of a share of the
-// ranges, the shares meeting in shared memory in a fixed order.
+// Joins a token's ranges: a CTA takes one query token, one key head and d /
+// gridDim.z of its dimensions; a thread one group head and four dimensions of a
+// share of the ranges, the shares meeting in shared memory in a fixed order.  (A
+// CTA finds its ranges first, at a cost of some trips to L2, so few CTAs with all
+// of a head's dimensions each are better than many with 32 as soon as they fill
+// the GPU: 25 us of the latter for 512 tokens and heads.)
 constexpr int kJoinThreads = 256;
 
 template <int D>
@@ -835,12 +841,11 @@ __global__ void __launch_bounds__(kJoinThreads) attn_shared_join(const __grid_co
   static_assert(kMaxShares <= kJoinThreads, "a thread per share");
   const AttnSharedArgs& a = p.a;
   const Plan& pl = p.pl;
-  const int tok = blockIdx.x, hk = blockIdx.y, d0 = blockIdx.z * 8;   // in groups of 4 dimensions
+  const int tok = blockIdx.x, hk = blockIdx.y, width4 = D / 4 / gridDim.z;   // in groups of 4 dimensions
   const int b = tok / a.steps, step = tok - b * a.steps;
   // launched while the first kernel runs; its results are there from here on
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const long long t_lo = p.tail_cost[b], t_hi = p.tail_cost[b + 1];
-  const long long total = pl.wp + p.tail_cost[a.batch];
   int n_prefix = 0, n_ranges = 0;
 
   // the shares that hold ranges of this token's two jobs (its prefix block, its
@@ -854,7 +859,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_shared_join(const __grid_co
   {
     bool has[2] = {false, false};
     if (threadIdx.x < pl.shares) {
-      const long long x0 = share_start(pl, total, threadIdx.x), x1 = share_start(pl, total, threadIdx.x + 1);
+      const long long x0 = p.starts[threadIdx.x], x1 = p.starts[threadIdx.x + 1];
       if (pl.np) {
         const long long pos = job[0] * (pl.ptiles * kCostPrefix + kCostJob);
         has[0] = tiles_before(x0, pos, kCostPrefix, pl.ptiles) < tiles_before(x1, pos, kCostPrefix, pl.ptiles);
@@ -889,7 +894,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_shared_join(const __grid_co
     __syncthreads();
   }
 
-  const int items = pl.G * 8;
+  const int items = pl.G * width4, d0 = blockIdx.z * width4;
   for (int i0 = 0; i0 < items; i0 += kJoinThreads) {
     const int width = min(items - i0, kJoinThreads), groups = kJoinThreads / width;
     const int grp = threadIdx.x / width, item = i0 + threadIdx.x % width;
@@ -1027,6 +1032,8 @@ cudaError_t launch_d(const AttnSharedArgs& a, cudaStream_t stream, int sms) {
   char* ws = static_cast<char*>(a.scratch);
   p.tail_cost = reinterpret_cast<long long*>(ws);
   ws += up256((size_t)(a.batch + 1) * 8);
+  p.starts = reinterpret_cast<long long*>(ws);
+  ws += up256((kMaxShares + 1) * 8);
   const size_t rows = slot_rows(p.pl, a.batch);
   p.ml = reinterpret_cast<float4*>(ws);
   ws += up256(rows * sizeof(float4));
@@ -1049,7 +1056,9 @@ cudaError_t launch_d(const AttnSharedArgs& a, cudaStream_t stream, int sms) {
   overlap.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   overlap.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.pl.ntok, p.pl.h_kv, D / 32);
+  int nz = 1;   // CTAs per token and key head
+  while (nz < D / 32 && (long long)p.pl.ntok * p.pl.h_kv * nz < 2LL * sms) nz *= 2;
+  cfg.gridDim = dim3(p.pl.ntok, p.pl.h_kv, nz);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
   cfg.attrs = &overlap;
@@ -1062,7 +1071,7 @@ cudaError_t launch_d(const AttnSharedArgs& a, cudaStream_t stream, int sms) {
 size_t attn_shared_scratch_bytes(int batch, int steps, int h_q, int h_kv, int d) {
   const Plan pl = make_plan(batch > 0 ? batch : 1, steps, h_q, h_kv, 1, kMaxShares);
   const size_t rows = slot_rows(pl, batch);
-  return up256((size_t)(batch + 1) * 8) + up256(rows * sizeof(float4)) + up256(rows * d * 4);
+  return up256((size_t)(batch + 1) * 8) + up256((kMaxShares + 1) * 8) + up256(rows * sizeof(float4)) + up256(rows * d * 4);
 }
 
 cudaError_t launch_attn_shared(const AttnSharedArgs& p, cudaStream_t stream) {
