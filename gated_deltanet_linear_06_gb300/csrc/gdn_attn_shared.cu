@@ -87,8 +87,7 @@ struct Plan {
 struct SharedParams {
   AttnSharedArgs a;
   Plan pl;
-  long long* tail_cost;        // [batch + 1] running cost of the tails (relative to wp)
-  long long* starts;           // [shares + 1] where each share begins
+  int2* span;                  // per job: the first and the last share with a range of it
   float4* ml;                  // (m, l half 0, l half 1, -) per slot row
   float* opart;                // per slot: [d / 4][rows][4]
 };
@@ -193,8 +192,11 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-__device__ __forceinline__ long long share_start(const Plan& pl, long long total, int c) {
-  return total * c / pl.shares;
+// Shares in use: none is shorter than a tile, so that the shares from a job's first
+// range to its last all have one.
+__device__ __forceinline__ int shares_of(const Plan& pl, long long total) {
+  constexpr int top = kCostPrefix > kCostTail ? kCostPrefix : kCostTail;
+  return (int)max(1LL, min((long long)pl.shares, total / top));
 }
 __device__ __forceinline__ int tail_tiles(int len) { return (len + kTile - 1) / kTile; }
 __device__ __forceinline__ long long tail_cost_of(int len) {
@@ -226,7 +228,7 @@ struct Cursor {
   bool prefix, valid, first, last;
   int hk, mb;          // key head; block of rows (prefix) or sequence (tail)
   int slot_job;        // prefix job, or tail job
-  int t, t1, keys;
+  int t, t0, t1, keys; // tile, the range's first and end, keys of the job
 
   __device__ __forceinline__ void init(const SharedParams& p, const Ctrl* c) {
     pos = c->pos0;
@@ -235,7 +237,7 @@ struct Cursor {
     job = c->job0;
     len = ahead = -1;
     seg = -1;
-    t = t1 = 0;
+    t = t0 = t1 = 0;
     valid = true;
     find(p);
   }
@@ -275,7 +277,7 @@ struct Cursor {
       pos += cost;
       ++job;
       if (a < b) {
-        t = a;
+        t = t0 = a;
         t1 = b;
         first = true;
         last = a + 1 == b;
@@ -370,84 +372,94 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     return;
   }
 
-  // ---- this CTA's share: the running cost of the tails, then a search ----
-  long long* scan = reinterpret_cast<long long*>(ring);   // [batch + 1] and warp totals, before the ring is used
-  long long* wsum = scan + GDN_ATTN_MAX_BATCH + 8;
-  {
-    constexpr int PER = 4;
-    static_assert(kThreads * PER >= GDN_ATTN_MAX_BATCH, "one pass");
-    long long v[PER], sum = 0;
-    for (int i = 0; i < PER; ++i) {
-      const int b = threadIdx.x * PER + i;
-      v[i] = 0;
-      if (b < a.batch && a.tail_width > 0) {
-        const int n = a.tail_len[b];
-        if ((n < 0 || (long long)n > (long long)a.tail_width * a.page) && blockIdx.x == 0)
-          record_status(a.status, GDN_ERR_DEVICE_BOUNDS);
-        v[i] = tail_cost_of(tail_length(a, b)) * pl.h_kv;
-      }
-      sum += v[i];
-    }
-    long long inc = sum;
-    for (int m = 1; m < 32; m <<= 1) {
-      const long long o = __shfl_up_sync(0xffffffffu, inc, m);
-      if (lane >= m) inc += o;
-    }
-    if (lane == 31) wsum[warp] = inc;
-    __syncthreads();
-    long long run = inc - sum;
-    for (int w = 0; w < warp; ++w) run += wsum[w];
-    for (int i = 0; i < PER; ++i) {
-      const int b = threadIdx.x * PER + i;
-      if (b <= a.batch) {
-        scan[b] = run;
-        if (blockIdx.x == 0) p.tail_cost[b] = run;
-      }
-      run += v[i];
-    }
-    __syncthreads();
-    if (blockIdx.x == 0 && threadIdx.x <= pl.shares)
-      p.starts[threadIdx.x] = share_start(pl, pl.wp + scan[a.batch], threadIdx.x);
-    if (threadIdx.x == 0) {
-      const long long total = pl.wp + scan[a.batch];
-      ctl->x0 = share_start(pl, total, share);
-      ctl->x1 = share_start(pl, total, share + 1);
-      if (ctl->x0 < pl.wp) {
-        const long long cost = pl.ptiles * kCostPrefix + kCostJob;
-        const long long j = ctl->x0 / cost;
-        ctl->job0 = (int)j;
-        ctl->pos0 = j * cost;
-      } else {
-        const long long x = ctl->x0 - pl.wp;
-        int lo = 0, hi = a.batch;      // the last b with scan[b] <= x
-        while (hi - lo > 1) {
-          const int mid = (lo + hi) >> 1;
-          if (scan[mid] <= x) lo = mid; else hi = mid;
-        }
-        ctl->job0 = pl.np + lo * pl.h_kv;
-        ctl->pos0 = pl.wp + scan[lo];
-      }
-      for (int s = 0; s < kMaxStages; ++s) {
-        tc::mbar_init(&ctl->k_full[s], 1);
-        tc::mbar_init(&ctl->v_full[s], 2);
-        tc::mbar_init(&ctl->landed[s], 1);
-        tc::mbar_init(&ctl->s_full[s], 1);
-        tc::mbar_init(&ctl->pv_done[s], 1);
-      }
-      for (int i = 0; i < 2; ++i) {
-        tc::mbar_init(&ctl->q_full[i], 1);
-        tc::mbar_init(&ctl->q_done[i], 1);
-        tc::mbar_init(&ctl->p_ready[i], 2 * kSoftWarps);
-      }
-      tc::mbar_init(&ctl->seg_done, 1);
-      tc::mbar_init(&ctl->s_free, 2 * kSoftWarps);
-      for (int i = 0; i < 4; ++i) tc::mbar_init(&ctl->pair[i], 2);
-      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    }
-  }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(tc::smem_u32(&ctl->tmem)));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+  }
+  if (warp == kCleanWarp) {
+    if (lane < kMaxStages) {
+      tc::mbar_init(&ctl->k_full[lane], 1);
+      tc::mbar_init(&ctl->v_full[lane], 2);
+      tc::mbar_init(&ctl->landed[lane], 1);
+      tc::mbar_init(&ctl->s_full[lane], 1);
+      tc::mbar_init(&ctl->pv_done[lane], 1);
+    } else if (lane < kMaxStages + 2) {
+      tc::mbar_init(&ctl->q_full[lane - kMaxStages], 1);
+      tc::mbar_init(&ctl->q_done[lane - kMaxStages], 1);
+      tc::mbar_init(&ctl->p_ready[lane - kMaxStages], 2 * kSoftWarps);
+    } else if (lane < kMaxStages + 6) {
+      tc::mbar_init(&ctl->pair[lane - kMaxStages - 2], 2);
+    } else if (lane == kMaxStages + 6) {
+      tc::mbar_init(&ctl->s_free, 2 * kSoftWarps);
+      tc::mbar_init(&ctl->seg_done, 1);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  // ---- this pair's share: the running cost of the tails, then a search ----
+  long long* scan = reinterpret_cast<long long*>(ring);   // [batch + 1] and warp totals, before the ring is used
+  long long* wsum = scan + GDN_ATTN_MAX_BATCH + 8;
+  long long tails = 0;
+  if (a.tail_width > 0) {
+    constexpr int PER = 4;
+    static_assert(kThreads * PER >= GDN_ATTN_MAX_BATCH, "one pass");
+    long long v[PER], sum = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int b = i * kThreads + threadIdx.x;
+      v[i] = 0;
+      if (b < a.batch) {
+        const int n = a.tail_len[b];
+        if ((n < 0 || n > a.tail_width * a.page) && blockIdx.x == 0) record_status(a.status, GDN_ERR_DEVICE_BOUNDS);
+        v[i] = tail_cost_of(clamp_tail(a, n)) * pl.h_kv;
+      }
+    }
+    // chunks of kThreads sequences, one after the other
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      if (i * kThreads >= a.batch) break;
+      long long inc = v[i];
+      for (int m = 1; m < 32; m <<= 1) {
+        const long long o = __shfl_up_sync(0xffffffffu, inc, m);
+        if (lane >= m) inc += o;
+      }
+      if (lane == 31) wsum[warp] = inc;
+      __syncthreads();
+      long long before = tails;
+      for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) before += wsum[w];
+        sum += wsum[w];
+      }
+      const int b = i * kThreads + threadIdx.x;
+      if (b < a.batch) scan[b] = before + inc - v[i];
+      tails = sum;
+      __syncthreads();
+    }
+  }
+  if (threadIdx.x == 0) {
+    const long long total = pl.wp + tails;
+    const int shares = shares_of(pl, total);
+    const long long x0 = share < shares ? total * share / shares : total;
+    const long long x1 = share < shares ? total * (share + 1) / shares : total;
+    ctl->x0 = x0;
+    ctl->x1 = x1;
+    if (x0 < pl.wp) {
+      const long long cost = pl.ptiles * kCostPrefix + kCostJob;
+      const long long j = x0 / cost;
+      ctl->job0 = (int)j;
+      ctl->pos0 = j * cost;
+    } else if (x0 < total) {
+      const long long x = x0 - pl.wp;
+      int lo = 0, hi = a.batch;      // the last b with scan[b] <= x
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (scan[mid] <= x) lo = mid; else hi = mid;
+      }
+      ctl->job0 = pl.np + lo * pl.h_kv;
+      ctl->pos0 = pl.wp + scan[lo];
+    } else {                         // nothing to do
+      ctl->job0 = pl.np + a.batch * pl.h_kv;
+      ctl->pos0 = total;
+    }
   }
   tc::fence_proxy_async();   // the scan's writes before the ring's copies
   tc::fence_before_sync();
@@ -801,6 +813,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (lane == 0) arrive_at(peer(tc::smem_u32(&ctl->p_ready[it & 1u]), 0));
       if (c.last) {
         const long long slot = c.slot_job + share;
+        // which shares hold the job's ranges, for the join
+        if (rank == 0 && warp == 2 && lane == 0) {
+          const int job = c.prefix ? c.slot_job : pl.np + c.slot_job;
+          if (c.t0 == 0) p.span[job].x = share;
+          if ((long long)c.t1 * kTile >= c.keys) p.span[job].y = share;
+        }
         done.pending = true;
         done.seg = (uint32_t)c.seg;
         done.rows = rows;
@@ -836,63 +854,25 @@ template <int D>
 __global__ void __launch_bounds__(kJoinThreads) attn_shared_join(const __grid_constant__ SharedParams p) {
   __shared__ float4 acc[kJoinThreads];
   __shared__ float2 stat[kJoinThreads];
-  __shared__ long long list[2 * kMaxShares];   // first slot row of each range
-  __shared__ int count[2][kJoinThreads / 32];
-  static_assert(kMaxShares <= kJoinThreads, "a thread per share");
   const AttnSharedArgs& a = p.a;
   const Plan& pl = p.pl;
   const int tok = blockIdx.x, hk = blockIdx.y, width4 = D / 4 / gridDim.z;   // in groups of 4 dimensions
   const int b = tok / a.steps, step = tok - b * a.steps;
-  // launched while the first kernel runs; its results are there from here on
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const long long t_lo = p.tail_cost[b], t_hi = p.tail_cost[b + 1];
-  int n_prefix = 0, n_ranges = 0;
-
-  // the shares that hold ranges of this token's two jobs (its prefix block, its
-  // tail) for this key head
+  // this token's two jobs for this key head, its prefix block and its tail: a range in
+  // share c has slot job + c
   const int blk = tok / pl.tpb;                            // block of a CTA's rows
   const int job[2] = {hk * pl.nmb + (blk >> 1), b * pl.h_kv + hk};
-  const long long cost_tail = (t_hi - t_lo) / pl.h_kv;
   const int stride[2] = {128, pl.R};                       // rows of a CTA's part of a slot
   const int in[2] = {(tok - blk * pl.tpb) * pl.G, step * pl.G};
-  const long long region[2] = {(blk & 1) * 128, (long long)(pl.np ? pl.np + pl.shares : 0) * 256};
-  {
-    bool has[2] = {false, false};
-    if (threadIdx.x < pl.shares) {
-      const long long x0 = p.starts[threadIdx.x], x1 = p.starts[threadIdx.x + 1];
-      if (pl.np) {
-        const long long pos = job[0] * (pl.ptiles * kCostPrefix + kCostJob);
-        has[0] = tiles_before(x0, pos, kCostPrefix, pl.ptiles) < tiles_before(x1, pos, kCostPrefix, pl.ptiles);
-      }
-      if (cost_tail > 0) {
-        const long long pos = pl.wp + t_lo + hk * cost_tail, n = (cost_tail - kCostJob) / kCostTail;
-        has[1] = tiles_before(x0, pos, kCostTail, n) < tiles_before(x1, pos, kCostTail, n);
-      }
-    }
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    unsigned bal[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      bal[k] = __ballot_sync(0xffffffffu, has[k]);
-      if (lane == 0) count[k][warp] = __popc(bal[k]);
-    }
-    __syncthreads();
-    // prefix ranges first, then the tail's, each in the order of the shares
-    int at = 0;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      int mine = at;
-      for (int w = 0; w < kJoinThreads / 32; ++w) {
-        if (w < warp) mine += count[k][w];
-        at += count[k][w];
-      }
-      if (has[k])
-        list[mine + __popc(bal[k] & ((1u << lane) - 1))] = region[k] + (long long)(job[k] + threadIdx.x) * (k ? pl.R : 256);
-      if (k == 0) n_prefix = at;
-    }
-    n_ranges = at;
-    __syncthreads();
-  }
+  const int apart[2] = {256, pl.R};                        // slots are so many rows apart
+  // launched while the first kernel runs; its results are there from here on
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int2 none = make_int2(0, -1);
+  const int2 pre = pl.np ? p.span[job[0]] : none;
+  const int2 own = a.tail_width > 0 && a.tail_len[b] > 0 ? p.span[pl.np + job[1]] : none;
+  const int n_prefix = pre.y - pre.x + 1, n_ranges = n_prefix + own.y - own.x + 1;
+  const long long first[2] = {(long long)(job[0] + pre.x) * 256 + (blk & 1) * 128,
+                              (long long)(pl.np ? pl.np + pl.shares : 0) * 256 + (long long)(job[1] + own.x) * pl.R};
 
   const int items = pl.G * width4, d0 = blockIdx.z * width4;
   for (int i0 = 0; i0 < items; i0 += kJoinThreads) {
@@ -905,7 +885,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_shared_join(const __grid_co
 #pragma unroll 4
       for (int i = grp; i < n_ranges; i += groups) {
         const int k = i >= n_prefix;
-        const long long origin = list[i];
+        const long long origin = (k ? first[1] : first[0]) + (long long)(k ? i - n_prefix : i) * (k ? apart[1] : apart[0]);
         const int r = (k ? in[1] : in[0]) + g;
         const float4 ml = p.ml[origin + r];
         const float4 v = reinterpret_cast<const float4*>(p.opart)[origin * (D / 4) + (long long)c4 * (k ? stride[1] : stride[0]) + r];
@@ -1030,10 +1010,8 @@ cudaError_t launch_d(const AttnSharedArgs& a, cudaStream_t stream, int sms) {
   p.pl = make_plan(a.batch, a.steps, a.h_q, a.h_kv, a.prefix_len,
                    sms < 2 ? 1 : (sms / 2 < kMaxShares ? sms / 2 : kMaxShares));
   char* ws = static_cast<char*>(a.scratch);
-  p.tail_cost = reinterpret_cast<long long*>(ws);
-  ws += up256((size_t)(a.batch + 1) * 8);
-  p.starts = reinterpret_cast<long long*>(ws);
-  ws += up256((kMaxShares + 1) * 8);
+  p.span = reinterpret_cast<int2*>(ws);
+  ws += up256(((size_t)p.pl.np + (size_t)a.batch * a.h_kv) * sizeof(int2));
   const size_t rows = slot_rows(p.pl, a.batch);
   p.ml = reinterpret_cast<float4*>(ws);
   ws += up256(rows * sizeof(float4));
@@ -1057,7 +1035,7 @@ cudaError_t launch_d(const AttnSharedArgs& a, cudaStream_t stream, int sms) {
   overlap.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   int nz = 1;   // CTAs per token and key head
-  while (nz < D / 32 && (long long)p.pl.ntok * p.pl.h_kv * nz < 2LL * sms) nz *= 2;
+  while (nz < D / 32 && (long long)p.pl.ntok * p.pl.h_kv * nz < 6LL * sms) nz *= 2;
   cfg.gridDim = dim3(p.pl.ntok, p.pl.h_kv, nz);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
@@ -1071,7 +1049,7 @@ cudaError_t launch_d(const AttnSharedArgs& a, cudaStream_t stream, int sms) {
 size_t attn_shared_scratch_bytes(int batch, int steps, int h_q, int h_kv, int d) {
   const Plan pl = make_plan(batch > 0 ? batch : 1, steps, h_q, h_kv, 1, kMaxShares);
   const size_t rows = slot_rows(pl, batch);
-  return up256((size_t)(batch + 1) * 8) + up256((kMaxShares + 1) * 8) + up256(rows * sizeof(float4)) + up256(rows * d * 4);
+  return up256(((size_t)pl.np + (size_t)batch * h_kv) * sizeof(int2)) + up256(rows * sizeof(float4)) + up256(rows * d * 4);
 }
 
 cudaError_t launch_attn_shared(const AttnSharedArgs& p, cudaStream_t stream) {
