@@ -5,30 +5,36 @@
 // layer costs its weights' bytes: 6 hidden inter per expert that any token
 // chose.  The products run on the tensor cores all the same (m16n8k16: 16
 // weight rows by 8 tokens), because their cost then does not grow with the
-// tokens that share an expert.  Columns are tokens by their own number; a group
-// of 8 tokens that an expert does not serve is skipped.
+// tokens that share an expert.
 //
 // Kernel 1, router logits: a warp per (expert, 8 tokens).  The chosen experts
 // hang on which logits are larger, so the sums are compensated: each lane adds
 // its products to S, which starts at a constant so large that it rounds them to
-// a coarse grid exactly, and what S drops goes to a second sum; the two join in
-// 64 bits.  Four operations a product, 4 us of 340 at 64 tokens.
+// a coarse grid exactly, and what S drops goes to a second sum.  Logits stay
+// pairs of fp32 from there on (fp64 additions run at 1/64 of the rate here: with
+// them the choice of 8 experts alone took 12 us).
 //
-// Kernel 2, one CTA per SM, everything else:
-//   - a warp streams weights through a ring of 16 KB stages (16 rows x 512
-//     columns by TMA, 128-byte swizzle): first the shared expert's, which need
-//     no router and load while kernel 1 runs, then its share of the chosen
-//     experts' gate and up rows, then of the down rows.  It runs ahead of the
-//     products as far as the ring goes, past the grid barrier between the two
-//     phases too: a step's down weights land while the last gate rows finish;
-//   - eight warps choose the experts (every CTA for itself, which is cheaper
-//     than another barrier), then multiply: warp w takes columns 64 w .. of each
-//     stage, and the eight partial sums meet in shared memory in a fixed order.
-//     Phase 1 tiles are 8 gate rows over the same 8 up rows, so silu(g) u forms
-//     in one thread; the router's weight is multiplied in there.  Phase 2 tiles
-//     are up to 16 output rows for ALL experts, so that a token's experts add up
-//     in registers, in ascending order, without atomics or partial results.
-// Nothing in a token's arithmetic depends on the other tokens.
+// Kernel 2, one CTA of 12 warps per SM, everything else:
+//   - the choice of experts, by every CTA for itself, which is cheaper than a
+//     grid barrier;
+//   - phase 1, tiles of 8 gate rows over the same 8 up rows, so that silu(g) u
+//     forms in one thread; columns are the expert's own tokens; four warps share
+//     a tile, each with every fourth chunk of 128 weight columns;
+//   - a grid barrier;
+//   - phase 2, up to 16 output rows per CTA for ALL experts, so that a token's
+//     experts add up in registers without atomics or partial results; columns
+//     are tokens by their number, a group of 8 that an expert does not serve is
+//     skipped; the CTA's warps deal out the chunks of 128 weight columns.
+// Every warp feeds itself: it has three stages of 4 KB (16 rows x 128 columns, by
+// TMA, 128-byte swizzle) and refills a stage as soon as it has multiplied it, so
+// 12 warps keep some 100 KB on their way and no warp waits for another's data.
+// The stages run ahead past the choice (the shared expert's weights load while
+// kernel 1 runs) and past the grid barrier (the first down weights land during
+// it).  (With one loading warp and stages that eight or sixteen warps multiplied
+// together, every stage cost the latency of its activations and the meetings of
+// the warps: 1500 clocks, where its bytes take 700.)
+// Which warp adds what depends on the expert's and the chunk's numbers alone, so
+// nothing in a token's arithmetic depends on the other tokens.
 //
 // The activations between the products are kept as two bf16 (16 bits of
 // significand): one bf16 would cost 2^-9 of each, more than the fp32 output
@@ -45,30 +51,31 @@
 namespace gdn {
 namespace {
 
-constexpr int kMoeWarps = 8;                          // product warps
-constexpr int kMoeThreads = 32 * (kMoeWarps + 1);
-constexpr int kCols = 64 * kMoeWarps;                 // weight columns of a stage
+constexpr int kTeam = 4, kTeams = 3, kMoeWarps = kTeam * kTeams, kMoeThreads = 32 * kMoeWarps;
+constexpr int kCols = 128;                            // weight columns of a stage
 constexpr uint32_t kStage = 16 * kCols * 2;
-constexpr int kStages = 9;
+constexpr int kStages = 3;                            // of each warp
 constexpr int kMaxExperts = 1024, kMaxPairs = GDN_MOE_MAX_TOKENS * 32;
 constexpr long long kBarrierBudget = 1LL << 31;       // clock cycles
 
 struct MoeSmem {
-  uint64_t full[kStages], empty[kStages], lists;
+  uint64_t full[kMoeWarps][kStages];
   int n_active;
   int gave_up;                         // a wait ran out: no later one waits
   int scan_a[kMoeWarps], scan_p[kMoeWarps];
   float4 red[2][kMoeWarps][32];
   uint32_t mask[kMaxExperts][2];       // tokens of an expert
   uint16_t expert[kMaxExperts];        // active experts, ascending
-  uint16_t base[kMaxExperts];          // first pair of an active expert
+  uint16_t base[kMaxExperts + 1];      // first pair of an active expert
   uint16_t rank[kMaxExperts];          // expert -> its place among the active
   float shared_w[GDN_MOE_MAX_TOKENS];  // the shared expert's factor
   uint16_t sel[kMaxPairs];             // chosen experts, token-major
   float sel_w[kMaxPairs];
   float pair_w[kMaxPairs];             // weights in the order of the pairs
+  uint8_t pair_t[kMaxPairs];           // and their tokens
 };
-constexpr uint32_t kMoeSmem = kStages * kStage + sizeof(MoeSmem) + 1024;
+constexpr uint32_t kRing = kMoeWarps * kStages * kStage;
+constexpr uint32_t kMoeSmem = kRing + sizeof(MoeSmem) + 1024;
 static_assert(kMoeSmem <= 227 * 1024, "shared memory");
 
 struct MoeMaps {
@@ -77,12 +84,18 @@ struct MoeMaps {
 
 struct MoeParams {
   MoeArgs a;
-  double* logit;        // [tokens][experts + 1]
+  float2* logit;        // [tokens][experts + 1], high and low part
   unsigned* barrier;    // arrivals of the grid barrier; zeroed by kernel 1
   uint16_t* act;        // [hi, lo][pairs][inter]
   uint16_t* s_act;      // [hi, lo][tokens][shared_inter]
   int rows3, tiles3;    // output rows per tile, tiles
 };
+
+// a + b as a rounded sum and its error (Knuth's two-sum).
+__device__ __forceinline__ float2 two_sum(float a, float b) {
+  const float s = a + b, bb = s - a;
+  return make_float2(s, (a - (s - bb)) + (b - bb));
+}
 
 // ---- kernel 1 ----
 __global__ void __launch_bounds__(256) moe_router_kernel(const MoeParams p) {
@@ -123,33 +136,45 @@ __global__ void __launch_bounds__(256) moe_router_kernel(const MoeParams p) {
 #pragma unroll
   for (int t = 0; t < 8; ++t) {
     if (t >= nt) break;
-    double v = (double)(S[t] - kGrid) + (double)lo[t];
-    for (int m = 16; m >= 1; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
-    if (lane == 0) p.logit[(size_t)(t0 + t) * (a.experts + 1) + e] = v;
+    // the lanes' pairs (S - grid, lo) join as pairs: the high parts' rounding is kept
+    float h = S[t] - kGrid, l = lo[t];
+#pragma unroll
+    for (int m = 16; m >= 1; m >>= 1) {
+      const float oh = __shfl_xor_sync(0xffffffffu, h, m), ol = __shfl_xor_sync(0xffffffffu, l, m);
+      const float2 r = two_sum(h, oh);
+      h = r.x;
+      l = (l + ol) + r.y;
+    }
+    if (lane == 0) p.logit[(size_t)(t0 + t) * (a.experts + 1) + e] = two_sum(h, l);
   }
 }
 
 // ---- kernel 2 ----
 
-// e^x for x <= 0 given in 64 bits: the fp32 rounding of the argument is put
-// back as a factor (at x = -80 it alone would cost 2^-18 of the result).
-__device__ __forceinline__ float exp_of(double x) {
-  const float h = (float)x;
-  return h < -200.0f ? 0.0f : expf(h) * (1.0f + (float)(x - (double)h));
+// e^(v - top) for v <= top, both pairs: what the difference's rounding to fp32
+// drops is put back as a factor (at -80 it alone would cost 2^-18 of the result).
+__device__ __forceinline__ float exp_of(float2 v, float2 top) {
+  const float2 d = two_sum(v.x, -top.x);
+  return d.x < -200.0f ? 0.0f : expf(d.x) * (1.0f + (d.y + (v.y - top.y)));
 }
 
-// A 64-bit key in the order of the doubles, NaN lowest.
-__device__ __forceinline__ unsigned long long order_key(double v) {
-  if (v != v) return 0;
-  const long long b = __double_as_longlong(v + 0.0);   // -0 and 0 alike
-  return (unsigned long long)(b ^ ((b >> 63) | (1ll << 63)));
+// A 64-bit key in the order of the pairs, NaN lowest, -0 like 0.
+__device__ __forceinline__ uint32_t order32(float v) {
+  const uint32_t b = __float_as_uint(v == 0.0f ? 0.0f : v);
+  return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
-__device__ __forceinline__ double order_value(unsigned long long k) {
-  return __longlong_as_double((long long)(k ^ (k >> 63 ? 1ull << 63 : ~0ull)));
+__device__ __forceinline__ float order32_value(uint32_t k) {
+  return __uint_as_float(k >> 31 ? k ^ 0x80000000u : ~k);
+}
+__device__ __forceinline__ unsigned long long order_key(float2 v) {
+  return v.x != v.x ? 0ull : ((unsigned long long)order32(v.x) << 32) | order32(v.y == v.y ? v.y : 0.0f);
+}
+__device__ __forceinline__ float2 order_value(unsigned long long k) {
+  return make_float2(order32_value((uint32_t)(k >> 32)), order32_value((uint32_t)k));
 }
 
-__device__ __forceinline__ void products_sync() {   // the product warps
-  asm volatile("bar.sync 1, %0;" ::"n"(32 * kMoeWarps) : "memory");
+__device__ __forceinline__ void team_sync(int team) {
+  asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(32 * kTeam) : "memory");
 }
 
 __device__ __forceinline__ void tma3(uint32_t dst, const CUtensorMap* tm, int x, int y, int z, uint64_t* mbar) {
@@ -220,15 +245,16 @@ __device__ __forceinline__ void load_b_cg(uint4 (&b)[2], const uint16_t* row, in
     b[h] = use && k + 32 * h < n ? __ldcg(reinterpret_cast<const uint4*>(row + k + 32 * h)) : make_uint4(0, 0, 0, 0);
 }
 
-// Top-k of one token by one warp, into sel / sel_w.
+// Top-k of one token by one warp, into sel / sel_w; 32 V experts at most.
+template <int V>
 __device__ void choose(const MoeParams& p, MoeSmem* sm, int t, int lane) {
   const MoeArgs& a = p.a;
-  const double* lg = p.logit + (size_t)t * (a.experts + 1);
-  unsigned long long key[kMaxExperts / 32];
+  const float2* lg = p.logit + (size_t)t * (a.experts + 1);
+  unsigned long long key[V];
   unsigned long long best = 0;
   int at = -1;
 #pragma unroll
-  for (int j = 0; j < kMaxExperts / 32; ++j) {
+  for (int j = 0; j < V; ++j) {
     if (j * 32 >= a.experts) break;
     const int e = j * 32 + lane;
     key[j] = e < a.experts ? order_key(__ldcg(lg + e)) : 0;
@@ -238,7 +264,7 @@ __device__ void choose(const MoeParams& p, MoeSmem* sm, int t, int lane) {
     }
   }
   uint32_t used = 0;
-  double top = 0.0;
+  float2 top = make_float2(0.0f, 0.0f);
   float den = 0.0f, sum = 0.0f, mine = 0.0f;
   for (int k = 0; k < a.top_k; ++k) {
     const uint32_t hi = at >= 0 ? (uint32_t)(best >> 32) : 0, mh = __reduce_max_sync(0xffffffffu, hi);
@@ -246,17 +272,17 @@ __device__ void choose(const MoeParams& p, MoeSmem* sm, int t, int lane) {
     const uint32_t lo = c1 ? (uint32_t)best : 0, ml = __reduce_max_sync(0xffffffffu, lo);
     const bool c2 = c1 && lo == ml;
     const int e = (int)__reduce_min_sync(0xffffffffu, c2 ? (uint32_t)(at * 32 + lane) : 0xffffffffu);
-    const double v = order_value(((unsigned long long)mh << 32) | ml);
+    const float2 v = order_value(((unsigned long long)mh << 32) | ml);
     if (k == 0) {   // the softmax's maximum and sum
       top = v;
 #pragma unroll
-      for (int j = 0; j < kMaxExperts / 32; ++j) {
+      for (int j = 0; j < V; ++j) {
         if (j * 32 >= a.experts) break;
-        if (j * 32 + lane < a.experts) den += exp_of(order_value(key[j]) - top);
+        if (j * 32 + lane < a.experts) den += exp_of(order_value(key[j]), top);
       }
       den = warp_sum(den);
     }
-    const float w = exp_of(v - top);
+    const float w = exp_of(v, top);
     sum += w;
     if (lane == k) mine = w;
     if (lane == 0) {
@@ -268,7 +294,7 @@ __device__ void choose(const MoeParams& p, MoeSmem* sm, int t, int lane) {
       best = 0;
       at = -1;
 #pragma unroll
-      for (int j = 0; j < kMaxExperts / 32; ++j) {
+      for (int j = 0; j < V; ++j) {
         if (j * 32 >= a.experts) break;
         if (j * 32 + lane < a.experts && !(used >> j & 1) && (at < 0 || key[j] > best)) {
           best = key[j];
@@ -286,14 +312,19 @@ __device__ void choose(const MoeParams& p, MoeSmem* sm, int t, int lane) {
       if (a.topk_w) a.topk_w[t * a.top_k + lane] = w;
     }
   }
-  if (lane == 0 && a.s_gate) sm->shared_w[t] = sigmoid((float)__ldcg(lg + a.experts));
+  if (lane == 0 && a.s_gate) sm->shared_w[t] = sigmoid(__ldcg(lg + a.experts).x);
+}
+
+// Tokens of a mask below token t.
+__device__ __forceinline__ int below(uint32_t m0, uint32_t m1, int t) {
+  return t < 32 ? __popc(m0 & ((1u << t) - 1u)) : __popc(m0) + __popc(m1 & ((1u << (t - 32)) - 1u));
 }
 
 // The active experts in ascending order, their first pairs, and the pairs' weights.
 __device__ void build_lists(const MoeParams& p, MoeSmem* sm, int tid) {
   const MoeArgs& a = p.a;
   const int warp = tid >> 5, lane = tid & 31;
-  constexpr int PER = kMaxExperts / (32 * kMoeWarps);
+  constexpr int PER = (kMaxExperts + kMoeThreads - 1) / kMoeThreads;
   int na = 0, np = 0;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
@@ -316,7 +347,7 @@ __device__ void build_lists(const MoeParams& p, MoeSmem* sm, int tid) {
     sm->scan_a[warp] = ia;
     sm->scan_p[warp] = ip;
   }
-  products_sync();
+  __syncthreads();
   ia -= na;
   ip -= np;
   int total = 0;
@@ -327,7 +358,10 @@ __device__ void build_lists(const MoeParams& p, MoeSmem* sm, int tid) {
     }
     total += sm->scan_a[w];
   }
-  if (tid == 0) sm->n_active = total;
+  if (tid == 0) {
+    sm->n_active = total;
+    sm->base[total] = (uint16_t)(a.tokens * a.top_k);
+  }
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int e = tid * PER + i;
@@ -342,19 +376,14 @@ __device__ void build_lists(const MoeParams& p, MoeSmem* sm, int tid) {
       }
     }
   }
-  products_sync();
-  for (int i = tid; i < a.tokens * a.top_k; i += 32 * kMoeWarps) {
+  __syncthreads();
+  for (int i = tid; i < a.tokens * a.top_k; i += kMoeThreads) {
     const int t = i / a.top_k, e = sm->sel[i];
-    const uint32_t below = t >= 32 ? 0xffffffffu : (1u << t) - 1u;
-    const int r = __popc(sm->mask[e][0] & below) + (t >= 32 ? __popc(sm->mask[e][1] & ((1u << (t - 32)) - 1u)) : 0);
-    sm->pair_w[sm->base[sm->rank[e]] + r] = sm->sel_w[i];
+    const int at = sm->base[sm->rank[e]] + below(sm->mask[e][0], sm->mask[e][1], t);
+    sm->pair_w[at] = sm->sel_w[i];
+    sm->pair_t[at] = (uint8_t)t;
   }
-  products_sync();
-}
-
-// Tokens of a mask below token t.
-__device__ __forceinline__ int below(uint32_t m0, uint32_t m1, int t) {
-  return t < 32 ? __popc(m0 & ((1u << t) - 1u)) : __popc(m0) + __popc(m1 & ((1u << (t - 32)) - 1u));
+  __syncthreads();
 }
 
 template <int NG>   // groups of 8 tokens
@@ -363,266 +392,329 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem[];
   const MoeArgs& a = p.a;
   const uint32_t raw = tc::smem_u32(smem), pad = (1024u - (raw & 1023u)) & 1023u;
-  uint8_t* const ring = smem + pad;
-  MoeSmem* sm = reinterpret_cast<MoeSmem*>(ring + kStages * kStage);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x, grid = gridDim.x;
-  if (tid == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      tc::mbar_init(&sm->full[s], 1);
-      tc::mbar_init(&sm->empty[s], kMoeWarps);
-    }
-    tc::mbar_init(&sm->lists, 1);
-    sm->gave_up = 0;
+  const int team = warp / kTeam, member = warp % kTeam;
+  MoeSmem* sm = reinterpret_cast<MoeSmem*>(smem + pad + kRing);
+  uint8_t* const ring = smem + pad + warp * kStages * kStage;          // this warp's
+  const uint32_t ring_a = raw + pad + warp * kStages * kStage;
+  if (lane == 0) {
+    for (int s = 0; s < kStages; ++s) tc::mbar_init(&sm->full[warp][s], 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  if (tid == 0) sm->gave_up = 0;
   for (int e = tid; e < a.experts; e += kMoeThreads) sm->mask[e][0] = sm->mask[e][1] = 0;
   __syncthreads();
 
   const int s_tiles = a.shared_inter >> 3, e_tiles = a.inter >> 3;   // 8-row tiles of an expert
-  int s = 0;
-  uint32_t ph = 0;
-  const auto step = [&]() {
-    if (++s == kStages) {
-      s = 0;
-      ph ^= 1u;
+  const int h_chunks = (a.hidden + kCols - 1) / kCols, tile_step = grid * kTeams;
+  const int j0 = a.shared_inter > 0 ? -1 : 0;                        // expert -1 is the shared one
+  int na = 0, n1 = s_tiles;                                          // active experts, phase 1 tiles
+  const auto cols_of = [&](int j) { return j < 0 ? a.shared_inter : a.inter; };
+  const auto chunks_of = [&](int j) { return (cols_of(j) + kCols - 1) / kCols; };
+
+  // This warp's stages in order: its chunks of its team's tiles, then its chunks
+  // of the CTA's output tiles.  One walk loads, kStages ahead; one multiplies.
+  struct Walk {
+    int i, j, c;     // tile; expert (of phase 1: at the tile's change); chunk
+  };
+  const auto first1 = [&]() { return Walk{cta * kTeams + team, 0, member}; };
+  const auto next1 = [&](Walk& w) {
+    w.c += kTeam;
+    if (w.c >= h_chunks) {
+      w.c = member;
+      w.i += tile_step;
     }
   };
-
-  if (warp == kMoeWarps) {
-    // ---- loads, by one thread ----
-    if (lane == 0) {
-      bool ok = true;
-      const uint32_t ring_a = raw + pad;
-      // One stage: columns c0 .. c0 + 511 of `rows` rows from y0 on (and of as many
-      // from y1 on, when y1 >= 0); K columns in all.
-      const auto load = [&](const CUtensorMap* m, const CUtensorMap* edge, int K, int c0, int rows, int y0, int y1) {
-        ok = moe_wait(a, sm, &sm->empty[s], ph ^ 1u);
-        if (!ok) return;
-        const uint32_t dst = ring_a + s * kStage;
-        const int parts = y1 >= 0 ? 2 : 1;
-        // whole blocks of 64 columns in one box; a chunk that holds the row's ragged
-        // end takes a box per block, the last of which TMA fills with zeros
-        if ((K & 63) == 0 || c0 + kCols <= (K & ~63)) {
-          mbar_expect_tx(&sm->full[s], (uint32_t)(parts * rows * kCols * 2));
-          tma3(dst, m, 0, y0, c0 >> 6, &sm->full[s]);
-          if (y1 >= 0) tma3(dst + kStage / 2, m, 0, y1, c0 >> 6, &sm->full[s]);
-        } else {
-          const int nb = (K - c0 + 63) >> 6;
-          mbar_expect_tx(&sm->full[s], (uint32_t)(parts * rows * nb * 128));
-          for (int b = 0; b < nb; ++b) {
-            tma2(dst + b * rows * 128, edge, c0 + b * 64, y0, &sm->full[s]);
-            if (y1 >= 0) tma2(dst + kStage / 2 + b * rows * 128, edge, c0 + b * 64, y1, &sm->full[s]);
-          }
-        }
-        step();
-      };
-      for (int i = cta; i < s_tiles && ok; i += grid)
-        for (int c0 = 0; c0 < a.hidden && ok; c0 += kCols)
-          load(&maps.s_gate_up, &maps.s_gate_up_edge, a.hidden, c0, 8, 8 * i, a.shared_inter + 8 * i);
-      if (ok) ok = moe_wait(a, sm, &sm->lists, 0);
-      const int na = ok ? sm->n_active : 0, n1 = s_tiles + na * e_tiles;
-      for (int i = cta + (s_tiles - cta + grid - 1 > 0 ? (s_tiles - cta + grid - 1) / grid * grid : 0); i < n1 && ok;
-           i += grid) {
-        const int j = (i - s_tiles) / e_tiles, r = (i - s_tiles - j * e_tiles) * 8;
-        const int y = sm->expert[j] * 2 * a.inter + r;
-        for (int c0 = 0; c0 < a.hidden && ok; c0 += kCols)
-          load(&maps.gate_up, &maps.gate_up_edge, a.hidden, c0, 8, y, y + a.inter);
+  const bool any1 = member < h_chunks;   // this member has chunks at all
+  const auto settle2 = [&](Walk& w) {    // on to the first chunk from w on that is this warp's
+    while (w.c >= chunks_of(w.j)) {
+      if (++w.j >= na) {
+        w.j = j0;
+        w.i += grid;
+        if (w.i >= p.tiles3) return;
       }
-      for (int i = cta; i < p.tiles3 && ok; i += grid) {
-        for (int c0 = 0; c0 < a.shared_inter && ok; c0 += kCols)
-          load(&maps.s_down, &maps.s_down_edge, a.shared_inter, c0, p.rows3, i * p.rows3, -1);
-        for (int j = 0; j < na && ok; ++j)
-          for (int c0 = 0; c0 < a.inter && ok; c0 += kCols)
-            load(&maps.down, &maps.down_edge, a.inter, c0, p.rows3, sm->expert[j] * a.hidden + i * p.rows3, -1);
+      const unsigned e = w.j < 0 ? 0u : sm->expert[w.j];
+      w.c = warp - (int)(e * (unsigned)chunks_of(w.j) % kMoeWarps);
+      if (w.c < 0) w.c += kMoeWarps;
+    }
+  };
+  const auto first2 = [&]() {
+    Walk w{cta, j0, 0};
+    if (w.i < p.tiles3) {
+      const unsigned e = w.j < 0 ? 0u : sm->expert[w.j];
+      w.c = warp - (int)(e * (unsigned)chunks_of(w.j) % kMoeWarps);
+      if (w.c < 0) w.c += kMoeWarps;
+      settle2(w);
+    }
+    return w;
+  };
+  const auto next2 = [&](Walk& w) {
+    w.c += kMoeWarps;
+    settle2(w);
+  };
+
+  // A stage: chunk c of `rows` rows from y0 on (and of as many from y1 on, when
+  // y1 >= 0); K columns in all.
+  int ls = 0;
+  const auto load = [&](const CUtensorMap* m, const CUtensorMap* edge, int K, int c, int rows, int y0, int y1) {
+    if (lane == 0) {
+      uint64_t* full = &sm->full[warp][ls];
+      const uint32_t dst = ring_a + ls * kStage;
+      const int c0 = c * kCols, parts = y1 >= 0 ? 2 : 1;
+      // whole blocks of 64 columns in one box; a chunk that holds the row's ragged
+      // end takes a box per block, the last of which TMA fills with zeros
+      if ((K & 63) == 0 || c0 + kCols <= (K & ~63)) {
+        mbar_expect_tx(full, (uint32_t)(parts * rows * kCols * 2));
+        tma3(dst, m, 0, y0, c0 >> 6, full);
+        if (y1 >= 0) tma3(dst + kStage / 2, m, 0, y1, c0 >> 6, full);
+      } else {
+        const int nb = min((K - c0 + 63) >> 6, 2);
+        mbar_expect_tx(full, (uint32_t)(parts * rows * nb * 128));
+        for (int b = 0; b < nb; ++b) {
+          tma2(dst + b * rows * 128, edge, c0 + b * 64, y0, full);
+          if (y1 >= 0) tma2(dst + kStage / 2 + b * rows * 128, edge, c0 + b * 64, y1, full);
+        }
       }
     }
-  } else {
-    // ---- the choice of experts ----
-    asm volatile("griddepcontrol.wait;" ::: "memory");   // kernel 1's logits
-    if (!a.s_gate)
-      for (int t = tid; t < a.tokens; t += 32 * kMoeWarps) sm->shared_w[t] = 1.0f;
-    for (int t = warp; t < a.tokens; t += kMoeWarps) choose(p, sm, t, lane);
-    products_sync();
-    build_lists(p, sm, tid);
-    if (tid == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(tc::smem_u32(&sm->lists)) : "memory");
-    const int na = sm->n_active, n1 = s_tiles + na * e_tiles;
+    if (++ls == kStages) ls = 0;
+  };
+  int ahead = 0;                 // stages loaded and not yet multiplied
+  Walk l1 = first1(), l2{0, 0, 0};
+  bool in2 = false;              // the loads have come to phase 2
+  // Fills the stages that are free; before the choice only with the shared expert.
+  const auto fill = [&](bool chosen) {
+    while (ahead < kStages) {
+      if (!in2) {
+        if (any1 && l1.i < n1) {
+          if (l1.i < s_tiles) {
+            load(&maps.s_gate_up, &maps.s_gate_up_edge, a.hidden, l1.c, 8, 8 * l1.i, a.shared_inter + 8 * l1.i);
+          } else {
+            const int j = (l1.i - s_tiles) / e_tiles;
+            const int y = sm->expert[j] * 2 * a.inter + (l1.i - s_tiles - j * e_tiles) * 8;
+            load(&maps.gate_up, &maps.gate_up_edge, a.hidden, l1.c, 8, y, y + a.inter);
+          }
+          next1(l1);
+          ++ahead;
+          continue;
+        }
+        if (!chosen) return;
+        in2 = true;
+        l2 = first2();
+      }
+      if (l2.i >= p.tiles3) return;
+      if (l2.j < 0)
+        load(&maps.s_down, &maps.s_down_edge, a.shared_inter, l2.c, p.rows3, l2.i * p.rows3, -1);
+      else
+        load(&maps.down, &maps.down_edge, a.inter, l2.c, p.rows3, sm->expert[l2.j] * a.hidden + l2.i * p.rows3, -1);
+      next2(l2);
+      ++ahead;
+    }
+  };
+  fill(false);
 
-    const int g = lane >> 2, t4 = lane & 3;
-    int flip = 0;
-    // this warp's 64 columns of the stage at hand: rows are `pitch` apart in the
-    // order of the stage's 128-byte lines, the upper eight `up` bytes on
-    const auto weights = [&](Frag& f, int line, uint32_t up) {
-      const uint8_t* at = ring + s * kStage + line * 128;
+  // ---- the choice of experts ----
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // kernel 1's logits
+  if (!a.s_gate)
+    for (int t = tid; t < a.tokens; t += kMoeThreads) sm->shared_w[t] = 1.0f;
+  for (int t = warp; t < a.tokens; t += kMoeWarps) {
+    if (a.experts <= 256) choose<8>(p, sm, t, lane);
+    else if (a.experts <= 512) choose<16>(p, sm, t, lane);
+    else choose<32>(p, sm, t, lane);
+  }
+  __syncthreads();
+  build_lists(p, sm, tid);
+  na = sm->n_active;
+  n1 = s_tiles + na * e_tiles;
+  fill(true);
+
+  const int g = lane >> 2, t4 = lane & 3;
+  int cs = 0;
+  uint32_t ph = 0;
+  // The weights of 64 columns: row g in line `line` of the stage's 128-byte lines,
+  // row g + 8 `up` bytes on.
+  const auto weights = [&](Frag& f, int line, uint32_t up) {
+    const uint8_t* at = ring + cs * kStage + line * 128;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t off = (uint32_t)(((t4 + 4 * h) ^ (line & 7)) << 4);
+      f.lo[h] = *reinterpret_cast<const uint4*>(at + off);
+      f.hi[h] = *reinterpret_cast<const uint4*>(at + off + up);
+    }
+  };
+  const auto refill = [&]() {    // this stage is multiplied
+    __syncwarp();
+    if (++cs == kStages) {
+      cs = 0;
+      ph ^= 1u;
+    }
+    --ahead;
+    fill(true);
+  };
+
+  // ---- phase 1: act = weight silu(gate) up ----
+  int flip = 0;
+  for (int i = cta * kTeams + team; i < n1; i += tile_step) {
+    const bool shared = i < s_tiles;
+    const int j = shared ? -1 : (i - s_tiles) / e_tiles, r0 = (shared ? i : i - s_tiles - j * e_tiles) * 8;
+    const int col0 = shared ? 0 : sm->base[j], cnt = shared ? a.tokens : sm->base[j + 1] - col0;
+    const uint16_t* x[NG];       // the rows of this lane's columns
+    float acc[NG][4];
+#pragma unroll
+    for (int n = 0; n < NG; ++n) {
+      const int c = 8 * n + g;
+      x[n] = c < cnt ? a.x + (size_t)(shared ? c : sm->pair_t[col0 + c]) * a.hidden + t4 * 8 : nullptr;
+      acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.0f;
+    }
+    for (int c = member; c < h_chunks; c += kTeam) {
+      uint4 b0[2][2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) load_b(b0[h], x[0] + c * kCols + 64 * h, 0, a.hidden - c * kCols - 64 * h - t4 * 8, x[0] != nullptr);
+      moe_wait(a, sm, &sm->full[warp][cs], ph);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const uint32_t off = (uint32_t)(((t4 + 4 * h) ^ (line & 7)) << 4);
-        f.lo[h] = *reinterpret_cast<const uint4*>(at + off);
-        f.hi[h] = *reinterpret_cast<const uint4*>(at + off + up);
-      }
-    };
-    const auto release = [&]() {
-      __syncwarp();
-      if (lane == 0)
-        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(tc::smem_u32(&sm->empty[s])) : "memory");
-      step();
-    };
-
-    // ---- phase 1: act = weight silu(gate) up ----
-    for (int i = cta; i < n1; i += grid) {
-      const bool shared = i < s_tiles;
-      const int j = shared ? 0 : (i - s_tiles) / e_tiles, r0 = (shared ? i : i - s_tiles - j * e_tiles) * 8;
-      uint32_t m0 = 0xffffffffu, m1 = 0xffffffffu;
-      if (!shared) {
-        const int e = sm->expert[j];
-        m0 = sm->mask[e][0];
-        m1 = sm->mask[e][1];
-      }
-      float acc[NG][4];
-      uint32_t groups = 0;
+        if (c * kCols + 64 * h >= a.hidden) break;
+        Frag f;
+        weights(f, h * 8 + g, kStage / 2);
+        mma_block(acc[0], f, b0[h]);
 #pragma unroll
-      for (int n = 0; n < NG; ++n) {
-        if ((n < 4 ? m0 >> (8 * n) : m1 >> (8 * n - 32)) & 0xffu) groups |= 1u << n;
-        if (8 * n >= a.tokens) groups &= ~(1u << n);
-        acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.0f;
-      }
-      for (int c0 = 0; c0 < a.hidden; c0 += kCols) {
-        const int k = c0 + warp * 64 + t4 * 8;
-        const bool in = c0 + warp * 64 < a.hidden;
-        uint4 b[2];
-        int first = __ffs(groups) - 1;
-        if (in) load_b(b, a.x + (size_t)(8 * first + g) * a.hidden, k, a.hidden, 8 * first + g < a.tokens);
-        moe_wait(a, sm, &sm->full[s], ph);
-        if (in) {
-          Frag f;
-          weights(f, warp * 8 + g, kStage / 2);
-#pragma unroll
-          for (int n = 0; n < NG; ++n)
-            if (groups >> n & 1) {
-              if (n != first)
-                load_b(b, a.x + (size_t)(8 * n + g) * a.hidden, k, a.hidden, 8 * n + g < a.tokens);
-              mma_block(acc[n], f, b);
-            }
-        }
-        release();
-      }
-      const int cols = shared ? a.shared_inter : a.inter;
-      uint16_t* const act = shared ? p.s_act : p.act;
-      const size_t plane = (size_t)(shared ? a.tokens : a.tokens * a.top_k) * cols;
-#pragma unroll
-      for (int n = 0; n < NG; ++n)
-        if (groups >> n & 1) {
-          sm->red[flip][warp][lane] = make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
-          products_sync();
-          const int r = tid & 7, t = 8 * n + (tid >> 3);
-          if (tid < 64 && t < a.tokens && ((t < 32 ? m0 >> t : m1 >> (t - 32)) & 1)) {
-            const int l = r * 4 + ((t & 7) >> 1), o = t & 1;
-            float gate = 0.0f, up = 0.0f;
-#pragma unroll
-            for (int w = 0; w < kMoeWarps; ++w) {
-              const float4 v = sm->red[flip][w][l];
-              gate += o ? v.y : v.x;
-              up += o ? v.w : v.z;
-            }
-            const int pair = shared ? t : sm->base[j] + below(m0, m1, t);
-            const float v = silu(gate) * up * (shared ? sm->shared_w[t] : sm->pair_w[pair]);
-            const uint16_t hi = f32_to_bf16(v);
-            const size_t at = (size_t)pair * cols + r0 + r;
-            act[at] = hi;
-            act[plane + at] = f32_to_bf16(v - bf16_to_f32(hi));
+        for (int n = 1; n < NG; ++n)
+          if (8 * n < cnt) {
+            uint4 b[2];
+            load_b(b, x[n] + c * kCols + 64 * h, 0, a.hidden - c * kCols - 64 * h - t4 * 8, x[n] != nullptr);
+            mma_block(acc[n], f, b);
           }
-          flip ^= 1;
-        }
+      }
+      refill();
     }
-
-    // ---- every CTA's activations are there ----
-    __threadfence();
-    products_sync();
-    if (tid == 0) {
-      atomicAdd(p.barrier, 1u);
-      const long long t0 = clock64();
-      while (true) {
-        unsigned n;
-        asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(n) : "l"(p.barrier) : "memory");
-        if (n >= (unsigned)grid) break;
-        if (clock64() - t0 > kBarrierBudget) {
-          record_status(a.status, GDN_ERR_DEVICE_TIMEOUT);
-          break;
-        }
-      }
-      __threadfence();
-    }
-    products_sync();
-
-    // ---- phase 2: y = sum over the experts of down act ----
-    for (int i = cta; i < p.tiles3; i += grid) {
-      float acc[NG][4];
+    // the team's four sums, in their order; lane (g, t4) of the first warp holds gate and
+    // up of row g for columns 2 t4 and 2 t4 + 1
+    const int cols = cols_of(j);
+    uint16_t* const act = shared ? p.s_act : p.act;
+    const size_t plane = (size_t)(shared ? a.tokens : a.tokens * a.top_k) * cols;
 #pragma unroll
-      for (int n = 0; n < NG; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.0f;
-      for (int j = a.shared_inter > 0 ? -1 : 0; j < na; ++j) {
-        const bool shared = j < 0;
-        const int cols = shared ? a.shared_inter : a.inter;
-        const uint16_t* act = shared ? p.s_act : p.act;
-        const size_t plane = (size_t)(shared ? a.tokens : a.tokens * a.top_k) * cols;
-        uint32_t m0 = 0xffffffffu, m1 = 0xffffffffu;
-        int base = 0;
-        if (!shared) {
-          const int e = sm->expert[j];
-          m0 = sm->mask[e][0];
-          m1 = sm->mask[e][1];
-          base = sm->base[j];
-        }
-        for (int c0 = 0; c0 < cols; c0 += kCols) {
-          const int k = c0 + warp * 64 + t4 * 8;
-          const bool in = c0 + warp * 64 < cols;
-          bool have = false;
-          Frag f;
+    for (int n = 0; n < NG; ++n)
+      if (8 * n < cnt) {
+        if (member > 0) sm->red[flip][warp][lane] = make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
+        team_sync(team);
+        if (member == 0) {
 #pragma unroll
-          for (int n = 0; n < NG; ++n) {
-            const uint32_t members = (n < 4 ? m0 >> (8 * n) : m1 >> (8 * n - 32)) & 0xffu;
-            if (members == 0 || 8 * n >= a.tokens) continue;
-            const int t = 8 * n + g;
-            const bool use = t < a.tokens && (members >> g & 1);
-            const uint16_t* row = act + (size_t)(shared ? (use ? t : 0) : base + (use ? below(m0, m1, t) : 0)) * cols;
-            uint4 hi[2], lo[2];
-            if (in) {
-              load_b_cg(hi, row, k, cols, use);
-              load_b_cg(lo, row + plane, k, cols, use);
-            }
-            if (!have) {
-              moe_wait(a, sm, &sm->full[s], ph);
-              have = true;
-              if (in) weights(f, warp * p.rows3 + g, 1024);
-            }
-            if (in) {
-              mma_block(acc[n], f, hi);
-              mma_block(acc[n], f, lo);
+          for (int w = 1; w < kTeam; ++w) {
+            const float4 v = sm->red[flip][warp + w][lane];
+            acc[n][0] += v.x;
+            acc[n][1] += v.y;
+            acc[n][2] += v.z;
+            acc[n][3] += v.w;
+          }
+#pragma unroll
+          for (int o = 0; o < 2; ++o) {
+            const int c = 8 * n + 2 * t4 + o;
+            if (c < cnt) {
+              const float v = silu(acc[n][o]) * acc[n][2 + o] * (shared ? sm->shared_w[c] : sm->pair_w[col0 + c]);
+              const uint16_t hi = f32_to_bf16(v);
+              const size_t at = (size_t)(col0 + c) * cols + r0 + g;
+              act[at] = hi;
+              act[plane + at] = f32_to_bf16(v - bf16_to_f32(hi));
             }
           }
-          release();
-        }
-      }
-#pragma unroll
-      for (int n = 0; n < NG; ++n) {
-        if (8 * n >= a.tokens) break;
-        sm->red[flip][warp][lane] = make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
-        products_sync();
-        const int r = tid & 15, t = 8 * n + (tid >> 4), h = i * p.rows3 + r;
-        if (tid < 128 && t < a.tokens && r < p.rows3 && h < a.hidden) {
-          const int l = (r & 7) * 4 + ((t & 7) >> 1);
-          float v = 0.0f;
-#pragma unroll
-          for (int w = 0; w < kMoeWarps; ++w) {
-            const float4 q = sm->red[flip][w][l];
-            v += r < 8 ? (t & 1 ? q.y : q.x) : (t & 1 ? q.w : q.z);
-          }
-          const size_t at = (size_t)t * a.hidden + h;
-          if (a.out_f32)
-            static_cast<float*>(a.y)[at] = v;
-          else
-            static_cast<uint16_t*>(a.y)[at] = f32_to_bf16(v);
         }
         flip ^= 1;
       }
+  }
+
+  // ---- every CTA's activations are there ----
+  __threadfence();
+  __syncthreads();
+  if (tid == 0) {
+    atomicAdd(p.barrier, 1u);
+    const long long t0 = clock64();
+    while (true) {
+      unsigned n;
+      asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(n) : "l"(p.barrier) : "memory");
+      if (n >= (unsigned)grid) break;
+      if (clock64() - t0 > kBarrierBudget) {
+        record_status(a.status, GDN_ERR_DEVICE_TIMEOUT);
+        break;
+      }
+    }
+    __threadfence();
+  }
+  __syncthreads();
+
+  // ---- phase 2: y = sum over the experts of down act ----
+  Walk w = first2();
+  flip = 0;   // the teams met differently often
+  for (int i = cta; i < p.tiles3; i += grid) {
+    float acc[NG][4];
+#pragma unroll
+    for (int n = 0; n < NG; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.0f;
+    while (w.i == i) {
+      const bool shared = w.j < 0;
+      const int cols = cols_of(w.j), k = w.c * kCols + t4 * 8;
+      uint32_t m0, m1;
+      int base = 0;
+      if (shared) {
+        m0 = a.tokens < 32 ? (1u << a.tokens) - 1u : 0xffffffffu;
+        m1 = a.tokens <= 32 ? 0u : (a.tokens < 64 ? (1u << (a.tokens - 32)) - 1u : 0xffffffffu);
+      } else {
+        const int e = sm->expert[w.j];
+        m0 = sm->mask[e][0];
+        m1 = sm->mask[e][1];
+        base = sm->base[w.j];
+      }
+      const uint16_t* act = shared ? p.s_act : p.act;
+      const size_t plane = (size_t)(shared ? a.tokens : a.tokens * a.top_k) * cols;
+      bool have = false;
+      Frag f[2];
+#pragma unroll
+      for (int n = 0; n < NG; ++n) {
+        const uint32_t members = (n < 4 ? m0 >> (8 * n) : m1 >> (8 * n - 32)) & 0xffu;
+        if (members == 0) continue;
+        const int t = 8 * n + g;
+        const bool use = members >> g & 1;
+        const uint16_t* row = act + (size_t)(use ? (shared ? t : base + below(m0, m1, t)) : 0) * cols;
+        uint4 hi[2][2], lo[2][2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          load_b_cg(hi[h], row, k + 64 * h, cols, use);
+          load_b_cg(lo[h], row + plane, k + 64 * h, cols, use);
+        }
+        if (!have) {
+          moe_wait(a, sm, &sm->full[warp][cs], ph);
+          have = true;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) weights(f[h], h * p.rows3 + g, 1024);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (w.c * kCols + 64 * h < cols) {
+            mma_block(acc[n], f[h], hi[h]);
+            mma_block(acc[n], f[h], lo[h]);
+          }
+      }
+      refill();
+      next2(w);
+    }
+#pragma unroll
+    for (int n = 0; n < NG; ++n) {
+      if (8 * n >= a.tokens) break;
+      sm->red[flip][warp][lane] = make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
+      __syncthreads();
+      const int r = tid & 15, t = 8 * n + (tid >> 4), h = i * p.rows3 + r;
+      if (tid < 128 && t < a.tokens && r < p.rows3 && h < a.hidden) {
+        const int l = (r & 7) * 4 + ((t & 7) >> 1);
+        float v = 0.0f;
+#pragma unroll
+        for (int q = 0; q < kMoeWarps; ++q) {
+          const float4 u = sm->red[flip][q][l];
+          v += r < 8 ? (t & 1 ? u.y : u.x) : (t & 1 ? u.w : u.z);
+        }
+        const size_t at = (size_t)t * a.hidden + h;
+        if (a.out_f32)
+          static_cast<float*>(a.y)[at] = v;
+        else
+          static_cast<uint16_t*>(a.y)[at] = f32_to_bf16(v);
+      }
+      flip ^= 1;
     }
   }
 }
@@ -640,7 +732,7 @@ PFN_cuTensorMapEncodeTiled_v12000 moe_encoder() {
   return fn;
 }
 
-// Weights [rows][K]: boxes of 8 blocks of 64 columns by box_rows rows (of whole
+// Weights [rows][K]: boxes of 2 blocks of 64 columns by box_rows rows (of whole
 // blocks), and boxes of one block (the ragged end of the rows included).
 bool weight_maps(CUtensorMap* whole, CUtensorMap* edge, const void* base, uint64_t rows, uint64_t K, uint32_t box_rows) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = moe_encoder();
@@ -708,7 +800,7 @@ cudaError_t launch_moe(const MoeArgs& a, cudaStream_t stream) {
   char* ws = static_cast<char*>(a.scratch);
   p.barrier = reinterpret_cast<unsigned*>(ws);
   ws += 256;
-  p.logit = reinterpret_cast<double*>(ws);
+  p.logit = reinterpret_cast<float2*>(ws);
   ws += up256(T * (a.experts + 1) * 8);
   p.act = reinterpret_cast<uint16_t*>(ws);
   ws += up256(T * a.top_k * a.inter * 4);
