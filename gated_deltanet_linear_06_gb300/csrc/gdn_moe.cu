@@ -67,6 +67,7 @@ struct MoeSmem {
   uint32_t mask[kMaxExperts][2];       // tokens of an expert
   uint16_t expert[kMaxExperts];        // active experts, ascending
   uint16_t base[kMaxExperts + 1];      // first pair of an active expert
+  uint8_t turn[kMaxExperts];           // the warp that takes an active expert's first down chunk
   uint16_t rank[kMaxExperts];          // expert -> its place among the active
   float shared_w[GDN_MOE_MAX_TOKENS];  // the shared expert's factor
   uint16_t sel[kMaxPairs];             // chosen experts, token-major
@@ -98,44 +99,55 @@ __device__ __forceinline__ float2 two_sum(float a, float b) {
 }
 
 // ---- kernel 1 ----
+// NT tokens per warp, UK steps of 256 columns with all their loads in flight.
+template <int NT, int UK>
 __global__ void __launch_bounds__(256) moe_router_kernel(const MoeParams p) {
   const MoeArgs& a = p.a;
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.barrier = 0;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x & 31, unit = blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int rows = a.experts + (a.s_gate ? 1 : 0), blocks = (a.tokens + 7) >> 3;
+  const int rows = a.experts + (a.s_gate ? 1 : 0), blocks = (a.tokens + NT - 1) / NT;
   if (unit >= rows * blocks) return;
-  const int e = unit / blocks, t0 = (unit - e * blocks) * 8, nt = min(8, a.tokens - t0);
-  const uint16_t* w = e < a.experts ? a.w_router + (size_t)e * a.hidden : a.s_gate;
-  const uint16_t* x = a.x + (size_t)t0 * a.hidden;
+  const int e = unit / blocks, t0 = (unit - e * blocks) * NT, nt = min(NT, a.tokens - t0);
+  const uint16_t* w = (e < a.experts ? a.w_router + (size_t)e * a.hidden : a.s_gate) + lane * 8;
+  const uint16_t* x[NT];
   constexpr float kGrid = 3072.0f;   // products go to S on a grid of 2^-12
-  float S[8], lo[8];
+  float S[NT], lo[NT];
 #pragma unroll
-  for (int t = 0; t < 8; ++t) {
+  for (int t = 0; t < NT; ++t) {
+    x[t] = a.x + (size_t)(t0 + min(t, nt - 1)) * a.hidden + lane * 8;   // (the last token again past the end)
     S[t] = kGrid;
     lo[t] = 0.0f;
   }
-  for (int k = lane * 8; k < a.hidden; k += 256) {
-    const uint4 wv = __ldg(reinterpret_cast<const uint4*>(w + k));
-    const uint32_t ww[4] = {wv.x, wv.y, wv.z, wv.w};
+  for (int k = 0; k < a.hidden; k += 256 * UK) {
+    uint4 wv[UK], xv[UK][NT];
 #pragma unroll
-    for (int t = 0; t < 8; ++t) {
-      if (t >= nt) break;
-      const uint4 xv = __ldg(reinterpret_cast<const uint4*>(x + (size_t)t * a.hidden + k));
-      const uint32_t xx[4] = {xv.x, xv.y, xv.z, xv.w};
+    for (int u = 0; u < UK; ++u) {
+      const bool in = k + 256 * u + lane * 8 < a.hidden;
+      wv[u] = in ? __ldg(reinterpret_cast<const uint4*>(w + k + 256 * u)) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float wf = __uint_as_float(i & 1 ? ww[i >> 1] & 0xffff0000u : ww[i >> 1] << 16);
-        const float xf = __uint_as_float(i & 1 ? xx[i >> 1] & 0xffff0000u : xx[i >> 1] << 16);
-        const float s = fmaf(xf, wf, S[t]);
-        lo[t] += fmaf(xf, wf, -(s - S[t]));   // exact: what S did not take
-        S[t] = s;
+      for (int t = 0; t < NT; ++t)
+        xv[u][t] = in ? __ldg(reinterpret_cast<const uint4*>(x[t] + k + 256 * u)) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int u = 0; u < UK; ++u) {
+      const uint32_t ww[4] = {wv[u].x, wv[u].y, wv[u].z, wv[u].w};
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const uint32_t xx[4] = {xv[u][t].x, xv[u][t].y, xv[u][t].z, xv[u][t].w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float wf = __uint_as_float(i & 1 ? ww[i >> 1] & 0xffff0000u : ww[i >> 1] << 16);
+          const float xf = __uint_as_float(i & 1 ? xx[i >> 1] & 0xffff0000u : xx[i >> 1] << 16);
+          const float s = fmaf(xf, wf, S[t]);
+          lo[t] += fmaf(xf, wf, -(s - S[t]));   // exact: what S did not take
+          S[t] = s;
+        }
       }
     }
   }
 #pragma unroll
-  for (int t = 0; t < 8; ++t) {
-    if (t >= nt) break;
+  for (int t = 0; t < NT; ++t) {
     // the lanes' pairs (S - grid, lo) join as pairs: the high parts' rounding is kept
     float h = S[t] - kGrid, l = lo[t];
 #pragma unroll
@@ -145,7 +157,7 @@ __global__ void __launch_bounds__(256) moe_router_kernel(const MoeParams p) {
       h = r.x;
       l = (l + ol) + r.y;
     }
-    if (lane == 0) p.logit[(size_t)(t0 + t) * (a.experts + 1) + e] = two_sum(h, l);
+    if (lane == 0 && t < nt) p.logit[(size_t)(t0 + t) * (a.experts + 1) + e] = two_sum(h, l);
   }
 }
 
@@ -254,15 +266,16 @@ __device__ void choose(const MoeParams& p, MoeSmem* sm, int t, int lane) {
   unsigned long long best = 0;
   int at = -1;
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    if (j * 32 >= a.experts) break;
+  for (int j = 0; j < V; ++j) {   // every load in flight at once
     const int e = j * 32 + lane;
-    key[j] = e < a.experts ? order_key(__ldcg(lg + e)) : 0;
-    if (e < a.experts && (at < 0 || key[j] > best)) {
+    key[j] = order_key(e < a.experts ? __ldcg(lg + e) : make_float2(0.0f, 0.0f));
+  }
+#pragma unroll
+  for (int j = 0; j < V; ++j)
+    if (j * 32 + lane < a.experts && (at < 0 || key[j] > best)) {
       best = key[j];
       at = j;
     }
-  }
   uint32_t used = 0;
   float2 top = make_float2(0.0f, 0.0f);
   float den = 0.0f, sum = 0.0f, mine = 0.0f;
@@ -276,10 +289,8 @@ __device__ void choose(const MoeParams& p, MoeSmem* sm, int t, int lane) {
     if (k == 0) {   // the softmax's maximum and sum
       top = v;
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        if (j * 32 >= a.experts) break;
+      for (int j = 0; j < V; ++j)
         if (j * 32 + lane < a.experts) den += exp_of(order_value(key[j]), top);
-      }
       den = warp_sum(den);
     }
     const float w = exp_of(v, top);
@@ -294,13 +305,11 @@ __device__ void choose(const MoeParams& p, MoeSmem* sm, int t, int lane) {
       best = 0;
       at = -1;
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        if (j * 32 >= a.experts) break;
+      for (int j = 0; j < V; ++j)
         if (j * 32 + lane < a.experts && !(used >> j & 1) && (at < 0 || key[j] > best)) {
           best = key[j];
           at = j;
         }
-      }
     }
   }
   __syncwarp();
@@ -371,6 +380,7 @@ __device__ void build_lists(const MoeParams& p, MoeSmem* sm, int tid) {
         sm->expert[ia] = (uint16_t)e;
         sm->base[ia] = (uint16_t)ip;
         sm->rank[e] = (uint16_t)ia;
+        sm->turn[ia] = (uint8_t)((unsigned)e * (unsigned)((a.inter + kCols - 1) / kCols) % kMoeWarps);
         ++ia;
         ip += n;
       }
@@ -410,7 +420,6 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
   const int j0 = a.shared_inter > 0 ? -1 : 0;                        // expert -1 is the shared one
   int na = 0, n1 = s_tiles;                                          // active experts, phase 1 tiles
   const auto cols_of = [&](int j) { return j < 0 ? a.shared_inter : a.inter; };
-  const auto chunks_of = [&](int j) { return (cols_of(j) + kCols - 1) / kCols; };
 
   // This warp's stages in order: its chunks of its team's tiles, then its chunks
   // of the CTA's output tiles.  One walk loads, kStages ahead; one multiplies.
@@ -426,24 +435,25 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
     }
   };
   const bool any1 = member < h_chunks;   // this member has chunks at all
+  const int i_chunks = (a.inter + kCols - 1) / kCols, s_chunks = (a.shared_inter + kCols - 1) / kCols;
+  const auto begin2 = [&](Walk& w) {     // this warp's first chunk of expert w.j
+    w.c = w.j < 0 ? warp : warp - sm->turn[w.j];
+    if (w.c < 0) w.c += kMoeWarps;
+  };
   const auto settle2 = [&](Walk& w) {    // on to the first chunk from w on that is this warp's
-    while (w.c >= chunks_of(w.j)) {
+    while (w.c >= (w.j < 0 ? s_chunks : i_chunks)) {
       if (++w.j >= na) {
         w.j = j0;
         w.i += grid;
         if (w.i >= p.tiles3) return;
       }
-      const unsigned e = w.j < 0 ? 0u : sm->expert[w.j];
-      w.c = warp - (int)(e * (unsigned)chunks_of(w.j) % kMoeWarps);
-      if (w.c < 0) w.c += kMoeWarps;
+      begin2(w);
     }
   };
   const auto first2 = [&]() {
     Walk w{cta, j0, 0};
     if (w.i < p.tiles3) {
-      const unsigned e = w.j < 0 ? 0u : sm->expert[w.j];
-      w.c = warp - (int)(e * (unsigned)chunks_of(w.j) % kMoeWarps);
-      if (w.c < 0) w.c += kMoeWarps;
+      begin2(w);
       settle2(w);
     }
     return w;
@@ -480,6 +490,13 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
   };
   int ahead = 0;                 // stages loaded and not yet multiplied
   Walk l1 = first1(), l2{0, 0, 0};
+  int y1 = 0;                    // row of l1's tile, once the experts are chosen
+  const auto row1 = [&]() {
+    if (l1.i >= s_tiles && l1.i < n1) {
+      const int j = (l1.i - s_tiles) / e_tiles;
+      y1 = sm->expert[j] * 2 * a.inter + (l1.i - s_tiles - j * e_tiles) * 8;
+    }
+  };
   bool in2 = false;              // the loads have come to phase 2
   // Fills the stages that are free; before the choice only with the shared expert.
   const auto fill = [&](bool chosen) {
@@ -489,11 +506,11 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
           if (l1.i < s_tiles) {
             load(&maps.s_gate_up, &maps.s_gate_up_edge, a.hidden, l1.c, 8, 8 * l1.i, a.shared_inter + 8 * l1.i);
           } else {
-            const int j = (l1.i - s_tiles) / e_tiles;
-            const int y = sm->expert[j] * 2 * a.inter + (l1.i - s_tiles - j * e_tiles) * 8;
-            load(&maps.gate_up, &maps.gate_up_edge, a.hidden, l1.c, 8, y, y + a.inter);
+            load(&maps.gate_up, &maps.gate_up_edge, a.hidden, l1.c, 8, y1, y1 + a.inter);
           }
+          const int was = l1.i;
           next1(l1);
+          if (l1.i != was) row1();
           ++ahead;
           continue;
         }
@@ -525,6 +542,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
   build_lists(p, sm, tid);
   na = sm->n_active;
   n1 = s_tiles + na * e_tiles;
+  row1();
   fill(true);
 
   const int g = lane >> 2, t4 = lane & 3;
@@ -541,14 +559,13 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
       f.hi[h] = *reinterpret_cast<const uint4*>(at + off + up);
     }
   };
-  const auto refill = [&]() {    // this stage is multiplied
+  const auto done = [&]() {      // this stage is multiplied
     __syncwarp();
     if (++cs == kStages) {
       cs = 0;
       ph ^= 1u;
     }
     --ahead;
-    fill(true);
   };
 
   // ---- phase 1: act = weight silu(gate) up ----
@@ -562,13 +579,15 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
 #pragma unroll
     for (int n = 0; n < NG; ++n) {
       const int c = 8 * n + g;
-      x[n] = c < cnt ? a.x + (size_t)(shared ? c : sm->pair_t[col0 + c]) * a.hidden + t4 * 8 : nullptr;
+      const int cc = min(c, cnt - 1);   // columns past the expert's tokens repeat the last: never written
+      x[n] = a.x + (size_t)(shared ? cc : sm->pair_t[col0 + cc]) * a.hidden + t4 * 8;
       acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.0f;
     }
     for (int c = member; c < h_chunks; c += kTeam) {
       uint4 b0[2][2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) load_b(b0[h], x[0] + c * kCols + 64 * h, 0, a.hidden - c * kCols - 64 * h - t4 * 8, x[0] != nullptr);
+      for (int h = 0; h < 2; ++h) load_b(b0[h], x[0] + c * kCols + 64 * h, 0, a.hidden - c * kCols - 64 * h - t4 * 8, true);
+      fill(true);                // the stage before's place, while these are on their way
       moe_wait(a, sm, &sm->full[warp][cs], ph);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -580,11 +599,11 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
         for (int n = 1; n < NG; ++n)
           if (8 * n < cnt) {
             uint4 b[2];
-            load_b(b, x[n] + c * kCols + 64 * h, 0, a.hidden - c * kCols - 64 * h - t4 * 8, x[n] != nullptr);
+            load_b(b, x[n] + c * kCols + 64 * h, 0, a.hidden - c * kCols - 64 * h - t4 * 8, true);
             mma_block(acc[n], f, b);
           }
       }
-      refill();
+      done();
     }
     // the team's four sums, in their order; lane (g, t4) of the first warp holds gate and
     // up of row g for columns 2 t4 and 2 t4 + 1
@@ -644,9 +663,10 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
   Walk w = first2();
   flip = 0;   // the teams met differently often
   for (int i = cta; i < p.tiles3; i += grid) {
-    float acc[NG][4];
+    float acc[NG][4], low[NG][4];
 #pragma unroll
-    for (int n = 0; n < NG; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.0f;
+    for (int n = 0; n < NG; ++n)
+      acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = low[n][0] = low[n][1] = low[n][2] = low[n][3] = 0.0f;
     while (w.i == i) {
       const bool shared = w.j < 0;
       const int cols = cols_of(w.j), k = w.c * kCols + t4 * 8;
@@ -679,6 +699,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
           load_b_cg(lo[h], row + plane, k + 64 * h, cols, use);
         }
         if (!have) {
+          fill(true);
           moe_wait(a, sm, &sm->full[warp][cs], ph);
           have = true;
 #pragma unroll
@@ -688,16 +709,17 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
         for (int h = 0; h < 2; ++h)
           if (w.c * kCols + 64 * h < cols) {
             mma_block(acc[n], f[h], hi[h]);
-            mma_block(acc[n], f[h], lo[h]);
+            mma_block(low[n], f[h], lo[h]);
           }
       }
-      refill();
+      done();
       next2(w);
     }
 #pragma unroll
     for (int n = 0; n < NG; ++n) {
       if (8 * n >= a.tokens) break;
-      sm->red[flip][warp][lane] = make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
+      sm->red[flip][warp][lane] =
+          make_float4(acc[n][0] + low[n][0], acc[n][1] + low[n][1], acc[n][2] + low[n][2], acc[n][3] + low[n][3]);
       __syncthreads();
       const int r = tid & 15, t = 8 * n + (tid >> 4), h = i * p.rows3 + r;
       if (tid < 128 && t < a.tokens && r < p.rows3 && h < a.hidden) {
@@ -817,8 +839,12 @@ cudaError_t launch_moe(const MoeArgs& a, cudaStream_t stream) {
       (!weight_maps(&m.s_gate_up, &m.s_gate_up_edge, a.s_gate_up, 2ull * a.shared_inter, a.hidden, 8) ||
        !weight_maps(&m.s_down, &m.s_down_edge, a.s_down, a.hidden, a.shared_inter, p.rows3)))
     return cudaErrorInvalidValue;
-  const int units = (a.experts + (p.a.s_gate ? 1 : 0)) * ((a.tokens + 7) / 8);
-  moe_router_kernel<<<(units + 7) / 8, 256, 0, stream>>>(p);
+  // one token: 2048 columns in flight per warp; more: 8 tokens share an expert's row
+  const int rows = a.experts + (p.a.s_gate ? 1 : 0);
+  if (a.tokens == 1)
+    moe_router_kernel<1, 8><<<(rows + 7) / 8, 256, 0, stream>>>(p);
+  else
+    moe_router_kernel<8, 1><<<(rows * ((a.tokens + 7) / 8) + 7) / 8, 256, 0, stream>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if (a.tokens <= 8) return launch_experts<1>(m, p, sms, stream);
   if (a.tokens <= 16) return launch_experts<2>(m, p, sms, stream);
