@@ -16,7 +16,9 @@
 //            what S drops goes to a second sum.  Logits stay pairs of fp32 from
 //            there on (fp64 additions run at 1/64 of the rate here: with them the
 //            choice of 8 experts alone took 12 us).
-//   choice   one CTA: top-k, a warp per token, and the lists of active experts.
+//   choice   a CTA per token: a bound from the lanes' maxima, then the few
+//            candidates above it count those before them (a warp that picked one
+//            maximum after the other took 15 us per token with 512 experts).
 //   gate_up  tiles of 8 gate rows over the same 8 up rows, so that silu(g) u forms
 //            in one thread; columns are the expert's own tokens; four warps share
 //            a tile, each with every fourth chunk of 128 weight columns.
@@ -32,8 +34,7 @@
 // (Measured on the way: stages multiplied by 8 or 16 warps together cost the
 // latency of their activations and the warps' meetings, 1500 clocks where the
 // bytes take 700; all phases in one cooperative kernel lost 4 us before its
-// start and ran its choice of experts, code that each CTA executes once, at the
-// speed of instruction fetches: 9 us for one token, 60 for 64.)
+// start, for the runtime lets such a launch begin only after the one before.)
 // Which warp adds what depends on the expert's and the chunk's numbers alone, so
 // nothing in a token's arithmetic depends on the other tokens.
 //
@@ -60,19 +61,28 @@ constexpr uint32_t kRing = kMoeWarps * kStages * kStage;
 constexpr int kMaxExperts = 1024, kMaxPairs = GDN_MOE_MAX_TOKENS * 32;
 constexpr int kRouterCols = 2048, kRouterWarps = 8;
 constexpr uint32_t kRouterSmem = 16 * kRouterCols * 2;
-constexpr int kChoiceThreads = 512;
+constexpr int kChoiceThreads = 256;
 
-// What the choice leaves to the products, in the workspace.
+// What the choice leaves to the products, in the workspace, token-major.
+struct Choice {
+  float shared_w[GDN_MOE_MAX_TOKENS];  // the shared expert's factors
+  float weight[kMaxPairs];
+  uint16_t expert[kMaxPairs];
+};
+
+// The active experts, ascending, and their tokens: each CTA of the products makes
+// them for itself.
 struct Lists {
   int n_active;
-  int pad[3];
-  float shared_w[GDN_MOE_MAX_TOKENS];  // the shared expert's factors
-  float pair_w[kMaxPairs];             // weights of the (expert, token) pairs, by expert, then token
-  uint32_t mask[kMaxExperts][2];       // tokens of an active expert
-  uint16_t expert[kMaxExperts];        // active experts, ascending
+  int scan_a[kMoeWarps], scan_p[kMoeWarps];
+  uint32_t mask[kMaxExperts][2];       // tokens, first of an expert, then of an active one
+  uint16_t expert[kMaxExperts];        // active experts
   uint16_t base[kMaxExperts + 8];      // their first pairs
-  uint8_t turn[kMaxExperts];           // the warp that takes an active expert's first down chunk
-  uint8_t pair_t[kMaxPairs];           // the pairs' tokens
+  uint16_t rank[kMaxExperts];          // expert -> its place among the active
+  uint16_t of_team[kTeams][kMaxExperts];   // places of the active experts e = team (mod kTeams)
+  int n_team[kTeams];
+  uint8_t pair_t[kMaxPairs];           // tokens of the (expert, token) pairs
+  float pair_w[kMaxPairs];             // and their weights
 };
 
 struct MoeMaps {
@@ -82,9 +92,9 @@ struct MoeMaps {
 struct MoeParams {
   MoeArgs a;
   float2* logit;        // [tokens][experts + 1], high and low part
-  Lists* lists;
-  uint16_t* act;        // [hi, lo][pairs][inter]
-  uint16_t* s_act;      // [hi, lo][tokens][shared_inter]
+  Choice* choice;
+  uint16_t* act;        // [hi, lo][pairs + 1][inter], the last row zeros
+  uint16_t* s_act;      // [hi, lo][tokens + 1][shared_inter], likewise
   int rows3, tiles3;    // output rows per tile, tiles
 };
 
@@ -113,6 +123,7 @@ __device__ __forceinline__ bool moe_wait(const MoeArgs& a, uint64_t* mbar, uint3
 }
 
 // ---- router ----
+template <int NT>   // tokens of a CTA
 __global__ void __launch_bounds__(32 * kRouterWarps) moe_router_kernel(const MoeParams p) {
   extern __shared__ __align__(128) uint8_t rows_raw[];
   __shared__ __align__(8) uint64_t full;
@@ -121,16 +132,16 @@ __global__ void __launch_bounds__(32 * kRouterWarps) moe_router_kernel(const Moe
   let_next_begin();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n_rows = a.experts + (a.s_gate ? 1 : 0);
-  const int e0 = blockIdx.x * 8, t0 = blockIdx.y * 8, ne = min(8, n_rows - e0), nt = min(8, a.tokens - t0);
+  const int e0 = blockIdx.x * 8, t0 = blockIdx.y * NT, ne = min(8, n_rows - e0), nt = min(NT, a.tokens - t0);
   if (threadIdx.x == 0) {
     tc::mbar_init(&full, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   __syncthreads();
   constexpr float kGrid = 3072.0f;   // products go to S on a grid of 2^-12
-  float S[8], lo[8];
+  float S[NT], lo[NT];
 #pragma unroll
-  for (int t = 0; t < 8; ++t) {
+  for (int t = 0; t < NT; ++t) {
     S[t] = kGrid;
     lo[t] = 0.0f;
   }
@@ -155,9 +166,8 @@ __global__ void __launch_bounds__(32 * kRouterWarps) moe_router_kernel(const Moe
         const uint4 wv = *reinterpret_cast<const uint4*>(rows + warp * kRouterCols + k);
         const uint32_t ww[4] = {wv.x, wv.y, wv.z, wv.w};
 #pragma unroll
-        for (int t = 0; t < 8; ++t) {
-          if (t >= nt) break;
-          const uint4 xv = *reinterpret_cast<const uint4*>(rows + (8 + t) * kRouterCols + k);
+        for (int t = 0; t < NT; ++t) {   // past the end the last token again
+          const uint4 xv = *reinterpret_cast<const uint4*>(rows + (8 + min(t, nt - 1)) * kRouterCols + k);
           const uint32_t xx[4] = {xv.x, xv.y, xv.z, xv.w};
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
@@ -174,8 +184,7 @@ __global__ void __launch_bounds__(32 * kRouterWarps) moe_router_kernel(const Moe
   }
   if (warp >= ne) return;
 #pragma unroll
-  for (int t = 0; t < 8; ++t) {
-    if (t >= nt) break;
+  for (int t = 0; t < NT; ++t) {
     // the lanes' pairs (S - grid, lo) join as pairs: the high parts' rounding is kept
     float h = S[t] - kGrid, l = lo[t];
 #pragma unroll
@@ -185,7 +194,7 @@ __global__ void __launch_bounds__(32 * kRouterWarps) moe_router_kernel(const Moe
       h = r.x;
       l = (l + ol) + r.y;
     }
-    if (lane == 0) p.logit[(size_t)(t0 + t) * (a.experts + 1) + e0 + warp] = two_sum(h, l);
+    if (lane == 0 && t < nt) p.logit[(size_t)(t0 + t) * (a.experts + 1) + e0 + warp] = two_sum(h, l);
   }
 }
 
@@ -218,101 +227,101 @@ __device__ __forceinline__ int below(uint32_t m0, uint32_t m1, int t) {
   return t < 32 ? __popc(m0 & ((1u << t) - 1u)) : __popc(m0) + __popc(m1 & ((1u << (t - 32)) - 1u));
 }
 
-struct ChoiceSmem {
-  uint32_t mask[kMaxExperts][2];
-  uint16_t rank[kMaxExperts], base[kMaxExperts];   // of an expert: its place among the active, its first pair
-  uint16_t sel[kMaxPairs];
-  float sel_w[kMaxPairs];
-  int scan_a[kChoiceThreads / 32], scan_p[kChoiceThreads / 32];
-};
-
-// 32 V experts at most.
-template <int V>
-__global__ void __launch_bounds__(kChoiceThreads, 1) moe_choice_kernel(const MoeParams p) {
-  __shared__ ChoiceSmem sm;
+// One token.  Of the 32 lanes' maxima the k-th largest bounds the k-th largest key
+// from below, so only keys from there on (some k of them) are candidates; a
+// candidate's rank is the number of candidates with a larger key, or an equal one
+// and a lower index.  Ranks below top_k are the choice, in order.
+__global__ void __launch_bounds__(kChoiceThreads) moe_choice_kernel(const MoeParams p) {
+  __shared__ unsigned long long key[kMaxExperts];
+  __shared__ uint16_t cand[kMaxExperts];
+  __shared__ int n_cand;
+  __shared__ float part[kChoiceThreads / 32];
+  __shared__ float chosen[32];
   const MoeArgs& a = p.a;
-  Lists& L = *p.lists;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  constexpr int kWarps = kChoiceThreads / 32;
+  const int tid = threadIdx.x, lane = tid & 31, t = blockIdx.x;
   let_next_begin();
-  for (int e = tid; e < a.experts; e += kChoiceThreads) sm.mask[e][0] = sm.mask[e][1] = 0;
-  __syncthreads();
+  if (tid == 0) n_cand = 0;
   wait_before();   // the logits
-  for (int t = warp; t < a.tokens; t += kWarps) {
-    const float2* lg = p.logit + (size_t)t * (a.experts + 1);
-    unsigned long long key[V];
-    unsigned long long best = 0;
-    int at = -1;
-#pragma unroll
-    for (int j = 0; j < V; ++j) {   // every load in flight at once
-      const int e = j * 32 + lane;
-      key[j] = order_key(e < a.experts ? __ldcg(lg + e) : make_float2(0.0f, 0.0f));
+  const float2* lg = p.logit + (size_t)t * (a.experts + 1);
+  for (int e = tid; e < a.experts; e += kChoiceThreads) key[e] = order_key(__ldcg(lg + e));
+  __syncthreads();
+  // every warp: the lanes' maxima, the softmax's maximum, the bound
+  unsigned long long m = 0;
+  for (int e = lane; e < a.experts; e += 32) m = max(m, key[e]);
+  const uint32_t mine = (uint32_t)(m >> 32), h = __reduce_max_sync(0xffffffffu, mine);
+  const uint32_t l = __reduce_max_sync(0xffffffffu, mine == h ? (uint32_t)m : 0u);
+  const float2 top = order_value(((unsigned long long)h << 32) | l);
+  int above = 0;
+  for (int o = 0; o < 32; ++o) {
+    const uint32_t v = __shfl_sync(0xffffffffu, mine, o);
+    above += v > mine || (v == mine && o < lane);
+  }
+  const uint32_t bound = __reduce_max_sync(0xffffffffu, above == a.top_k - 1 ? mine : 0u);
+  float den = 0.0f;
+  for (int e = tid; e < a.experts; e += kChoiceThreads) {
+    const unsigned long long k = key[e];
+    den += exp_of(order_value(k), top);
+    if ((uint32_t)(k >> 32) >= bound) cand[atomicAdd(&n_cand, 1)] = (uint16_t)e;
+  }
+  den = warp_sum(den);
+  if (lane == 0) part[tid >> 5] = den;
+  __syncthreads();
+  const int n = n_cand;
+  for (int i = tid; i < n; i += kChoiceThreads) {
+    const int e = cand[i];
+    const unsigned long long k = key[e];
+    int rank = 0;
+    for (int o = 0; o < n; ++o) {
+      const int f = cand[o];
+      rank += key[f] > k || (key[f] == k && f < e);
     }
-    const float shared_logit = a.s_gate ? __ldcg(lg + a.experts).x : 0.0f;
-#pragma unroll
-    for (int j = 0; j < V; ++j)
-      if (j * 32 + lane < a.experts && (at < 0 || key[j] > best)) {
-        best = key[j];
-        at = j;
-      }
-    uint32_t used = 0;
-    float2 top = make_float2(0.0f, 0.0f);
-    float den = 0.0f, sum = 0.0f, mine = 0.0f;
-    for (int k = 0; k < a.top_k; ++k) {
-      const uint32_t hi = at >= 0 ? (uint32_t)(best >> 32) : 0, mh = __reduce_max_sync(0xffffffffu, hi);
-      const bool c1 = at >= 0 && hi == mh;
-      const uint32_t lo = c1 ? (uint32_t)best : 0, ml = __reduce_max_sync(0xffffffffu, lo);
-      const bool c2 = c1 && lo == ml;
-      const int e = (int)__reduce_min_sync(0xffffffffu, c2 ? (uint32_t)(at * 32 + lane) : 0xffffffffu);
-      const float2 v = order_value(((unsigned long long)mh << 32) | ml);
-      if (k == 0) {   // the softmax's maximum and sum
-        top = v;
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-          if (j * 32 + lane < a.experts) den += exp_of(order_value(key[j]), top);
-        den = warp_sum(den);
-      }
-      const float w = exp_of(v, top);
-      sum += w;
-      if (lane == k) mine = w;
-      if (lane == 0) {
-        sm.sel[t * a.top_k + k] = (uint16_t)e;
-        atomicOr(&sm.mask[e][t >> 5], 1u << (t & 31));
-      }
-      if ((e & 31) == lane) {
-        used |= 1u << (e >> 5);
-        best = 0;
-        at = -1;
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-          if (j * 32 + lane < a.experts && !(used >> j & 1) && (at < 0 || key[j] > best)) {
-            best = key[j];
-            at = j;
-          }
-      }
+    if (rank < a.top_k) {
+      chosen[rank] = exp_of(order_value(k), top);
+      p.choice->expert[t * a.top_k + rank] = (uint16_t)e;
+      if (a.topk_id) a.topk_id[t * a.top_k + rank] = e;
     }
-    __syncwarp();
-    if (lane < a.top_k) {
-      const float w = mine / (a.renorm ? sum : den);
-      sm.sel_w[t * a.top_k + lane] = w;
-      if (a.topk_id) a.topk_id[t * a.top_k + lane] = sm.sel[t * a.top_k + lane];
-      if (a.topk_w) a.topk_w[t * a.top_k + lane] = w;
-    }
-    if (lane == 0) L.shared_w[t] = a.s_gate ? sigmoid(shared_logit) : 1.0f;
   }
   __syncthreads();
+  if (tid < 32) {
+    float sum = 0.0f;   // in the order of the ranks, or of the warps
+    if (a.renorm)
+      for (int k = 0; k < a.top_k; ++k) sum += chosen[k];
+    else
+      for (int w = 0; w < kChoiceThreads / 32; ++w) sum += part[w];
+    if (lane < a.top_k) {
+      const float w = chosen[lane] / sum;
+      p.choice->weight[t * a.top_k + lane] = w;
+      if (a.topk_w) a.topk_w[t * a.top_k + lane] = w;
+    }
+    if (lane == 0) p.choice->shared_w[t] = a.s_gate ? sigmoid(__ldcg(lg + a.experts).x) : 1.0f;
+  }
+}
 
-  // the active experts in ascending order and their first pairs
-  constexpr int PER = kMaxExperts / kChoiceThreads;
+// ---- products ----
+
+// The lists, by all threads of a CTA: `pairs` with the pairs' tokens and weights,
+// else with the teams' experts.
+template <bool pairs>
+__device__ __forceinline__ void make_lists(const MoeParams& p, Lists& L) {
+  const MoeArgs& a = p.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, n = a.tokens * a.top_k;
+  for (int e = tid; e < a.experts; e += kMoeThreads) L.mask[e][0] = L.mask[e][1] = 0;
+  __syncthreads();
+  for (int i = tid; i < n; i += kMoeThreads) {
+    const int t = i / a.top_k;
+    atomicOr(&L.mask[__ldcg(&p.choice->expert[i])][t >> 5], 1u << (t & 31));
+  }
+  __syncthreads();
+  constexpr int PER = (kMaxExperts + kMoeThreads - 1) / kMoeThreads;
+  uint32_t m0[PER], m1[PER];
   int na = 0, np = 0;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int e = tid * PER + i;
-    if (e < a.experts) {
-      const int n = __popc(sm.mask[e][0]) + __popc(sm.mask[e][1]);
-      na += n > 0;
-      np += n;
-    }
+    m0[i] = e < a.experts ? L.mask[e][0] : 0;
+    m1[i] = e < a.experts ? L.mask[e][1] : 0;
+    na += (m0[i] | m1[i]) != 0;
+    np += __popc(m0[i]) + __popc(m1[i]);
   }
   int ia = na, ip = np;
   for (int m = 1; m < 32; m <<= 1) {
@@ -323,53 +332,53 @@ __global__ void __launch_bounds__(kChoiceThreads, 1) moe_choice_kernel(const Moe
     }
   }
   if (lane == 31) {
-    sm.scan_a[warp] = ia;
-    sm.scan_p[warp] = ip;
+    L.scan_a[warp] = ia;
+    L.scan_p[warp] = ip;
   }
-  __syncthreads();
+  __syncthreads();   // (and every mask is in registers)
   ia -= na;
   ip -= np;
-  int total = 0;
-  for (int w = 0; w < kWarps; ++w) {
+  for (int w = 0; w < kMoeWarps; ++w)
     if (w < warp) {
-      ia += sm.scan_a[w];
-      ip += sm.scan_p[w];
+      ia += L.scan_a[w];
+      ip += L.scan_p[w];
     }
-    total += sm.scan_a[w];
-  }
-  if (tid == 0) {
-    L.n_active = total;
-    L.base[total] = (uint16_t)(a.tokens * a.top_k);
-  }
-  const unsigned chunks = (unsigned)((a.inter + kCols - 1) / kCols);
 #pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int e = tid * PER + i;
-    if (e < a.experts) {
-      const uint32_t m0 = sm.mask[e][0], m1 = sm.mask[e][1];
-      const int n = __popc(m0) + __popc(m1);
-      if (n > 0) {
-        L.expert[ia] = (uint16_t)e;
-        L.base[ia] = (uint16_t)ip;
-        L.mask[ia][0] = m0;
-        L.mask[ia][1] = m1;
-        L.turn[ia] = (uint8_t)((unsigned)e * chunks % kMoeWarps);
-        sm.base[e] = (uint16_t)ip;
-        ++ia;
-        ip += n;
-      }
+  for (int i = 0; i < PER; ++i)
+    if ((m0[i] | m1[i]) != 0) {
+      const int e = tid * PER + i;
+      L.expert[ia] = (uint16_t)e;
+      L.base[ia] = (uint16_t)ip;
+      L.mask[ia][0] = m0[i];
+      L.mask[ia][1] = m1[i];
+      L.rank[e] = (uint16_t)ia;
+      ++ia;
+      ip += __popc(m0[i]) + __popc(m1[i]);
     }
+  if (tid == kMoeThreads - 1) {
+    L.n_active = ia;
+    L.base[ia] = (uint16_t)ip;
   }
   __syncthreads();
-  for (int i = tid; i < a.tokens * a.top_k; i += kChoiceThreads) {
-    const int t = i / a.top_k, e = sm.sel[i];
-    const int at = sm.base[e] + below(sm.mask[e][0], sm.mask[e][1], t);
-    L.pair_w[at] = sm.sel_w[i];
-    L.pair_t[at] = (uint8_t)t;
+  if (pairs) {
+    for (int i = tid; i < n; i += kMoeThreads) {
+      const int t = i / a.top_k, j = L.rank[__ldcg(&p.choice->expert[i])];
+      const int at = L.base[j] + below(L.mask[j][0], L.mask[j][1], t);
+      L.pair_w[at] = __ldcg(&p.choice->weight[i]);
+      L.pair_t[at] = (uint8_t)t;
+    }
+  } else if (warp < kTeams) {
+    int n_mine = 0;
+    for (int j = lane; j - lane < L.n_active; j += 32) {
+      const bool in = j < L.n_active && L.expert[j] % kTeams == warp;
+      const uint32_t b = __ballot_sync(0xffffffffu, in);
+      if (in) L.of_team[warp][n_mine + __popc(b & ((1u << lane) - 1u))] = (uint16_t)j;
+      n_mine += __popc(b);
+    }
+    if (lane == 0) L.n_team[warp] = n_mine;
   }
+  __syncthreads();
 }
-
-// ---- products ----
 
 __device__ __forceinline__ void tma3(uint32_t dst, const CUtensorMap* tm, int x, int y, int z, uint64_t* mbar) {
   asm volatile(
@@ -444,9 +453,7 @@ __device__ __forceinline__ void load_a(Frag& f, const uint8_t* stage, int line, 
 struct ProductSmem {
   uint64_t full[kMoeWarps][kStages];
   float4 red[2][kMoeWarps][32];
-  uint32_t mask[kMaxExperts][2];
-  uint16_t expert[kMaxExperts], base[kMaxExperts + 8];
-  uint8_t turn[kMaxExperts];
+  Lists lists;
 };
 constexpr uint32_t kProductSmem = kRing + sizeof(ProductSmem) + 1024;
 static_assert(kProductSmem <= 227 * 1024, "shared memory");
@@ -490,25 +497,30 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
         ly = 8 * li;
         if (li >= s_tiles && li < n_tiles) {
           const int j = (li - s_tiles) / e_tiles;
-          ly = sm->expert[j] * 2 * a.inter + (li - s_tiles - j * e_tiles) * 8;
+          ly = sm->lists.expert[j] * 2 * a.inter + (li - s_tiles - j * e_tiles) * 8;
         }
       }
     }
   };
   fill();          // of the shared expert
-  wait_before();   // the lists
+  wait_before();   // the choice
   let_next_begin();
-  const Lists& L = *p.lists;
-  const int na = __ldcg(&L.n_active);
-  for (int i = tid; i <= na; i += kMoeThreads) {
-    sm->expert[i] = __ldcg(&L.expert[i]);
-    sm->base[i] = __ldcg(&L.base[i]);
-  }
-  __syncthreads();
+  Lists& L = sm->lists;
+  make_lists<true>(p, L);
+  const int na = L.n_active;
   n_tiles = s_tiles + na * e_tiles;
   if (li >= s_tiles && li < n_tiles) {
     const int j = (li - s_tiles) / e_tiles;
-    ly = sm->expert[j] * 2 * a.inter + (li - s_tiles - j * e_tiles) * 8;
+    ly = L.expert[j] * 2 * a.inter + (li - s_tiles - j * e_tiles) * 8;
+  }
+
+  // the row of zeros after the last pair's, for tokens that an expert does not serve
+  if (cta == grid - 1) {
+    const int np = a.tokens * a.top_k;
+    for (int i = tid; i < 2 * a.inter; i += kMoeThreads)
+      p.act[(size_t)np * a.inter + i + (i >= a.inter ? (size_t)np * a.inter : 0)] = 0;
+    for (int i = tid; i < 2 * a.shared_inter; i += kMoeThreads)
+      p.s_act[(size_t)a.tokens * a.shared_inter + i + (i >= a.shared_inter ? (size_t)a.tokens * a.shared_inter : 0)] = 0;
   }
 
   const int g = lane >> 2, t4 = lane & 3;
@@ -518,21 +530,30 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
   for (int i = i0; i < n_tiles; i += tile_step) {
     const bool shared = i < s_tiles;
     const int j = shared ? -1 : (i - s_tiles) / e_tiles, r0 = (shared ? i : i - s_tiles - j * e_tiles) * 8;
-    const int col0 = shared ? 0 : sm->base[j], cnt = shared ? a.tokens : sm->base[j + 1] - col0;
+    const int col0 = shared ? 0 : L.base[j], cnt = shared ? a.tokens : L.base[j + 1] - col0;
     const uint16_t* x[NG];       // the rows of this lane's columns
     float acc[NG][4];
 #pragma unroll
     for (int n = 0; n < NG; ++n) {
       const int c = min(8 * n + g, cnt - 1);   // columns past the expert's tokens repeat the last: never written
-      x[n] = a.x + (size_t)(shared ? c : (int)__ldcg(&L.pair_t[col0 + c])) * a.hidden + t4 * 8;
+      x[n] = a.x + (size_t)(shared ? c : (int)L.pair_t[col0 + c]) * a.hidden + t4 * 8;
       acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.0f;
     }
-    for (int c = member; c < h_chunks; c += kTeam) {
-      uint4 b[4];
-      const int k = c * kCols, left = a.hidden - k - t4 * 8;   // columns from this lane's first on
+    uint4 b[4];                  // a chunk's activations, asked for one chunk ahead
+    const auto load_x = [&](int k) {
+      if (k + kCols <= a.hidden) {
 #pragma unroll
-      for (int h = 0; h < 4; ++h)
-        b[h] = 32 * h < left ? *reinterpret_cast<const uint4*>(x[0] + k + 32 * h) : make_uint4(0, 0, 0, 0);
+        for (int h = 0; h < 4; ++h) b[h] = *reinterpret_cast<const uint4*>(x[0] + k + 32 * h);
+      } else {
+        const int left = a.hidden - k - t4 * 8;                // columns from this lane's first on
+#pragma unroll
+        for (int h = 0; h < 4; ++h)
+          b[h] = 32 * h < left ? *reinterpret_cast<const uint4*>(x[0] + k + 32 * h) : make_uint4(0, 0, 0, 0);
+      }
+    };
+    load_x(member * kCols);
+    for (int c = member; c < h_chunks; c += kTeam) {
+      const int k = c * kCols, left = a.hidden - k - t4 * 8;
       fill();                    // the stage before's place, while these are on their way
       ok = ok && moe_wait(a, &full[cs], ph);
 #pragma unroll
@@ -544,14 +565,15 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
 #pragma unroll
         for (int n = 1; n < NG; ++n)
           if (8 * n < cnt) {
-            uint4 bn[2];
+            uint4 bm[2];
 #pragma unroll
             for (int q = 0; q < 2; ++q)
-              bn[q] = 64 * h + 32 * q < left ? *reinterpret_cast<const uint4*>(x[n] + k + 64 * h + 32 * q)
+              bm[q] = 64 * h + 32 * q < left ? *reinterpret_cast<const uint4*>(x[n] + k + 64 * h + 32 * q)
                                              : make_uint4(0, 0, 0, 0);
-            mma_block(acc[n], f, bn);
+            mma_block(acc[n], f, bm);
           }
       }
+      load_x(k + kTeam * kCols);
       __syncwarp();
       ++free_stages;
       if (++cs == kStages) {
@@ -564,7 +586,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
     // up of row g for columns 2 t4 and 2 t4 + 1
     const int cols = shared ? a.shared_inter : a.inter;
     uint16_t* const act = shared ? p.s_act : p.act;
-    const size_t plane = (size_t)(shared ? a.tokens : a.tokens * a.top_k) * cols;
+    const size_t plane = (size_t)((shared ? a.tokens : a.tokens * a.top_k) + 1) * cols;
 #pragma unroll
     for (int n = 0; n < NG; ++n)
       if (8 * n < cnt) {
@@ -583,7 +605,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
           for (int o = 0; o < 2; ++o) {
             const int c = 8 * n + 2 * t4 + o;
             if (c < cnt) {
-              const float v = silu(acc[n][o]) * acc[n][2 + o] * __ldcg(shared ? &L.shared_w[c] : &L.pair_w[col0 + c]);
+              const float v = silu(acc[n][o]) * acc[n][2 + o] * (shared ? __ldcg(&p.choice->shared_w[c]) : L.pair_w[col0 + c]);
               const uint16_t hi = f32_to_bf16(v);
               const size_t at = (size_t)(col0 + c) * cols + r0 + g;
               act[at] = hi;
@@ -611,56 +633,72 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
     for (int s = 0; s < kStages; ++s) tc::mbar_init(&full[s], 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  // The lists were complete before the launch that ran the gate and up products let
+  // The choice was complete before the launch that ran the gate and up products let
   // this one begin; only its activations are still to come.
-  const Lists& L = *p.lists;
-  const int na = __ldcg(&L.n_active);
-  for (int i = tid; i <= na; i += kMoeThreads) {
-    sm->base[i] = __ldcg(&L.base[i]);
-    if (i < na) {
-      sm->expert[i] = __ldcg(&L.expert[i]);
-      sm->turn[i] = __ldcg(&L.turn[i]);
-      const uint2 m = __ldcg(reinterpret_cast<const uint2*>(L.mask[i]));
-      sm->mask[i][0] = m.x;
-      sm->mask[i][1] = m.y;
-    }
-  }
-  __syncthreads();
-  const int j0 = a.shared_inter > 0 ? -1 : 0;                        // expert -1 is the shared one
+  Lists& L = sm->lists;
+  make_lists<false>(p, L);
   const int i_chunks = (a.inter + kCols - 1) / kCols, s_chunks = (a.shared_inter + kCols - 1) / kCols;
 
-  // This warp's chunks in order: of output tile i, expert j, chunk c.  One walk
-  // loads, kStages ahead; one multiplies.
+  // A team takes every third expert, its four warps every fourth chunk; of the shared
+  // expert a warp takes every twelfth chunk.  A CTA begins with its own one of the
+  // experts, so that the CTAs do not all read the same activations at once.  All
+  // this hangs on the experts', the chunks' and the CTA's numbers alone.
+  const int team = warp / kTeam, member = warp % kTeam, n_team = L.n_team[team];
+  const uint16_t* const of_team = L.of_team[team];
+  int start = 0;
+  {
+    const int from = (int)((long long)cta * a.experts / grid);
+    for (int lo = 0, hi = n_team; lo < hi;) {   // the first one not below `from`
+      const int mid = (lo + hi) >> 1;
+      if (L.expert[of_team[mid]] < from) lo = mid + 1; else hi = mid;
+      start = lo;
+    }
+    if (start == n_team) start = 0;
+  }
+  // This warp's chunks in order, the loads kStages ahead of the products: of output
+  // tile i, expert j (the team's n-th; -1: the shared one), chunk c.
   struct Walk {
-    int i, j, c;
+    int i, n, j, c;
   };
-  const auto settle = [&](Walk& w) {     // on to the first chunk from w on that is this warp's
+  const auto settle = [&](Walk& w) {     // on to the first chunk from w on that exists
     while (w.c >= (w.j < 0 ? s_chunks : i_chunks)) {
-      if (++w.j >= na) {
-        w.j = j0;
+      if (++w.n >= n_team) {
+        w.n = -1;
         w.i += grid;
         if (w.i >= p.tiles3) return;
+        w.j = -1;
+        w.c = warp;
+      } else {
+        w.j = of_team[start + w.n < n_team ? start + w.n : start + w.n - n_team];
+        w.c = member;
       }
-      w.c = w.j < 0 ? warp : warp - sm->turn[w.j];
-      if (w.c < 0) w.c += kMoeWarps;
     }
   };
-  Walk w{cta, j0, j0 < 0 ? warp : warp - sm->turn[0]};
-  if (w.c < 0) w.c += kMoeWarps;
-  if (w.i < p.tiles3) settle(w);
-  Walk l = w;
-  int ls = 0, free_stages = kStages;
+  Walk l{cta, -1, -1, warp};
+  if (l.i < p.tiles3) settle(l);
+  // loaded and not yet multiplied, oldest first
+  constexpr int kEnd = 0x7fffffff;
+  int qi[kStages], qj[kStages], qc[kStages], ls = 0, queued = 0;
+#pragma unroll
+  for (int s = 0; s < kStages; ++s) qi[s] = kEnd;
   const auto fill = [&]() {
-    while (free_stages > 0 && l.i < p.tiles3) {
+    while (queued < kStages && l.i < p.tiles3) {
       const bool shared = l.j < 0;
       if (lane == 0)
         load_stage(ring_a + ls * kStage, &full[ls], shared ? &maps.s_whole : &maps.whole,
                    shared ? &maps.s_edge : &maps.edge, shared ? a.shared_inter : a.inter, l.c, p.rows3,
-                   (shared ? 0 : sm->expert[l.j] * a.hidden) + l.i * p.rows3, -1);
+                   (shared ? 0 : L.expert[l.j] * a.hidden) + l.i * p.rows3, -1);
       __syncwarp();
-      --free_stages;
+#pragma unroll
+      for (int s = 0; s < kStages; ++s)
+        if (s == queued) {
+          qi[s] = l.i;
+          qj[s] = l.j;
+          qc[s] = l.c;
+        }
+      ++queued;
       if (++ls == kStages) ls = 0;
-      l.c += kMoeWarps;
+      l.c += l.j < 0 ? kMoeWarps : kTeam;
       settle(l);
     }
   };
@@ -671,67 +709,96 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
   int cs = 0, flip = 0;
   uint32_t ph = 0;
   bool ok = true;   // after a wait that gave up no later one waits
+  // the tokens of an expert, and this lane's row of the activations for one of them
+  const auto members_of = [&](int j, uint32_t& m0, uint32_t& m1) {
+    if (j < 0) {
+      m0 = a.tokens < 32 ? (1u << a.tokens) - 1u : 0xffffffffu;
+      m1 = a.tokens <= 32 ? 0u : (a.tokens < 64 ? (1u << (a.tokens - 32)) - 1u : 0xffffffffu);
+    } else {
+      m0 = L.mask[j][0];
+      m1 = L.mask[j][1];
+    }
+  };
+  const int np = a.tokens * a.top_k;
+  const auto load_act = [&](uint4* hi, uint4* lo, int j, int c, uint32_t m0, uint32_t m1, int n) {
+    const bool shared = j < 0;
+    const int cols = shared ? a.shared_inter : a.inter, zero = shared ? a.tokens : np;   // the row of zeros
+    const int k = c * kCols + t4 * 8, t = 8 * n + g;
+    const bool use = (n < 4 ? m0 >> t : m1 >> (t - 32)) & 1;
+    const int at = use ? (shared ? t : L.base[j] + below(m0, m1, t)) : zero;
+    const uint16_t* row = (shared ? p.s_act : p.act) + ((size_t)at * cols + k);
+    const uint16_t* row_lo = row + (size_t)(zero + 1) * cols;
+    if ((c + 1) * kCols <= cols) {
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        hi[h] = __ldcg(reinterpret_cast<const uint4*>(row + 32 * h));
+        lo[h] = __ldcg(reinterpret_cast<const uint4*>(row_lo + 32 * h));
+      }
+    } else {
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        hi[h] = lo[h] = make_uint4(0, 0, 0, 0);
+        if (k + 32 * h < cols) {
+          hi[h] = __ldcg(reinterpret_cast<const uint4*>(row + 32 * h));
+          lo[h] = __ldcg(reinterpret_cast<const uint4*>(row_lo + 32 * h));
+        }
+      }
+    }
+  };
+  const auto first_group = [](uint32_t m0, uint32_t m1) { return m0 ? (__ffs(m0) - 1) >> 3 : 4 + ((__ffs(m1) - 1) >> 3); };
+  // a chunk's first group's activations, asked for one chunk ahead
+  uint4 hi[4], lo[4];
+  uint32_t m0 = 0, m1 = 0;
+  int first = 0;
+  const auto ask = [&]() {
+    if (qi[0] == kEnd) return;
+    members_of(qj[0], m0, m1);
+    first = NG == 1 ? 0 : first_group(m0, m1);
+    // (unrolled over the groups so that each load's shifts are constants)
+#pragma unroll
+    for (int n = 0; n < NG; ++n)
+      if (n == first) load_act(hi, lo, qj[0], qc[0], m0, m1, n);
+  };
+  ask();
   for (int i = cta; i < p.tiles3; i += grid) {
     float acc[NG][4], low[NG][4];
 #pragma unroll
-    for (int n = 0; n < NG; ++n)
-      acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = low[n][0] = low[n][1] = low[n][2] = low[n][3] = 0.0f;
-    while (w.i == i) {
-      const bool shared = w.j < 0;
-      const int cols = shared ? a.shared_inter : a.inter, k = w.c * kCols, left = cols - k - t4 * 8;
-      uint32_t m0, m1;
-      int base = 0;
-      if (shared) {
-        m0 = a.tokens < 32 ? (1u << a.tokens) - 1u : 0xffffffffu;
-        m1 = a.tokens <= 32 ? 0u : (a.tokens < 64 ? (1u << (a.tokens - 32)) - 1u : 0xffffffffu);
-      } else {
-        m0 = sm->mask[w.j][0];
-        m1 = sm->mask[w.j][1];
-        base = sm->base[w.j];
-      }
-      const uint16_t* act = (shared ? p.s_act : p.act) + k + t4 * 8;
-      const size_t plane = (size_t)(shared ? a.tokens : a.tokens * a.top_k) * cols;
-      bool have = false;
+    for (int n = 0; n < NG; ++n) {
+      acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.0f;
+      low[n][0] = low[n][1] = low[n][2] = low[n][3] = 0.0f;
+    }
+    while (qi[0] == i) {
+      const int j = qj[0], c = qc[0], cols = j < 0 ? a.shared_inter : a.inter;
+      ok = ok && moe_wait(a, &full[cs], ph);
       Frag f[2];
 #pragma unroll
+      for (int h = 0; h < 2; ++h) load_a(f[h], ring + cs * kStage, h * p.rows3 + g, 1024, t4);
+#pragma unroll
       for (int n = 0; n < NG; ++n) {
-        const uint32_t members = (n < 4 ? m0 >> (8 * n) : m1 >> (8 * n - 32)) & 0xffu;
-        if (members == 0) continue;
-        const int t = 8 * n + g;
-        const bool use = members >> g & 1;
-        const int have_cols = use ? left : 0;
-        const uint16_t* row = act + (size_t)(use ? (shared ? t : base + below(m0, m1, t)) : 0) * cols;
-        uint4 hi[4], lo[4];
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          hi[h] = lo[h] = make_uint4(0, 0, 0, 0);
-          if (32 * h < have_cols) {
-            hi[h] = __ldcg(reinterpret_cast<const uint4*>(row + 32 * h));
-            lo[h] = __ldcg(reinterpret_cast<const uint4*>(row + plane + 32 * h));
-          }
-        }
-        if (!have) {
-          fill();                // the stage before's place, while these are on their way
-          ok = ok && moe_wait(a, &full[cs], ph);
-          have = true;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) load_a(f[h], ring + cs * kStage, h * p.rows3 + g, 1024, t4);
-        }
+        if (NG > 1 && ((n < 4 ? m0 >> (8 * n) : m1 >> (8 * n - 32)) & 0xffu) == 0) continue;
+        if (n != first) load_act(hi, lo, j, c, m0, m1, n);
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          if (k + 64 * h < cols) {
+          if (c * kCols + 64 * h < cols) {
             mma_block(acc[n], f[h], hi + 2 * h);
             mma_block(low[n], f[h], lo + 2 * h);
           }
       }
       __syncwarp();
-      ++free_stages;
       if (++cs == kStages) {
         cs = 0;
         ph ^= 1u;
       }
-      w.c += kMoeWarps;
-      settle(w);
+#pragma unroll
+      for (int s = 0; s + 1 < kStages; ++s) {
+        qi[s] = qi[s + 1];
+        qj[s] = qj[s + 1];
+        qc[s] = qc[s + 1];
+      }
+      qi[kStages - 1] = kEnd;
+      --queued;
+      ask();
+      fill();                    // while the activations are on their way
     }
 #pragma unroll
     for (int n = 0; n < NG; ++n) {
@@ -830,8 +897,8 @@ cudaError_t launch_products(const MoeMaps& up, const MoeMaps& down, const MoePar
 
 size_t moe_scratch_bytes(int tokens, int, int inter, int experts, int top_k, int shared_inter) {
   const size_t T = tokens > 0 ? tokens : 1;
-  return up256(sizeof(Lists)) + up256(T * (experts + 1) * 8) + up256(T * top_k * inter * 4) +
-         up256(T * shared_inter * 4);
+  return up256(sizeof(Choice)) + up256(T * (experts + 1) * 8) + up256((T * top_k + 1) * inter * 4) +
+         up256((T + 1) * shared_inter * 4);
 }
 
 cudaError_t launch_moe(const MoeArgs& a, cudaStream_t stream) {
@@ -844,12 +911,12 @@ cudaError_t launch_moe(const MoeArgs& a, cudaStream_t stream) {
   if (a.shared_inter == 0) p.a.s_gate = nullptr;
   const size_t T = a.tokens;
   char* ws = static_cast<char*>(a.scratch);
-  p.lists = reinterpret_cast<Lists*>(ws);
-  ws += up256(sizeof(Lists));
+  p.choice = reinterpret_cast<Choice*>(ws);
+  ws += up256(sizeof(Choice));
   p.logit = reinterpret_cast<float2*>(ws);
   ws += up256(T * (a.experts + 1) * 8);
   p.act = reinterpret_cast<uint16_t*>(ws);
-  ws += up256(T * a.top_k * a.inter * 4);
+  ws += up256((T * a.top_k + 1) * a.inter * 4);
   p.s_act = reinterpret_cast<uint16_t*>(ws);
   // output rows: tiles of at most 16, as many as give every CTA the same number
   const int per = (a.hidden + 16 * sms - 1) / (16 * sms);
@@ -864,13 +931,13 @@ cudaError_t launch_moe(const MoeArgs& a, cudaStream_t stream) {
        !weight_maps(&down.s_whole, &down.s_edge, a.s_down, a.hidden, a.shared_inter, p.rows3)))
     return cudaErrorInvalidValue;
   const int rows = a.experts + (p.a.s_gate ? 1 : 0);
-  if ((e = cudaFuncSetAttribute(moe_router_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRouterSmem)) !=
-      cudaSuccess)
+  const int nt = a.tokens == 1 ? 1 : 8;   // eight tokens share an expert's row
+  const auto router = nt == 1 ? moe_router_kernel<1> : moe_router_kernel<8>;
+  if ((e = cudaFuncSetAttribute(router, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRouterSmem)) != cudaSuccess)
     return e;
-  moe_router_kernel<<<dim3((rows + 7) / 8, (a.tokens + 7) / 8), 32 * kRouterWarps, kRouterSmem, stream>>>(p);
+  router<<<dim3((rows + 7) / 8, (a.tokens + nt - 1) / nt), 32 * kRouterWarps, kRouterSmem, stream>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  const auto choice = a.experts <= 256 ? moe_choice_kernel<8> : a.experts <= 512 ? moe_choice_kernel<16> : moe_choice_kernel<32>;
-  if ((e = launch_early(choice, dim3(1), kChoiceThreads, 0, stream, p)) != cudaSuccess) return e;
+  if ((e = launch_early(moe_choice_kernel, dim3(a.tokens), kChoiceThreads, 0, stream, p)) != cudaSuccess) return e;
   if (a.tokens <= 8) return launch_products<1>(up, down, p, sms, stream);
   if (a.tokens <= 16) return launch_products<2>(up, down, p, sms, stream);
   if (a.tokens <= 32) return launch_products<4>(up, down, p, sms, stream);
