@@ -26,9 +26,9 @@
 //            experts add up in registers without atomics or partial results;
 //            columns are tokens by their number, a group of 8 that an expert does
 //            not serve is skipped; the CTA's warps deal out the chunks.
-// In the last two every warp feeds itself: it has three stages of 4 KB (16 rows x
+// In the last two every warp feeds itself: it has two stages of 4 KB (16 rows x
 // 128 columns, by TMA, 128-byte swizzle) and refills a stage once it has
-// multiplied it, so 12 warps keep some 100 KB on their way and no warp waits for
+// multiplied it, so 16 warps keep some 100 KB on their way and no warp waits for
 // another's data.  The shared expert's weights load before the choice is made,
 // and a CTA's first down weights before the last gate rows of others are done.
 // (Measured on the way: stages multiplied by 8 or 16 warps together cost the
@@ -53,10 +53,10 @@
 namespace gdn {
 namespace {
 
-constexpr int kTeam = 4, kTeams = 3, kMoeWarps = kTeam * kTeams, kMoeThreads = 32 * kMoeWarps;
+constexpr int kTeam = 4, kTeams = 4, kMoeWarps = kTeam * kTeams, kMoeThreads = 32 * kMoeWarps;
 constexpr int kCols = 128;                            // weight columns of a stage
 constexpr uint32_t kStage = 16 * kCols * 2;
-constexpr int kStages = 3;                            // of each warp
+constexpr int kStages = 2;                            // of each warp
 constexpr uint32_t kRing = kMoeWarps * kStages * kStage;
 constexpr int kMaxExperts = 1024, kMaxPairs = GDN_MOE_MAX_TOKENS * 32;
 constexpr int kRouterCols = 2048, kRouterWarps = 8;
@@ -535,10 +535,12 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
     float acc[NG][4];
 #pragma unroll
     for (int n = 0; n < NG; ++n) {
+      if (n > 0 && 8 * n >= cnt) continue;
       const int c = min(8 * n + g, cnt - 1);   // columns past the expert's tokens repeat the last: never written
       x[n] = a.x + (size_t)(shared ? c : (int)L.pair_t[col0 + c]) * a.hidden + t4 * 8;
-      acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.0f;
     }
+#pragma unroll
+    for (int n = 0; n < NG; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.0f;
     uint4 b[4];                  // a chunk's activations, asked for one chunk ahead
     const auto load_x = [&](int k) {
       if (k + kCols <= a.hidden) {
@@ -639,8 +641,8 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
   make_lists<false>(p, L);
   const int i_chunks = (a.inter + kCols - 1) / kCols, s_chunks = (a.shared_inter + kCols - 1) / kCols;
 
-  // A team takes every third expert, its four warps every fourth chunk; of the shared
-  // expert a warp takes every twelfth chunk.  A CTA begins with its own one of the
+  // A team takes every fourth expert, its four warps every fourth chunk; of the shared
+  // expert a warp takes every sixteenth chunk.  A CTA begins with its own one of the
   // experts, so that the CTAs do not all read the same activations at once.  All
   // this hangs on the experts', the chunks' and the CTA's numbers alone.
   const int team = warp / kTeam, member = warp % kTeam, n_team = L.n_team[team];
@@ -761,11 +763,10 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
   };
   ask();
   for (int i = cta; i < p.tiles3; i += grid) {
-    float acc[NG][4], low[NG][4];
+    float acc[NG][4];
 #pragma unroll
     for (int n = 0; n < NG; ++n) {
       acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.0f;
-      low[n][0] = low[n][1] = low[n][2] = low[n][3] = 0.0f;
     }
     while (qi[0] == i) {
       const int j = qj[0], c = qc[0], cols = j < 0 ? a.shared_inter : a.inter;
@@ -781,7 +782,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
         for (int h = 0; h < 2; ++h)
           if (c * kCols + 64 * h < cols) {
             mma_block(acc[n], f[h], hi + 2 * h);
-            mma_block(low[n], f[h], lo + 2 * h);
+            mma_block(acc[n], f[h], lo + 2 * h);
           }
       }
       __syncwarp();
@@ -803,8 +804,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
 #pragma unroll
     for (int n = 0; n < NG; ++n) {
       if (8 * n >= a.tokens) break;
-      sm->red[flip][warp][lane] =
-          make_float4(acc[n][0] + low[n][0], acc[n][1] + low[n][1], acc[n][2] + low[n][2], acc[n][3] + low[n][3]);
+      sm->red[flip][warp][lane] = make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
       __syncthreads();
       const int r = tid & 15, t = 8 * n + (tid >> 4), h = i * p.rows3 + r;
       if (tid < 128 && t < a.tokens && r < p.rows3 && h < a.hidden) {
