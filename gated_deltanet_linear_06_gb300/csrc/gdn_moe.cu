@@ -23,9 +23,11 @@
 //            in one thread; columns are the expert's own tokens; four warps share
 //            a tile, each with every fourth chunk of 128 weight columns.
 //   down     up to 16 output rows per CTA for ALL experts, so that a token's
-//            experts add up in registers without atomics or partial results;
-//            columns are tokens by their number, a group of 8 that an expert does
-//            not serve is skipped; the CTA's warps deal out the chunks.
+//            experts add up on the SM without atomics or partial results: columns
+//            are the expert's own tokens, a chunk's product is added to the warp's
+//            own [token][row] sums in shared memory, and the warps' sums meet at
+//            the end.  (With all tokens as columns and the sums in registers, 64
+//            tokens took 40 % more instructions, and the instructions bound it.)
 // In the last two every warp feeds itself: it has two stages of 4 KB (16 rows x
 // 128 columns, by TMA, 128-byte swizzle) and refills a stage once it has
 // multiplied it, so 16 warps keep some 100 KB on their way and no warp waits for
@@ -73,16 +75,17 @@ struct Choice {
 // The active experts, ascending, and their tokens: each CTA of the products makes
 // them for itself.
 struct Lists {
-  int n_active;
+  int n_active, n_team[kTeams];
   int scan_a[kMoeWarps], scan_p[kMoeWarps];
   uint32_t mask[kMaxExperts][2];       // tokens, first of an expert, then of an active one
   uint16_t expert[kMaxExperts];        // active experts
   uint16_t base[kMaxExperts + 8];      // their first pairs
   uint16_t rank[kMaxExperts];          // expert -> its place among the active
-  uint16_t of_team[kTeams][kMaxExperts];   // places of the active experts e = team (mod kTeams)
-  int n_team[kTeams];
   uint8_t pair_t[kMaxPairs];           // tokens of the (expert, token) pairs
-  float pair_w[kMaxPairs];             // and their weights
+  union {
+    float pair_w[kMaxPairs];                 // gate_up: and their weights
+    uint16_t of_team[kTeams][kMaxExperts];   // down: places of the active experts e = team (mod kTeams)
+  };
 };
 
 struct MoeMaps {
@@ -299,9 +302,8 @@ __global__ void __launch_bounds__(kChoiceThreads) moe_choice_kernel(const MoePar
 
 // ---- products ----
 
-// The lists, by all threads of a CTA: `pairs` with the pairs' tokens and weights,
-// else with the teams' experts.
-template <bool pairs>
+// The lists, by all threads of a CTA, with the pairs' weights or the teams' experts.
+template <bool weights>
 __device__ __forceinline__ void make_lists(const MoeParams& p, Lists& L) {
   const MoeArgs& a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, n = a.tokens * a.top_k;
@@ -360,14 +362,13 @@ __device__ __forceinline__ void make_lists(const MoeParams& p, Lists& L) {
     L.base[ia] = (uint16_t)ip;
   }
   __syncthreads();
-  if (pairs) {
-    for (int i = tid; i < n; i += kMoeThreads) {
-      const int t = i / a.top_k, j = L.rank[__ldcg(&p.choice->expert[i])];
-      const int at = L.base[j] + below(L.mask[j][0], L.mask[j][1], t);
-      L.pair_w[at] = __ldcg(&p.choice->weight[i]);
-      L.pair_t[at] = (uint8_t)t;
-    }
-  } else if (warp < kTeams) {
+  for (int i = tid; i < n; i += kMoeThreads) {
+    const int t = i / a.top_k, j = L.rank[__ldcg(&p.choice->expert[i])];
+    const int at = L.base[j] + below(L.mask[j][0], L.mask[j][1], t);
+    if (weights) L.pair_w[at] = __ldcg(&p.choice->weight[i]);
+    L.pair_t[at] = (uint8_t)t;
+  }
+  if (!weights && warp < kTeams) {
     int n_mine = 0;
     for (int j = lane; j - lane < L.n_active; j += 32) {
       const bool in = j < L.n_active && L.expert[j] % kTeams == warp;
@@ -452,11 +453,15 @@ __device__ __forceinline__ void load_a(Frag& f, const uint8_t* stage, int line, 
 
 struct ProductSmem {
   uint64_t full[kMoeWarps][kStages];
-  float4 red[2][kMoeWarps][32];
   Lists lists;
+  float4 red[2][kMoeWarps][32];        // gate_up; in its place down's sums
 };
-constexpr uint32_t kProductSmem = kRing + sizeof(ProductSmem) + 1024;
-static_assert(kProductSmem <= 227 * 1024, "shared memory");
+constexpr uint32_t kGateUpSmem = kRing + sizeof(ProductSmem) + 1024;
+constexpr int kSumRow = 17;            // a token's 16 sums, and one to spread the banks
+constexpr uint32_t down_smem(int tokens) {
+  return kRing + offsetof(ProductSmem, red) + kMoeWarps * tokens * kSumRow * 4 + 1024;
+}
+static_assert(kGateUpSmem <= 227 * 1024 && down_smem(GDN_MOE_MAX_TOKENS) <= 227 * 1024, "shared memory");
 
 template <int NG>   // groups of 8 tokens
 __global__ void __launch_bounds__(kMoeThreads, 1)
@@ -620,7 +625,6 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
   }
 }
 
-template <int NG>
 __global__ void __launch_bounds__(kMoeThreads, 1)
     moe_down_kernel(const __grid_constant__ MoeMaps maps, const __grid_constant__ MoeParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -708,26 +712,16 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
   wait_before();   // the activations
 
   const int g = lane >> 2, t4 = lane & 3;
-  int cs = 0, flip = 0;
+  int cs = 0;
   uint32_t ph = 0;
   bool ok = true;   // after a wait that gave up no later one waits
-  // the tokens of an expert, and this lane's row of the activations for one of them
-  const auto members_of = [&](int j, uint32_t& m0, uint32_t& m1) {
-    if (j < 0) {
-      m0 = a.tokens < 32 ? (1u << a.tokens) - 1u : 0xffffffffu;
-      m1 = a.tokens <= 32 ? 0u : (a.tokens < 64 ? (1u << (a.tokens - 32)) - 1u : 0xffffffffu);
-    } else {
-      m0 = L.mask[j][0];
-      m1 = L.mask[j][1];
-    }
-  };
+  // Columns 8 n .. of an expert (pairs base + 8 n ..): this lane's activations.
   const int np = a.tokens * a.top_k;
-  const auto load_act = [&](uint4* hi, uint4* lo, int j, int c, uint32_t m0, uint32_t m1, int n) {
+  const auto load_act = [&](uint4* hi, uint4* lo, int j, int c, int n) {
     const bool shared = j < 0;
     const int cols = shared ? a.shared_inter : a.inter, zero = shared ? a.tokens : np;   // the row of zeros
-    const int k = c * kCols + t4 * 8, t = 8 * n + g;
-    const bool use = (n < 4 ? m0 >> t : m1 >> (t - 32)) & 1;
-    const int at = use ? (shared ? t : L.base[j] + below(m0, m1, t)) : zero;
+    const int k = c * kCols + t4 * 8, base = shared ? 0 : L.base[j], cnt = (shared ? a.tokens : L.base[j + 1]) - base;
+    const int at = 8 * n + g < cnt ? base + 8 * n + g : zero;
     const uint16_t* row = (shared ? p.s_act : p.act) + ((size_t)at * cols + k);
     const uint16_t* row_lo = row + (size_t)(zero + 1) * cols;
     if ((c + 1) * kCols <= cols) {
@@ -747,43 +741,41 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
       }
     }
   };
-  const auto first_group = [](uint32_t m0, uint32_t m1) { return m0 ? (__ffs(m0) - 1) >> 3 : 4 + ((__ffs(m1) - 1) >> 3); };
-  // a chunk's first group's activations, asked for one chunk ahead
-  uint4 hi[4], lo[4];
-  uint32_t m0 = 0, m1 = 0;
-  int first = 0;
-  const auto ask = [&]() {
-    if (qi[0] == kEnd) return;
-    members_of(qj[0], m0, m1);
-    first = NG == 1 ? 0 : first_group(m0, m1);
-    // (unrolled over the groups so that each load's shifts are constants)
-#pragma unroll
-    for (int n = 0; n < NG; ++n)
-      if (n == first) load_act(hi, lo, qj[0], qc[0], m0, m1, n);
-  };
-  ask();
+  float* const sums = reinterpret_cast<float*>(sm->red);
+  float* const mine = sums + warp * a.tokens * kSumRow;
+  uint4 hi[4], lo[4];            // of the first 8 columns, asked for one chunk ahead
+  if (qi[0] != kEnd) load_act(hi, lo, qj[0], qc[0], 0);
   for (int i = cta; i < p.tiles3; i += grid) {
-    float acc[NG][4];
-#pragma unroll
-    for (int n = 0; n < NG; ++n) {
-      acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.0f;
-    }
+    for (int k = lane; k < a.tokens * kSumRow; k += 32) mine[k] = 0.0f;
+    __syncwarp();
     while (qi[0] == i) {
-      const int j = qj[0], c = qc[0], cols = j < 0 ? a.shared_inter : a.inter;
+      const int j = qj[0], c = qc[0];
+      const bool shared = j < 0;
+      const int cols = shared ? a.shared_inter : a.inter, base = shared ? 0 : L.base[j];
+      const int cnt = (shared ? a.tokens : L.base[j + 1]) - base;
       ok = ok && moe_wait(a, &full[cs], ph);
       Frag f[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) load_a(f[h], ring + cs * kStage, h * p.rows3 + g, 1024, t4);
-#pragma unroll
-      for (int n = 0; n < NG; ++n) {
-        if (NG > 1 && ((n < 4 ? m0 >> (8 * n) : m1 >> (8 * n - 32)) & 0xffu) == 0) continue;
-        if (n != first) load_act(hi, lo, j, c, m0, m1, n);
+      for (int n = 0; 8 * n < cnt; ++n) {
+        if (n > 0) load_act(hi, lo, j, c, n);
+        float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f}, low[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int h = 0; h < 2; ++h)
           if (c * kCols + 64 * h < cols) {
-            mma_block(acc[n], f[h], hi + 2 * h);
-            mma_block(acc[n], f[h], lo + 2 * h);
+            mma_block(acc, f[h], hi + 2 * h);
+            mma_block(low, f[h], lo + 2 * h);
           }
+        // lane (g, t4) holds rows g, g + 8 of columns 2 t4, 2 t4 + 1
+#pragma unroll
+        for (int o = 0; o < 2; ++o) {
+          const int col = 8 * n + 2 * t4 + o;
+          if (col < cnt) {
+            float* y = mine + (shared ? col : (int)L.pair_t[base + col]) * kSumRow + g;
+            y[0] += acc[o] + low[o];
+            y[8] += acc[2 + o] + low[2 + o];
+          }
+        }
       }
       __syncwarp();
       if (++cs == kStages) {
@@ -798,31 +790,24 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
       }
       qi[kStages - 1] = kEnd;
       --queued;
-      ask();
+      if (qi[0] != kEnd) load_act(hi, lo, qj[0], qc[0], 0);
       fill();                    // while the activations are on their way
     }
-#pragma unroll
-    for (int n = 0; n < NG; ++n) {
-      if (8 * n >= a.tokens) break;
-      sm->red[flip][warp][lane] = make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
-      __syncthreads();
-      const int r = tid & 15, t = 8 * n + (tid >> 4), h = i * p.rows3 + r;
-      if (tid < 128 && t < a.tokens && r < p.rows3 && h < a.hidden) {
-        const int at_lane = (r & 7) * 4 + ((t & 7) >> 1);
+    __syncthreads();
+    for (int k = tid; k < a.tokens * 16; k += kMoeThreads) {
+      const int r = k & 15, t = k >> 4, h = i * p.rows3 + r;
+      if (r < p.rows3 && h < a.hidden) {
         float v = 0.0f;
 #pragma unroll
-        for (int q = 0; q < kMoeWarps; ++q) {
-          const float4 u = sm->red[flip][q][at_lane];
-          v += r < 8 ? (t & 1 ? u.y : u.x) : (t & 1 ? u.w : u.z);
-        }
+        for (int q = 0; q < kMoeWarps; ++q) v += sums[(q * a.tokens + t) * kSumRow + r];
         const size_t at = (size_t)t * a.hidden + h;
         if (a.out_f32)
           static_cast<float*>(a.y)[at] = v;
         else
           static_cast<uint16_t*>(a.y)[at] = f32_to_bf16(v);
       }
-      flip ^= 1;
     }
+    __syncthreads();
   }
 }
 
@@ -888,9 +873,10 @@ cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, int threads, uint
 
 template <int NG>
 cudaError_t launch_products(const MoeMaps& up, const MoeMaps& down, const MoeParams& p, int sms, cudaStream_t stream) {
-  cudaError_t e = launch_early(moe_gate_up_kernel<NG>, dim3(sms), kMoeThreads, kProductSmem, stream, up, p);
+  cudaError_t e = launch_early(moe_gate_up_kernel<NG>, dim3(sms), kMoeThreads, kGateUpSmem, stream, up, p);
   if (e != cudaSuccess) return e;
-  return launch_early(moe_down_kernel<NG>, dim3(p.tiles3 < sms ? p.tiles3 : sms), kMoeThreads, kProductSmem, stream, down, p);
+  return launch_early(moe_down_kernel, dim3(p.tiles3 < sms ? p.tiles3 : sms), kMoeThreads, down_smem(p.a.tokens), stream,
+                      down, p);
 }
 
 }  // namespace
