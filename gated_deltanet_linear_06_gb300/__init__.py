@@ -196,8 +196,8 @@ def gdn_prefill_segment_tokens_for(dims: Dims, n_seqs: int, total_tokens: int, s
 
 
 def _stream(stream) -> int | None:
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:                 # the current stream's handle, without a Stream object
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
 

@@ -419,23 +419,27 @@ __device__ __forceinline__ void mma_block(float (&c)[4], const Frag& f, const ui
 }
 
 // A warp's stage: chunk c of `rows` rows from y0 on (and of as many from y1 on,
-// when y1 >= 0); K columns in all.  Whole blocks of 64 columns come in one box; a
-// chunk that holds the row's ragged end takes a box per block, the last of which
-// TMA fills with zeros.  By one lane.
-__device__ __noinline__ void load_stage(uint32_t dst, uint64_t* full, const CUtensorMap* whole, const CUtensorMap* edge,
-                                        int K, int c, int rows, int y0, int y1) {
-  const int c0 = c * kCols, parts = y1 >= 0 ? 2 : 1;
-  if ((K & 63) == 0 || c0 + kCols <= (K & ~63)) {
-    mbar_expect_tx(full, (uint32_t)(parts * rows * kCols * 2));
-    tma3(dst, whole, 0, y0, c0 >> 6, full);
-    if (y1 >= 0) tma3(dst + kStage / 2, whole, 0, y1, c0 >> 6, full);
+// when y1 >= 0); K columns in all.  By one lane.  Whole blocks of 64 columns come
+// in one box; a chunk that holds the row's ragged end takes a box per block, the
+// last of which TMA fills with zeros.
+__device__ __noinline__ void load_ragged(uint32_t dst, uint64_t* full, const CUtensorMap* edge, int K, int c, int rows,
+                                         int y0, int y1) {
+  const int c0 = c * kCols, parts = y1 >= 0 ? 2 : 1, nb = min((K - c0 + 63) >> 6, 2);
+  mbar_expect_tx(full, (uint32_t)(parts * rows * nb * 128));
+  for (int b = 0; b < nb; ++b) {
+    tma2(dst + b * rows * 128, edge, c0 + b * 64, y0, full);
+    if (y1 >= 0) tma2(dst + kStage / 2 + b * rows * 128, edge, c0 + b * 64, y1, full);
+  }
+}
+template <bool two>
+__device__ __forceinline__ void load_stage(uint32_t dst, uint64_t* full, const CUtensorMap* whole,
+                                           const CUtensorMap* edge, int K, int c, int rows, int y0, int y1) {
+  if ((K & 63) == 0 || (c + 1) * kCols <= (K & ~63)) {
+    mbar_expect_tx(full, (uint32_t)((two ? 2 : 1) * rows * kCols * 2));
+    tma3(dst, whole, 0, y0, c * (kCols / 64), full);
+    if (two) tma3(dst + kStage / 2, whole, 0, y1, c * (kCols / 64), full);
   } else {
-    const int nb = min((K - c0 + 63) >> 6, 2);
-    mbar_expect_tx(full, (uint32_t)(parts * rows * nb * 128));
-    for (int b = 0; b < nb; ++b) {
-      tma2(dst + b * rows * 128, edge, c0 + b * 64, y0, full);
-      if (y1 >= 0) tma2(dst + kStage / 2 + b * rows * 128, edge, c0 + b * 64, y1, full);
-    }
+    load_ragged(dst, full, edge, K, c, rows, y0, two ? y1 : -1);
   }
 }
 
@@ -490,7 +494,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
     while (free_stages > 0 && li < n_tiles) {
       const bool shared = li < s_tiles;
       if (lane == 0)
-        load_stage(ring_a + ls * kStage, &full[ls], shared ? &maps.s_whole : &maps.whole,
+        load_stage<true>(ring_a + ls * kStage, &full[ls], shared ? &maps.s_whole : &maps.whole,
                    shared ? &maps.s_edge : &maps.edge, a.hidden, lc, 8, ly, ly + (shared ? a.shared_inter : a.inter));
       __syncwarp();
       --free_stages;
@@ -563,22 +567,33 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
       const int k = c * kCols, left = a.hidden - k - t4 * 8;
       fill();                    // the stage before's place, while these are on their way
       ok = ok && moe_wait(a, &full[cs], ph);
+      Frag f[2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (k + 64 * h >= a.hidden) break;
-        Frag f;
-        load_a(f, ring + cs * kStage, h * 8 + g, kStage / 2, t4);
-        mma_block(acc[0], f, b + 2 * h);
+      for (int h = 0; h < 2; ++h) load_a(f[h], ring + cs * kStage, h * 8 + g, kStage / 2, t4);
 #pragma unroll
-        for (int n = 1; n < NG; ++n)
-          if (8 * n < cnt) {
-            uint4 bm[2];
+      for (int n = 0; n < NG; ++n) {
+        if (n > 0 && 8 * n >= cnt) break;
+        // the next group's activations are asked for before this one's products while
+        // there are registers, after them with eight groups
+        uint4 bm[4];
+        const auto load_group = [&](uint4* to) {
+          if (n + 1 < NG && 8 * (n + 1) < cnt) {
 #pragma unroll
-            for (int q = 0; q < 2; ++q)
-              bm[q] = 64 * h + 32 * q < left ? *reinterpret_cast<const uint4*>(x[n] + k + 64 * h + 32 * q)
-                                             : make_uint4(0, 0, 0, 0);
-            mma_block(acc[n], f, bm);
+            for (int q = 0; q < 4; ++q)
+              to[q] = 32 * q < left ? *reinterpret_cast<const uint4*>(x[n + 1 < NG ? n + 1 : 0] + k + 32 * q)
+                                    : make_uint4(0, 0, 0, 0);
           }
+        };
+        if (NG <= 4) load_group(bm);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (k + 64 * h < a.hidden) mma_block(acc[n], f[h], b + 2 * h);
+        if (NG <= 4) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) b[q] = bm[q];
+        } else {
+          load_group(b);
+        }
       }
       load_x(k + kTeam * kCols);
       __syncwarp();
@@ -691,7 +706,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
     while (queued < kStages && l.i < p.tiles3) {
       const bool shared = l.j < 0;
       if (lane == 0)
-        load_stage(ring_a + ls * kStage, &full[ls], shared ? &maps.s_whole : &maps.whole,
+        load_stage<false>(ring_a + ls * kStage, &full[ls], shared ? &maps.s_whole : &maps.whole,
                    shared ? &maps.s_edge : &maps.edge, shared ? a.shared_inter : a.inter, l.c, p.rows3,
                    (shared ? 0 : L.expert[l.j] * a.hidden) + l.i * p.rows3, -1);
       __syncwarp();
@@ -759,12 +774,13 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
       for (int h = 0; h < 2; ++h) load_a(f[h], ring + cs * kStage, h * p.rows3 + g, 1024, t4);
       for (int n = 0; 8 * n < cnt; ++n) {
         if (n > 0) load_act(hi, lo, j, c, n);
-        float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f}, low[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        // four chains: a product's latency is 38 clocks
+        float acc[2][4] = {}, low[2][4] = {};
 #pragma unroll
         for (int h = 0; h < 2; ++h)
           if (c * kCols + 64 * h < cols) {
-            mma_block(acc, f[h], hi + 2 * h);
-            mma_block(low, f[h], lo + 2 * h);
+            mma_block(acc[h], f[h], hi + 2 * h);
+            mma_block(low[h], f[h], lo + 2 * h);
           }
         // lane (g, t4) holds rows g, g + 8 of columns 2 t4, 2 t4 + 1
 #pragma unroll
@@ -772,8 +788,8 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
           const int col = 8 * n + 2 * t4 + o;
           if (col < cnt) {
             float* y = mine + (shared ? col : (int)L.pair_t[base + col]) * kSumRow + g;
-            y[0] += acc[o] + low[o];
-            y[8] += acc[2 + o] + low[2 + o];
+            y[0] += (acc[0][o] + acc[1][o]) + (low[0][o] + low[1][o]);
+            y[8] += (acc[0][2 + o] + acc[1][2 + o]) + (low[0][2 + o] + low[1][2 + o]);
           }
         }
       }
