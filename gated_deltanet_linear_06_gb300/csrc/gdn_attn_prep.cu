@@ -88,6 +88,12 @@ __global__ void __launch_bounds__(kPrepWarps * 32, 3)
     w.hi = min(rows, w.r + sh.per_item);
   };
   const auto load = [&](uint4 (&raw)[kPrepBatch], const Place& w) {
+    if (w.r + STEP <= sh.nq && w.r + STEP <= w.hi) {   // query heads only: most batches
+      const uint16_t* src = p.q + w.t * p.q_st + (w.r + sub) * p.q_sh + 8 * l;
+#pragma unroll
+      for (int u = 0; u < kPrepBatch; ++u) raw[u] = *reinterpret_cast<const uint4*>(src + u * RPW * p.q_sh);
+      return;
+    }
 #pragma unroll
     for (int u = 0; u < kPrepBatch; ++u) {
       const int r = w.r + u * RPW + sub;
@@ -154,14 +160,11 @@ __global__ void __launch_bounds__(kPrepWarps * 32, 3)
         s[i] = sign * sv.x, s[i + 1] = sign * sv.y, s[i + 2] = sign * sv.z, s[i + 3] = sign * sv.w;
       }
     }
-#pragma unroll
-    for (int u = 0; u < kPrepBatch; ++u) {
-      if (now.r + u * RPW >= now.hi) break;   // the whole warp
-      const int r = now.r + u * RPW + sub;
-      const bool is_q = r < sh.nq, is_v = r >= sh.nq + sh.nk;
+    // one row: its norm with weights `nw` (null: none) and its rotation
+    const auto turn_row = [&](const uint4& in, bool norm, const float* nw) -> uint4 {
       float y[8];
       {
-        const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+        const uint32_t w[4] = {in.x, in.y, in.z, in.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           y[2 * i] = __uint_as_float(w[i] << 16);
@@ -173,10 +176,10 @@ __global__ void __launch_bounds__(kPrepWarps * 32, 3)
       for (int i = 0; i < 8; ++i) ss = fmaf(y[i], y[i], ss);
 #pragma unroll
       for (int m = LPR / 2; m >= 1; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
-      if (is_q ? p.q_w != nullptr : p.k_w != nullptr) {
+      if (norm) {
         const float inv = rsqrtf(ss * (1.0f / D) + p.eps);
-        const float4 w0 = *reinterpret_cast<const float4*>(&norm_w[is_q ? 0 : 1][8 * l]);
-        const float4 w1 = *reinterpret_cast<const float4*>(&norm_w[is_q ? 0 : 1][8 * l + 4]);
+        const float4 w0 = *reinterpret_cast<const float4*>(nw + 8 * l);
+        const float4 w1 = *reinterpret_cast<const float4*>(nw + 8 * l + 4);
         const float w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
         for (int i = 0; i < 8; ++i) y[i] = y[i] * inv * w[i];
@@ -200,20 +203,33 @@ __global__ void __launch_bounds__(kPrepWarps * 32, 3)
           }
         }
       }
-      if (r < now.hi) {
+      return make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
+                        pack_bf16x2(y[6], y[7]));
+    };
+    if (now.r + STEP <= sh.nq && now.r + STEP <= now.hi) {   // query heads only
+      uint16_t* out = p.q_out + (now.t * sh.nq + now.r + sub) * D + 8 * l;
+#pragma unroll
+      for (int u = 0; u < kPrepBatch; ++u)
+        *reinterpret_cast<uint4*>(out + u * RPW * D) = turn_row(raw[u], p.q_w != nullptr, norm_w[0]);
+    } else {
+#pragma unroll
+      for (int u = 0; u < kPrepBatch; ++u) {
+        if (now.r + u * RPW >= now.hi) break;   // the whole warp
+        const int r = now.r + u * RPW + sub;
+        const bool is_q = r < sh.nq, is_v = r >= sh.nq + sh.nk;
         uint4 o = raw[u];
-        if (!is_v) {
-          o.x = pack_bf16x2(y[0], y[1]);
-          o.y = pack_bf16x2(y[2], y[3]);
-          o.z = pack_bf16x2(y[4], y[5]);
-          o.w = pack_bf16x2(y[6], y[7]);
+        if (now.r + u * RPW < sh.nq + sh.nk) {  // (values alone: the whole warp)
+          const uint4 y = turn_row(raw[u], is_q ? p.q_w != nullptr : p.k_w != nullptr, norm_w[is_q ? 0 : 1]);
+          if (!is_v) o = y;
         }
-        if (is_q) {
-          *reinterpret_cast<uint4*>(p.q_out + (now.t * sh.nq + r) * D + 8 * l) = o;
-        } else if (dst >= 0) {
-          const int h = r - sh.nq - (is_v ? sh.nk : 0);
-          uint16_t* cache = is_v ? p.v_cache : p.k_cache;
-          *reinterpret_cast<uint4*>(cache + (dst * p.h_kv + h) * D + 8 * l) = o;
+        if (r < now.hi) {
+          if (is_q) {
+            *reinterpret_cast<uint4*>(p.q_out + (now.t * sh.nq + r) * D + 8 * l) = o;
+          } else if (dst >= 0) {
+            const int h = r - sh.nq - (is_v ? sh.nk : 0);
+            uint16_t* cache = is_v ? p.v_cache : p.k_cache;
+            *reinterpret_cast<uint4*>(cache + (dst * p.h_kv + h) * D + 8 * l) = o;
+          }
         }
       }
     }
