@@ -40,9 +40,11 @@
 // Which warp adds what depends on the expert's and the chunk's numbers alone, so
 // nothing in a token's arithmetic depends on the other tokens.
 //
-// The activations between the products are kept as two bf16 (16 bits of
-// significand): one bf16 would cost 2^-9 of each, more than the fp32 output
-// holds; the second product on the low half costs tensor time, not bytes.
+// The activations between the products are kept as sums of bf16, because the
+// tensor cores take both operands in one 16-bit type: two (16 bits of
+// significand) for a bf16 output, where one would cost 2^-9 of each, and three
+// (24 bits) for an fp32 output.  The products on the low parts cost tensor time,
+// not bytes.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -96,8 +98,8 @@ struct MoeParams {
   MoeArgs a;
   float2* logit;        // [tokens][experts + 1], high and low part
   Choice* choice;
-  uint16_t* act;        // [hi, lo][pairs + 1][inter], the last row zeros
-  uint16_t* s_act;      // [hi, lo][tokens + 1][shared_inter], likewise
+  uint16_t* act;        // [part][pairs + 1][inter], the last row zeros; two parts, or three
+  uint16_t* s_act;      // [part][tokens + 1][shared_inter], likewise
   int rows3, tiles3;    // output rows per tile, tiles
 };
 
@@ -526,10 +528,11 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
   // the row of zeros after the last pair's, for tokens that an expert does not serve
   if (cta == grid - 1) {
     const int np = a.tokens * a.top_k;
-    for (int i = tid; i < 2 * a.inter; i += kMoeThreads)
-      p.act[(size_t)np * a.inter + i + (i >= a.inter ? (size_t)np * a.inter : 0)] = 0;
-    for (int i = tid; i < 2 * a.shared_inter; i += kMoeThreads)
-      p.s_act[(size_t)a.tokens * a.shared_inter + i + (i >= a.shared_inter ? (size_t)a.tokens * a.shared_inter : 0)] = 0;
+    for (int part = 0; part < (a.out_f32 ? 3 : 2); ++part) {
+      for (int i = tid; i < a.inter; i += kMoeThreads) p.act[((size_t)(part + 1) * (np + 1) - 1) * a.inter + i] = 0;
+      for (int i = tid; i < a.shared_inter; i += kMoeThreads)
+        p.s_act[((size_t)(part + 1) * (a.tokens + 1) - 1) * a.shared_inter + i] = 0;
+    }
   }
 
   const int g = lane >> 2, t4 = lane & 3;
@@ -630,8 +633,11 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
               const float v = silu(acc[n][o]) * acc[n][2 + o] * (shared ? __ldcg(&p.choice->shared_w[c]) : L.pair_w[col0 + c]);
               const uint16_t hi = f32_to_bf16(v);
               const size_t at = (size_t)(col0 + c) * cols + r0 + g;
+              const float rest = v - bf16_to_f32(hi);   // exact
+              const uint16_t lo = f32_to_bf16(rest);
               act[at] = hi;
-              act[plane + at] = f32_to_bf16(v - bf16_to_f32(hi));
+              act[plane + at] = lo;
+              if (a.out_f32) act[2 * plane + at] = f32_to_bf16(rest - bf16_to_f32(lo));
             }
           }
         }
@@ -640,6 +646,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
   }
 }
 
+template <int P>   // parts of an activation
 __global__ void __launch_bounds__(kMoeThreads, 1)
     moe_down_kernel(const __grid_constant__ MoeMaps maps, const __grid_constant__ MoeParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -732,34 +739,32 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
   bool ok = true;   // after a wait that gave up no later one waits
   // Columns 8 n .. of an expert (pairs base + 8 n ..): this lane's activations.
   const int np = a.tokens * a.top_k;
-  const auto load_act = [&](uint4* hi, uint4* lo, int j, int c, int n) {
+  const auto load_act = [&](uint4 (&x)[P][4], int j, int c, int n) {
     const bool shared = j < 0;
     const int cols = shared ? a.shared_inter : a.inter, zero = shared ? a.tokens : np;   // the row of zeros
     const int k = c * kCols + t4 * 8, base = shared ? 0 : L.base[j], cnt = (shared ? a.tokens : L.base[j + 1]) - base;
     const int at = 8 * n + g < cnt ? base + 8 * n + g : zero;
     const uint16_t* row = (shared ? p.s_act : p.act) + ((size_t)at * cols + k);
-    const uint16_t* row_lo = row + (size_t)(zero + 1) * cols;
+    const size_t plane = (size_t)(zero + 1) * cols;
     if ((c + 1) * kCols <= cols) {
 #pragma unroll
-      for (int h = 0; h < 4; ++h) {
-        hi[h] = __ldcg(reinterpret_cast<const uint4*>(row + 32 * h));
-        lo[h] = __ldcg(reinterpret_cast<const uint4*>(row_lo + 32 * h));
-      }
+      for (int part = 0; part < P; ++part)
+#pragma unroll
+        for (int h = 0; h < 4; ++h) x[part][h] = __ldcg(reinterpret_cast<const uint4*>(row + part * plane + 32 * h));
     } else {
 #pragma unroll
-      for (int h = 0; h < 4; ++h) {
-        hi[h] = lo[h] = make_uint4(0, 0, 0, 0);
-        if (k + 32 * h < cols) {
-          hi[h] = __ldcg(reinterpret_cast<const uint4*>(row + 32 * h));
-          lo[h] = __ldcg(reinterpret_cast<const uint4*>(row_lo + 32 * h));
+      for (int part = 0; part < P; ++part)
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          x[part][h] = make_uint4(0, 0, 0, 0);
+          if (k + 32 * h < cols) x[part][h] = __ldcg(reinterpret_cast<const uint4*>(row + part * plane + 32 * h));
         }
-      }
     }
   };
   float* const sums = reinterpret_cast<float*>(sm->red);
   float* const mine = sums + warp * a.tokens * kSumRow;
-  uint4 hi[4], lo[4];            // of the first 8 columns, asked for one chunk ahead
-  if (qi[0] != kEnd) load_act(hi, lo, qj[0], qc[0], 0);
+  uint4 x[P][4];                 // of the first 8 columns, asked for one chunk ahead
+  if (qi[0] != kEnd) load_act(x, qj[0], qc[0], 0);
   for (int i = cta; i < p.tiles3; i += grid) {
     for (int k = lane; k < a.tokens * kSumRow; k += 32) mine[k] = 0.0f;
     __syncwarp();
@@ -773,14 +778,15 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
 #pragma unroll
       for (int h = 0; h < 2; ++h) load_a(f[h], ring + cs * kStage, h * p.rows3 + g, 1024, t4);
       for (int n = 0; 8 * n < cnt; ++n) {
-        if (n > 0) load_act(hi, lo, j, c, n);
+        if (n > 0) load_act(x, j, c, n);
         // four chains: a product's latency is 38 clocks
         float acc[2][4] = {}, low[2][4] = {};
 #pragma unroll
         for (int h = 0; h < 2; ++h)
           if (c * kCols + 64 * h < cols) {
-            mma_block(acc[h], f[h], hi + 2 * h);
-            mma_block(low[h], f[h], lo + 2 * h);
+            mma_block(acc[h], f[h], x[0] + 2 * h);
+#pragma unroll
+            for (int part = 1; part < P; ++part) mma_block(low[h], f[h], x[part] + 2 * h);
           }
         // lane (g, t4) holds rows g, g + 8 of columns 2 t4, 2 t4 + 1
 #pragma unroll
@@ -806,7 +812,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
       }
       qi[kStages - 1] = kEnd;
       --queued;
-      if (qi[0] != kEnd) load_act(hi, lo, qj[0], qc[0], 0);
+      if (qi[0] != kEnd) load_act(x, qj[0], qc[0], 0);
       fill();                    // while the activations are on their way
     }
     __syncthreads();
@@ -891,7 +897,7 @@ template <int NG>
 cudaError_t launch_products(const MoeMaps& up, const MoeMaps& down, const MoeParams& p, int sms, cudaStream_t stream) {
   cudaError_t e = launch_early(moe_gate_up_kernel<NG>, dim3(sms), kMoeThreads, kGateUpSmem, stream, up, p);
   if (e != cudaSuccess) return e;
-  return launch_early(moe_down_kernel, dim3(p.tiles3 < sms ? p.tiles3 : sms), kMoeThreads, down_smem(p.a.tokens), stream,
+  return launch_early(p.a.out_f32 ? moe_down_kernel<3> : moe_down_kernel<2>, dim3(p.tiles3 < sms ? p.tiles3 : sms), kMoeThreads, down_smem(p.a.tokens), stream,
                       down, p);
 }
 
@@ -899,8 +905,8 @@ cudaError_t launch_products(const MoeMaps& up, const MoeMaps& down, const MoePar
 
 size_t moe_scratch_bytes(int tokens, int, int inter, int experts, int top_k, int shared_inter) {
   const size_t T = tokens > 0 ? tokens : 1;
-  return up256(sizeof(Choice)) + up256(T * (experts + 1) * 8) + up256((T * top_k + 1) * inter * 4) +
-         up256((T + 1) * shared_inter * 4);
+  return up256(sizeof(Choice)) + up256(T * (experts + 1) * 8) + up256((T * top_k + 1) * inter * 6) +
+         up256((T + 1) * shared_inter * 6);
 }
 
 cudaError_t launch_moe(const MoeArgs& a, cudaStream_t stream) {
@@ -918,7 +924,7 @@ cudaError_t launch_moe(const MoeArgs& a, cudaStream_t stream) {
   p.logit = reinterpret_cast<float2*>(ws);
   ws += up256(T * (a.experts + 1) * 8);
   p.act = reinterpret_cast<uint16_t*>(ws);
-  ws += up256((T * a.top_k + 1) * a.inter * 4);
+  ws += up256((T * a.top_k + 1) * a.inter * 6);
   p.s_act = reinterpret_cast<uint16_t*>(ws);
   // output rows: tiles of at most 16, as many as give every CTA the same number
   const int per = (a.hidden + 16 * sms - 1) / (16 * sms);

@@ -596,8 +596,9 @@ gdn_status gdn_attn_decode_shared(const gdn_attn_dims* dims, int page, long long
  * hidden, inter and shared_inter are multiples of 8, at most 16384; experts at
  * most 1024; top_k at most 32.  Router logits are summed so that they are exact
  * to about 48 bits; everything else is summed in fp32, the activations between
- * the two products are carried as pairs of bf16 (16 bits of significand).  A
- * token's result does not depend on the other tokens of the call, bit for bit.
+ * the two products are carried as sums of two bf16 (16 bits of significand) for a
+ * bf16 output and of three (24 bits) for an fp32 output.  A token's result does
+ * not depend on the other tokens of the call, bit for bit.
  */
 typedef struct gdn_moe_dims {
   int hidden;
