@@ -17,7 +17,7 @@
 
 namespace {
 
-constexpr int kVersion = 310;  // 0.3.1: the decode step from host buffers
+constexpr int kVersion = 400;  // 0.4.0: the attention layer's and the expert layer's operators
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -53,11 +53,11 @@ const char* gdn_status_string(gdn_status s) {
   switch (s) {
     case GDN_OK: return "GDN_OK";
     case GDN_ERR_INVALID_ARG: return "GDN_ERR_INVALID_ARG: null or misaligned pointer, bad size or inconsistent dims";
-    case GDN_ERR_UNSUPPORTED: return "GDN_ERR_UNSUPPORTED: dims outside the compiled fast path (d_k = d_v = 128, conv_w = 4, chunk = 64, h_v/h_k in {1,2,4}, h_k <= 64)";
-    case GDN_ERR_WORKSPACE: return "GDN_ERR_WORKSPACE: workspace missing or smaller than gdn_workspace_bytes()";
+    case GDN_ERR_UNSUPPORTED: return "GDN_ERR_UNSUPPORTED: dims outside the compiled fast path (d_k = d_v = 128, conv_w = 4, chunk = 64, h_v/h_k in {1,2,4}, h_k <= 64), or a limit that include/gdn.h states for the call";
+    case GDN_ERR_WORKSPACE: return "GDN_ERR_WORKSPACE: workspace missing, misaligned or smaller than the call's _workspace_bytes()";
     case GDN_ERR_CUDA: return "GDN_ERR_CUDA: a CUDA runtime call failed";
     case GDN_ERR_DEVICE_TIMEOUT: return "GDN_ERR_DEVICE_TIMEOUT: a bounded device-side wait gave up";
-    case GDN_ERR_DEVICE_BOUNDS: return "GDN_ERR_DEVICE_BOUNDS: cu_seqlens or a slot index out of range";
+    case GDN_ERR_DEVICE_BOUNDS: return "GDN_ERR_DEVICE_BOUNDS: cu_seqlens, a length, or a slot, page or axis index out of range";
   }
   return "unknown gdn_status";
 }

@@ -43,12 +43,15 @@
  *     a call's launches; the outputs and states are then undefined.
  *   - All device pointers must be 16-byte aligned.  Tensors are dense and
  *     row-major in the shapes given below.
+ *   - Some calls are several kernels, which may begin while the one before them in
+ *     the same call still runs; work enqueued before the call is complete when its
+ *     first kernel begins, and the call is when its last one ends.
  *   - Activations (qkv, z, a, b), conv weights and the prefill output are
  *     bf16 (raw uint16 bit patterns).  A_log, dt_bias, norm_w and both
  *     states are fp32.
- *   - The only dims compiled are d_k = d_v = 128, conv_w = 4, chunk = 64,
+ *   - The only gdn_dims compiled are d_k = d_v = 128, conv_w = 4, chunk = 64,
  *     h_v / h_k in {1, 2, 4}, h_k <= 64; anything else returns
- *     GDN_ERR_UNSUPPORTED.
+ *     GDN_ERR_UNSUPPORTED.  The attention and expert calls state their limits.
  *   - No exception crosses this boundary.
  */
 #ifndef GDN_H
@@ -64,11 +67,11 @@ extern "C" {
 typedef enum gdn_status {
   GDN_OK = 0,
   GDN_ERR_INVALID_ARG = 1,    /* null or misaligned pointer, bad size, inconsistent dims */
-  GDN_ERR_UNSUPPORTED = 2,    /* dims outside the compiled fast path */
-  GDN_ERR_WORKSPACE = 3,      /* workspace missing or smaller than gdn_workspace_bytes */
+  GDN_ERR_UNSUPPORTED = 2,    /* dims outside the compiled fast path, or a limit the call states */
+  GDN_ERR_WORKSPACE = 3,      /* workspace missing, misaligned or too small */
   GDN_ERR_CUDA = 4,           /* a CUDA runtime call failed (launch, attribute, copy) */
   GDN_ERR_DEVICE_TIMEOUT = 5, /* device word: a bounded device-side wait gave up */
-  GDN_ERR_DEVICE_BOUNDS = 6   /* device word: cu_seqlens or a slot index out of range */
+  GDN_ERR_DEVICE_BOUNDS = 6   /* device word: cu_seqlens, a length or an index out of range */
 } gdn_status;
 
 /* Layer dimensions.  d_k / d_v: key / value head size; conv_w: conv width;
