@@ -249,7 +249,8 @@ cudaError_t launch_d(const AttnPrepArgs& p, cudaStream_t stream, int sms) {
   const int rows = sh.nq + sh.nk + sh.nv;
   const int iters = (rows + RPW - 1) / RPW;   // warp iterations of a token
   // one token per warp when that gives every SM two rounds of 32 warps, else
-  // shares of its heads down to one row per lane group
+  // shares of its heads down to one row per lane group (choosing the share that
+  // fills whole rounds best made no difference at 2049 tokens: 16.4 us both)
   const long long want = (long long)sms * 64;
   long long per = (p.tokens * iters + want - 1) / want;
   if (per < 1) per = 1;

@@ -867,10 +867,10 @@ __global__ void __launch_bounds__(kJoinThreads) attn_shared_join(const __grid_co
   const int apart[2] = {256, pl.R};                        // slots are so many rows apart
   // launched while the first kernel runs; its results are there from here on
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int2 none = make_int2(0, -1);
+  const int2 none = make_int2(0, -1);   // no range
   const int2 pre = pl.np ? p.span[job[0]] : none;
   const int2 own = a.tail_width > 0 && a.tail_len[b] > 0 ? p.span[pl.np + job[1]] : none;
-  const int n_prefix = pre.y - pre.x + 1, n_ranges = n_prefix + own.y - own.x + 1;
+  const int n_prefix = pre.y - pre.x + 1;
   const long long first[2] = {(long long)(job[0] + pre.x) * 256 + (blk & 1) * 128,
                               (long long)(pl.np ? pl.np + pl.shares : 0) * 256 + (long long)(job[1] + own.x) * pl.R};
 
@@ -881,23 +881,49 @@ __global__ void __launch_bounds__(kJoinThreads) attn_shared_join(const __grid_co
     const int c4 = d0 + item / pl.G, g = item % pl.G;
     float M = -INFINITY, L = 0.0f;
     float4 o = make_float4(0, 0, 0, 0);
+    const int h = hk * pl.G + g;
+    uint2 gt = make_uint2(0, 0);
+    if (a.gate && threadIdx.x < width)   // on its way under the sums
+      gt = *reinterpret_cast<const uint2*>(a.gate + tok * a.gate_st + h * a.gate_sh + 4 * c4);
     if (grp < groups) {
-#pragma unroll 4
-      for (int i = grp; i < n_ranges; i += groups) {
-        const int k = i >= n_prefix;
-        const long long origin = (k ? first[1] : first[0]) + (long long)(k ? i - n_prefix : i) * (k ? apart[1] : apart[0]);
-        const int r = (k ? in[1] : in[0]) + g;
-        const float4 ml = p.ml[origin + r];
-        const float4 v = reinterpret_cast<const float4*>(p.opart)[origin * (D / 4) + (long long)c4 * (k ? stride[1] : stride[0]) + r];
-        const float mn = fmaxf(M, ml.x);
-        const float f = mn == -INFINITY ? 1.0f : ex2(M - mn), w = mn == -INFINITY ? 0.0f : ex2(ml.x - mn);
-        L = L * f + (ml.y + ml.z) * w;
-        o.x = o.x * f + v.x * w;
-        o.y = o.y * f + v.y * w;
-        o.z = o.z * f + v.z * w;
-        o.w = o.w * f + v.w * w;
-        M = mn;
-      }
+      // a job's ranges, four at a time: their loads are all in flight before the first
+      // is added
+      const auto join = [&](const float4* ml, const float4* v, int n, long long ml_step, long long v_step) {
+        for (int i = grp; i < n; i += 4 * groups) {
+          float4 mv[4], vv[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int r = i + u * groups;
+            mv[u] = r < n ? ml[r * ml_step] : make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
+            vv[u] = r < n ? v[r * v_step] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          }
+          float mn = M;
+#pragma unroll
+          for (int u = 0; u < 4; ++u) mn = fmaxf(mn, mv[u].x);
+          if (mn == -INFINITY) continue;   // rows that see nothing so far
+          const float f = ex2(M - mn);
+          L *= f;
+          o.x *= f;
+          o.y *= f;
+          o.z *= f;
+          o.w *= f;
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const float w = ex2(mv[u].x - mn);
+            L += (mv[u].y + mv[u].z) * w;
+            o.x += vv[u].x * w;
+            o.y += vv[u].y * w;
+            o.z += vv[u].z * w;
+            o.w += vv[u].w * w;
+          }
+          M = mn;
+        }
+      };
+      const float4* part = reinterpret_cast<const float4*>(p.opart);
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        join(p.ml + first[k] + in[k] + g, part + first[k] * (D / 4) + (long long)c4 * stride[k] + in[k] + g,
+             k ? own.y - own.x + 1 : n_prefix, apart[k], (long long)apart[k] * (D / 4));
     }
     acc[threadIdx.x] = o;
     stat[threadIdx.x] = make_float2(M, L);
@@ -919,9 +945,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_shared_join(const __grid_co
       // no key seen: zeros.  (A NaN sum stays NaN.)
       const float inv = L == 0.0f ? 0.0f : 1.0f / L;
       float r[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
-      const int h = hk * pl.G + g;
       if (a.gate) {
-        const uint2 gt = *reinterpret_cast<const uint2*>(a.gate + tok * a.gate_st + h * a.gate_sh + 4 * c4);
         r[0] *= sigmoid(__uint_as_float(gt.x << 16));
         r[1] *= sigmoid(__uint_as_float(gt.x & 0xffff0000u));
         r[2] *= sigmoid(__uint_as_float(gt.y << 16));

@@ -304,11 +304,43 @@ __global__ void __launch_bounds__(kChoiceThreads) moe_choice_kernel(const MoePar
 
 // ---- products ----
 
+// The teams' experts, a warp per team.
+__device__ __forceinline__ void team_lists(Lists& L, int warp, int lane) {
+  if (warp >= kTeams) return;
+  int n = 0;
+  for (int j = lane; j - lane < L.n_active; j += 32) {
+    const bool in = j < L.n_active && L.expert[j] % kTeams == warp;
+    const uint32_t b = __ballot_sync(0xffffffffu, in);
+    if (in) L.of_team[warp][n + __popc(b & ((1u << lane) - 1u))] = (uint16_t)j;
+    n += __popc(b);
+  }
+  if (lane == 0) L.n_team[warp] = n;
+}
+
 // The lists, by all threads of a CTA, with the pairs' weights or the teams' experts.
 template <bool weights>
 __device__ __forceinline__ void make_lists(const MoeParams& p, Lists& L) {
   const MoeArgs& a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, n = a.tokens * a.top_k;
+  if (a.tokens == 1) {   // the choice, sorted (1 us less than by the way of all experts)
+    if (tid < n) {
+      const int e = __ldcg(&p.choice->expert[tid]);
+      int r = 0;
+      for (int o = 0; o < n; ++o) r += __shfl_sync(__activemask(), e, o) < e;
+      L.expert[r] = (uint16_t)e;
+      L.base[r] = (uint16_t)r;
+      L.pair_t[r] = 0;
+      if (weights) L.pair_w[r] = __ldcg(&p.choice->weight[tid]);
+    }
+    if (tid == 0) {
+      L.n_active = n;
+      L.base[n] = (uint16_t)n;
+    }
+    __syncthreads();
+    if (!weights) team_lists(L, warp, lane);
+    __syncthreads();
+    return;
+  }
   for (int e = tid; e < a.experts; e += kMoeThreads) L.mask[e][0] = L.mask[e][1] = 0;
   __syncthreads();
   for (int i = tid; i < n; i += kMoeThreads) {
@@ -370,16 +402,7 @@ __device__ __forceinline__ void make_lists(const MoeParams& p, Lists& L) {
     if (weights) L.pair_w[at] = __ldcg(&p.choice->weight[i]);
     L.pair_t[at] = (uint8_t)t;
   }
-  if (!weights && warp < kTeams) {
-    int n_mine = 0;
-    for (int j = lane; j - lane < L.n_active; j += 32) {
-      const bool in = j < L.n_active && L.expert[j] % kTeams == warp;
-      const uint32_t b = __ballot_sync(0xffffffffu, in);
-      if (in) L.of_team[warp][n_mine + __popc(b & ((1u << lane) - 1u))] = (uint16_t)j;
-      n_mine += __popc(b);
-    }
-    if (lane == 0) L.n_team[warp] = n_mine;
-  }
+  if (!weights) team_lists(L, warp, lane);
   __syncthreads();
 }
 
