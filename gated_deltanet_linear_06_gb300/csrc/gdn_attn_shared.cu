@@ -486,19 +486,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int rsh = 31 - __clz(rpb), shift = 31 - __clz(a.page);
     bool ok = true, prev_whole = true;
     uint32_t loaded = 0, segs = 0;
-    // row of the cache where piece `lane` of c's tile begins
-    auto piece = [&](const Cursor& c) -> int {
-      const int row = c.t * kTile + (lane << rsh);
+    // the page where piece `lane` of c's tile lies, as the table has it: looked at only
+    // when the tile is loaded, so that nothing waits for the table
+    auto page_of = [&](const Cursor& c) -> int {
       if (!c.valid || (lane << rsh) >= c.count()) return 0;
       const int32_t* table = c.prefix ? a.prefix_pages : a.tail_pages + (size_t)c.mb * a.tail_width;
-      int pg = __ldg(table + (row >> shift));
+      return __ldg(table + ((c.t * kTile + (lane << rsh)) >> shift));
+    };
+    // the row of the cache where that piece begins
+    auto row_of = [&](const Cursor& c, int pg) -> int {
       if (pg < 0 || pg >= a.n_pages) {
         record_status(a.status, GDN_ERR_DEVICE_BOUNDS);
         pg = 0;
       }
-      return (int)(((long long)pg << shift) + (row & (a.page - 1)));
+      return (int)(((long long)pg << shift) + ((c.t * kTile + (lane << rsh)) & (a.page - 1)));
     };
-    int rows_n = piece(cn), rows_k = 0, rows_v = 0;
+    int page_n = page_of(cn), rows_k = 0, rows_v = 0;
     const auto tile_rows = [&](int n) { return ((n + rpb - 1) >> rsh) << rsh; };   // rows of its boxes
     auto load_k = [&]() {
       if (ck.first) {
@@ -565,15 +568,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // ck steps to the tile cn has looked up, cn to the one after
     auto advance = [&]() {
       rows_v = rows_k;
-      rows_k = rows_n;
+      rows_k = row_of(cn, page_n);
       ck = cn;
       cn.next(p);
-      rows_n = piece(cn);
+      page_n = page_of(cn);
     };
     if (ck.valid) {
-      rows_k = rows_n;
+      rows_k = row_of(cn, page_n);
       cn.next(p);
-      rows_n = piece(cn);
+      page_n = page_of(cn);
       load_k();
       while (ok && cv.valid) {
         advance();
