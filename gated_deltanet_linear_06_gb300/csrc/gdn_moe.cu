@@ -86,9 +86,22 @@ struct Lists {
   uint8_t pair_t[kMaxPairs];           // tokens of the (expert, token) pairs
   union {
     float pair_w[kMaxPairs];                 // gate_up: and their weights
-    uint16_t of_team[kTeams][kMaxExperts];   // down: places of the active experts e = team (mod kTeams)
+    uint32_t of_team[kTeams][kMaxExperts / kTeams];   // down: the active experts e = team (mod kTeams), as Entry
   };
 };
+
+// An expert and its pairs in one word: number, first pair, pairs.
+struct Entry {
+  static constexpr uint32_t kShared = 1u << 31;   // the shared expert: all tokens, in order
+  static __device__ __forceinline__ uint32_t of(int e, int base, int cnt) {
+    return (uint32_t)e | (uint32_t)base << 10 | (uint32_t)cnt << 21;
+  }
+  static __device__ __forceinline__ int expert(uint32_t v) { return v & 1023; }
+  static __device__ __forceinline__ int base(uint32_t v) { return v >> 10 & 2047; }
+  static __device__ __forceinline__ int count(uint32_t v) { return v >> 21 & 127; }
+  static __device__ __forceinline__ bool shared(uint32_t v) { return (int32_t)v < 0; }
+};
+static_assert(kMaxExperts <= 1024 && kMaxPairs <= 2048 && GDN_MOE_MAX_TOKENS < 128, "an entry's fields");
 
 struct MoeMaps {
   CUtensorMap whole, edge, s_whole, s_edge;   // of the experts, of the shared expert
@@ -143,7 +156,7 @@ __global__ void __launch_bounds__(32 * kRouterWarps) moe_router_kernel(const Moe
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   __syncthreads();
-  constexpr float kGrid = 3072.0f;   // products go to S on a grid of 2^-12
+  constexpr float kGrid = 1.5f * 2048;   // products go to S on a grid of 2^-12
   float S[NT], lo[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
@@ -311,7 +324,7 @@ __device__ __forceinline__ void team_lists(Lists& L, int warp, int lane) {
   for (int j = lane; j - lane < L.n_active; j += 32) {
     const bool in = j < L.n_active && L.expert[j] % kTeams == warp;
     const uint32_t b = __ballot_sync(0xffffffffu, in);
-    if (in) L.of_team[warp][n + __popc(b & ((1u << lane) - 1u))] = (uint16_t)j;
+    if (in) L.of_team[warp][n + __popc(b & ((1u << lane) - 1u))] = Entry::of(L.expert[j], L.base[j], L.base[j + 1] - L.base[j]);
     n += __popc(b);
   }
   if (lane == 0) L.n_team[warp] = n;
@@ -701,29 +714,32 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
   // experts, so that the CTAs do not all read the same activations at once.  All
   // this hangs on the experts', the chunks' and the CTA's numbers alone.
   const int team = warp / kTeam, member = warp % kTeam, n_team = L.n_team[team];
-  const uint16_t* const of_team = L.of_team[team];
+  const uint32_t* const of_team = L.of_team[team];
   int start = 0;
   {
     const int from = (int)((long long)cta * a.experts / grid);
     for (int lo = 0, hi = n_team; lo < hi;) {   // the first one not below `from`
       const int mid = (lo + hi) >> 1;
-      if (L.expert[of_team[mid]] < from) lo = mid + 1; else hi = mid;
+      if (Entry::expert(of_team[mid]) < from) lo = mid + 1; else hi = mid;
       start = lo;
     }
     if (start == n_team) start = 0;
   }
   // This warp's chunks in order, the loads kStages ahead of the products: of output
-  // tile i, expert j (the team's n-th; -1: the shared one), chunk c.
+  // tile i, expert j (the team's n-th; at n = -1 the shared one), chunk c.
+  const uint32_t all = Entry::kShared | Entry::of(0, 0, a.tokens);
   struct Walk {
-    int i, n, j, c;
+    int i, n;
+    uint32_t j;
+    int c;
   };
   const auto settle = [&](Walk& w) {     // on to the first chunk from w on that exists
-    while (w.c >= (w.j < 0 ? s_chunks : i_chunks)) {
+    while (w.c >= (Entry::shared(w.j) ? s_chunks : i_chunks)) {
       if (++w.n >= n_team) {
         w.n = -1;
         w.i += grid;
         if (w.i >= p.tiles3) return;
-        w.j = -1;
+        w.j = all;
         w.c = warp;
       } else {
         w.j = of_team[start + w.n < n_team ? start + w.n : start + w.n - n_team];
@@ -731,20 +747,21 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
       }
     }
   };
-  Walk l{cta, -1, -1, warp};
+  Walk l{cta, -1, all, warp};
   if (l.i < p.tiles3) settle(l);
   // loaded and not yet multiplied, oldest first
   constexpr int kEnd = 0x7fffffff;
-  int qi[kStages], qj[kStages], qc[kStages], ls = 0, queued = 0;
+  int qi[kStages], qc[kStages], ls = 0, queued = 0;
+  uint32_t qj[kStages];
 #pragma unroll
   for (int s = 0; s < kStages; ++s) qi[s] = kEnd;
   const auto fill = [&]() {
     while (queued < kStages && l.i < p.tiles3) {
-      const bool shared = l.j < 0;
+      const bool shared = Entry::shared(l.j);
       if (lane == 0)
         load_stage<false>(ring_a + ls * kStage, &full[ls], shared ? &maps.s_whole : &maps.whole,
                    shared ? &maps.s_edge : &maps.edge, shared ? a.shared_inter : a.inter, l.c, p.rows3,
-                   (shared ? 0 : L.expert[l.j] * a.hidden) + l.i * p.rows3, -1);
+                   Entry::expert(l.j) * a.hidden + l.i * p.rows3, -1);
       __syncwarp();
 #pragma unroll
       for (int s = 0; s < kStages; ++s)
@@ -755,7 +772,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
         }
       ++queued;
       if (++ls == kStages) ls = 0;
-      l.c += l.j < 0 ? kMoeWarps : kTeam;
+      l.c += shared ? kMoeWarps : kTeam;
       settle(l);
     }
   };
@@ -768,27 +785,21 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
   bool ok = true;   // after a wait that gave up no later one waits
   // Columns 8 n .. of an expert (pairs base + 8 n ..): this lane's activations.
   const int np = a.tokens * a.top_k;
-  const auto load_act = [&](uint4 (&x)[P][4], int j, int c, int n) {
-    const bool shared = j < 0;
-    const int cols = shared ? a.shared_inter : a.inter, zero = shared ? a.tokens : np;   // the row of zeros
-    const int k = c * kCols + t4 * 8, base = shared ? 0 : L.base[j], cnt = (shared ? a.tokens : L.base[j + 1]) - base;
-    const int at = 8 * n + g < cnt ? base + 8 * n + g : zero;
-    const uint16_t* row = (shared ? p.s_act : p.act) + ((size_t)at * cols + k);
-    const size_t plane = (size_t)(zero + 1) * cols;
-    if ((c + 1) * kCols <= cols) {
+  const auto load_act = [&](uint4 (&x)[P][4], uint32_t j, int c, int n) {
+    const bool shared = Entry::shared(j);
+    const int cols = shared ? a.shared_inter : a.inter;
+    const int k = c * kCols + t4 * 8, base = Entry::base(j), cnt = Entry::count(j);
+    // (lanes past the last pair ask for nothing: most experts have one token, and
+    // 32 lanes' requests took the load unit 64 clocks)
+    const uint16_t* row = (shared ? p.s_act : p.act) + ((size_t)(base + 8 * n + g) * cols + k);
+    const size_t plane = (size_t)((shared ? a.tokens : np) + 1) * cols;
 #pragma unroll
-      for (int part = 0; part < P; ++part)
+    for (int part = 0; part < P; ++part)
 #pragma unroll
-        for (int h = 0; h < 4; ++h) x[part][h] = __ldcg(reinterpret_cast<const uint4*>(row + part * plane + 32 * h));
-    } else {
-#pragma unroll
-      for (int part = 0; part < P; ++part)
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          x[part][h] = make_uint4(0, 0, 0, 0);
-          if (k + 32 * h < cols) x[part][h] = __ldcg(reinterpret_cast<const uint4*>(row + part * plane + 32 * h));
-        }
-    }
+      for (int h = 0; h < 4; ++h) {
+        x[part][h] = make_uint4(0, 0, 0, 0);
+        if (8 * n + g < cnt && k + 32 * h < cols) x[part][h] = __ldcg(reinterpret_cast<const uint4*>(row + part * plane + 32 * h));
+      }
   };
   float* const sums = reinterpret_cast<float*>(sm->red);
   float* const mine = sums + warp * a.tokens * kSumRow;
@@ -798,16 +809,30 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
     for (int k = lane; k < a.tokens * kSumRow; k += 32) mine[k] = 0.0f;
     __syncwarp();
     while (qi[0] == i) {
-      const int j = qj[0], c = qc[0];
-      const bool shared = j < 0;
-      const int cols = shared ? a.shared_inter : a.inter, base = shared ? 0 : L.base[j];
-      const int cnt = (shared ? a.tokens : L.base[j + 1]) - base;
+      const uint32_t j = qj[0];
+      const int c = qc[0];
+      const bool shared = Entry::shared(j);
+      const int cols = shared ? a.shared_inter : a.inter, base = Entry::base(j), cnt = Entry::count(j);
+      // where this lane's first two columns add up
+      int to[2];
+#pragma unroll
+      for (int o = 0; o < 2; ++o) {
+        const int col = 2 * t4 + o;
+        to[o] = shared ? col : (col < cnt ? (int)L.pair_t[base + col] : 0);
+      }
       ok = ok && moe_wait(a, &full[cs], ph);
       Frag f[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) load_a(f[h], ring + cs * kStage, h * p.rows3 + g, 1024, t4);
       for (int n = 0; 8 * n < cnt; ++n) {
-        if (n > 0) load_act(x, j, c, n);
+        if (n > 0) {
+          load_act(x, j, c, n);
+#pragma unroll
+          for (int o = 0; o < 2; ++o) {
+            const int col = 8 * n + 2 * t4 + o;
+            to[o] = shared ? col : (col < cnt ? (int)L.pair_t[base + col] : 0);
+          }
+        }
         // four chains: a product's latency is 38 clocks
         float acc[2][4] = {}, low[2][4] = {};
 #pragma unroll
@@ -822,7 +847,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
         for (int o = 0; o < 2; ++o) {
           const int col = 8 * n + 2 * t4 + o;
           if (col < cnt) {
-            float* y = mine + (shared ? col : (int)L.pair_t[base + col]) * kSumRow + g;
+            float* y = mine + to[o] * kSumRow + g;
             y[0] += (acc[0][o] + acc[1][o]) + (low[0][o] + low[1][o]);
             y[8] += (acc[0][2 + o] + acc[1][2 + o]) + (low[0][2 + o] + low[1][2 + o]);
           }
