@@ -111,8 +111,8 @@ struct MoeParams {
   MoeArgs a;
   float2* logit;        // [tokens][experts + 1], high and low part
   Choice* choice;
-  uint16_t* act;        // [part][pairs + 1][inter], the last row zeros; two parts, or three
-  uint16_t* s_act;      // [part][tokens + 1][shared_inter], likewise
+  uint16_t* act;        // [part][pairs][inter]; two parts, or three
+  uint16_t* s_act;      // [part][tokens][shared_inter]
   int rows3, tiles3;    // output rows per tile, tiles
 };
 
@@ -561,16 +561,6 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
     ly = L.expert[j] * 2 * a.inter + (li - s_tiles - j * e_tiles) * 8;
   }
 
-  // the row of zeros after the last pair's, for tokens that an expert does not serve
-  if (cta == grid - 1) {
-    const int np = a.tokens * a.top_k;
-    for (int part = 0; part < (a.out_f32 ? 3 : 2); ++part) {
-      for (int i = tid; i < a.inter; i += kMoeThreads) p.act[((size_t)(part + 1) * (np + 1) - 1) * a.inter + i] = 0;
-      for (int i = tid; i < a.shared_inter; i += kMoeThreads)
-        p.s_act[((size_t)(part + 1) * (a.tokens + 1) - 1) * a.shared_inter + i] = 0;
-    }
-  }
-
   const int g = lane >> 2, t4 = lane & 3;
   int cs = 0, flip = 0;
   uint32_t ph = 0;
@@ -584,13 +574,16 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
 #pragma unroll
     for (int n = 0; n < NG; ++n) {
       if (n > 0 && 8 * n >= cnt) continue;
-      const int c = min(8 * n + g, cnt - 1);   // columns past the expert's tokens repeat the last: never written
+      const int c = min(8 * n + g, cnt - 1);
       x[n] = a.x + (size_t)(shared ? c : (int)L.pair_t[col0 + c]) * a.hidden + t4 * 8;
     }
 #pragma unroll
     for (int n = 0; n < NG; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.0f;
-    uint4 b[4];                  // a chunk's activations, asked for one chunk ahead
+    // a chunk's activations, asked for one chunk ahead; lanes past the expert's tokens
+    // ask for none (the requests of all 32 lanes take the load unit 64 clocks)
+    uint4 b[4] = {};
     const auto load_x = [&](int k) {
+      if (g >= cnt) return;
       if (k + kCols <= a.hidden) {
 #pragma unroll
         for (int h = 0; h < 4; ++h) b[h] = *reinterpret_cast<const uint4*>(x[0] + k + 32 * h);
@@ -614,12 +607,12 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
         if (n > 0 && 8 * n >= cnt) break;
         // the next group's activations are asked for before this one's products while
         // there are registers, after them with eight groups
-        uint4 bm[4];
+        uint4 bm[4] = {};
         const auto load_group = [&](uint4* to) {
           if (n + 1 < NG && 8 * (n + 1) < cnt) {
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-              to[q] = 32 * q < left ? *reinterpret_cast<const uint4*>(x[n + 1 < NG ? n + 1 : 0] + k + 32 * q)
+              to[q] = 32 * q < left && 8 * (n + 1) + g < cnt ? *reinterpret_cast<const uint4*>(x[n + 1 < NG ? n + 1 : 0] + k + 32 * q)
                                     : make_uint4(0, 0, 0, 0);
           }
         };
@@ -653,7 +646,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
     // up of row g for columns 2 t4 and 2 t4 + 1
     const int cols = shared ? a.shared_inter : a.inter;
     uint16_t* const act = shared ? p.s_act : p.act;
-    const size_t plane = (size_t)((shared ? a.tokens : a.tokens * a.top_k) + 1) * cols;
+    const size_t plane = (size_t)(shared ? a.tokens : a.tokens * a.top_k) * cols;
 #pragma unroll
     for (int n = 0; n < NG; ++n)
       if (8 * n < cnt) {
@@ -792,7 +785,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
     // (lanes past the last pair ask for nothing: most experts have one token, and
     // 32 lanes' requests took the load unit 64 clocks)
     const uint16_t* row = (shared ? p.s_act : p.act) + ((size_t)(base + 8 * n + g) * cols + k);
-    const size_t plane = (size_t)((shared ? a.tokens : np) + 1) * cols;
+    const size_t plane = (size_t)(shared ? a.tokens : np) * cols;
 #pragma unroll
     for (int part = 0; part < P; ++part)
 #pragma unroll
@@ -959,8 +952,8 @@ cudaError_t launch_products(const MoeMaps& up, const MoeMaps& down, const MoePar
 
 size_t moe_scratch_bytes(int tokens, int, int inter, int experts, int top_k, int shared_inter) {
   const size_t T = tokens > 0 ? tokens : 1;
-  return up256(sizeof(Choice)) + up256(T * (experts + 1) * 8) + up256((T * top_k + 1) * inter * 6) +
-         up256((T + 1) * shared_inter * 6);
+  return up256(sizeof(Choice)) + up256(T * (experts + 1) * 8) + up256(T * top_k * inter * 6) +
+         up256(T * shared_inter * 6);
 }
 
 cudaError_t launch_moe(const MoeArgs& a, cudaStream_t stream) {
@@ -978,7 +971,7 @@ cudaError_t launch_moe(const MoeArgs& a, cudaStream_t stream) {
   p.logit = reinterpret_cast<float2*>(ws);
   ws += up256(T * (a.experts + 1) * 8);
   p.act = reinterpret_cast<uint16_t*>(ws);
-  ws += up256((T * a.top_k + 1) * a.inter * 6);
+  ws += up256(T * a.top_k * a.inter * 6);
   p.s_act = reinterpret_cast<uint16_t*>(ws);
   // output rows: tiles of at most 16, as many as give every CTA the same number
   const int per = (a.hidden + 16 * sms - 1) / (16 * sms);
