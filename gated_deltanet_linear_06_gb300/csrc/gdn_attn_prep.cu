@@ -18,6 +18,11 @@
 // its heads.  Two rows per lane group are loaded while the two before them are
 // turned, the next token's first ones included: without that the kernel waited
 // for its loads more than it worked (262 us for 32768 tokens, 671 MB).
+//
+// Measured: 32768 tokens of 16 + 2 + 2 heads of 256 (671 MB) 121 us, 5.55 TB/s or
+// 82 % of a plain copy's rate; 2049 tokens of 32 + 8 + 8 heads of 128 with three
+// axes (50 MB) 16.6 us, where a warp has one or two rounds and their latency
+// shows; 8 tokens 5 us, all latency, under a launch that takes the host 13.
 #include "../../include/gdn.h"
 #include "gdn_common.cuh"
 #include "gdn_launch.h"
