@@ -446,8 +446,7 @@ __device__ __forceinline__ void tma2(uint32_t dst, const CUtensorMap* tm, int x,
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -795,21 +794,29 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
     const int k = c * kCols + t4 * 8, base = Entry::base(j), cnt = Entry::count(j);
     // (lanes past the last pair ask for nothing: most experts have one token, and the
     // requests of all 32 lanes, 7 of 8 for zeros, took the load unit 64 clocks a
-    // warp: 204 us for 64 tokens where 143 now are)
+    // warp: 204 us for 64 tokens where 143 then were.  What they hold meets only
+    // columns that nobody reads.)
+    if (8 * n + g >= cnt) return;
     const uint16_t* row = (shared ? p.s_act : p.act) + ((size_t)(base + 8 * n + g) * cols + k);
     const size_t plane = (size_t)(shared ? a.tokens : np) * cols;
+    if ((c + 1) * kCols <= cols) {
 #pragma unroll
-    for (int part = 0; part < P; ++part)
+      for (int part = 0; part < P; ++part)
 #pragma unroll
-      for (int h = 0; h < 4; ++h) {
-        x[part][h] = make_uint4(0, 0, 0, 0);
-        if (8 * n + g < cnt && k + 32 * h < cols)
-          x[part][h] = __ldcg(reinterpret_cast<const uint4*>(row + part * plane + 32 * h));
-      }
+        for (int h = 0; h < 4; ++h) x[part][h] = __ldcg(reinterpret_cast<const uint4*>(row + part * plane + 32 * h));
+    } else {
+#pragma unroll
+      for (int part = 0; part < P; ++part)
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          x[part][h] = make_uint4(0, 0, 0, 0);
+          if (k + 32 * h < cols) x[part][h] = __ldcg(reinterpret_cast<const uint4*>(row + part * plane + 32 * h));
+        }
+    }
   };
   float* const sums = reinterpret_cast<float*>(sm->red);
   float* const mine = sums + warp * a.tokens * kSumRow;
-  uint4 x[P][4];                 // of the first 8 columns, asked for one chunk ahead
+  uint4 x[P][4] = {};            // of the first 8 columns, asked for one chunk ahead
   if (qi[0] != kEnd) load_act(x, qj[0], qc[0], 0);
   for (int i = cta; i < p.tiles3; i += grid) {
     for (int k = lane; k < a.tokens * kSumRow; k += 32) mine[k] = 0.0f;
