@@ -42,10 +42,10 @@
 //
 // Measured, all four (hidden 2048; router, choice, gate_up, down apart in us): one
 // token through 8 of 256 experts of 512 25 us (4, 4, 11, 9, overlapped); 16 tokens
-// 117 (8, 5, 66, 47); 64 tokens through 10 of 512 experts 416 (21, 6, 259, 143),
+// 115 (8, 5, 65, 44); 64 tokens through 10 of 512 experts 412 (21, 6, 260, 135),
 // 5.6 TB/s or 82 % of a copy's rate; 5 tokens through 6 of 64 experts of 1408 with an
-// fp32 result 95 (8, 4, 48, 47).  gate_up runs at the memory's rate.  down's warps
-// are bound by their own chains, and few experts spread unevenly over the four
+// fp32 result 91 (8, 4, 48, 43).  gate_up runs at the memory's rate.  down's warps
+// are bound by their instructions (some 400 a chunk), and few experts spread unevenly over the four
 // teams (21 to 32 chunks a warp at 16 tokens).
 //
 // The activations between the products are kept as sums of bf16, because the
@@ -794,7 +794,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
     const int k = c * kCols + t4 * 8, base = Entry::base(j), cnt = Entry::count(j);
     // (lanes past the last pair ask for nothing: most experts have one token, and the
     // requests of all 32 lanes, 7 of 8 for zeros, took the load unit 64 clocks a
-    // warp: 204 us for 64 tokens where 143 then were.  What they hold meets only
+    // warp: 204 us for 64 tokens where 135 now are.  What they hold meets only
     // columns that nobody reads.)
     if (8 * n + g >= cnt) return;
     const uint16_t* row = (shared ? p.s_act : p.act) + ((size_t)(base + 8 * n + g) * cols + k);
