@@ -195,6 +195,9 @@ def gdn_prefill_segment_tokens_for(dims: Dims, n_seqs: int, total_tokens: int, s
                                                 int(total_tokens), int(sms))
 
 
+_BF16, _F32, _F64, _I32, _U8 = torch.bfloat16, torch.float32, torch.float64, torch.int32, torch.uint8
+
+
 def _stream(stream) -> int | None:
     if stream is None:                 # the current stream's handle, without a Stream object
         return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
@@ -204,7 +207,10 @@ def _stream(stream) -> int | None:
 def _ptr(t, dtype, name, numel=None):
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor):
+    try:                               # the usual case: every look at a tensor takes the host some 50 ns
+        if t.is_cuda and t.dtype is dtype and (numel is None or t.numel() == numel) and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
         return t                       # a raw device address, passed through
     if not t.is_cuda or t.dtype != dtype or not t.is_contiguous():
         raise ValueError(f"{name}: want a contiguous CUDA {dtype} tensor, "
@@ -555,6 +561,8 @@ def _view(t, name, tokens, heads, d):
     if t is None:
         return None, 0, 0
     sh, st = t.shape, t.stride()
+    if sh == (tokens, heads, d) and st[2] == 1 and t.is_cuda and t.dtype is _BF16:   # the usual case
+        return t.data_ptr(), st[0], st[1]
     if not t.is_cuda or t.dtype != torch.bfloat16 or len(sh) < 3 or sh[-2] != heads or sh[-1] != d \
             or (d > 1 and st[-1] != 1) or t.numel() != tokens * heads * d:
         raise ValueError(f"{name}: want a CUDA bfloat16 tensor of [{tokens}, {heads}, {d}] with its "
@@ -570,27 +578,26 @@ def gdn_attn_prep(dims: AttnDims, q, k, v, q_norm_w, k_norm_w, inv_freq, freq_ax
     """q and k norms, rotary positions and the cache write in one pass.  q, k
     and v are [T, heads, d] views (None leaves one out); the caches are
     [pages, page, h_kv, d] or [rows, h_kv, d]; slot [T] int32 names each token's row."""
-    f32, i32 = torch.float32, torch.int32
-    d, rot = dims.d, dims.rot
-    lead = next((x for x in (q, k, v) if x is not None), None)
-    T = int(lead.shape[0]) if lead is not None else 0
-    vq, vk, vv = (_view(q, "q", T, dims.h_q, d), _view(k, "k", T, dims.h_kv, d),
-                  _view(v, "v", T, dims.h_kv, d))
+    f32, i32 = _F32, _I32
+    h_q, h_kv, d, rot, n_axes = dims.h_q, dims.h_kv, dims.d, dims.rot, dims.n_axes
+    lead = q if q is not None else k if k is not None else v
+    T = lead.shape[0] if lead is not None else 0
     rows = 0
     for cache, x in ((k_cache, k), (v_cache, v)):
         if x is not None:
-            n = cache.numel() // (dims.h_kv * d)
-            if n * dims.h_kv * d != cache.numel() or (rows and n != rows):
+            n, rest = divmod(cache.numel(), h_kv * d)
+            if rest or (rows and n != rows):
                 raise ValueError("k_cache, v_cache: want the same whole number of [h_kv, d] rows")
             rows = n
-    axes = None if dims.n_axes <= 1 or freq_axis is None else _ptr(freq_axis, i32, "freq_axis", rot // 2)
     st = lib().gdn_attn_prep(
-        ctypes.byref(dims), T, *vq, *vk, *vv, _ptr(q_norm_w, f32, "q_norm_w", d),
-        _ptr(k_norm_w, f32, "k_norm_w", d), _ptr(inv_freq, torch.float64, "inv_freq", rot // 2), axes,
-        _ptr(pos, i32, "pos", max(dims.n_axes, 1) * T), _ptr(slot, i32, "slot", T), rows,
-        _ptr(q_out, torch.bfloat16, "q_out", T * dims.h_q * d) if q is not None else None,
-        _ptr(k_cache, torch.bfloat16, "k_cache") if k is not None else None,
-        _ptr(v_cache, torch.bfloat16, "v_cache") if v is not None else None,
+        ctypes.byref(dims), T, *_view(q, "q", T, h_q, d), *_view(k, "k", T, h_kv, d), *_view(v, "v", T, h_kv, d),
+        _ptr(q_norm_w, f32, "q_norm_w", d), _ptr(k_norm_w, f32, "k_norm_w", d),
+        _ptr(inv_freq, _F64, "inv_freq", rot // 2),
+        None if n_axes <= 1 else _ptr(freq_axis, i32, "freq_axis", rot // 2),
+        _ptr(pos, i32, "pos", max(n_axes, 1) * T), _ptr(slot, i32, "slot", T), rows,
+        _ptr(q_out, _BF16, "q_out", T * h_q * d) if q is not None else None,
+        _ptr(k_cache, _BF16, "k_cache") if k is not None else None,
+        _ptr(v_cache, _BF16, "v_cache") if v is not None else None,
         _ptr(device_status, i32, "device_status", 1), _stream(stream))
     _check(st, "gdn_attn_prep")
 
@@ -604,22 +611,22 @@ def gdn_attn_decode_shared(dims: AttnDims, q, k_cache, v_cache, prefix_pages, pr
     """Attention of q [B, steps, h_q, d] over a prefix that all sequences share
     (its pages, prefix_len tokens) and each sequence's own tail (tail_pages
     [B, width], tail_len [B]); the caches are [pages, page, h_kv, d]."""
-    bf, i32 = torch.bfloat16, torch.int32
-    B, S = int(q.shape[0]), int(q.shape[1])
-    n, L = B * S * dims.h_q * dims.d, int(prefix_len)
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.shape[2] != dims.h_kv or \
-            k_cache.shape[3] != dims.d:
+    bf, i32 = _BF16, _I32
+    B, S = q.shape[:2]
+    h_q, d, caches = dims.h_q, dims.d, k_cache.shape
+    n, L = B * S * h_q * d, int(prefix_len)
+    if len(caches) != 4 or caches != v_cache.shape or caches[2] != dims.h_kv or caches[3] != d:
         raise ValueError("k_cache, v_cache: want [pages, page, h_kv, d], both alike")
-    pages, page = int(k_cache.shape[0]), int(k_cache.shape[1])
+    pages, page = caches[:2]
     if L > 0 and (prefix_pages is None or prefix_pages.numel() < -(-L // page)):
         raise ValueError("prefix_pages: fewer pages than the prefix has")
     width = 0 if tail_pages is None else int(tail_pages.shape[-1])
-    g, g_st, g_sh = _view(gate, "gate", B * S, dims.h_q, dims.d)
+    g, g_st, g_sh = _view(gate, "gate", B * S, h_q, d)
     st = lib().gdn_attn_decode_shared(
         ctypes.byref(dims), page, pages, B, S, _ptr(q, bf, "q", n), _ptr(k_cache, bf, "k_cache"),
         _ptr(v_cache, bf, "v_cache"), _ptr(prefix_pages, i32, "prefix_pages"), L,
         _ptr(tail_pages, i32, "tail_pages", B * width), width, _ptr(tail_len, i32, "tail_len", B),
-        g, g_st, g_sh, _ptr(out, bf, "out", n), _ptr(workspace, torch.uint8, "workspace"),
+        g, g_st, g_sh, _ptr(out, bf, "out", n), _ptr(workspace, _U8, "workspace"),
         workspace.numel(), _ptr(device_status, i32, "device_status", 1), _stream(stream))
     _check(st, "gdn_attn_decode_shared")
 
@@ -632,7 +639,7 @@ def gdn_moe_step(dims: MoeDims, x, w_router, w_gate_up, w_down, y, workspace, w_
                  w_shared_down=None, w_shared_gate=None, topk_id=None, topk_w=None,
                  device_status=None, stream=None):
     """A whole mixture-of-experts layer: x [T, hidden] -> y [T, hidden] (bf16 or fp32)."""
-    bf, f32, i32 = torch.bfloat16, torch.float32, torch.int32
+    bf, f32, i32 = _BF16, _F32, _I32
     T, H, I, E, Is = int(x.shape[0]), dims.hidden, dims.inter, dims.experts, dims.shared_inter
     if y.dtype not in (bf, f32):
         raise ValueError("y: want bfloat16 or float32")
@@ -643,7 +650,7 @@ def gdn_moe_step(dims: MoeDims, x, w_router, w_gate_up, w_down, y, workspace, w_
         _ptr(w_shared_down, bf, "w_shared_down", H * Is), _ptr(w_shared_gate, bf, "w_shared_gate", H),
         _ptr(y, y.dtype, "y", T * H), GDN_DTYPE_F32 if y.dtype == f32 else GDN_DTYPE_BF16,
         _ptr(topk_id, i32, "topk_id", T * dims.top_k), _ptr(topk_w, f32, "topk_w", T * dims.top_k),
-        _ptr(workspace, torch.uint8, "workspace"), workspace.numel(),
+        _ptr(workspace, _U8, "workspace"), workspace.numel(),
         _ptr(device_status, i32, "device_status", 1), _stream(stream))
     _check(st, "gdn_moe_step")
 
