@@ -19,10 +19,11 @@
 // turned, the next token's first ones included: without that the kernel waited
 // for its loads more than it worked (262 us for 32768 tokens, 671 MB).
 //
-// Measured: 32768 tokens of 16 + 2 + 2 heads of 256 (671 MB) 121 us, 5.55 TB/s or
-// 82 % of a plain copy's rate; 2049 tokens of 32 + 8 + 8 heads of 128 with three
-// axes (50 MB) 16.6 us, where a warp has one or two rounds and their latency
-// shows; 8 tokens 5 us, all latency, under a launch that takes the host 13.
+// Measured: 32768 tokens of 16 + 2 + 2 heads of 256 (671 MB) 119 us, 5.63 TB/s or
+// 83 % of a plain copy's rate; 2049 tokens of 32 + 8 + 8 heads of 128 with three
+// axes (50 MB) 16.7 us, where a warp has one or two rounds and their latency
+// shows (18.4 before the launch passed under the kernel before it); 8 tokens 5 us,
+// all latency, under a call that takes the host 10.
 #include "../../include/gdn.h"
 #include "gdn_common.cuh"
 #include "gdn_launch.h"
@@ -52,6 +53,10 @@ __global__ void __launch_bounds__(kPrepWarps * 32, 3)
   __shared__ __align__(16) float cosv[kPrepWarps][kMaxFreq], sinv[kPrepWarps][kMaxFreq];
   __shared__ __align__(16) float norm_w[2][D];
 
+  // Launched while the kernel before it runs, whose results are there from here on;
+  // only then may the next be, so that no kernel overlaps more than its neighbour.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = lane / LPR, l = lane % LPR;
   const int nf = p.rot >> 1;
@@ -266,11 +271,16 @@ cudaError_t launch_d(const AttnPrepArgs& p, cudaStream_t stream, int sms) {
   const long long blocks = (sh.items + kPrepWarps - 1) / kPrepWarps;
   const long long cap = (long long)sms * 3;
   const unsigned grid = (unsigned)(blocks < cap ? blocks : cap);
-  if (p.pairs)
-    attn_prep_kernel<D, true><<<grid, kPrepWarps * 32, 0, stream>>>(p, sh);
-  else
-    attn_prep_kernel<D, false><<<grid, kPrepWarps * 32, 0, stream>>>(p, sh);
-  return cudaGetLastError();
+  cudaLaunchAttribute overlap;
+  overlap.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  overlap.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kPrepWarps * 32);
+  cfg.stream = stream;
+  cfg.attrs = &overlap;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, p.pairs ? attn_prep_kernel<D, true> : attn_prep_kernel<D, false>, p, sh);
 }
 
 }  // namespace

@@ -49,9 +49,9 @@
 // bf16 as well as P <= 1 does, and the sums are fp32), so almost never.
 //
 // Measured, both launches: 64 sequences on a prefix of 32768 (16 query heads, 2 key
-// heads, d = 256) 52 us, 665 TFLOP/s of useful products; 256 sequences on 32768
+// heads, d = 256) 51 us, 680 TFLOP/s of useful products; 256 sequences on 32768
 // 168 us, 830; 256 on 4096 with tails up to 3000 169 us, 4.9 TB/s; one sequence
-// of 833 keys 12 us, all latency.  A prefix tile takes some 2700 clocks: 2048 of
+// of 833 keys 13 us, all latency.  A prefix tile takes some 2700 clocks: 2048 of
 // products, next to 2000 of softmax on the other side of the same barriers; a
 // tail's tile costs as many clocks of products for its few rows.  The rest of a call
 // is 2.5 us before the first tile and 8 to 10 in the join.  Tables of 16-row pages
@@ -409,6 +409,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  // launched while the kernel before it runs: its results are there from here on
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   // ---- this pair's share: the running cost of the tails, then a search ----
   long long* scan = reinterpret_cast<long long*>(ring);   // [batch + 1] and warp totals, before the ring is used
   long long* wsum = scan + GDN_ATTN_MAX_BATCH + 8;
@@ -883,6 +885,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_shared_join(const __grid_co
   const int in[2] = {(tok - blk * pl.tpb) * pl.G, step * pl.G};
   const int apart[2] = {256, pl.R};                        // slots are so many rows apart
   // launched while the first kernel runs; its results are there from here on
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int2 none = make_int2(0, -1);   // no range
   const int2 pre = pl.np ? p.span[job[0]] : none;
@@ -1068,20 +1071,23 @@ cudaError_t launch_d(const AttnSharedArgs& a, cudaStream_t stream, int sms) {
   if ((e = cudaFuncSetAttribute(attn_shared_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 (int)C::SMEM)) != cudaSuccess)
     return e;
-  attn_shared_kernel<D><<<2 * p.pl.shares, kThreads, C::SMEM, stream>>>(tk, tv, tqp, tqt, p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  // the join's launch passes under the first kernel
+  // each launch passes under the kernel before it
   cudaLaunchAttribute overlap;
   overlap.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   overlap.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * p.pl.shares);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = stream;
+  cfg.attrs = &overlap;
+  cfg.numAttrs = 1;
+  if ((e = cudaLaunchKernelEx(&cfg, attn_shared_kernel<D>, tk, tv, tqp, tqt, p)) != cudaSuccess) return e;
   int nz = 1;   // CTAs per token and key head
   while (nz < D / 32 && (long long)p.pl.ntok * p.pl.h_kv * nz < 6LL * sms) nz *= 2;
   cfg.gridDim = dim3(p.pl.ntok, p.pl.h_kv, nz);
   cfg.blockDim = dim3(kJoinThreads);
-  cfg.stream = stream;
-  cfg.attrs = &overlap;
-  cfg.numAttrs = 1;
+  cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, attn_shared_join<D>, p);
 }
 

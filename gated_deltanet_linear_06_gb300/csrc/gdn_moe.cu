@@ -7,7 +7,8 @@
 // weight rows by 8 tokens), because their cost then does not grow with the
 // tokens that share an expert.
 //
-// Four launches, each begun while the one before it runs (programmatic
+// Four launches, each begun while the one before it (the call's first: the caller's
+// last) runs (programmatic
 // dependent launch), so that between them only data is waited for:
 //   router   logits: a CTA takes 8 experts and 8 tokens, one warp an expert.  The
 //            chosen experts hang on which logits are larger, so the sums are
@@ -41,7 +42,7 @@
 // nothing in a token's arithmetic depends on the other tokens.
 //
 // Measured, all four (hidden 2048; router, choice, gate_up, down apart in us): one
-// token through 8 of 256 experts of 512 25 us (4, 4, 11, 9, overlapped); 16 tokens
+// token through 8 of 256 experts of 512 23 us (4, 4, 11, 9, overlapped); 16 tokens
 // 115 (8, 5, 65, 44); 64 tokens through 10 of 512 experts 412 (21, 6, 260, 135),
 // 5.6 TB/s or 82 % of a copy's rate; 5 tokens through 6 of 64 experts of 1408 with an
 // fp32 result 91 (8, 4, 48, 43).  gate_up runs at the memory's rate.  down's warps
@@ -155,7 +156,6 @@ __global__ void __launch_bounds__(32 * kRouterWarps) moe_router_kernel(const Moe
   __shared__ __align__(8) uint64_t full;
   uint16_t* const rows = reinterpret_cast<uint16_t*>(rows_raw);   // 8 experts, 8 tokens
   const MoeArgs& a = p.a;
-  let_next_begin();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n_rows = a.experts + (a.s_gate ? 1 : 0);
   const int e0 = blockIdx.x * 8, t0 = blockIdx.y * NT, ne = min(8, n_rows - e0), nt = min(NT, a.tokens - t0);
@@ -164,6 +164,10 @@ __global__ void __launch_bounds__(32 * kRouterWarps) moe_router_kernel(const Moe
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   __syncthreads();
+  // The kernel before this call is done; only then may the next begin, for the products
+  // load weights before they wait.
+  wait_before();
+  let_next_begin();
   constexpr float kGrid = 1.5f * 2048;   // products go to S on a grid of 2^-12
   float S[NT], lo[NT];
 #pragma unroll
@@ -780,6 +784,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
     }
   };
   fill();
+  let_next_begin();
   wait_before();   // the activations
 
   const int g = lane >> 2, t4 = lane & 3;
@@ -1008,10 +1013,9 @@ cudaError_t launch_moe(const MoeArgs& a, cudaStream_t stream) {
   const int rows = a.experts + (p.a.s_gate ? 1 : 0);
   const int nt = a.tokens == 1 ? 1 : 8;   // eight tokens share an expert's row
   const auto router = nt == 1 ? moe_router_kernel<1> : moe_router_kernel<8>;
-  if ((e = cudaFuncSetAttribute(router, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRouterSmem)) != cudaSuccess)
+  if ((e = launch_early(router, dim3((rows + 7) / 8, (a.tokens + nt - 1) / nt), 32 * kRouterWarps, kRouterSmem, stream,
+                        p)) != cudaSuccess)
     return e;
-  router<<<dim3((rows + 7) / 8, (a.tokens + nt - 1) / nt), 32 * kRouterWarps, kRouterSmem, stream>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if ((e = launch_early(moe_choice_kernel, dim3(a.tokens), kChoiceThreads, 0, stream, p)) != cudaSuccess) return e;
   if (a.tokens <= 8) return launch_products<1>(up, down, p, sms, stream);
   if (a.tokens <= 16) return launch_products<2>(up, down, p, sms, stream);
