@@ -21,7 +21,7 @@
 //
 // Measured: 32768 tokens of 16 + 2 + 2 heads of 256 (671 MB) 119 us, 5.63 TB/s or
 // 83 % of a plain copy's rate; 2049 tokens of 32 + 8 + 8 heads of 128 with three
-// axes (50 MB) 16.7 us, where a warp has one or two rounds and their latency
+// axes (50 MB) 16.1 us, where a warp has one or two rounds and their latency
 // shows (18.4 before the launch passed under the kernel before it); 8 tokens 5 us,
 // all latency, under a call that takes the host 10.
 #include "../../include/gdn.h"
@@ -53,10 +53,8 @@ __global__ void __launch_bounds__(kPrepWarps * 32, 3)
   __shared__ __align__(16) float cosv[kPrepWarps][kMaxFreq], sinv[kPrepWarps][kMaxFreq];
   __shared__ __align__(16) float norm_w[2][D];
 
-  // Launched while the kernel before it runs, whose results are there from here on;
-  // only then may the next be, so that no kernel overlaps more than its neighbour.
+  // launched as the kernel before it ends, whose results are there from here on
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = lane / LPR, l = lane % LPR;
   const int nf = p.rot >> 1;

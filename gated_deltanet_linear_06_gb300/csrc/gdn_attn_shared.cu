@@ -49,7 +49,7 @@
 // bf16 as well as P <= 1 does, and the sums are fp32), so almost never.
 //
 // Measured, both launches: 64 sequences on a prefix of 32768 (16 query heads, 2 key
-// heads, d = 256) 51 us, 680 TFLOP/s of useful products; 256 sequences on 32768
+// heads, d = 256) 50 us, 690 TFLOP/s of useful products; 256 sequences on 32768
 // 168 us, 830; 256 on 4096 with tails up to 3000 169 us, 4.9 TB/s; one sequence
 // of 833 keys 13 us, all latency.  A prefix tile takes some 2700 clocks: 2048 of
 // products, next to 2000 of softmax on the other side of the same barriers; a
@@ -884,8 +884,9 @@ __global__ void __launch_bounds__(kJoinThreads) attn_shared_join(const __grid_co
   const int stride[2] = {128, pl.R};                       // rows of a CTA's part of a slot
   const int in[2] = {(tok - blk * pl.tpb) * pl.G, step * pl.G};
   const int apart[2] = {256, pl.R};                        // slots are so many rows apart
-  // launched while the first kernel runs; its results are there from here on
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // Launched while the first kernel runs; its results are there from here on.  (The
+  // next call's kernel is not let begin before this one ends: its CTAs then took the
+  // SMs as they fell free, 176 us a call for 169 at 256 sequences.)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int2 none = make_int2(0, -1);   // no range
   const int2 pre = pl.np ? p.span[job[0]] : none;
