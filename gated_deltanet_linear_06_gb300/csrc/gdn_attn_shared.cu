@@ -204,6 +204,9 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// What a maximum is subtracted as: where no score but -inf (or NaN) was met, 0.
+__device__ __forceinline__ float finite_base(float m) { return m == -INFINITY ? 0.0f : m; }
+
 // Shares in use: none is shorter than a tile, so that the shares from a job's first
 // range to its last all have one.
 __device__ __forceinline__ int shares_of(const Plan& pl, long long total) {
@@ -810,7 +813,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
           }
         }
-        const float mu = m == -INFINITY ? 0.0f : m;
+        const float mu = finite_base(m);
         float pk[32];
         float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
@@ -918,11 +921,18 @@ __global__ void __launch_bounds__(kJoinThreads) attn_shared_join(const __grid_co
             mv[u] = r < n ? ml[r * ml_step] : make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
             vv[u] = r < n ? v[r * v_step] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
           }
-          float mn = M;
+          // Only a range with a sum counts (one without saw no key).  A NaN sum counts,
+          // though its maximum may be NaN or -inf (fmaxf drops NaN): the row is NaN then.
+          float mn = M, sum[4];
+          bool any = false;
 #pragma unroll
-          for (int u = 0; u < 4; ++u) mn = fmaxf(mn, mv[u].x);
-          if (mn == -INFINITY) continue;   // rows that see nothing so far
-          const float f = ex2(M - mn);
+          for (int u = 0; u < 4; ++u) {
+            sum[u] = mv[u].y + mv[u].z;
+            any |= sum[u] != 0.0f;
+            if (sum[u] != 0.0f) mn = fmaxf(mn, mv[u].x);
+          }
+          if (!any) continue;   // rows that see nothing so far
+          const float base = finite_base(mn), f = ex2(M - base);
           L *= f;
           o.x *= f;
           o.y *= f;
@@ -930,8 +940,9 @@ __global__ void __launch_bounds__(kJoinThreads) attn_shared_join(const __grid_co
           o.w *= f;
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
-            const float w = ex2(mv[u].x - mn);
-            L += (mv[u].y + mv[u].z) * w;
+            if (sum[u] == 0.0f) continue;
+            const float w = ex2(mv[u].x - base);
+            L += sum[u] * w;
             o.x += vv[u].x * w;
             o.y += vv[u].y * w;
             o.z += vv[u].z * w;
@@ -953,9 +964,9 @@ __global__ void __launch_bounds__(kJoinThreads) attn_shared_join(const __grid_co
       for (int q = 1; q < groups; ++q) {
         const float2 st = stat[q * width + threadIdx.x];
         const float4 v = acc[q * width + threadIdx.x];
-        const float mn = fmaxf(M, st.x);
-        if (mn == -INFINITY) continue;
-        const float f = ex2(M - mn), w = ex2(st.x - mn);
+        if (st.y == 0.0f) continue;
+        const float mn = fmaxf(M, st.x), base = finite_base(mn);
+        const float f = ex2(M - base), w = ex2(st.x - base);
         L = L * f + st.y * w;
         o.x = o.x * f + v.x * w;
         o.y = o.y * f + v.y * w;
