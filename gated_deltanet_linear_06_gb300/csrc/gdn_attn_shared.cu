@@ -37,7 +37,8 @@
 //              cores idle for some 500 clocks at each change between them, 1000
 //              of a tile's 3400; now one's barriers pass under the other's
 //              products.)
-//   warp 11    a tail's last V tile: zeros in the rows past its end
+//   warp 11    a tail's last V tile: zeros in the rows past its end, and for infinities
+//              and NaN of tokens that not all of its queries see
 //   warps 2-9  softmax: a thread holds half a row's 128 scores; P goes back to
 //              tensor memory as bf16 and is read from there as the A operand
 // TMEM: O (d columns), one score tile (128), two weight tiles (64 each).  The
@@ -57,6 +58,13 @@
 // is 2.5 us before the first tile and 8 to 10 in the join.  Tables of 16-row pages
 // cost 16 copies a tile instead of 4, some 150 clocks each: pages of 64 rows or
 // more are better (17 sequences of 4 steps on 5000, pages of 16: 43 us).
+//
+// Masks.  A masked key's weight is zero, but zero times an infinity is NaN, and one
+// product serves all rows of a job.  So what the product reads of V is finite
+// wherever some row does not see it: rows past a job's end are zeros, and of a
+// tail's last steps - 1 tokens, which its earlier queries do not see, infinities
+// and NaN are.  The join adds those to the rows that do see them (a positive weight
+// times an infinity is that infinity).
 //
 // Rounding: weights P to bf16 (half a step, 2^-8 of each weight), because the
 // tensor cores take both operands in one 16-bit type; scores, maxima, sums and
@@ -100,6 +108,7 @@ struct SharedParams {
   AttnSharedArgs a;
   Plan pl;
   int2* span;                  // per job: the first and the last share with a range of it
+  uint8_t* hidden;             // per tail job [last tile with hidden tokens, the one before][CTA]: any not finite
   float4* ml;                  // (m, l half 0, l half 1, -) per slot row
   float* opart;                // per slot: [d / 4][rows][4]
 };
@@ -135,7 +144,7 @@ struct Ctrl {
   uint64_t pv_done[kMaxStages];   // a tile's O product is done, and so is its V stage
   uint64_t q_full[2], q_done[2], p_ready[2];
   uint64_t s_free;                // the scores are in registers
-  uint64_t landed[kMaxStages];    // this CTA's half of a V tile that ends inside 16 keys, by its stage
+  uint64_t landed[kMaxStages];    // this CTA's half of a V tile that is to be cleaned, by its stage
   uint64_t seg_done;              // a segment's last O product
   uint64_t pair[4];            // the two warps of a row quarter
   uint32_t tmem;
@@ -317,6 +326,18 @@ struct Cursor {
   }
 };
 
+// Whether a tile's V passes the cleaning warp before its product: a tail or a prefix
+// ends in it inside 16 keys, or it holds some of the last steps - 1 tokens of a tail.
+template <bool several>
+__device__ __forceinline__ bool cleaned(const AttnSharedArgs& a, const Cursor& c) {
+  return (c.count() & 15) != 0 || (several && !c.prefix && c.keys - c.t * kTile < kTile + a.steps - 1);
+}
+
+// Infinities and NaN of two bf16; zeros in a finite one's place.
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) {
+  return ((w & 0x7f80u) == 0x7f80u ? w & 0xffffu : 0u) | ((w & 0x7f800000u) == 0x7f800000u ? w & 0xffff0000u : 0u);
+}
+
 // Position in a ring of N stages.
 template <int N>
 struct Ring {
@@ -368,7 +389,35 @@ __device__ __forceinline__ void tmem_ld64(uint32_t taddr, float (&v)[64]) {
   for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// 16-byte piece `c16` of a row of a V stage, whose pieces of pages are `rpb` rows.
 template <int D>
+__device__ __forceinline__ uint4* v_chunk(uint8_t* v, int row, int c16, int rpb) {
+  constexpr int VROW = Cfg<D>::VROW, per = VROW / 16;
+  const int in = row & (rpb - 1);
+  return reinterpret_cast<uint4*>(v + (row - in) * D + (c16 / per) * (rpb * VROW) + in * VROW + (c16 % per) * 16);
+}
+
+// Zeros for the infinities and NaN in rows [from, n) of a V stage, by one warp;
+// whether there were any.  (Not inlined, and not in the kernel for one query token:
+// in that kernel's body it cost the prefix's tiles, which never come here, 1000 clocks
+// each, 49 -> 56 us for 64 sequences, and as a call still 1 us.)
+template <int D>
+__device__ __noinline__ bool clear_not_finite(uint8_t* v, int from, int n, int rpb) {
+  bool found = false;
+  for (int w = threadIdx.x & 31; w < (n - from) * (D / 16); w += 32) {
+    uint4* const at = v_chunk<D>(v, from + w / (D / 16), w % (D / 16), rpb);
+    const uint4 x = *at;
+    const uint4 bad = make_uint4(not_finite(x.x), not_finite(x.y), not_finite(x.z), not_finite(x.w));
+    if (bad.x | bad.y | bad.z | bad.w) {
+      *at = make_uint4(x.x ^ bad.x, x.y ^ bad.y, x.z ^ bad.z, x.w ^ bad.w);
+      found = true;
+    }
+  }
+  return __any_sync(0xffffffffu, found);
+}
+
+// several: more than one query token a sequence.
+template <int D, bool several>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     attn_shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                        const __grid_constant__ CUtensorMap tm_qp, const __grid_constant__ CUtensorMap tm_qt,
@@ -564,10 +613,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int n = cv.count();
       ok = wait_for(a, &ctl->pv_done[rv.s], rv.ph ^ 1u);
       if (!ok) return;
-      // as for K, with an arrival of each CTA; a tile that ends inside 16 keys reports
-      // to its own CTA, whose cleaning warp then arrives
+      // as for K, with an arrival of each CTA; a tile to be cleaned reports to its own
+      // CTA, whose cleaning warp then arrives
       uint32_t mbar = peer(tc::smem_u32(&ctl->v_full[rv.s]), 0);
-      if (n & 15) {
+      if (cleaned<several>(a, cv)) {
         mbar = peer(tc::smem_u32(&ctl->landed[rv.s]), rank);
         if (lane == 0) mbar_expect_tx(&ctl->landed[rv.s], (uint32_t)tile_rows(n) * D);
       } else if (lane == 0) {
@@ -673,28 +722,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       c.next(p);
     }
   } else if (warp == kCleanWarp) {
-    // ---- the rows past a tail's end ----
-    // A masked key has weight zero, but zero times a stale NaN is NaN: its values in
-    // the last 16 rows that the product reads become zeros.
+    // ---- values that a row of the job does not see ----
+    // The last 16 rows that the product reads: zeros past the end.  Tokens that only
+    // some queries of a sequence see: no infinities or NaN.
     Cursor c;
     c.init(p, ctl);
     Ring<C::NV> rv;
     uint32_t phases = 0;      // one bit per stage: its use of `landed` that comes next
     bool ok = true;
-    const int rpb = a.page < 64 ? a.page : 64, rsh = 31 - __clz(rpb);
+    const int rpb = a.page < 64 ? a.page : 64;
+    constexpr int chunks = D / 16;   // 16-byte pieces of a row
     for (; c.valid; c.next(p), rv.step()) {
+      if (!cleaned<several>(a, c)) continue;
       const int n = c.count();
-      if ((n & 15) == 0) continue;
       ok = wait_for(a, &ctl->landed[rv.s], (phases >> rv.s) & 1u);
       if (!ok) break;
       phases ^= 1u << rv.s;
-      uint8_t* v = ring + (C::NK + rv.s) * C::STAGE + (((n >> rsh) * D) << rsh);
-      constexpr int per = C::VROW / 16, chunks = per * C::VBLK;   // 16-byte pieces of a row
-      for (int w = lane; w < (16 - (n & 15)) * chunks; w += 32) {
-        const int row = (n & (rpb - 1)) + w / chunks, c16 = w % chunks;
-        *reinterpret_cast<uint4*>(v + (c16 / per) * (rpb * C::VROW) + row * C::VROW + (c16 % per) * 16) =
-            make_uint4(0, 0, 0, 0);
+      uint8_t* const v = ring + (C::NK + rv.s) * C::STAGE;
+      const int from = max(c.keys - a.steps + 1 - c.t * kTile, 0);   // the first hidden token
+      if (several && !c.prefix && from < n) {
+        const bool found = clear_not_finite<D>(v, from, n, rpb);
+        // for the join: by CTA, and whether more of the hidden tokens come in the next tile
+        if (lane == 0) p.hidden[c.slot_job * 4 + (c.keys - c.t * kTile > kTile ? 2 : 0) + rank] = found;
       }
+      for (int w = lane; w < (-n & 15) * chunks; w += 32)
+        *v_chunk<D>(v, n + w / chunks, w % chunks, rpb) = make_uint4(0, 0, 0, 0);
       tc::fence_proxy_async();
       __syncwarp();
       if (lane == 0) arrive_at(peer(tc::smem_u32(&ctl->v_full[rv.s]), 0));
@@ -872,7 +924,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // the GPU: 25 us of the latter for 512 tokens and heads.)
 constexpr int kJoinThreads = 256;
 
-template <int D>
+// (Of several query tokens a sequence the first kernel leaves out what is not finite
+// in the last ones' values.)
+template <int D, bool several>
 __global__ void __launch_bounds__(kJoinThreads) attn_shared_join(const __grid_constant__ SharedParams p) {
   __shared__ float4 acc[kJoinThreads];
   __shared__ float2 stat[kJoinThreads];
@@ -897,6 +951,17 @@ __global__ void __launch_bounds__(kJoinThreads) attn_shared_join(const __grid_co
   const int n_prefix = pre.y - pre.x + 1;
   const long long first[2] = {(long long)(job[0] + pre.x) * 256 + (blk & 1) * 128,
                               (long long)(pl.np ? pl.np + pl.shares : 0) * 256 + (long long)(job[1] + own.x) * pl.R};
+
+  // The tokens that this one sees and some other query of its sequence does not: [from,
+  // see), none unless the first kernel left something out among them.
+  int from = 0, see = 0;
+  if (several) {
+    const int len = tail_length(a, b);
+    const uchar4 found = *reinterpret_cast<const uchar4*>(p.hidden + job[1] * 4);
+    from = max(len - a.steps + 1, 0);
+    if (len > 0 && (found.x | found.y | (from / kTile < (len - 1) / kTile ? found.z | found.w : 0)) != 0)
+      see = len - (a.steps - 1 - step);
+  }
 
   const int items = pl.G * width4, d0 = blockIdx.z * width4;
   for (int i0 = 0; i0 < items; i0 += kJoinThreads) {
@@ -977,6 +1042,20 @@ __global__ void __launch_bounds__(kJoinThreads) attn_shared_join(const __grid_co
       // no key seen: zeros.  (A NaN sum stays NaN.)
       const float inv = L == 0.0f ? 0.0f : 1.0f / L;
       float r[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
+      if (several) {
+#pragma unroll 1
+        for (int j = from; j < see; ++j) {
+          const int pg = a.tail_pages[(size_t)b * a.tail_width + j / a.page];
+          if (pg < 0 || pg >= a.n_pages) continue;
+          const size_t at = ((size_t)pg * a.page + j % a.page) * pl.h_kv + hk;
+          const uint2 v = *reinterpret_cast<const uint2*>(a.v_cache + at * D + 4 * c4);
+          const uint32_t x = not_finite(v.x), y = not_finite(v.y);
+          r[0] += __uint_as_float(x << 16);
+          r[1] += __uint_as_float(x & 0xffff0000u);
+          r[2] += __uint_as_float(y << 16);
+          r[3] += __uint_as_float(y & 0xffff0000u);
+        }
+      }
       if (a.gate) {
         r[0] *= sigmoid(__uint_as_float(gt.x << 16));
         r[1] *= sigmoid(__uint_as_float(gt.x & 0xffff0000u));
@@ -1068,6 +1147,8 @@ cudaError_t launch_d(const AttnSharedArgs& a, cudaStream_t stream, int sms) {
   char* ws = static_cast<char*>(a.scratch);
   p.span = reinterpret_cast<int2*>(ws);
   ws += up256(((size_t)p.pl.np + (size_t)a.batch * a.h_kv) * sizeof(int2));
+  p.hidden = reinterpret_cast<uint8_t*>(ws);
+  ws += up256((size_t)a.batch * a.h_kv * 4);
   const size_t rows = slot_rows(p.pl, a.batch);
   p.ml = reinterpret_cast<float4*>(ws);
   ws += up256(rows * sizeof(float4));
@@ -1080,7 +1161,8 @@ cudaError_t launch_d(const AttnSharedArgs& a, cudaStream_t stream, int sms) {
   tk = tv = tqp;
   if (cached && (!cache_map(&tk, a, a.k_cache, false) || !cache_map(&tv, a, a.v_cache, true))) return cudaErrorInvalidValue;
   cudaError_t e;
-  if ((e = cudaFuncSetAttribute(attn_shared_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  const auto kernel = a.steps > 1 ? attn_shared_kernel<D, true> : attn_shared_kernel<D, false>;
+  if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 (int)C::SMEM)) != cudaSuccess)
     return e;
   // each launch passes under the kernel before it
@@ -1094,13 +1176,13 @@ cudaError_t launch_d(const AttnSharedArgs& a, cudaStream_t stream, int sms) {
   cfg.stream = stream;
   cfg.attrs = &overlap;
   cfg.numAttrs = 1;
-  if ((e = cudaLaunchKernelEx(&cfg, attn_shared_kernel<D>, tk, tv, tqp, tqt, p)) != cudaSuccess) return e;
+  if ((e = cudaLaunchKernelEx(&cfg, kernel, tk, tv, tqp, tqt, p)) != cudaSuccess) return e;
   int nz = 1;   // CTAs per token and key head
   while (nz < D / 32 && (long long)p.pl.ntok * p.pl.h_kv * nz < 6LL * sms) nz *= 2;
   cfg.gridDim = dim3(p.pl.ntok, p.pl.h_kv, nz);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, attn_shared_join<D>, p);
+  return cudaLaunchKernelEx(&cfg, a.steps > 1 ? attn_shared_join<D, true> : attn_shared_join<D, false>, p);
 }
 
 }  // namespace
@@ -1108,7 +1190,8 @@ cudaError_t launch_d(const AttnSharedArgs& a, cudaStream_t stream, int sms) {
 size_t attn_shared_scratch_bytes(int batch, int steps, int h_q, int h_kv, int d) {
   const Plan pl = make_plan(batch > 0 ? batch : 1, steps, h_q, h_kv, 1, kMaxShares);
   const size_t rows = slot_rows(pl, batch);
-  return up256(((size_t)pl.np + (size_t)batch * h_kv) * sizeof(int2)) + up256(rows * sizeof(float4)) + up256(rows * d * 4);
+  return up256(((size_t)pl.np + (size_t)batch * h_kv) * sizeof(int2)) + up256((size_t)batch * h_kv * 4) +
+         up256(rows * sizeof(float4)) + up256(rows * d * 4);
 }
 
 cudaError_t launch_attn_shared(const AttnSharedArgs& p, cudaStream_t stream) {

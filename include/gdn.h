@@ -545,7 +545,8 @@ gdn_status gdn_attn_prep(const gdn_attn_dims* dims, long long tokens, const void
  * themselves: query i sees the tail's tokens 0 .. tail_len[b] - steps + i.
  *   out = softmax(scale q [K_prefix; K_tail]^T) [V_prefix; V_tail] * sigmoid(gate)
  * The prefix is read once for the whole batch.  A query that sees no token at
- * all gives zeros.
+ * all gives zeros.  A token that a query does not see does not reach it, whatever
+ * its key and value hold; an infinity or NaN that it sees does.
  *
  *   page          tokens per page: 16, 32, 64, 128 or 256
  *   n_pages       pages of the caches
