@@ -73,6 +73,7 @@
 #include <cudaTypedefs.h>
 
 #include "../../include/gdn.h"
+#include "gdn_attn_ranges.h"
 #include "gdn_common.cuh"
 #include "gdn_launch.h"
 #include "gdn_prefill.cuh"
@@ -946,11 +947,12 @@ __global__ void __launch_bounds__(kJoinThreads) attn_shared_join(const __grid_co
   // SMs as they fell free, 176 us a call for 169 at 256 sequences.)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int2 none = make_int2(0, -1);   // no range
-  const int2 pre = pl.np ? p.span[job[0]] : none;
-  const int2 own = a.tail_width > 0 && a.tail_len[b] > 0 ? p.span[pl.np + job[1]] : none;
-  const int n_prefix = pre.y - pre.x + 1;
-  const long long first[2] = {(long long)(job[0] + pre.x) * 256 + (blk & 1) * 128,
-                              (long long)(pl.np ? pl.np + pl.shares : 0) * 256 + (long long)(job[1] + own.x) * pl.R};
+  const int2 pre_at = pl.np ? p.span[job[0]] : none;
+  const int2 own_at = a.tail_width > 0 && a.tail_len[b] > 0 ? p.span[pl.np + job[1]] : none;
+  const Ranges pre = ranges_of(pre_at.x, pre_at.y, pl.shares), own = ranges_of(own_at.x, own_at.y, pl.shares);
+  const long long first[2] = {
+      (long long)(job[0] + pre.first) * 256 + (blk & 1) * 128,
+      (long long)(pl.np ? pl.np + pl.shares : 0) * 256 + (long long)(job[1] + own.first) * pl.R};
 
   // The tokens that this one sees and some other query of its sequence does not: [from,
   // see), none unless the first kernel left something out among them.
@@ -1020,7 +1022,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_shared_join(const __grid_co
 #pragma unroll
       for (int k = 0; k < 2; ++k)
         join(p.ml + first[k] + in[k] + g, part + first[k] * (D / 4) + (long long)c4 * stride[k] + in[k] + g,
-             k ? own.y - own.x + 1 : n_prefix, apart[k], (long long)apart[k] * (D / 4));
+             k ? own.count : pre.count, apart[k], (long long)apart[k] * (D / 4));
     }
     acc[threadIdx.x] = o;
     stat[threadIdx.x] = make_float2(M, L);
