@@ -439,10 +439,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     return;
   }
 
-  if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(tc::smem_u32(&ctl->tmem)));
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
-  }
   if (warp == kCleanWarp) {
     if (lane < kMaxStages) {
       tc::mbar_init(&ctl->k_full[lane], 1);
@@ -464,6 +460,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
   // launched while the kernel before it runs: its results are there from here on
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  // Tensor memory only now: held before, it could be what the kernel before this one
+  // waits for, and neither would end.
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(tc::smem_u32(&ctl->tmem)));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+  }
   // ---- this pair's share: the running cost of the tails, then a search ----
   long long* scan = reinterpret_cast<long long*>(ring);   // [batch + 1] and warp totals, before the ring is used
   long long* wsum = scan + GDN_ATTN_MAX_BATCH + 8;
