@@ -134,7 +134,8 @@ __device__ __forceinline__ float2 two_sum(float a, float b) {
   return make_float2(s, (a - (s - bb)) + (b - bb));
 }
 
-// After a wait that gave up the results are unspecified; the status word tells.
+// One wait of a warp, all its lanes alike (they meet again right after it).  After a
+// wait that gave up the results are unspecified; the status word tells.
 __device__ __forceinline__ bool moe_wait(const MoeArgs& a, uint64_t* mbar, uint32_t parity) {
   uint32_t done;
   asm volatile(
@@ -144,7 +145,8 @@ __device__ __forceinline__ bool moe_wait(const MoeArgs& a, uint64_t* mbar, uint3
       : "=r"(done)
       : "r"(tc::smem_u32(mbar)), "r"(parity)
       : "memory");
-  if (done || tc::mbar_wait(mbar, parity, kWaitBudget)) return true;
+  if (__all_sync(0xffffffffu, done)) return true;
+  if (__all_sync(0xffffffffu, tc::mbar_wait(mbar, parity, kWaitBudget))) return true;
   record_status(a.status, GDN_ERR_DEVICE_TIMEOUT);
   return false;
 }
@@ -541,8 +543,11 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
   int n_tiles = s_tiles;
   // the loads' place: tile, chunk, the tile's rows; free stages
   int li = member < h_chunks ? i0 : 0x7fffffff, lc = member, ly = 8 * i0, ls = 0, free_stages = kStages;
+  // After a wait that gave up no later one waits and nothing more is asked for (a stage
+  // whose copy is late is still armed); what is on its way had that wait to arrive in.
+  bool ok = true;
   const auto fill = [&]() {
-    while (free_stages > 0 && li < n_tiles) {
+    while (ok && free_stages > 0 && li < n_tiles) {
       const bool shared = li < s_tiles;
       if (lane == 0)
         load_stage<true>(ring_a + ls * kStage, &full[ls], shared ? &maps.s_whole : &maps.whole,
@@ -577,7 +582,6 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
   const int g = lane >> 2, t4 = lane & 3;
   int cs = 0, flip = 0;
   uint32_t ph = 0;
-  bool ok = true;   // after a wait that gave up no later one waits
   for (int i = i0; i < n_tiles; i += tile_step) {
     const bool shared = i < s_tiles;
     const int j = shared ? -1 : (i - s_tiles) / e_tiles, r0 = (shared ? i : i - s_tiles - j * e_tiles) * 8;
@@ -762,8 +766,9 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
   uint32_t qj[kStages];
 #pragma unroll
   for (int s = 0; s < kStages; ++s) qi[s] = kEnd;
+  bool ok = true;   // after a wait that gave up no later one waits, and nothing more is asked for
   const auto fill = [&]() {
-    while (queued < kStages && l.i < p.tiles3) {
+    while (ok && queued < kStages && l.i < p.tiles3) {
       const bool shared = Entry::shared(l.j);
       if (lane == 0)
         load_stage<false>(ring_a + ls * kStage, &full[ls], shared ? &maps.s_whole : &maps.whole,
@@ -791,7 +796,6 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
   const int g = lane >> 2, t4 = lane & 3;
   int cs = 0;
   uint32_t ph = 0;
-  bool ok = true;   // after a wait that gave up no later one waits
   // Columns 8 n .. of an expert (pairs base + 8 n ..): this lane's activations.
   const int np = a.tokens * a.top_k;
   const auto load_act = [&](uint4 (&x)[P][4], uint32_t j, int c, int n) {

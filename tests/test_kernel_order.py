@@ -34,3 +34,20 @@ def test_tensor_memory_is_taken_after_the_kernel_before_is_done():
             seen += 1
             assert wait.start() < alloc.start(), (path, name)
     assert seen >= 1
+
+
+def test_no_copy_is_asked_for_after_a_wait_that_gave_up():
+    # A stage whose copy did not arrive in time is still armed: arming it again for another
+    # copy would be an arrival too many.  Every loop that fills stages asks for `ok` first.
+    seen = 0
+    for path, name, body in kernels():
+        for m in re.finditer(r"const auto fill = \[&\]\(\) \{\s*while \(([^{]*)\) \{", body):
+            seen += 1
+            assert m.group(1).startswith("ok && "), (path, name, m.group(1))
+            assert re.search(r"bool ok = true;", body[:m.start()]), (path, name)
+    assert seen == 2
+    # ... and the lanes of a warp agree on `ok`
+    src = open(os.path.join(CSRC, "gdn_moe.cu")).read()
+    wait = src[src.index("bool moe_wait("):]
+    wait = wait[:wait.index("\n}")]
+    assert re.search(r"__all_sync\(0xffffffffu, tc::mbar_wait\(", wait) and "__all_sync(0xffffffffu, done)" in wait
