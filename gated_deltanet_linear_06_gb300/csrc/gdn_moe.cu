@@ -12,11 +12,15 @@
 // dependent launch), so that between them only data is waited for:
 //   router   logits: a CTA takes 8 experts and 8 tokens, one warp an expert.  The
 //            chosen experts hang on which logits are larger, so the sums are
-//            compensated: each lane adds its products to S, which starts at a
-//            constant so large that it rounds them to a coarse grid exactly, and
-//            what S drops goes to a second sum.  Logits stay pairs of fp32 from
-//            there on (fp64 additions run at 1/64 of the rate here: with them the
-//            choice of 8 experts alone took 12 us).
+//            compensated: the products are exact in fp32, a lane adds them to two
+//            sums S and what each addition drops (Knuth's two-sum) to a second
+//            sum beside each.  With n products a sum the error is below
+//            ((n + 6) 2^-24)^2 of the products' sizes, whatever their scale, and
+//            some 2^-45 as a rule.  (S on a grid fixed for logits of size 1 cost 4
+//            operations a product where this costs 7, of which fp32 pairs do two at
+//            once, but kept no more than fp32 at 2^-14 of that size and beyond
+//            2^10.)  Logits stay pairs of fp32 from there on (fp64 additions run at
+//            1/64 of the rate here: with them the choice of 8 experts alone took 12 us).
 //   choice   a CTA per token: a bound from the lanes' maxima, then the few
 //            candidates above it count those before them (a warp that picked one
 //            maximum after the other took 15 us per token with 512 experts).
@@ -134,6 +138,21 @@ __device__ __forceinline__ float2 two_sum(float a, float b) {
   return make_float2(s, (a - (s - bb)) + (b - bb));
 }
 
+__device__ __forceinline__ float2 bf16_pair(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+// S += x w, and what the sum's rounding drops to lo: two two-sums of S and the exact
+// product x w, in pairs.
+__device__ __forceinline__ void add_product(float2& S, float2& lo, float2 x, float2 w) {
+  const float2 minus = make_float2(-1.0f, -1.0f);
+  const float2 s = __ffma2_rn(x, w, S);
+  const float2 nb = __ffma2_rn(s, minus, S);                       // -(s - S), what s took of x w
+  const float2 of_S = __ffma2_rn(__fadd2_rn(s, nb), minus, S);     // what s dropped of S
+  const float2 of_xw = __ffma2_rn(x, w, nb);                       // ... and of x w
+  lo = __fadd2_rn(lo, __fadd2_rn(of_S, of_xw));
+  S = s;
+}
+
 // One wait of a warp, all its lanes alike (they meet again right after it).  After a
 // wait that gave up the results are unspecified; the status word tells.
 __device__ __forceinline__ bool moe_wait(const MoeArgs& a, uint64_t* mbar, uint32_t parity) {
@@ -170,13 +189,9 @@ __global__ void __launch_bounds__(32 * kRouterWarps) moe_router_kernel(const Moe
   // load weights before they wait.
   wait_before();
   let_next_begin();
-  constexpr float kGrid = 1.5f * 2048;   // products go to S on a grid of 2^-12
-  float S[NT], lo[NT];
+  float2 S[NT], lo[NT];   // of even and of odd columns
 #pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    S[t] = kGrid;
-    lo[t] = 0.0f;
-  }
+  for (int t = 0; t < NT; ++t) S[t] = lo[t] = make_float2(0.0f, 0.0f);
   bool ok = true;
   uint32_t ph = 0;
   for (int k0 = 0; k0 < a.hidden; k0 += kRouterCols, ph ^= 1u) {
@@ -202,13 +217,7 @@ __global__ void __launch_bounds__(32 * kRouterWarps) moe_router_kernel(const Moe
           const uint4 xv = *reinterpret_cast<const uint4*>(rows + (8 + min(t, nt - 1)) * kRouterCols + k);
           const uint32_t xx[4] = {xv.x, xv.y, xv.z, xv.w};
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float wf = __uint_as_float(i & 1 ? ww[i >> 1] & 0xffff0000u : ww[i >> 1] << 16);
-            const float xf = __uint_as_float(i & 1 ? xx[i >> 1] & 0xffff0000u : xx[i >> 1] << 16);
-            const float s = fmaf(xf, wf, S[t]);
-            lo[t] += fmaf(xf, wf, -(s - S[t]));   // exact: what S did not take
-            S[t] = s;
-          }
+          for (int i = 0; i < 4; ++i) add_product(S[t], lo[t], bf16_pair(xx[i]), bf16_pair(ww[i]));
         }
       }
     }
@@ -217,8 +226,9 @@ __global__ void __launch_bounds__(32 * kRouterWarps) moe_router_kernel(const Moe
   if (warp >= ne) return;
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    // the lanes' pairs (S - grid, lo) join as pairs: the high parts' rounding is kept
-    float h = S[t] - kGrid, l = lo[t];
+    // the sums (S, lo) join as pairs: the high parts' rounding is kept
+    const float2 both = two_sum(S[t].x, S[t].y);
+    float h = both.x, l = (lo[t].x + lo[t].y) + both.y;
 #pragma unroll
     for (int m = 16; m >= 1; m >>= 1) {
       const float oh = __shfl_xor_sync(0xffffffffu, h, m), ol = __shfl_xor_sync(0xffffffffu, l, m);

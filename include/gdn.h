@@ -598,11 +598,14 @@ gdn_status gdn_attn_decode_shared(const gdn_attn_dims* dims, int page, long long
  *   topk_id      null or int32 [tokens][top_k];  topk_w null or fp32 [tokens][top_k]
  *   workspace    >= gdn_moe_step_workspace_bytes, 256-byte aligned
  * hidden, inter and shared_inter are multiples of 8, at most 16384; experts at
- * most 1024; top_k at most 32.  Router logits are summed so that they are exact
- * to about 48 bits; everything else is summed in fp32, the activations between
- * the two products are carried as sums of two bf16 (16 bits of significand) for a
- * bf16 output and of three (24 bits) for an fp32 output.  A token's result does
- * not depend on the other tokens of the call, bit for bit.
+ * most 1024; top_k at most 32.  Router logits are compensated sums in pairs of
+ * fp32: two logits are in their exact order when they are further apart than
+ * 2 (hidden / 64 + 10)^2 2^-48 of the sum of their products' sizes (2^-36 at hidden
+ * 2048; some 2^-45 as a rule), at any scale that fp32 holds.  Everything else is
+ * summed in fp32; the activations between the two products are carried as sums of
+ * two bf16 (16 bits of significand) for a bf16 output and of three (24 bits) for an
+ * fp32 output.  A token's result does not depend on the other tokens of the call,
+ * bit for bit.
  */
 typedef struct gdn_moe_dims {
   int hidden;
