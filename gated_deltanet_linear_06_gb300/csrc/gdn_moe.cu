@@ -236,7 +236,9 @@ __global__ void __launch_bounds__(32 * kRouterWarps) moe_router_kernel(const Moe
       h = r.x;
       l = (l + ol) + r.y;
     }
-    if (lane == 0 && t < nt) p.logit[(size_t)(t0 + t) * (a.experts + 1) + e0 + warp] = two_sum(h, l);
+    // (an infinite or NaN sum has no remainder: what was dropped on the way is NaN then)
+    if (lane == 0 && t < nt)
+      p.logit[(size_t)(t0 + t) * (a.experts + 1) + e0 + warp] = isfinite(h) ? two_sum(h, l) : make_float2(h, 0.0f);
   }
 }
 
@@ -325,11 +327,12 @@ __global__ void __launch_bounds__(kChoiceThreads) moe_choice_kernel(const MoePar
   }
   __syncthreads();
   if (tid < 32) {
-    float sum = 0.0f;   // in the order of the ranks, or of the warps
-    if (a.renorm)
+    float sum = 0.0f;   // in the order of the warps, or of the ranks
+    for (int w = 0; w < kChoiceThreads / 32; ++w) sum += part[w];
+    if (a.renorm && sum == sum) {   // with a NaN among the logits all of the softmax is NaN
+      sum = 0.0f;
       for (int k = 0; k < a.top_k; ++k) sum += chosen[k];
-    else
-      for (int w = 0; w < kChoiceThreads / 32; ++w) sum += part[w];
+    }
     if (lane < a.top_k) {
       const float w = chosen[lane] / sum;
       p.choice->weight[t * a.top_k + lane] = w;

@@ -601,7 +601,9 @@ gdn_status gdn_attn_decode_shared(const gdn_attn_dims* dims, int page, long long
  * most 1024; top_k at most 32.  Router logits are compensated sums in pairs of
  * fp32: two logits are in their exact order when they are further apart than
  * 2 (hidden / 64 + 10)^2 2^-48 of the sum of their products' sizes (2^-36 at hidden
- * 2048; some 2^-45 as a rule), at any scale that fp32 holds.  Everything else is
+ * 2048; some 2^-45 as a rule), at any scale that fp32 holds.  A NaN logit is chosen
+ * last; a token with a NaN or a positively infinite one has NaN for its weights and
+ * its y, with renorm as without, as softmax gives them.  Everything else is
  * summed in fp32; the activations between the two products are carried as sums of
  * two bf16 (16 bits of significand) for a bf16 output and of three (24 bits) for an
  * fp32 output.  A token's result does not depend on the other tokens of the call,

@@ -87,3 +87,54 @@ def test_weights_of_long_rows(H, scale):
         if renorm:
             want = want / want.sum(-1, keepdim=True)
         assert ((wts - want).abs() <= 2.0 ** -20 * want + 2.0 ** -149).all()
+
+
+@pytest.mark.parametrize("renorm", [0, 1])
+@pytest.mark.parametrize("H", [64, 2056])
+def test_a_router_row_that_is_not_finite_shows(H, renorm):
+    g = torch.Generator().manual_seed(7)
+    x = torch.randn(5, H, generator=g).to(BF)
+    x[:, 11] = torch.tensor([1.0, 2.0, 0.5, 3.0, -1.0]).to(BF)
+    w = (torch.randn(40, H, generator=g) * H ** -0.5).to(BF)
+    good_ids, good_w, good_y = route(x, w, 4, renorm)
+    for value in (NAN, INF, -INF):
+        bad = w.clone()
+        bad[17, 11] = value                       # logits NaN, or infinite of the token's sign
+        ids, wts, y = route(x, bad, 4, renorm)
+        for t in range(5):
+            logits = x[t].double() @ bad.double().t()
+            p = torch.softmax(logits, -1)         # NaN throughout with a NaN or a positive infinity
+            assert len(set(ids[t].tolist())) == 4 and (ids[t] >= 0).all() and (ids[t] < 40).all()
+            if p.isnan().any():
+                assert wts[t].isnan().all() and y[t].isnan().all()
+                assert bool((logits == INF).any()) == (17 in ids[t].tolist())
+            else:                                 # a weight of zero, the others as they would be
+                order = torch.sort(-logits, stable=True).indices[:4]
+                assert torch.equal(ids[t], order)
+                want = p[order] / (p[order].sum() if renorm else 1.0)
+                assert ((wts[t] - want).abs() <= 2.0 ** -20 * want).all() and y[t].isfinite().all()
+
+
+def test_an_infinite_gate_of_the_shared_expert_opens_or_closes_it():
+    g = torch.Generator().manual_seed(3)
+    x = torch.randn(2, 64, generator=g).to(BF)
+    x[:, 5] = torch.tensor([1.0, -1.0]).to(BF)
+    w = (torch.randn(8, 64, generator=g) * 0.1).to(BF)
+    sg = torch.zeros(64, dtype=BF)
+    sg[5] = INF
+    far = sg.clone()
+    far[5] = 200.0                                # its sigmoid is 1 or 0 in fp32
+    _, _, a = route(x, w, 2, sg=sg)
+    _, _, b = route(x, w, 2, sg=far)
+    assert torch.equal(a, b)
+
+
+def test_choosing_a_damaged_expert_among_all():
+    # every expert chosen: the NaN one comes last, and the weights are NaN
+    g = torch.Generator().manual_seed(9)
+    x = torch.randn(3, 64, generator=g).to(BF)
+    w = (torch.randn(6, 64, generator=g) * 0.1).to(BF)
+    w[2, 0] = NAN
+    for renorm in (0, 1):
+        ids, wts, y = route(x, w, 6, renorm)
+        assert (ids[:, 5] == 2).all() and wts.isnan().all() and y.isnan().all()
