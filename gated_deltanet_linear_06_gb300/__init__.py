@@ -562,15 +562,16 @@ def _view(t, name, tokens, heads, d):
         return None, 0, 0
     sh, st = t.shape, t.stride()
     if sh == (tokens, heads, d) and st[2] == 1 and t.is_cuda and t.dtype is _BF16:   # the usual case
-        return t.data_ptr(), st[0], st[1]
+        return t.data_ptr(), st[0] if tokens > 1 else 0, st[1] if heads > 1 else 0
     if not t.is_cuda or t.dtype != torch.bfloat16 or len(sh) < 3 or sh[-2] != heads or sh[-1] != d \
             or (d > 1 and st[-1] != 1) or t.numel() != tokens * heads * d:
         raise ValueError(f"{name}: want a CUDA bfloat16 tensor of [{tokens}, {heads}, {d}] with its "
                          f"last dimension contiguous, got {t.dtype} {tuple(sh)} strides {st}")
-    for i in range(len(sh) - 3):
-        if sh[i] > 1 and st[i] != st[i + 1] * sh[i + 1]:
+    lead = [(n, s) for n, s in zip(sh[:-2], st[:-2]) if n != 1]   # a size of one has no stride that matters
+    for (_, s), (n, inner) in zip(lead, lead[1:]):
+        if s != inner * n:
             raise ValueError(f"{name}: tokens are not evenly apart (strides {st})")
-    return t.data_ptr(), st[-3], st[-2]
+    return t.data_ptr(), lead[-1][1] if lead else 0, st[-2] if heads > 1 else 0
 
 
 def gdn_attn_prep(dims: AttnDims, q, k, v, q_norm_w, k_norm_w, inv_freq, freq_axis, pos, q_out,
