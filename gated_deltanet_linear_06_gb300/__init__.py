@@ -200,7 +200,10 @@ _BF16, _F32, _F64, _I32, _U8 = torch.bfloat16, torch.float32, torch.float64, tor
 
 def _stream(stream) -> int | None:
     if stream is None:                 # the current stream's handle, without a Stream object
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        try:
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        except AttributeError:         # private to torch: the public way where they are gone
+            stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
 
