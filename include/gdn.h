@@ -526,7 +526,8 @@ typedef struct gdn_attn_dims {
  *              axis out of range reads as axis 0)
  *   q_out      bf16 [tokens][h_q][d]; it may be q itself when q is dense
  *   k_cache, v_cache  bf16 [cache_rows][h_kv][d]
- * Two tokens with the same slot leave one of their rows there.
+ * Slots that are not negative have to differ: of two tokens with the same slot, each
+ * 16 bytes of the row in either cache may be the one's or the other's.
  */
 gdn_status gdn_attn_prep(const gdn_attn_dims* dims, long long tokens, const void* q,
                          long long q_token_stride, long long q_head_stride, const void* k,
@@ -565,6 +566,9 @@ gdn_status gdn_attn_prep(const gdn_attn_dims* dims, long long tokens, const void
  * A page index outside [0, n_pages) or a tail length outside
  * [0, tail_width * page] sets GDN_ERR_DEVICE_BOUNDS; the sequences that reach it
  * have unspecified outputs (nothing outside the caches is read).
+ * Before it meets the values, each softmax weight is rounded to bf16, which moves out
+ * by at most 2^-8 sum p |v| (times the gate's sigmoid) besides its own rounding;
+ * everything else, the weights' sum among it, is fp32.
  * The order of a row's sums depends on the batch, the lengths and the GPU's SM
  * count, and on nothing else: equal calls give equal bits, but a sequence's last
  * bits may differ between batches.
