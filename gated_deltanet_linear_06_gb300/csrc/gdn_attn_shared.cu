@@ -57,7 +57,8 @@
 // tail's tile costs as many clocks of products for its few rows.  The rest of a call
 // is 2.5 us before the first tile and 8 to 10 in the join.  Tables of 16-row pages
 // cost 16 copies a tile instead of 4, some 150 clocks each: pages of 64 rows or
-// more are better (17 sequences of 4 steps on 5000, pages of 16: 43 us).
+// more are better (17 sequences of 4 steps on 5000, pages of 16: 43 us, of which 1.3
+// for the look at the tails' last values).
 //
 // Masks.  A masked key's weight is zero, but zero times an infinity is NaN, and one
 // product serves all rows of a job.  So what the product reads of V is finite

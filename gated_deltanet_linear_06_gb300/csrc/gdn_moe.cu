@@ -7,9 +7,9 @@
 // weight rows by 8 tokens), because their cost then does not grow with the
 // tokens that share an expert.
 //
-// Four launches, each begun while the one before it runs (the first: as the caller's
-// last ends) (programmatic
-// dependent launch), so that between them only data is waited for:
+// Four launches by programmatic dependent launch, each begun while the one before it
+// runs (the first: as the caller's last ends), so that between them only data is
+// waited for:
 //   router   logits: a CTA takes 8 experts and 8 tokens, one warp an expert.  The
 //            chosen experts hang on which logits are larger, so the sums are
 //            compensated: the products are exact in fp32, a lane adds them to two
@@ -18,8 +18,8 @@
 //            ((n + 6) 2^-24)^2 of the products' sizes, whatever their scale, and
 //            some 2^-45 as a rule.  (S on a grid fixed for logits of size 1 cost 4
 //            operations a product where this costs 7, of which fp32 pairs do two at
-//            once, but kept no more than fp32 at 2^-14 of that size and beyond
-//            2^10.)  Logits stay pairs of fp32 from there on (fp64 additions run at
+//            once (64 tokens 21 us for 26.5, 16 tokens 8 for 9.5), but kept no more
+//            than fp32 for activations of 1e-4 and sums beyond 2^10.)  Logits stay pairs of fp32 from there on (fp64 additions run at
 //            1/64 of the rate here: with them the choice of 8 experts alone took 12 us).
 //   choice   a CTA per token: a bound from the lanes' maxima, then the few
 //            candidates above it count those before them (a warp that picked one
@@ -46,12 +46,14 @@
 // nothing in a token's arithmetic depends on the other tokens.
 //
 // Measured, all four (hidden 2048; router, choice, gate_up, down apart in us): one
-// token through 8 of 256 experts of 512 22.6 us (4, 4, 11, 9, overlapped); 16 tokens
-// 115 (8, 5, 65, 44); 64 tokens through 10 of 512 experts 412 (21, 6, 260, 135),
+// token through 8 of 256 experts of 512 22.4 us (4, 5, 11, 10, overlapped); 16 tokens
+// 117 (10, 5, 65, 45); 64 tokens through 10 of 512 experts 415 (27, 6, 260, 135),
 // 5.6 TB/s or 82 % of a copy's rate; 5 tokens through 6 of 64 experts of 1408 with an
-// fp32 result 91 (8, 4, 48, 43).  gate_up runs at the memory's rate.  down's warps
+// fp32 result 89 to 95 (9, 4, 47, 43).  gate_up runs at the memory's rate.  down's warps
 // are bound by their instructions (some 400 a chunk), and few experts spread unevenly over the four
-// teams (21 to 32 chunks a warp at 16 tokens).
+// teams (21 to 32 chunks a warp at 16 tokens).  A team's four warps take every fourth
+// chunk of 128 columns: experts of 512 keep all of them busy alike, of 128 or 256 one or
+// two of four, of 768 two twice as long as the others.
 //
 // The activations between the products are kept as sums of bf16, because the
 // tensor cores take both operands in one 16-bit type: two (16 bits of
