@@ -19,8 +19,9 @@
 //            some 2^-45 as a rule.  (S on a grid fixed for logits of size 1 cost 4
 //            operations a product where this costs 7, of which fp32 pairs do two at
 //            once (64 tokens 21 us for 26.5, 16 tokens 8 for 9.5), but kept no more
-//            than fp32 for activations of 1e-4 and sums beyond 2^10.)  Logits stay pairs of fp32 from there on (fp64 additions run at
-//            1/64 of the rate here: with them the choice of 8 experts alone took 12 us).
+//            than fp32 for activations of 1e-4 and sums beyond 2^10.)  Logits stay
+//            pairs of fp32 from there on (fp64 additions run at 1/64 of the rate here:
+//            with them the choice of 8 experts alone took 12 us).
 //   choice   a CTA per token: a bound from the lanes' maxima, then the few
 //            candidates above it count those before them (a warp that picked one
 //            maximum after the other took 15 us per token with 512 experts).
