@@ -700,9 +700,10 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
             const int c = 8 * n + 2 * t4 + o;
             if (c < cnt) {
               const float v = acc[n][o] / (1.0f + expf(-acc[n][o])) * acc[n][2 + o] * (shared ? __ldcg(&p.choice->shared_w[c]) : L.pair_w[col0 + c]);
-              const uint16_t hi = f32_to_bf16(v);
+              uint16_t hi = f32_to_bf16(v);
+              if ((hi & 0x7fff) == 0x7f80 && isfinite(v)) --hi;   // the largest bf16
               const size_t at = (size_t)(col0 + c) * cols + r0 + g;
-              const float rest = v - bf16_to_f32(hi);   // exact
+              const float rest = isinf(v) ? 0.0f : v - bf16_to_f32(hi);   // exact
               const uint16_t lo = f32_to_bf16(rest);
               act[at] = hi;
               act[plane + at] = lo;
