@@ -163,6 +163,17 @@ def lib() -> ctypes.CDLL:
             L.gdn_moe_step.restype = ctypes.c_int
             L.gdn_moe_step.argtypes = [MP, ctypes.c_int] + [_P] * 8 + [ctypes.c_int] + [_P] * 3 + \
                 [ctypes.c_size_t, _P, _P]
+            L.gdn_kv4_page_bytes.restype = ctypes.c_size_t
+            L.gdn_kv4_page_bytes.argtypes = [AP, ctypes.c_int]
+            L.gdn_kv4_store.restype = ctypes.c_int
+            L.gdn_kv4_store.argtypes = [AP, ctypes.c_int, ll, ll] + [_P, ll, ll] * 2 + [_P] * 4
+            L.gdn_kv4_load.restype = ctypes.c_int
+            L.gdn_kv4_load.argtypes = [AP, ctypes.c_int, ll, ll] + [_P] * 4 + [ctypes.c_int, _P, _P]
+            L.gdn_attn_decode_kv4_workspace_bytes.restype = ctypes.c_size_t
+            L.gdn_attn_decode_kv4_workspace_bytes.argtypes = [AP, ctypes.c_int, ctypes.c_int]
+            L.gdn_attn_decode_kv4.restype = ctypes.c_int
+            L.gdn_attn_decode_kv4.argtypes = [AP, ctypes.c_int, ll, ctypes.c_int, ctypes.c_int] + [_P] * 3 + \
+                [ctypes.c_int, _P, _P, ll, ll, _P, _P, ctypes.c_size_t, _P, _P]
             L.gdn_read_device_status.restype = ctypes.c_int
             L.gdn_read_device_status.argtypes = [_P, _P, ctypes.POINTER(ctypes.c_int32)]
             _lib = L
@@ -657,6 +668,72 @@ def gdn_moe_step(dims: MoeDims, x, w_router, w_gate_up, w_down, y, workspace, w_
         _ptr(workspace, _U8, "workspace"), workspace.numel(),
         _ptr(device_status, i32, "device_status", 1), _stream(stream))
     _check(st, "gdn_moe_step")
+
+
+def gdn_kv4_page_bytes(dims: AttnDims, page: int) -> int:
+    """Bytes of one page of the 4-bit cache ([h_kv, page / 16, 18 d])."""
+    return lib().gdn_kv4_page_bytes(ctypes.byref(dims), int(page))
+
+
+def _kv4_cache(dims, cache):
+    """Address, page size and page count of a 4-bit cache [pages, h_kv, page / 16, 18 d]."""
+    sh = cache.shape
+    if len(sh) != 4 or sh[1] != dims.h_kv or sh[3] != 18 * dims.d:
+        raise ValueError(f"cache: want uint8 [pages, h_kv, page / 16, 18 d], got {tuple(sh)}")
+    return _ptr(cache, _U8, "cache"), 16 * sh[2], sh[0]
+
+
+def gdn_kv4_store(dims: AttnDims, k, v, cache, slot=None, device_status=None, stream=None):
+    """Rows of k and v ([T, h_kv, d] views, None leaves one out) into the 4-bit cache
+    [pages, h_kv, page / 16, 18 d] uint8; slot [T] int32 names each token's row."""
+    h, d = dims.h_kv, dims.d
+    lead = k if k is not None else v
+    T = lead.shape[0] if lead is not None else 0
+    addr, page, pages = _kv4_cache(dims, cache)
+    st = lib().gdn_kv4_store(
+        ctypes.byref(dims), page, pages, T, *_view(k, "k", T, h, d), *_view(v, "v", T, h, d),
+        _ptr(slot, _I32, "slot", T), addr, _ptr(device_status, _I32, "device_status", 1), _stream(stream))
+    _check(st, "gdn_kv4_store")
+
+
+def gdn_kv4_load(dims: AttnDims, cache, k_out, v_out, slot=None, device_status=None, stream=None):
+    """Rows of the 4-bit cache into k_out and v_out ([T, h_kv, d] bf16 or fp32, None
+    leaves one out); slot [T] int32 names each row (None: rows 0 .. T - 1)."""
+    lead = k_out if k_out is not None else v_out
+    T, dt = (lead.shape[0], lead.dtype) if lead is not None else (0, _BF16)
+    if dt not in (_BF16, _F32):
+        raise ValueError("k_out, v_out: want bfloat16 or float32")
+    n = T * dims.h_kv * dims.d
+    addr, page, pages = _kv4_cache(dims, cache)
+    st = lib().gdn_kv4_load(
+        ctypes.byref(dims), page, pages, T, _ptr(slot, _I32, "slot", T), addr, _ptr(k_out, dt, "k_out", n),
+        _ptr(v_out, dt, "v_out", n), GDN_DTYPE_F32 if dt is _F32 else GDN_DTYPE_BF16,
+        _ptr(device_status, _I32, "device_status", 1), _stream(stream))
+    _check(st, "gdn_kv4_load")
+
+
+def gdn_attn_decode_kv4_workspace_bytes(dims: AttnDims, batch: int, steps: int = 1) -> int:
+    return lib().gdn_attn_decode_kv4_workspace_bytes(ctypes.byref(dims), int(batch), int(steps))
+
+
+def gdn_attn_decode_kv4(dims: AttnDims, q, cache, table, lens, out, workspace, gate=None,
+                        device_status=None, stream=None):
+    """Attention of q [B, steps, h_q, d] over the 4-bit cache [pages, h_kv, page / 16,
+    18 d]: sequence b holds lens[b] tokens in the pages of table [B, width], its query
+    tokens last."""
+    bf, i32 = _BF16, _I32
+    B, S = q.shape[:2]
+    h_q, d = dims.h_q, dims.d
+    n = B * S * h_q * d
+    addr, page, pages = _kv4_cache(dims, cache)
+    width = 0 if table is None else int(table.shape[-1])
+    g, g_st, g_sh = _view(gate, "gate", B * S, h_q, d)
+    st = lib().gdn_attn_decode_kv4(
+        ctypes.byref(dims), page, pages, B, S, _ptr(q, bf, "q", n), addr, _ptr(table, i32, "table", B * width),
+        width, _ptr(lens, i32, "lens", B), g, g_st, g_sh, _ptr(out, bf, "out", n),
+        _ptr(workspace, _U8, "workspace"), workspace.numel(), _ptr(device_status, i32, "device_status", 1),
+        _stream(stream))
+    _check(st, "gdn_attn_decode_kv4")
 
 
 def gdn_read_device_status(status_word, stream=None) -> int:

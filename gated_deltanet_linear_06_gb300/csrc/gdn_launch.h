@@ -172,4 +172,34 @@ struct MoeArgs {
 cudaError_t launch_moe(const MoeArgs& p, cudaStream_t stream);
 size_t moe_scratch_bytes(int tokens, int hidden, int inter, int experts, int top_k, int shared_inter);
 
+// gdn_kv4_store and gdn_kv4_load: rows of k and v into the 4-bit cache and out of it.
+// Element strides; a null k or v (k_out or v_out) leaves that part out.
+struct Kv4RowsArgs {
+  const uint16_t *k, *v;   // of a load: the outputs, to say which there are
+  long long k_st, k_sh, v_st, v_sh;
+  const int32_t* slot;
+  uint8_t* cache;
+  void *k_out, *v_out;
+  int32_t* status;
+  long long tokens, cache_rows;
+  int h_kv, d, page;
+  bool out_f32;
+};
+cudaError_t launch_kv4_store(const Kv4RowsArgs& p, cudaStream_t stream);
+cudaError_t launch_kv4_load(const Kv4RowsArgs& p, cudaStream_t stream);
+
+struct AttnKv4Args {
+  const uint16_t *q, *gate;
+  const uint8_t* cache;
+  const int32_t *table, *len;
+  long long n_pages, gate_st, gate_sh;
+  uint16_t* out;
+  void* scratch;
+  int32_t* status;
+  int batch, steps, h_q, h_kv, d, page, width;
+  float scale;
+};
+cudaError_t launch_attn_kv4(const AttnKv4Args& p, cudaStream_t stream);
+size_t attn_kv4_scratch_bytes(int batch, int steps, int h_q, int h_kv, int d);
+
 }  // namespace gdn

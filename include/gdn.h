@@ -631,6 +631,90 @@ gdn_status gdn_moe_step(const gdn_moe_dims* dims, int tokens, const void* x, con
                         int out_dtype, int32_t* topk_id, float* topk_w, void* workspace,
                         size_t workspace_bytes, int32_t* device_status, void* stream);
 
+/*
+ * The attention layers' cache in 4 bits.  A quarter of the bytes of the bf16 cache and
+ * an eighth of that again for scales: 4.5 bits a value.
+ *   gdn_kv4_store        rows of k and v into the cache (after gdn_attn_prep's norms and
+ *                        positions: its k_cache and v_cache arguments can be plain rows)
+ *   gdn_kv4_load         rows out of it, as bf16 or fp32
+ *   gdn_attn_decode_kv4  attention over it, a page table for each sequence
+ *
+ * Values.  The d channels of a token and head are held in groups of 32.  Of a group x
+ * of bf16, with m its element of largest magnitude (the positive one where +m and -m
+ * both occur), s = -m / 8 and code c = clamp(rint(x / s), -8, 7), ties to even; it
+ * stands for s c, exactly.  A group whose |m| is below 2^-90 is held as zeros; one with
+ * an infinity or a NaN in it reads back as NaN throughout.
+ *
+ * Cache.  uint8 [n_pages][h_kv][page / 16][18 d], page 16, 32, 64, 128 or 256 tokens;
+ * cache row r = page_index * page + offset is one token.  16 tokens of a head are a unit
+ * of 18 d bytes: 8 d of K codes, 8 d of V codes, and bf16 scales [token][d / 32 of K |
+ * d / 32 of V].  Code + 8 is four bits; eight of them are a 32-bit word, and words stand
+ * in 16-byte vectors [vector][32 lanes][4 words].  For token j of the unit and channel c,
+ * word w = (j / 8) * (d / 32) + c / 32 is word w % 4 of vector w / 4, in
+ *   K: lane (j % 8) * 4 + (c % 32) / 8, nibble (c % 8) / 2 + 4 (c % 2) (nibble 0 the lowest
+ *      four bits), the whole word then rotated left by 3 bits;
+ *   V: lane (c % 32) / 4 * 4 + (j % 8) / 2, nibble c % 4 + 4 (j % 2).
+ * A row's bytes are its own: storing one leaves every other row as it was.
+ */
+size_t gdn_kv4_page_bytes(const gdn_attn_dims* dims, int page); /* 0 for invalid arguments */
+
+/*
+ *   tokens     rows in the list
+ *   k, v       bf16, element strides (token, head), multiples of 8, the d elements of a
+ *              head contiguous; null: that part of the rows stays as it is
+ *   slot       int32 [tokens]: the cache row of each; negative: not stored (a load gives
+ *              zeros).  Null: token t is row t.  A row at or past n_pages * page sets
+ *              GDN_ERR_DEVICE_BOUNDS and counts as negative.  Rows to be stored have to
+ *              differ: of two alike, each piece may be the one's or the other's.
+ *   cache      as above, n_pages pages
+ *   k_out, v_out  [tokens][h_kv][d], bf16 or fp32 per out_dtype; null: not wanted
+ */
+gdn_status gdn_kv4_store(const gdn_attn_dims* dims, int page, long long n_pages, long long tokens,
+                         const void* k, long long k_token_stride, long long k_head_stride,
+                         const void* v, long long v_token_stride, long long v_head_stride,
+                         const int32_t* slot, void* cache, int32_t* device_status, void* stream);
+gdn_status gdn_kv4_load(const gdn_attn_dims* dims, int page, long long n_pages, long long tokens,
+                        const int32_t* slot, const void* cache, void* k_out, void* v_out,
+                        int out_dtype, int32_t* device_status, void* stream);
+
+/*
+ * Attention of a batch over the 4-bit cache.  Sequence b holds len[b] tokens in the pages
+ * that its row of the table names, the last `steps` of which are its query tokens
+ * themselves: query i sees tokens 0 .. len[b] - steps + i.
+ *   out = softmax(scale q K^T) V * sigmoid(gate)
+ * A query that sees no token gives zeros.  A token that a query does not see does not
+ * reach it, whatever the cache holds there; a NaN that it sees does.  Sequences may
+ * share pages (a prefix's are then read from memory about once).
+ *
+ *   batch, steps  at most GDN_ATTN_MAX_BATCH and GDN_ATTN_MAX_STEPS; steps * h_q / h_kv
+ *                 at most GDN_ATTN_MAX_ROWS
+ *   q             bf16 [batch][steps][h_q][d]
+ *   cache         as above
+ *   table         int32 [batch][table_width], entries past a sequence's end unread; null
+ *                 when table_width is 0
+ *   len           int32 [batch], device: a call's launches do not depend on the lengths,
+ *                 so a captured step stays valid while they grow
+ *   gate          null, or bf16 with element strides (token, head), multiples of 8,
+ *                 token = b * steps + i
+ *   out           bf16 [batch][steps][h_q][d]
+ *   workspace     >= gdn_attn_decode_kv4_workspace_bytes, 256-byte aligned
+ * A length outside [0, table_width * page] or a page index outside [0, n_pages) sets
+ * GDN_ERR_DEVICE_BOUNDS: the sequence counts as empty, and the outputs of one that
+ * reaches such a page are unspecified (nothing outside the cache is read).
+ * Each softmax weight times its token's scale is rounded to bf16 before it meets the codes,
+ * which moves out by at most 2^-8 sum p |v| besides its own rounding; everything else is
+ * fp32.  Magnitudes of q are to be below 2^110.  Equal calls give equal bits; the order
+ * of a row's sums, and with it the last bits, depends on the batch, the lengths and the
+ * GPU's SM count.
+ */
+size_t gdn_attn_decode_kv4_workspace_bytes(const gdn_attn_dims* dims, int batch, int steps);
+gdn_status gdn_attn_decode_kv4(const gdn_attn_dims* dims, int page, long long n_pages, int batch,
+                               int steps, const void* q, const void* cache, const int32_t* table,
+                               int table_width, const int32_t* len, const void* gate,
+                               long long gate_token_stride, long long gate_head_stride, void* out,
+                               void* workspace, size_t workspace_bytes, int32_t* device_status,
+                               void* stream);
+
 /* Waits for the stream, then reads a device status word (the first 4 bytes
  * of a prefill workspace, or a decode device_status word) into *code:
  * GDN_OK or the first device-side error recorded.  Returns GDN_ERR_CUDA if
