@@ -40,6 +40,9 @@ class GdnError(RuntimeError):
         super().__init__(f"{where}: {gdn_status_string(status)}")
 
 
+_BF16, _F32, _F64, _I32, _U8 = torch.bfloat16, torch.float32, torch.float64, torch.int32, torch.uint8
+
+
 class Dims(ctypes.Structure):
     """gdn_dims."""
     _fields_ = [("h_k", ctypes.c_int), ("h_v", ctypes.c_int), ("d_k", ctypes.c_int),
@@ -73,6 +76,42 @@ def make_moe_dims(hidden=2048, inter=512, experts=256, top_k=8, shared_inter=0,
 def make_dims(h_k=16, h_v=32, d_k=128, d_v=128, conv_w=4, chunk=64, l2_eps=1e-6,
               rms_eps=1e-6) -> Dims:
     return Dims(h_k, h_v, d_k, d_v, conv_w, chunk, l2_eps, rms_eps)
+
+
+class PagePool(ctypes.Structure):
+    """gdn_page_pool; ``keep`` holds the tensors it points into."""
+    _fields_ = [("n_pages", ctypes.c_int), ("page", ctypes.c_int), ("n_seqs", ctypes.c_int),
+                ("width", ctypes.c_int), ("refs", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("len", ctypes.c_void_p)]
+
+
+class PageCaches(ctypes.Structure):
+    """gdn_page_caches; ``keep`` holds the tensors it points into."""
+    _fields_ = [("n", ctypes.c_int), ("base", ctypes.POINTER(ctypes.c_void_p)),
+                ("page_bytes", ctypes.POINTER(ctypes.c_size_t))]
+
+
+def make_page_pool(refs, table, lens, page: int) -> PagePool:
+    """A pool over device int32 tensors: refs [n_pages], table [n_seqs, width], lens [n_seqs]."""
+    if table.dim() != 2 or refs.dim() != 1 or lens.dim() != 1 or table.shape[0] != lens.shape[0]:
+        raise ValueError("want refs [n_pages], table [n_seqs, width] and lens [n_seqs]")
+    p = PagePool(refs.numel(), int(page), table.shape[0], table.shape[1], _ptr(refs, _I32, "refs"),
+                 _ptr(table, _I32, "table"), _ptr(lens, _I32, "lens"))
+    p.keep = (refs, table, lens)
+    return p
+
+
+def make_page_caches(caches) -> PageCaches:
+    """The caches that follow one pool's tables: contiguous tensors [n_pages, ...]."""
+    caches = tuple(caches)
+    if len({c.shape[0] for c in caches}) > 1:
+        raise ValueError("caches: want as many pages in each")
+    base = (ctypes.c_void_p * max(1, len(caches)))(*(_ptr(c, c.dtype, "cache") for c in caches))
+    size = (ctypes.c_size_t * max(1, len(caches)))(
+        *(c.numel() // max(1, c.shape[0]) * c.element_size() for c in caches))
+    p = PageCaches(len(caches), base, size)
+    p.keep, p.pages = (caches, base, size), caches[0].shape[0] if caches else 0
+    return p
 
 
 _lib = None
@@ -174,6 +213,22 @@ def lib() -> ctypes.CDLL:
             L.gdn_attn_decode_kv4.restype = ctypes.c_int
             L.gdn_attn_decode_kv4.argtypes = [AP, ctypes.c_int, ll, ctypes.c_int, ctypes.c_int] + [_P] * 3 + \
                 [ctypes.c_int, _P, _P, ll, ll, _P, _P, ctypes.c_size_t, _P, _P]
+            PP, PC, ci = ctypes.POINTER(PagePool), ctypes.POINTER(PageCaches), ctypes.c_int
+            tail = [_P, ctypes.c_size_t, _P, _P]      # workspace, its bytes, status, stream
+            L.gdn_pages_workspace_bytes.restype = ctypes.c_size_t
+            L.gdn_pages_workspace_bytes.argtypes = [PP]
+            L.gdn_pages_extend.restype = ctypes.c_int
+            L.gdn_pages_extend.argtypes = [PP, _P, ci, ci, _P, _P] + tail
+            L.gdn_pages_trim.restype = ctypes.c_int
+            L.gdn_pages_trim.argtypes = [PP, PC, _P, ci, _P] + tail
+            L.gdn_pages_fork.restype = ctypes.c_int
+            L.gdn_pages_fork.argtypes = [PP, PC, _P, _P, ci] + tail
+            L.gdn_pages_free.restype = ctypes.c_int
+            L.gdn_pages_free.argtypes = [PP, _P, ci] + tail
+            L.gdn_pages_compact.restype = ctypes.c_int
+            L.gdn_pages_compact.argtypes = [PP, PC, _P] + tail
+            L.gdn_pages_copy.restype = ctypes.c_int
+            L.gdn_pages_copy.argtypes = [PC, ci, _P, PC, ci, _P, ci, _P, _P]
             L.gdn_read_device_status.restype = ctypes.c_int
             L.gdn_read_device_status.argtypes = [_P, _P, ctypes.POINTER(ctypes.c_int32)]
             _lib = L
@@ -204,9 +259,6 @@ def gdn_prefill_segment_tokens_for(dims: Dims, n_seqs: int, total_tokens: int, s
     """gdn_prefill's segment length on a GPU with `sms` SMs (no device needed)."""
     return lib().gdn_prefill_segment_tokens_for(ctypes.byref(dims), int(n_seqs),
                                                 int(total_tokens), int(sms))
-
-
-_BF16, _F32, _F64, _I32, _U8 = torch.bfloat16, torch.float32, torch.float64, torch.int32, torch.uint8
 
 
 def _stream(stream) -> int | None:
@@ -734,6 +786,82 @@ def gdn_attn_decode_kv4(dims: AttnDims, q, cache, table, lens, out, workspace, g
         _ptr(workspace, _U8, "workspace"), workspace.numel(), _ptr(device_status, i32, "device_status", 1),
         _stream(stream))
     _check(st, "gdn_attn_decode_kv4")
+
+
+def gdn_pages_workspace_bytes(pool: PagePool) -> int:
+    return lib().gdn_pages_workspace_bytes(ctypes.byref(pool))
+
+
+def _pool_caches(pool, caches):
+    if caches is None:
+        return None
+    if caches.n and caches.pages != pool.n_pages:
+        raise ValueError(f"caches: want {pool.n_pages} pages each, as the pool has")
+    return ctypes.byref(caches)
+
+
+def gdn_pages_extend(pool: PagePool, slot, workspace, seq=None, count=None, device_status=None, stream=None):
+    """Sequences seq [n] (None: the first n) grow by slot's [n, steps] tokens, or by
+    count [n] of them; slot receives the new tokens' cache rows."""
+    i32 = _I32
+    n, steps = slot.shape
+    st = lib().gdn_pages_extend(
+        ctypes.byref(pool), _ptr(seq, i32, "seq", n), n, steps, _ptr(count, i32, "count", n),
+        _ptr(slot, i32, "slot"), _ptr(workspace, _U8, "workspace"), workspace.numel(),
+        _ptr(device_status, i32, "device_status", 1), _stream(stream))
+    _check(st, "gdn_pages_extend")
+
+
+def gdn_pages_trim(pool: PagePool, caches, new_len, workspace, seq=None, device_status=None, stream=None):
+    """Sequences seq [n] (None: the first n) keep their first new_len [n] tokens."""
+    i32, n = _I32, new_len.numel()
+    st = lib().gdn_pages_trim(
+        ctypes.byref(pool), _pool_caches(pool, caches), _ptr(seq, i32, "seq", n), n, _ptr(new_len, i32, "new_len"),
+        _ptr(workspace, _U8, "workspace"), workspace.numel(), _ptr(device_status, i32, "device_status", 1),
+        _stream(stream))
+    _check(st, "gdn_pages_trim")
+
+
+def gdn_pages_fork(pool: PagePool, caches, src, dst, workspace, device_status=None, stream=None):
+    """Empty sequences dst [n] become what src [n] are: pages shared, partly filled ones copied."""
+    i32, n = _I32, src.numel()
+    st = lib().gdn_pages_fork(
+        ctypes.byref(pool), _pool_caches(pool, caches), _ptr(src, i32, "src"), _ptr(dst, i32, "dst", n), n,
+        _ptr(workspace, _U8, "workspace"), workspace.numel(), _ptr(device_status, i32, "device_status", 1),
+        _stream(stream))
+    _check(st, "gdn_pages_fork")
+
+
+def gdn_pages_free(pool: PagePool, seq, workspace, device_status=None, stream=None):
+    """Sequences seq [n] give up their pages and hold no tokens."""
+    i32, n = _I32, seq.numel()
+    st = lib().gdn_pages_free(
+        ctypes.byref(pool), _ptr(seq, i32, "seq"), n, _ptr(workspace, _U8, "workspace"), workspace.numel(),
+        _ptr(device_status, i32, "device_status", 1), _stream(stream))
+    _check(st, "gdn_pages_free")
+
+
+def gdn_pages_compact(pool: PagePool, caches, workspace, n_live=None, device_status=None, stream=None):
+    """Pages in use become pages 0 .. n_live - 1, in every cache and table."""
+    i32 = _I32
+    st = lib().gdn_pages_compact(
+        ctypes.byref(pool), _pool_caches(pool, caches), _ptr(n_live, i32, "n_live", 1),
+        _ptr(workspace, _U8, "workspace"), workspace.numel(), _ptr(device_status, i32, "device_status", 1),
+        _stream(stream))
+    _check(st, "gdn_pages_compact")
+
+
+def gdn_pages_copy(src: PageCaches, dst: PageCaches, src_page=None, dst_page=None, n=None, device_status=None,
+                   stream=None):
+    """Pages src_page [n] of every cache of src to pages dst_page [n] of dst's (None: 0 .. n - 1)."""
+    i32 = _I32
+    if n is None:
+        lead = src_page if src_page is not None else dst_page
+        n = lead.numel() if lead is not None else min(src.pages, dst.pages)
+    st = lib().gdn_pages_copy(
+        ctypes.byref(src), src.pages, _ptr(src_page, i32, "src_page", n), ctypes.byref(dst), dst.pages,
+        _ptr(dst_page, i32, "dst_page", n), n, _ptr(device_status, i32, "device_status", 1), _stream(stream))
+    _check(st, "gdn_pages_copy")
 
 
 def gdn_read_device_status(status_word, stream=None) -> int:

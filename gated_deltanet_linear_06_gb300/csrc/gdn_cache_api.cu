@@ -1,4 +1,4 @@
-// gdn_cache_api.cu -- the extern "C" surface of the 4-bit cache: validation and launch,
+// gdn_cache_api.cu -- the extern "C" surface of the 4-bit cache and of the pages' pool: validation and launch,
 // on the same terms as gdn_api.cu (nothing is launched and nothing touched on a refused
 // argument).
 #include <cuda_runtime.h>
@@ -42,6 +42,60 @@ gdn_status check_decode(const gdn_attn_dims* d, int batch, int steps) {
     return GDN_ERR_UNSUPPORTED;
   return GDN_OK;
 }
+
+gdn_status check_pool(const gdn_page_pool* p) {
+  if (!p || p->n_pages < 0 || p->page < 1 || p->n_seqs < 0 || p->width < 0) return GDN_ERR_INVALID_ARG;
+  if (p->n_seqs > GDN_PAGES_MAX_SEQS || p->n_pages > 0x7fffffff / p->page || p->width > 0x7fffffff / p->page)
+    return GDN_ERR_UNSUPPORTED;
+  return GDN_OK;
+}
+
+// The pool's arrays and the workspace of a call that has something to do.
+gdn_status check_pool_memory(const gdn_page_pool* p, const void* workspace, size_t workspace_bytes) {
+  if ((p->n_pages > 0 && !p->refs) || (p->n_seqs > 0 && !p->len) || (p->n_seqs > 0 && p->width > 0 && !p->table) ||
+      !maybe16(p->refs) || !maybe16(p->table) || !maybe16(p->len))
+    return GDN_ERR_INVALID_ARG;
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < gdn::pages_scratch_bytes(p->n_pages, p->n_seqs))
+    return GDN_ERR_WORKSPACE;
+  return GDN_OK;
+}
+
+gdn_status check_list(const gdn_page_pool* p, const int32_t* seq, int n) {
+  if (n < 0 || !maybe16(seq) || n > p->n_seqs) return GDN_ERR_INVALID_ARG;
+  return n > GDN_PAGES_MAX_LIST ? GDN_ERR_UNSUPPORTED : GDN_OK;
+}
+
+// Copies within one set of caches, or between two alike.
+gdn_status check_caches(const gdn_page_caches* src, const gdn_page_caches* dst, gdn::PageMoves& m) {
+  m = {};
+  if (!src) return GDN_OK;
+  if (src->n < 0 || (dst && dst->n != src->n)) return GDN_ERR_INVALID_ARG;
+  if (src->n > GDN_PAGES_MAX_CACHES) return GDN_ERR_UNSUPPORTED;
+  if (src->n > 0 && (!src->base || !src->page_bytes || (dst && (!dst->base || !dst->page_bytes))))
+    return GDN_ERR_INVALID_ARG;
+  long long pieces = 0;
+  for (int i = 0; i < src->n; ++i) {
+    const size_t bytes = src->page_bytes[i];
+    if (!need16(src->base[i]) || (dst && (!need16(dst->base[i]) || dst->page_bytes[i] != bytes)) || bytes == 0 ||
+        bytes % 16 != 0)
+      return GDN_ERR_INVALID_ARG;
+    if (bytes > (size_t(1) << 32)) return GDN_ERR_UNSUPPORTED;
+    m.first[i] = (int)pieces;
+    m.src[i] = static_cast<const uint8_t*>(src->base[i]);
+    m.dst[i] = static_cast<uint8_t*>(dst ? dst->base[i] : src->base[i]);
+    m.bytes[i] = (long long)bytes;
+    pieces += gdn::page_pieces(bytes);
+  }
+  m.caches = src->n;
+  m.first[m.caches] = (int)pieces;   // at most 128 * 2^20
+  return GDN_OK;
+}
+
+gdn::PagePool pool_of(const gdn_page_pool* p) {
+  return gdn::PagePool{p->n_pages, p->page, p->n_seqs, p->width, p->refs, p->table, p->len};
+}
+
+gdn_status launched(cudaError_t e) { return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA; }
 
 }  // namespace
 
@@ -159,6 +213,108 @@ gdn_status gdn_attn_decode_kv4(const gdn_attn_dims* dims, int page, long long n_
   p.width = table_width;
   p.scale = dims->scale > 0.0f ? dims->scale : 1.0f / sqrtf((float)dims->d);
   return gdn::launch_attn_kv4(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+size_t gdn_pages_workspace_bytes(const gdn_page_pool* pool) {
+  if (check_pool(pool) != GDN_OK) return 0;
+  return gdn::pages_scratch_bytes(pool->n_pages, pool->n_seqs);
+}
+
+gdn_status gdn_pages_extend(const gdn_page_pool* pool, const int32_t* seq, int n, int steps, const int32_t* count,
+                            int32_t* slot, void* workspace, size_t workspace_bytes, int32_t* device_status,
+                            void* stream) {
+  gdn::TraceRange trace_range("gdn_pages_extend");
+  gdn_status st = check_pool(pool);
+  if (st == GDN_OK) st = check_list(pool, seq, n);
+  if (st != GDN_OK) return st;
+  if (steps < 0 || !aligned(device_status, 4) || !maybe16(count)) return GDN_ERR_INVALID_ARG;
+  if (n == 0 || steps == 0) return GDN_OK;
+  if (!need16(slot)) return GDN_ERR_INVALID_ARG;
+  if ((st = check_pool_memory(pool, workspace, workspace_bytes)) != GDN_OK) return st;
+  return launched(gdn::launch_pages_extend(pool_of(pool), gdn::PageList{seq, n}, steps, count, slot, workspace,
+                                           device_status, static_cast<cudaStream_t>(stream)));
+}
+
+gdn_status gdn_pages_trim(const gdn_page_pool* pool, const gdn_page_caches* caches, const int32_t* seq, int n,
+                          const int32_t* new_len, void* workspace, size_t workspace_bytes, int32_t* device_status,
+                          void* stream) {
+  gdn::TraceRange trace_range("gdn_pages_trim");
+  gdn::PageMoves m;
+  gdn_status st = check_pool(pool);
+  if (st == GDN_OK) st = check_list(pool, seq, n);
+  if (st == GDN_OK) st = check_caches(caches, nullptr, m);
+  if (st != GDN_OK) return st;
+  if (!aligned(device_status, 4)) return GDN_ERR_INVALID_ARG;
+  if (n == 0) return GDN_OK;
+  if (!need16(new_len)) return GDN_ERR_INVALID_ARG;
+  if ((st = check_pool_memory(pool, workspace, workspace_bytes)) != GDN_OK) return st;
+  return launched(gdn::launch_pages_trim(pool_of(pool), &m, gdn::PageList{seq, n}, new_len, workspace, device_status,
+                                         static_cast<cudaStream_t>(stream)));
+}
+
+gdn_status gdn_pages_fork(const gdn_page_pool* pool, const gdn_page_caches* caches, const int32_t* src,
+                          const int32_t* dst, int n, void* workspace, size_t workspace_bytes, int32_t* device_status,
+                          void* stream) {
+  gdn::TraceRange trace_range("gdn_pages_fork");
+  gdn::PageMoves m;
+  gdn_status st = check_pool(pool);
+  if (st == GDN_OK) st = check_list(pool, dst, n);
+  if (st == GDN_OK) st = check_caches(caches, nullptr, m);
+  if (st != GDN_OK) return st;
+  if (!aligned(device_status, 4)) return GDN_ERR_INVALID_ARG;
+  if (n == 0) return GDN_OK;
+  if (!need16(src) || !need16(dst)) return GDN_ERR_INVALID_ARG;
+  if ((st = check_pool_memory(pool, workspace, workspace_bytes)) != GDN_OK) return st;
+  return launched(gdn::launch_pages_fork(pool_of(pool), &m, src, dst, n, workspace, device_status,
+                                         static_cast<cudaStream_t>(stream)));
+}
+
+gdn_status gdn_pages_free(const gdn_page_pool* pool, const int32_t* seq, int n, void* workspace,
+                          size_t workspace_bytes, int32_t* device_status, void* stream) {
+  gdn::TraceRange trace_range("gdn_pages_free");
+  gdn_status st = check_pool(pool);
+  if (st == GDN_OK) st = check_list(pool, seq, n);
+  if (st != GDN_OK) return st;
+  if (!aligned(device_status, 4)) return GDN_ERR_INVALID_ARG;
+  if (n == 0) return GDN_OK;
+  if ((st = check_pool_memory(pool, workspace, workspace_bytes)) != GDN_OK) return st;
+  return launched(gdn::launch_pages_free(pool_of(pool), gdn::PageList{seq, n}, workspace, device_status,
+                                         static_cast<cudaStream_t>(stream)));
+}
+
+gdn_status gdn_pages_compact(const gdn_page_pool* pool, const gdn_page_caches* caches, int32_t* n_live,
+                             void* workspace, size_t workspace_bytes, int32_t* device_status, void* stream) {
+  gdn::TraceRange trace_range("gdn_pages_compact");
+  gdn::PageMoves m;
+  gdn_status st = check_pool(pool);
+  if (st == GDN_OK) st = check_caches(caches, nullptr, m);
+  if (st != GDN_OK) return st;
+  if (!aligned(device_status, 4) || !aligned(n_live, 4)) return GDN_ERR_INVALID_ARG;
+  if (pool->n_pages == 0 && !n_live) return GDN_OK;
+  if ((st = check_pool_memory(pool, workspace, workspace_bytes)) != GDN_OK) return st;
+  return launched(gdn::launch_pages_compact(pool_of(pool), &m, n_live, workspace, device_status,
+                                            static_cast<cudaStream_t>(stream)));
+}
+
+gdn_status gdn_pages_copy(const gdn_page_caches* src, int src_pages, const int32_t* src_page,
+                          const gdn_page_caches* dst, int dst_pages, const int32_t* dst_page, int n,
+                          int32_t* device_status, void* stream) {
+  gdn::TraceRange trace_range("gdn_pages_copy");
+  gdn::PageMoves m;
+  if (!src || !dst) return GDN_ERR_INVALID_ARG;
+  const gdn_status st = check_caches(src, dst, m);
+  if (st != GDN_OK) return st;
+  if (src_pages < 0 || dst_pages < 0 || n < 0 || !maybe16(src_page) || !maybe16(dst_page) ||
+      !aligned(device_status, 4) || (!src_page && n > src_pages) || (!dst_page && n > dst_pages))
+    return GDN_ERR_INVALID_ARG;
+  if (n == 0 || m.caches == 0) return GDN_OK;
+  m.from = src_page;
+  m.to = dst_page;
+  m.src_pages = src_pages;
+  m.dst_pages = dst_pages;
+  m.n = n;
+  m.status = device_status;
+  return launched(gdn::launch_pages_copy(m, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -202,4 +202,37 @@ struct AttnKv4Args {
 cudaError_t launch_attn_kv4(const AttnKv4Args& p, cudaStream_t stream);
 size_t attn_kv4_scratch_bytes(int batch, int steps, int h_q, int h_kv, int d);
 
+// gdn_pages_*: the pool's arrays, lists of sequences (null: 0 .. n - 1), copies of pages.
+struct PagePool {
+  int n_pages, page, n_seqs, width;
+  int32_t *refs, *table, *len;
+};
+struct PageList {
+  const int32_t* seq;
+  int n;
+};
+constexpr int kMaxPageCaches = 128;
+struct PageMoves {
+  const int32_t *from, *to;        // nullable: pair i is page i
+  int32_t* status;
+  int n, src_pages, dst_pages;
+  int caches;
+  int first[kMaxPageCaches + 1];   // a warp's pieces of a page, of the caches before each
+  const uint8_t* src[kMaxPageCaches];
+  uint8_t* dst[kMaxPageCaches];
+  long long bytes[kMaxPageCaches];
+};
+int page_pieces(size_t page_bytes);
+cudaError_t launch_pages_extend(const PagePool& p, const PageList& l, int steps, const int32_t* count, int32_t* slot,
+                                void* scratch, int32_t* status, cudaStream_t stream);
+cudaError_t launch_pages_trim(const PagePool& p, const PageMoves* caches, const PageList& l, const int32_t* new_len,
+                              void* scratch, int32_t* status, cudaStream_t stream);
+cudaError_t launch_pages_fork(const PagePool& p, const PageMoves* caches, const int32_t* src, const int32_t* dst, int n,
+                              void* scratch, int32_t* status, cudaStream_t stream);
+cudaError_t launch_pages_free(const PagePool& p, const PageList& l, void* scratch, int32_t* status, cudaStream_t stream);
+cudaError_t launch_pages_compact(const PagePool& p, const PageMoves* caches, int32_t* n_live, void* scratch,
+                                 int32_t* status, cudaStream_t stream);
+cudaError_t launch_pages_copy(const PageMoves& m, cudaStream_t stream);
+size_t pages_scratch_bytes(int n_pages, int n_seqs);
+
 }  // namespace gdn

@@ -715,6 +715,88 @@ gdn_status gdn_attn_decode_kv4(const gdn_attn_dims* dims, int page, long long n_
                                void* workspace, size_t workspace_bytes, int32_t* device_status,
                                void* stream);
 
+/*
+ * The pool that cache pages come from (the source pages' "two-group paged pool", its group
+ * of KV pages; the group of fixed states is gdn_state_copy's).  All its integers are
+ * device arrays of the caller's, which the calls below keep in step with each other:
+ *   refs   int32 [n_pages]          tables that hold the page; 0 (or less): it is free
+ *   table  int32 [n_seqs][width]    each sequence's pages in order, entries past its end
+ *                                   unread: what gdn_attn_decode_kv4 takes
+ *   len    int32 [n_seqs]           tokens of each sequence
+ * A pool starts as zeros; page: tokens of a page.  Every layer's cache whose rows follow the
+ * same tables takes part in the copies: gdn_page_caches names up to GDN_PAGES_MAX_CACHES
+ * arrays of n_pages pages, page_bytes[i] (a multiple of 16, at most 2^32) apart, 4-bit or
+ * bf16 (K and V then are two); base and page_bytes are host arrays, read during the call.
+ *
+ *   extend   sequence seq[i] grows by count[i] tokens (0 .. steps; all by steps when count
+ *            is null): pages are added as needed, and slot[i][j] is the cache row of its
+ *            new token j (-1 for j >= count[i]), for gdn_attn_prep and gdn_kv4_store
+ *   trim     sequence seq[i] keeps its first new_len[i] <= len tokens; where it then ends
+ *            inside a page that other tables hold too, it gets a copy of its own
+ *   fork     sequence dst[i], which holds no tokens, becomes what src[i] is when the call
+ *            begins: whole pages are shared, a partly filled last one is copied.  A
+ *            sequence may be forked several times in a call
+ *   free     sequence seq[i] gives up all its pages and holds no tokens
+ *   compact  pages in use move so that they are pages 0 .. n_live - 1 (each of those beyond
+ *            to the lowest free one, in order) and every table follows; *n_live, if given, a
+ *            device word, is set
+ *   copy     page src_page[i] of every cache of one set to page dst_page[i] of another's
+ *            (or the same): swapping pages out and in; no pool is involved
+ * Trimmed and freed sequences' entries become -1; a page whose count drops to 0 is free.
+ * Pages that calls add are the lowest free ones, in the order of the list.  A page that is
+ * not full belongs to one table alone (extend writes into it), which these calls see to.
+ *
+ *   seq, src, dst  int32 [n], device; a null seq is sequences 0 .. n - 1.  n at most n_seqs
+ *                  and GDN_PAGES_MAX_LIST
+ *   slot           int32 [n][steps]
+ *   caches         null, or no arrays: the tables alone are changed
+ *   workspace      >= gdn_pages_workspace_bytes, 256-byte aligned
+ * extend, trim, fork and free are done whole or not at all: a sequence out of range or
+ * named twice (as dst, of fork), a length or count that may not be, a fork into a sequence
+ * that holds tokens, or too few free pages sets GDN_ERR_DEVICE_BOUNDS and changes
+ * nothing (extend then gives -1 for all slots).  So does a page index out of range in a
+ * table or in copy's lists, but it is only passed over.  copy's pairs run at the same time:
+ * no destination may be another pair's, source or destination.
+ */
+#define GDN_PAGES_MAX_SEQS 65536
+#define GDN_PAGES_MAX_LIST 8192
+#define GDN_PAGES_MAX_CACHES 128
+
+typedef struct gdn_page_pool {
+  int n_pages;
+  int page;
+  int n_seqs;
+  int width;
+  int32_t* refs;
+  int32_t* table;
+  int32_t* len;
+} gdn_page_pool;
+
+typedef struct gdn_page_caches {
+  int n;
+  void* const* base;
+  const size_t* page_bytes;
+} gdn_page_caches;
+
+size_t gdn_pages_workspace_bytes(const gdn_page_pool* pool);
+gdn_status gdn_pages_extend(const gdn_page_pool* pool, const int32_t* seq, int n, int steps,
+                            const int32_t* count, int32_t* slot, void* workspace,
+                            size_t workspace_bytes, int32_t* device_status, void* stream);
+gdn_status gdn_pages_trim(const gdn_page_pool* pool, const gdn_page_caches* caches,
+                          const int32_t* seq, int n, const int32_t* new_len, void* workspace,
+                          size_t workspace_bytes, int32_t* device_status, void* stream);
+gdn_status gdn_pages_fork(const gdn_page_pool* pool, const gdn_page_caches* caches,
+                          const int32_t* src, const int32_t* dst, int n, void* workspace,
+                          size_t workspace_bytes, int32_t* device_status, void* stream);
+gdn_status gdn_pages_free(const gdn_page_pool* pool, const int32_t* seq, int n, void* workspace,
+                          size_t workspace_bytes, int32_t* device_status, void* stream);
+gdn_status gdn_pages_compact(const gdn_page_pool* pool, const gdn_page_caches* caches,
+                             int32_t* n_live, void* workspace, size_t workspace_bytes,
+                             int32_t* device_status, void* stream);
+gdn_status gdn_pages_copy(const gdn_page_caches* src, int src_pages, const int32_t* src_page,
+                          const gdn_page_caches* dst, int dst_pages, const int32_t* dst_page, int n,
+                          int32_t* device_status, void* stream);
+
 /* Waits for the stream, then reads a device status word (the first 4 bytes
  * of a prefill workspace, or a decode device_status word) into *code:
  * GDN_OK or the first device-side error recorded.  Returns GDN_ERR_CUDA if
