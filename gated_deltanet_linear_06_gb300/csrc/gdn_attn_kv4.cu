@@ -1,6 +1,8 @@
 // gdn_attn_kv4.cu -- attention of a batch of sequences over the 4-bit paged cache.
 #include <math.h>
 
+#include <type_traits>
+
 #include "../../include/gdn.h"
 #include "gdn_kv4.cuh"
 #include "gdn_launch.h"
@@ -10,7 +12,13 @@ namespace gdn {
 namespace {
 
 constexpr long long kWaitClocks = 2000000000LL;   // a second or so: a copy that has not come by then never will
-constexpr float kSlack = 20.0f;                    // binary orders between a row's reference and its maximum
+// A row's weights are 2^(score - ref); at an update of ref the largest is 2^(kTop - v), with
+// 2^v above the size of every scale of V so far.  Scores may grow by kGrow binary orders and
+// scales by kWide before the next update: a weight times a scale stays below 2^15, in fp16.
+constexpr float kTop = 8.0f, kGrow = 4.0f;
+constexpr int kWide = 3;
+constexpr int kLeastV = -93;                       // scales are zero or at least 2^-93
+constexpr float kStored = 28.0f;                   // shares are stored with weights up to 2^(kTop - kStored)
 constexpr int kMinItems = 2;                       // units that a warp takes at least
 constexpr int kMaxCtas = 160;                      // the workspace has room for
 constexpr int kMaxWarps = 16;
@@ -32,26 +40,35 @@ struct Kv4Params {
   float* part;               // per slot and row: d sums
 };
 
-// Rows (of 8) that a warp takes at once: two blocks where there are that many rows and
-// the accumulators leave room.
 template <int D, int NT>
 struct Cfg {
-  static constexpr int WARPS = D == 256 ? 8 : (NT == 1 ? 16 : 12);
-  static constexpr int STAGE = kv4::unit_bytes(D);
-  static constexpr int STAGES = D == 256 ? 5 : (D == 128 ? (NT == 1 ? 5 : 7) : (NT == 1 ? 10 : 12));
-  static constexpr int SMEM = WARPS * STAGES * STAGE;
+  static constexpr int R = D / 32;
+  static constexpr int UNITS = D == 256 && NT == 2 ? 1 : 2;   // met at once: a stage
+  static constexpr bool QREG = NT * R <= 8;          // q's operands in registers, else in shared memory
+  static constexpr bool BREG = NT * R <= 2;          // and the sums of their channels
+  static constexpr int WARPS = D == 64 && NT == 1 ? 12 : 8;
+  static constexpr int UNIT = kv4::unit_bytes(D), STAGE = UNITS * UNIT;
+  static constexpr int STAGES = D == 256 ? (NT == 1 ? 2 : 3) : (D == 128 ? 4 : 5);
+  static constexpr int QBYTES = QREG ? 0 : NT * R * 512, BBYTES = BREG ? 0 : NT * R * 64;   // a warp's
+  static constexpr int SMEM = WARPS * (STAGES * STAGE + QBYTES + BBYTES);
+  static_assert(SMEM <= 216 * 1024 && UNITS * STAGES <= 32, "shared memory, bits of `bad`");
 };
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));   // subnormal results count: scales of V may be huge
   return y;
 }
 
-__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+// d = a b + c over fp16, fp32 sums.
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, float c0,
+                                    float c1, float c2, float c3) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+}
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  mma(d, a, b0, b1, d[0], d[1], d[2], d[3]);
 }
 
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
@@ -60,13 +77,63 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   return y;
 }
 
-// Two codes, at bits 3..6 and 19..22 of x, as bf16 values code - 8: with the exponent of
-// 16 the bits read 16 + code, and 24 is taken off exactly.
-__device__ __forceinline__ uint32_t values(uint32_t x) {
-  uint32_t y;
-  asm("lop3.b32 %0, %1, 0x00780078, 0x41804180, 0xea;" : "=r"(y) : "r"(x));   // (x & mask) | base
-  asm("sub.rn.bf16x2 %0, %0, %1;" : "+r"(y) : "r"(0x41c041c0u));
-  return y;
+// Codes as fp16 values, two in a word: four bits anywhere among the ten of a significand,
+// under an exponent of zero, are that code times 2^(place - 24), exactly (a subnormal number,
+// which the tensor cores take as it is).  The other operand or the end result makes up for
+// the power of two, and a product takes off the 8 that each code is too much.
+constexpr uint32_t kAt0 = 0x000f000fu, kAt4 = 0x00f000f0u, kAt2 = 0x003c003cu, kAt6 = 0x03c003c0u;
+constexpr uint32_t kLess8At0 = 0x80088008u, kLess8At4 = 0x80808080u;   // -8 at those places
+
+__device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {   // bf16 pairs; a NaN gives way
+  const __nv_bfloat162 m = __hmax2(__habs2(reinterpret_cast<__nv_bfloat162&>(a)), __habs2(reinterpret_cast<__nv_bfloat162&>(b)));
+  return reinterpret_cast<const uint32_t&>(m);
+}
+
+__device__ __forceinline__ bool try_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred P1;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 P1, [%1], %2;\n\t"
+      "selp.b32 %0, 1, 0, P1;\n\t}\n"
+      : "=r"(ok)
+      : "r"(tc::smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// W words (a multiple of 2) from shared memory, in the widest loads.
+template <int W>
+__device__ __forceinline__ void words_at(uint32_t (&w)[W], const uint8_t* p) {
+  if constexpr (W % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < W; i += 4) {
+      const uint4 x = *reinterpret_cast<const uint4*>(p + 4 * i);
+      w[i] = x.x, w[i + 1] = x.y, w[i + 2] = x.z, w[i + 3] = x.w;
+    }
+  } else if constexpr (W == 2) {
+    const uint2 x = *reinterpret_cast<const uint2*>(p);
+    w[0] = x.x, w[1] = x.y;
+  } else {
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
+  }
+}
+
+// A lane's words of K's or V's codes of a unit: of both halves of its tokens, per group.
+template <int D>
+__device__ __forceinline__ void codes_at(uint32_t (&w0)[D / 32], uint32_t (&w1)[D / 32], const uint8_t* p, int lane) {
+  constexpr int NV = D / 64;
+  const uint4* v = reinterpret_cast<const uint4*>(p) + lane;
+  if constexpr (NV == 1) {
+    const uint4 x = v[0];
+    w0[0] = x.x, w0[1] = x.y, w1[0] = x.z, w1[1] = x.w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV / 2; ++i) {
+      const uint4 x = v[i * 32], y = v[(i + NV / 2) * 32];
+      w0[4 * i] = x.x, w0[4 * i + 1] = x.y, w0[4 * i + 2] = x.z, w0[4 * i + 3] = x.w;
+      w1[4 * i] = y.x, w1[4 * i + 1] = y.y, w1[4 * i + 2] = y.z, w1[4 * i + 3] = y.w;
+    }
+  }
 }
 
 __device__ __forceinline__ float lo_f32(uint32_t x) { return __uint_as_float(x << 16); }
@@ -119,8 +186,7 @@ struct Item {
   int b, job, u, n;          // sequence, job of it, unit, units of the sequence
 };
 
-__device__ __forceinline__ void next_item(const Kv4Params& p, const long long* before, Item& it) {
-  if (++it.u < it.n) return;
+__device__ __forceinline__ void next_job(const Kv4Params& p, const long long* before, Item& it) {
   it.u = 0;
   if (++it.job < p.pl.jobs_per_seq) return;
   it.job = 0;
@@ -133,9 +199,8 @@ __device__ __forceinline__ void next_item(const Kv4Params& p, const long long* b
 template <int D, int NT>
 __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) attn_kv4_kernel(Kv4Params p) {
   using C = Cfg<D, NT>;
-  constexpr int R = D / 32;                  // groups
-  constexpr int NV = D / 64;                 // vectors of a lane
-  constexpr bool QREG = NT * R <= 8;
+  constexpr int R = C::R;                    // groups
+  constexpr bool QREG = C::QREG, BREG = C::BREG;
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ long long before[GDN_ATTN_MAX_BATCH + 1];
   __shared__ long long warp_sums[kMaxWarps];
@@ -174,73 +239,155 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) attn_kv4_kernel(Kv4
       use.u = (int)(rest - (long long)use.job * use.n);
     }
     Item ask = use;
-    long long asked = x0;
+    long long to_ask = x1 - x0;              // units not yet asked for
     const int upp = a.page / kv4::kUnit;     // units of a page
     int entry = 0, entry_b = -1, entry_0 = 0;   // this lane's of 32 entries of a sequence's table
-    uint32_t bad = 0;                        // stages whose page there is not
-    const uint32_t ring0 = tc::smem_u32(ring) + warp * C::STAGES * C::STAGE;
+    int left = 0;                            // units of the page that `src` is in, from there on
+    bool there = false;                      // is there such a page?
+    const uint8_t* src = a.cache;
+    uint32_t bad = 0;                        // units of the stages whose page there is not
+    const uint32_t stages = tc::smem_u32(ring) + warp * C::STAGES * C::STAGE;
     int put = 0, get = 0;
     uint32_t parity = 0;
 
-    const auto request = [&]() {             // one more unit into the ring
-      const int pg = ask.u / upp;
-      if (ask.b != entry_b || pg < entry_0 || pg >= entry_0 + 32) {
+    const auto find_page = [&]() {
+      const int pg = ask.u / upp, at = ask.u - pg * upp;
+      if (ask.b != entry_b || pg - entry_0 >= 32 || pg < entry_0) {
         entry_b = ask.b;
         entry_0 = pg;
         entry = pg + lane < a.width ? a.table[(long long)ask.b * a.width + pg + lane] : -1;
       }
       const int page = __shfl_sync(0xffffffffu, entry, pg - entry_0);
-      const bool there = page >= 0 && page < a.n_pages;
+      there = page >= 0 && page < a.n_pages;
       if (!there && lane == 0) record_status(a.status, GDN_ERR_DEVICE_BOUNDS);
-      bad = there ? bad & ~(1u << put) : bad | 1u << put;
-      if (there && lane == 0) {
-        const uint8_t* src = a.cache + (((long long)page * a.h_kv + ask.job / p.pl.blocks) * upp + ask.u % upp) * C::STAGE;
-        const uint32_t b = tc::smem_u32(bar + put);
-        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(b), "r"(C::STAGE) : "memory");
-        asm volatile(
-            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                ring0 + put * C::STAGE),
-            "l"(src), "r"(C::STAGE), "r"(b)
-            : "memory");
-      } else if (lane == 0) {                // nothing comes: the stage's turn ends at once
-        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(tc::smem_u32(bar + put)) : "memory");
+      left = min(upp - at, ask.n - ask.u);
+      src = a.cache + (((long long)page * a.h_kv + ask.job / p.pl.blocks) * upp + at) * C::UNIT;
+    };
+    const auto copy = [&](int unit, int bytes) {
+      asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                       stages + put * C::STAGE + unit * C::UNIT),
+                   "l"(src), "r"(bytes), "r"(tc::smem_u32(bar + put))
+                   : "memory");
+    };
+    // One more stage: of one job's units as many as it holds, in one copy where they are of
+    // one page.
+    const auto request = [&]() {
+      int units = min(C::UNITS, ask.n - ask.u);
+      if (units > to_ask) units = (int)to_ask;
+      to_ask -= units;
+      // (armed before the first copy, with what there will be)
+      if (left == 0) find_page();
+      const int first = min(left, units);
+      int bytes = there ? first * C::UNIT : 0;
+      bad &= ~(((1u << C::UNITS) - 1) << (put * C::UNITS));
+      if (!there) bad |= ((1u << first) - 1) << (put * C::UNITS);
+      if (C::UNITS == 1 || first == units) {
+        if (lane == 0) {
+          asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(tc::smem_u32(bar + put)), "r"(bytes)
+                       : "memory");
+          if (there) copy(0, bytes);
+        }
+        src += first * C::UNIT;
+        ask.u += first;
+        left -= first;
+      } else {                               // the second unit is another page's
+        const uint8_t* src0 = src;
+        const bool there0 = there;
+        ++ask.u;
+        find_page();
+        if (!there) bad |= 2u << (put * C::UNITS);
+        if (lane == 0) {
+          asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(tc::smem_u32(bar + put)),
+                       "r"(bytes + (there ? C::UNIT : 0))
+                       : "memory");
+          if (there) copy(1, C::UNIT);
+          const uint8_t* src1 = src;
+          src = src0;
+          if (there0) copy(0, C::UNIT);
+          src = src1;
+        }
+        src += C::UNIT;
+        ++ask.u;
+        --left;
       }
       put = put + 1 == C::STAGES ? 0 : put + 1;
-      ++asked;
-      next_item(p, before, ask);
+      if (ask.u == ask.n) next_job(p, before, ask);
     };
-    while (asked < x1 && asked < x0 + C::STAGES) request();
+    for (int i = 0; i < C::STAGES && to_ask > 0; ++i) request();
 
-    long long x = x0;
-    while (x < x1 && ok) {
+    long long rest = x1 - x0;                // units not yet met
+    while (rest > 0 && ok) {
       // one job's units, or this warp's share of them
       const long long slot = (long long)use.b * p.pl.jobs_per_seq + use.job + worker;
       const int hk = use.job / p.pl.blocks, row0 = use.job % p.pl.blocks * (8 * NT);
       const int len = a.len[use.b];
-      const long long left = x1 - x;
-      const int end = use.n - use.u < left ? use.n : use.u + (int)left;
-      // q as the second operand: row g of a block of 8, a group's channels 8 t .. 8 t + 7
+      const int end = use.n - use.u < rest ? use.n : use.u + (int)rest;
+
+      // q as the second operand: row g of a block of 8, a group's channels 8 t .. 8 t + 7, as
+      // fp16 with the row's largest value between 2^10 and 2^11 (what that rounds is below
+      // 2^-34 of it); channels that meet codes at place 2 16 times that.  base: what the 8s
+      // add to rows 2 t and 2 t + 1, taken off.
       uint4 q[QREG ? NT : 1][QREG ? R : 1];
-      const auto q_row = [&](int n, int r) -> uint4 {
+      float4 base[BREG ? NT : 1][BREG ? R : 1];
+      uint8_t* const qs = ring + C::WARPS * C::STAGES * C::STAGE + warp * (C::QBYTES + C::BBYTES);
+      float4* const bs = reinterpret_cast<float4*>(qs + C::QBYTES) + t;
+      float scale[NT][2];                    // of the scores of rows 2 t and 2 t + 1
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
         const int row = row0 + 8 * n + g;
-        if (row >= p.pl.R) return make_uint4(0, 0, 0, 0);
         const long long at = (long long)use.b * a.steps + row / p.pl.G;
-        return *reinterpret_cast<const uint4*>(a.q + (at * a.h_q + hk * p.pl.G + row % p.pl.G) * D + 32 * r + 8 * t);
-      };
-      if constexpr (QREG) {
+        const uint16_t* from = a.q + (at * a.h_q + hk * p.pl.G + row % p.pl.G) * D + 8 * t;
+        uint4 raw[R];
+        float most = 0.0f;
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int r = 0; r < R; ++r) {
+          raw[r] = row < p.pl.R ? *reinterpret_cast<const uint4*>(from + 32 * r) : make_uint4(0, 0, 0, 0);
+          const uint32_t w[4] = {raw[r].x, raw[r].y, raw[r].z, raw[r].w};
 #pragma unroll
-          for (int r = 0; r < R; ++r) q[n][r] = q_row(n, r);
+          for (int i = 0; i < 4; ++i) most = fmaxf(most, fmaxf(fabsf(lo_f32(w[i])), fabsf(hi_f32(w[i]))));
+        }
+        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+        // 2^10 over the power of two in `most`, at most 2^126 (a row of nothing but tiny numbers)
+        const uint32_t ex = min(264 - min((int)(__float_as_uint(most) >> 23), 254), 253);
+        const float up = __uint_as_float(ex << 23), down = __uint_as_float((254 - ex) << 23);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) scale[n][i] = p.qscale * 0x1p18f * __shfl_sync(0xffffffffu, down, (2 * t + i) * 4);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const uint32_t w[4] = {raw[r].x, raw[r].y, raw[r].z, raw[r].w};
+          uint32_t h[4];
+          float sum = 0.0f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float m = i % 2 == 0 ? 16.0f : 1.0f;
+            h[i] = pack_f16x2(lo_f32(w[i]) * up * m, hi_f32(w[i]) * up * m);
+            const float2 x = __half22float2(reinterpret_cast<const __half2&>(h[i]));
+            sum = fmaf(i % 2 == 0 ? -0x1p-19f : -0x1p-15f, x.x + x.y, sum);
+          }
+          sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+          sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+          const float sum0 = __shfl_sync(0xffffffffu, sum, 8 * t), sum1 = __shfl_sync(0xffffffffu, sum, 8 * t + 4);
+          const float4 sums = make_float4(sum0, sum1, sum0, sum1);
+          if constexpr (QREG) q[n][r] = make_uint4(h[0], h[1], h[2], h[3]);
+          else *reinterpret_cast<uint4*>(qs + (n * R + r) * 512 + lane * 16) = make_uint4(h[0], h[1], h[2], h[3]);
+          if constexpr (BREG) base[n][r] = sums;
+          else if (g == 0) bs[(n * R + r) * 4] = sums;
+        }
       }
+      if constexpr (!BREG) __syncwarp();
       // the last token that rows 2 t and 2 t + 1 of each block see
       int last[NT][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) last[n][i] = len - a.steps + min((row0 + 8 * n + 2 * t + i) / p.pl.G, a.steps - 1);
-      const int all_see = len - a.steps;     // tokens up to this one are seen by every row
+        for (int i = 0; i < 2; ++i)
+          last[n][i] = min(len - a.steps + min((row0 + 8 * n + 2 * t + i) / p.pl.G, a.steps - 1), end * kv4::kUnit - 1);
+      const int past = min(len, end * kv4::kUnit);   // tokens from here on are no row's, or another share's
+      const int all_see = min(len - a.steps, end * kv4::kUnit - 1);   // up to here every row's
       float o[NT][R][2][4], ref[NT][2], sum[NT][2];
+      int v = kLeastV;                       // 2^v: above every scale of V at the last update
+      uint32_t fresh = (1u << (2 * NT)) - 1;   // this lane's rows that have not seen a score
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -249,167 +396,184 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) attn_kv4_kernel(Kv4
           for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[n][r][i][e] = 0.0f;
-        ref[n][0] = ref[n][1] = -3.402823466e38f;
+        ref[n][0] = ref[n][1] = 0.0f;
         sum[n][0] = sum[n][1] = 0.0f;
       }
 
-#pragma unroll 1
-      for (int u = use.u; u < end; ++u, ++x) {
-        ok = __all_sync(0xffffffffu, tc::mbar_wait(bar + get, parity, kWaitClocks));
-        if (!ok) break;
-        const uint8_t* st = ring + (warp * C::STAGES + get) * C::STAGE;
-        if (!(bad >> get & 1)) {
-          // scores: tokens g and g + 8 by rows 2 t, 2 t + 1
-          float s[NT][4];
+      // A stage of units from u on; at the edge some row does not see all of their tokens.
+      const auto meet = [&](int u, const uint8_t* st, uint32_t gone, auto at_edge) {
+        constexpr bool edge = decltype(at_edge)::value;
+        constexpr int NU = C::UNITS;
+        const int j = u * kv4::kUnit + g;    // this lane's tokens: j + 16 k, j + 16 k + 8
+        // scores: tokens g and g + 8 of each unit by rows 2 t, 2 t + 1
+        float s[NU][NT][4];
+#pragma unroll
+        for (int k = 0; k < NU; ++k) {
+          uint32_t ks[2][R / 2];             // scales of tokens g and g + 8, two groups a word
+#pragma unroll
+          for (int h = 0; h < 2; ++h) words_at<R / 2>(ks[h], st + k * C::UNIT + 16 * D + (g + 8 * h) * (D / 8));
+          uint32_t w0[R], w1[R];
+          codes_at<D>(w0, w1, st + k * C::UNIT, lane);
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[n][e] = 0.0f;
-          const uint8_t* sc = st + 16 * D + g * (D / 8);
-          uint32_t ks[2][R / 2], vs[2][R / 2];   // scales of tokens g and g + 8, two groups a word
+            for (int e = 0; e < 4; ++e) s[k][n][e] = 0.0f;
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
+          for (int r = 0; r < R; ++r) {
+            uint32_t f[2][4];
 #pragma unroll
-            for (int i = 0; i < R / 2; ++i) {
-              ks[h][i] = *reinterpret_cast<const uint32_t*>(sc + h * D + 4 * i);
-              vs[h][i] = *reinterpret_cast<const uint32_t*>(sc + h * D + R * 2 + 4 * i);
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t x = __funnelshift_r(w0[r], w0[r], 1 + 8 * i), y = __funnelshift_r(w1[r], w1[r], 1 + 8 * i);
+              f[i][0] = x & kAt2;
+              f[i][1] = y & kAt2;
+              f[i][2] = x & kAt6;
+              f[i][3] = y & kAt6;
             }
-          const uint4* kv = reinterpret_cast<const uint4*>(st) + lane;
+            const float s0 = r % 2 ? hi_f32(ks[0][r / 2]) : lo_f32(ks[0][r / 2]);
+            const float s1 = r % 2 ? hi_f32(ks[1][r / 2]) : lo_f32(ks[1][r / 2]);
 #pragma unroll
-          for (int v = 0; v < (NV + 1) / 2; ++v) {
-            // words of token g and of token g + 8
-            uint32_t w0[4], w1[4];
-            if constexpr (NV == 1) {
-              const uint4 x4 = kv[0];
-              w0[0] = x4.x, w0[1] = x4.y, w1[0] = x4.z, w1[1] = x4.w;
-            } else {
-              const uint4 x4 = kv[v * 32], y4 = kv[(v + NV / 2) * 32];
-              w0[0] = x4.x, w0[1] = x4.y, w0[2] = x4.z, w0[3] = x4.w;
-              w1[0] = y4.x, w1[1] = y4.y, w1[2] = y4.z, w1[3] = y4.w;
-            }
-#pragma unroll
-            for (int k = 0; k < (NV == 1 ? 2 : 4); ++k) {
-              const int r = 4 * v + k;
-              float c[NT][4];
-#pragma unroll
-              for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) c[n][e] = 0.0f;
-              uint32_t f[2][4];
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                f[i][0] = values(__funnelshift_r(w0[k], w0[k], 8 * i));
-                f[i][1] = values(__funnelshift_r(w1[k], w1[k], 8 * i));
-                f[i][2] = values(__funnelshift_r(w0[k], w0[k], 8 * i + 4));
-                f[i][3] = values(__funnelshift_r(w1[k], w1[k], 8 * i + 4));
-              }
-#pragma unroll
-              for (int n = 0; n < NT; ++n) {
-                const uint4 qq = QREG ? q[QREG ? n : 0][QREG ? r : 0] : q_row(n, r);
-                mma(c[n], f[0], qq.x, qq.y);
-                mma(c[n], f[1], qq.z, qq.w);
-              }
-              const float s0 = r % 2 ? hi_f32(ks[0][r / 2]) : lo_f32(ks[0][r / 2]);
-              const float s1 = r % 2 ? hi_f32(ks[1][r / 2]) : lo_f32(ks[1][r / 2]);
-#pragma unroll
-              for (int n = 0; n < NT; ++n) {
-                s[n][0] = fmaf(c[n][0], s0, s[n][0]);
-                s[n][1] = fmaf(c[n][1], s0, s[n][1]);
-                s[n][2] = fmaf(c[n][2], s1, s[n][2]);
-                s[n][3] = fmaf(c[n][3], s1, s[n][3]);
-              }
+            for (int n = 0; n < NT; ++n) {
+              uint4 qq;
+              float4 bb;
+              if constexpr (QREG) qq = q[n][r];
+              else qq = *reinterpret_cast<const uint4*>(qs + (n * R + r) * 512 + lane * 16);
+              if constexpr (BREG) bb = base[n][r];
+              else bb = bs[(n * R + r) * 4];
+              float c[4];
+              mma(c, f[0], qq.x, qq.y, bb.x, bb.y, bb.z, bb.w);
+              mma(c, f[1], qq.z, qq.w);
+              s[k][n][0] = fmaf(c[0], s0, s[k][n][0]);
+              s[k][n][1] = fmaf(c[1], s0, s[k][n][1]);
+              s[k][n][2] = fmaf(c[2], s1, s[k][n][2]);
+              s[k][n][3] = fmaf(c[3], s1, s[k][n][3]);
             }
           }
-          // weights
-          const int j = u * kv4::kUnit + g;
-          const bool edge = u * kv4::kUnit + kv4::kUnit - 1 > all_see;
-          bool over = false;
+        }
+        // the widest scale of V: a lane looks at one word of each of its tokens
+        uint32_t widest = 0;
+#pragma unroll
+        for (int k = 0; k < NU; ++k)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t w = *reinterpret_cast<const uint32_t*>(st + k * C::UNIT + 16 * D + (g + 8 * h) * (D / 8) + D / 16 +
+                                                            t % (R / 2) * 4);
+            if (edge && (j + 16 * k + 8 * h >= past || gone >> k & 1)) w = 0;   // whatever the cache holds there
+            widest = max_abs2(widest, w);
+          }
+        const float wide = fmaxf(fmaxf(lo_f32(widest), hi_f32(widest)), 0.0f);   // (0 for NaN)
+        bool over = fresh != 0 || (__float_as_int(wide) >> 23) >= v + kWide + 127;
+        const float room = kTop + kGrow - (float)v;
+#pragma unroll
+        for (int k = 0; k < NU; ++k)
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              s[n][e] *= p.qscale;
-              if (edge && j + e / 2 * 8 > last[n][e % 2]) s[n][e] = -INFINITY;
-              over = over || s[n][e] > ref[n][e % 2];
+              s[k][n][e] = fmaf(s[k][n][e], scale[n][e % 2], -ref[n][e % 2]);
+              if (edge && (j + 16 * k + e / 2 * 8 > last[n][e % 2] || gone >> k & 1)) s[k][n][e] = -INFINITY;
+              over = over || s[k][n][e] > room;
             }
-          if (__any_sync(0xffffffffu, over)) {
+        if (__any_sync(0xffffffffu, over)) {
+          float w = wide;
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+          for (int k = 1; k <= 16; k <<= 1) w = fmaxf(w, __shfl_xor_sync(0xffffffffu, w, k));
+          const int v1 = min(max(v, (__float_as_int(w) >> 23) - 126), 126);
 #pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                float m = fmaxf(s[n][i], s[n][2 + i]);
+          for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int k = 4; k <= 16; k <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
-                if (m > ref[n][i]) {
-                  const float to = m + kSlack, f = ex2(ref[n][i] - to);
-                  ref[n][i] = to;
-                  sum[n][i] *= f;
+            for (int i = 0; i < 2; ++i) {
+              // largest score, less ref: of these units and of those before
+              float m = -INFINITY;
 #pragma unroll
-                  for (int r = 0; r < R; ++r)
+              for (int k = 0; k < NU; ++k) m = fmaxf(m, fmaxf(s[k][n][i], s[k][n][2 + i]));
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                      o[n][r][k][i] *= f;
-                      o[n][r][k][2 + i] *= f;
-                    }
+              for (int k = 4; k <= 16; k <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
+              const bool first = fresh >> (2 * n + i) & 1;
+              if (!first) m = fmaxf(m, kTop - (float)v);
+              const float to = ref[n][i] + (m - (kTop - (float)v1)), by = ref[n][i] - to;
+              if (by != 0.0f && m != -INFINITY) {
+                const float f = first ? 1.0f : ex2(by);
+                ref[n][i] = to;
+                sum[n][i] *= f;
+#pragma unroll
+                for (int k = 0; k < NU; ++k) {
+                  s[k][n][i] += by;
+                  s[k][n][2 + i] += by;
                 }
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                  for (int k = 0; k < 2; ++k) {
+                    o[n][r][k][i] *= f;
+                    o[n][r][k][2 + i] *= f;
+                  }
               }
-          }
+              if (m != -INFINITY) fresh &= ~(1u << (2 * n + i));
+            }
+          v = v1;
+        }
+#pragma unroll
+        for (int k = 0; k < NU; ++k)
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              s[n][e] = ex2(s[n][e] - ref[n][e % 2]);
-              sum[n][e % 2] += s[n][e];
+              s[k][n][e] = ex2(s[k][n][e]);
+              sum[n][e % 2] += s[k][n][e];
             }
-          // outputs: channels by rows, over the 16 tokens
-          const uint4* vv = reinterpret_cast<const uint4*>(st + 8 * D) + lane;
+        // outputs: channels by rows, over the 16 tokens of each unit
+        const uint32_t less8[4] = {kLess8At0, kLess8At4, kLess8At0, kLess8At4};
 #pragma unroll
-          for (int v = 0; v < (NV + 1) / 2; ++v) {
-            uint32_t w0[4], w1[4];
-            if constexpr (NV == 1) {
-              const uint4 x4 = vv[0];
-              w0[0] = x4.x, w0[1] = x4.y, w1[0] = x4.z, w1[1] = x4.w;
-            } else {
-              const uint4 x4 = vv[v * 32], y4 = vv[(v + NV / 2) * 32];
-              w0[0] = x4.x, w0[1] = x4.y, w0[2] = x4.z, w0[3] = x4.w;
-              w1[0] = y4.x, w1[1] = y4.y, w1[2] = y4.z, w1[3] = y4.w;
-            }
+        for (int k = 0; k < NU; ++k) {
+          uint32_t vs[2][R / 2];
 #pragma unroll
-            for (int k = 0; k < (NV == 1 ? 2 : 4); ++k) {
-              const int r = 4 * v + k;
-              const float s0 = r % 2 ? hi_f32(vs[0][r / 2]) : lo_f32(vs[0][r / 2]);
-              const float s1 = r % 2 ? hi_f32(vs[1][r / 2]) : lo_f32(vs[1][r / 2]);
-              uint32_t f[2][4];
-              f[0][0] = values(w0[k] << 3);
-              f[0][1] = values(w0[k] >> 1);
-              f[0][2] = values(w1[k] << 3);
-              f[0][3] = values(w1[k] >> 1);
-              f[1][0] = values(w0[k] >> 5);
-              f[1][1] = values(w0[k] >> 9);
-              f[1][2] = values(w1[k] >> 5);
-              f[1][3] = values(w1[k] >> 9);
+          for (int h = 0; h < 2; ++h) words_at<R / 2>(vs[h], st + k * C::UNIT + 16 * D + (g + 8 * h) * (D / 8) + D / 16);
+          uint32_t w0[R], w1[R];
+          codes_at<D>(w0, w1, st + k * C::UNIT + 8 * D, lane);
 #pragma unroll
-              for (int n = 0; n < NT; ++n) {
-                float e0 = s[n][0] * s0, e1 = s[n][1] * s0, e2 = s[n][2] * s1, e3 = s[n][3] * s1;
-                if (edge) {                  // whatever the scale of a token that is not seen
-                  if (j > last[n][0]) e0 = 0.0f;
-                  if (j > last[n][1]) e1 = 0.0f;
-                  if (j + 8 > last[n][0]) e2 = 0.0f;
-                  if (j + 8 > last[n][1]) e3 = 0.0f;
-                }
-                const uint32_t b0 = transpose8(pack_bf16x2(e0, e1)), b1 = transpose8(pack_bf16x2(e2, e3));
-                mma(o[n][r][0], f[0], b0, b1);
-                mma(o[n][r][1], f[1], b0, b1);
+          for (int r = 0; r < R; ++r) {
+            const float s0 = r % 2 ? hi_f32(vs[0][r / 2]) : lo_f32(vs[0][r / 2]);
+            const float s1 = r % 2 ? hi_f32(vs[1][r / 2]) : lo_f32(vs[1][r / 2]);
+            const uint32_t x1 = w0[r] >> 8, y1 = w1[r] >> 8;
+            const uint32_t f[2][4] = {{w0[r] & kAt0, w0[r] & kAt4, w1[r] & kAt0, w1[r] & kAt4},
+                                      {x1 & kAt0, x1 & kAt4, y1 & kAt0, y1 & kAt4}};
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              float e0 = s[k][n][0] * s0, e1 = s[k][n][1] * s0, e2 = s[k][n][2] * s1, e3 = s[k][n][3] * s1;
+              if constexpr (edge) {          // whatever the scale of a token that is not seen
+                const int at = gone >> k & 1 ? 0x7fffffff - 16 : j + 16 * k;
+                if (at > last[n][0]) e0 = 0.0f;
+                if (at > last[n][1]) e1 = 0.0f;
+                if (at + 8 > last[n][0]) e2 = 0.0f;
+                if (at + 8 > last[n][1]) e3 = 0.0f;
+              }
+              const uint32_t b0 = transpose8(pack_f16x2(e0, e1)), b1 = transpose8(pack_f16x2(e2, e3));
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                mma(o[n][r][i], less8, b0, b1);
+                mma(o[n][r][i], f[i], b0, b1);
               }
             }
           }
         }
+      };
+
+#pragma unroll 1
+      for (int u = use.u; u < end; u += C::UNITS) {
+        if (!__all_sync(0xffffffffu, try_wait(bar + get, parity)))
+          ok = __all_sync(0xffffffffu, tc::mbar_wait(bar + get, parity, kWaitClocks));
+        if (!ok) break;
+        const uint8_t* st = ring + (warp * C::STAGES + get) * C::STAGE;
+        const uint32_t gone = bad >> (get * C::UNITS) & ((1u << C::UNITS) - 1);
+        if ((u + C::UNITS) * kv4::kUnit - 1 > all_see || gone != 0) meet(u, st, gone, std::true_type());
+        else meet(u, st, 0u, std::false_type());
         __syncwarp();
         get = get + 1 == C::STAGES ? 0 : get + 1;
         parity ^= get == 0;
-        if (asked < x1) request();
+        if (to_ask > 0) request();
       }
-      // the share's sums into its slot
+      // the share's sums into its slot, as with weights that do not go by V's scales
+      const float stored = __uint_as_float((uint32_t)(v - (int)kStored + 127) << 23);
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -418,20 +582,24 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) attn_kv4_kernel(Kv4
 #pragma unroll
           for (int k = 4; k <= 16; k <<= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
           const long long row = slot * (8 * NT) + 8 * n + 2 * t + i;
-          if (g == 0) p.ml[row] = make_float2(ref[n][i], l);
+          if (g == 0) p.ml[row] = make_float2(ref[n][i] - ((float)v - kStored), l * stored);
 #pragma unroll
           for (int r = 0; r < R; ++r)
             *reinterpret_cast<float4*>(p.part + row * D + 32 * r + 4 * g) =
-                make_float4(o[n][r][0][i], o[n][r][0][2 + i], o[n][r][1][i], o[n][r][1][2 + i]);
+                make_float4(o[n][r][0][i] * 0x1p24f * stored, o[n][r][0][2 + i] * 0x1p20f * stored,
+                            o[n][r][1][i] * 0x1p24f * stored, o[n][r][1][2 + i] * 0x1p20f * stored);
         }
-      use.u = end - 1;
-      next_item(p, before, use);
+      if (!ok) break;
+      rest -= end - use.u;
+      use.u = end;
+      if (end == use.n) next_job(p, before, use);
     }
     if (!ok) {                               // a copy did not come: wait for the others, then leave
       if (lane == 0) record_status(a.status, GDN_ERR_DEVICE_TIMEOUT);
-      for (long long y = x + 1; y < asked; ++y) {
+      for (int i = 1; i < C::STAGES; ++i) {
         get = get + 1 == C::STAGES ? 0 : get + 1;
         parity ^= get == 0;
+        if (get == put) break;               // stages from here on hold nothing asked for
         tc::mbar_wait(bar + get, parity, kWaitClocks);
       }
     }

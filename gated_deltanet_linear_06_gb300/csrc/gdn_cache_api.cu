@@ -183,7 +183,7 @@ gdn_status gdn_attn_decode_kv4(const gdn_attn_dims* dims, int page, long long n_
   if (st == GDN_OK) st = check_cache(page, n_pages);
   if (st != GDN_OK) return st;
   if (table_width < 0 || !aligned(device_status, 4)) return GDN_ERR_INVALID_ARG;
-  if (table_width > 0x7fffffffLL / page) return GDN_ERR_UNSUPPORTED;
+  if (table_width > (1 << 30) / page) return GDN_ERR_UNSUPPORTED;
   if (batch == 0) return GDN_OK;
   if (!need16(q) || !need16(out) || !need16(len) || !maybe16(gate) || !maybe16(table) ||
       (table_width > 0 && (!table || !need16(cache) || n_pages < 1)) ||

@@ -691,7 +691,7 @@ gdn_status gdn_kv4_load(const gdn_attn_dims* dims, int page, long long n_pages, 
  *   q             bf16 [batch][steps][h_q][d]
  *   cache         as above
  *   table         int32 [batch][table_width], entries past a sequence's end unread; null
- *                 when table_width is 0
+ *                 when table_width is 0; table_width * page at most 2^30
  *   len           int32 [batch], device: a call's launches do not depend on the lengths,
  *                 so a captured step stays valid while they grow
  *   gate          null, or bf16 with element strides (token, head), multiples of 8,
@@ -701,9 +701,11 @@ gdn_status gdn_kv4_load(const gdn_attn_dims* dims, int page, long long n_pages, 
  * A length outside [0, table_width * page] or a page index outside [0, n_pages) sets
  * GDN_ERR_DEVICE_BOUNDS: the sequence counts as empty, and the outputs of one that
  * reaches such a page are unspecified (nothing outside the cache is read).
- * Each softmax weight times its token's scale is rounded to bf16 before it meets the codes,
- * which moves out by at most 2^-8 sum p |v| besides its own rounding; everything else is
- * fp32.  Magnitudes of q are to be below 2^110.  Equal calls give equal bits; the order
+ * Each softmax weight times its token's scale is rounded to fp16 (at a power of two that
+ * keeps it in range) before it meets the codes, which moves out by at most 2^-11 sum p |v|
+ * besides its own rounding; everything else is fp32, with steps of the largest magnitude M
+ * in a value's group where values cancel (2^-17 sum p M).  Magnitudes of k are to be below
+ * 2^100.  Equal calls give equal bits; the order
  * of a row's sums, and with it the last bits, depends on the batch, the lengths and the
  * GPU's SM count.
  */

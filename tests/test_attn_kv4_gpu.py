@@ -1,11 +1,15 @@
 """gdn_attn_decode_kv4 against softmax attention in 64 bits over the values that the
 cache stands for.
 
-Tolerance, with A = sum p |v|: a weight times its token's scale is rounded to bf16, off by
-at most 2^-8 of itself, so the sum by 2^-8 A; fp32 scores and exponentials move the
+Tolerance, with A = sum p |v|: a weight times its token's scale is rounded to fp16, off by
+at most 2^-11 of itself, so the sum by 2^-11 A; fp32 scores and exponentials move the
 weights by less than 2^-11 together (scores below 2^7 here, sums of 256 products at
 2^-24 each of their sizes' sum); the result is rounded once, 2^-8 |o|.  The gate multiplies
-all of it."""
+all of it.  Codes meet the weights as 0 .. 15 and 8 times the weights are taken off, both in
+fp32: a sum passes through 8 scales (M, the largest magnitude that a group holds) times
+its weights.  A tensor-core product adds 17 terms (16 tokens' and the sum so far), each of
+which may lose what is below a step of the largest, 2^-23 of it; two products a unit make
+2 * 17 * 2^-23 < 2^-17 sum p M."""
 import pytest
 import torch
 
@@ -58,6 +62,8 @@ def reference(x, scale=None):
     B, S, hq, d = q.shape
     G = hq // x["dims"].h_kv
     out, size = torch.zeros_like(q), torch.zeros_like(q)
+    if k is not None:
+        most = v.abs().unflatten(-1, (-1, 32)).amax(-1, keepdim=True).expand(-1, -1, -1, 32).flatten(-2)
     at = 0
     for b, n_all in enumerate(x["host"]):
         for i in range(S):
@@ -67,7 +73,8 @@ def reference(x, scale=None):
             kk, vv = k[at:at + n].repeat_interleave(G, 1), v[at:at + n].repeat_interleave(G, 1)
             p = torch.softmax(torch.einsum("nhd,hd->hn", kk, q[b, i]) * (scale or d ** -0.5), -1)
             out[b, i] = torch.einsum("hn,nhd->hd", p, vv)
-            size[b, i] = torch.einsum("hn,nhd->hd", p, vv.abs())
+            # (in units of the tolerance of a weight, 2^-10 with the scores' share)
+            size[b, i] = torch.einsum("hn,nhd->hd", p, vv.abs() + 2 ** -7 * most[at:at + n].repeat_interleave(G, 1))
         at += n_all
     if x["gate"] is not None:
         f = torch.sigmoid(x["gate"][..., d:].double())
@@ -91,7 +98,7 @@ def check(x, scale=None):
     got = call(x, status=status)
     assert gdn.gdn_read_device_status(status) == 0
     want, size = reference(x, scale)
-    tol = 2 ** -8 * (size + want.abs()) + 2 ** -11 * size + 1e-30
+    tol = 2 ** -8 * want.abs() + 2 ** -10 * size + 1e-30
     worst = ((got.double() - want).abs() / tol).max().item()
     assert worst <= 1, worst
     return got
@@ -145,7 +152,7 @@ def test_peaked_and_growing_scores():
     # keys that grow along the sequence: the largest score so far moves again and again
     x = build(1, 1, 8, 1, 128, 32, [700], seed=6, gate=False)
     n = torch.arange(700)
-    k = torch.randn(700, 1, 128) * (0.02 * n[:, None, None])
+    k = torch.randn(700, 1, 128, generator=torch.Generator().manual_seed(5)) * (0.02 * n[:, None, None])
     gdn.gdn_kv4_store(x["dims"], k.to(BF).to(DEV), None, x["cache"], slot=x["slot"].to(DEV))
     check(x)
 
@@ -178,7 +185,7 @@ def test_what_a_query_does_not_see_does_not_reach_it():
 def test_values_at_the_ends_of_bf16():
     for size in (3.0e38, 2.0 ** -88):
         x = build(1, 1, 8, 1, 64, 16, [100], seed=9, gate=False)
-        v = (torch.rand(100, 1, 64) * 2 - 1) * size
+        v = (torch.rand(100, 1, 64, generator=torch.Generator().manual_seed(1)) * 2 - 1) * size
         gdn.gdn_kv4_store(x["dims"], None, v.to(BF).to(DEV), x["cache"], slot=x["slot"].to(DEV))
         check(x)
 
@@ -222,7 +229,7 @@ def test_shared_pages_and_equal_calls():
     for b, n in enumerate([500, 500, 130, 64, 1]):
         z = dict(x, q=x["q"][b:b + 1], gate=x["gate"][b:b + 1], host=[n], slot=x["slot"][:n])
         want, size = reference(z)
-        tol = 2 ** -8 * (size + want.abs()) + 2 ** -11 * size
+        tol = 2 ** -8 * want.abs() + 2 ** -10 * size
         assert ((one[b:b + 1].double() - want).abs() <= tol).all()
 
 
