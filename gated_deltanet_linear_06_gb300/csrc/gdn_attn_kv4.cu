@@ -4,6 +4,7 @@
 #include <type_traits>
 
 #include "../../include/gdn.h"
+#include "gdn_attn_ranges.h"
 #include "gdn_kv4.cuh"
 #include "gdn_launch.h"
 #include "gdn_tc.cuh"
@@ -35,7 +36,7 @@ struct Kv4Params {
   AttnKv4Args a;
   Kv4Plan pl;
   float qscale;              // scale * log2(e)
-  long long* before;         // [batch + 1] units of the sequences before each
+  int2* span;                // per job: the first and the last worker with a share of it
   float2* ml;                // per slot and row: (reference, sum)
   float* part;               // per slot and row: d sums
 };
@@ -214,8 +215,6 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) attn_kv4_kernel(Kv4
     for (int i = 0; i < C::STAGES; ++i) tc::mbar_init(bar + i, 1);
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   sum_units(a, before, warp_sums, blockIdx.x == 0);
-  if (blockIdx.x == 0)
-    for (int b = threadIdx.x; b <= a.batch; b += blockDim.x) p.before[b] = before[b];
 
   // This warp's items, and where the first one is.
   const long long total = before[a.batch] * p.pl.jobs_per_seq;
@@ -318,10 +317,13 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) attn_kv4_kernel(Kv4
     long long rest = x1 - x0;                // units not yet met
     while (rest > 0 && ok) {
       // one job's units, or this warp's share of them
-      const long long slot = (long long)use.b * p.pl.jobs_per_seq + use.job + worker;
+      const int job = use.b * p.pl.jobs_per_seq + use.job;
+      const long long slot = (long long)job + worker;
       const int hk = use.job / p.pl.blocks, row0 = use.job % p.pl.blocks * (8 * NT);
       const int len = a.len[use.b];
       const int end = use.n - use.u < rest ? use.n : use.u + (int)rest;
+      if (lane == 0 && use.u == 0) p.span[job].x = worker;
+      if (lane == 0 && end == use.n) p.span[job].y = worker;
 
       // q as the second operand: row g of a block of 8, a group's channels 8 t .. 8 t + 7, as
       // fp16 with the row's largest value between 2^10 and 2^11 (what that rounds is below
@@ -609,75 +611,84 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) attn_kv4_kernel(Kv4
 
 constexpr int kJoinThreads = 256;
 
-// Joins the shares of each row: 2^(ref_i - M) of each, over the sum of the sums.
+// Joins the shares of each row: 2^(ref_i - M) of each, over the sum of the sums.  A CTA
+// takes kJoinThreads / LANES / groups rows (of up to 128 channels), `groups` lane groups to a
+// row, each every groups-th share with four shares' loads in flight.
 template <int D, int NT>
-__global__ void __launch_bounds__(kJoinThreads) attn_kv4_join(Kv4Params p) {
-  constexpr int LANES = D / 4;
-  constexpr int GROUPS = kJoinThreads / LANES;
+__global__ void __launch_bounds__(kJoinThreads) attn_kv4_join(Kv4Params p, int groups) {
+  constexpr int LANES = D / 4 < 32 ? D / 4 : 32, CHUNKS = D / 4 / LANES;
   __shared__ float4 acc[kJoinThreads];
   __shared__ float2 stat[kJoinThreads];
   const AttnKv4Args& a = p.a;
-  const int b = blockIdx.x / a.steps, step = blockIdx.x % a.steps, h = blockIdx.y;
-  const int hk = h / p.pl.G, row = step * p.pl.G + h % p.pl.G;
-  const int c4 = threadIdx.x % LANES, grp = threadIdx.x / LANES;
+  const int per = kJoinThreads / LANES / groups;   // rows of a CTA
+  const int set = threadIdx.x / LANES, grp = set % groups;
+  const long long item = (long long)blockIdx.x * per + set / groups, items = (long long)a.batch * a.steps * a.h_q * CHUNKS;
+  const bool mine = item < items;
+  const int c4 = mine ? (int)(item % CHUNKS) * LANES + threadIdx.x % LANES : 0;
+  const long long out_row = mine ? item / CHUNKS : 0;         // [b][step][h]
+  const int h = (int)(out_row % a.h_q), tok = (int)(out_row / a.h_q);
+  const int b = tok / a.steps, step = tok - b * a.steps;
+  const int hk = h / p.pl.G, row = step * p.pl.G + h - hk * p.pl.G;
+  const int job = b * p.pl.jobs_per_seq + hk * p.pl.blocks + row / (8 * NT);
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const long long n_before = p.before[b], n = p.before[b + 1] - n_before;
-  const long long total = p.before[a.batch] * p.pl.jobs_per_seq;
-  const int job = hk * p.pl.blocks + row / (8 * NT);
+  uint2 gt = make_uint2(0, 0);
+  if (mine && a.gate && grp == 0)              // on its way under the sums
+    gt = *reinterpret_cast<const uint2*>(a.gate + (long long)tok * a.gate_st + h * a.gate_sh + 4 * c4);
+  const int len = a.len[b];
+  const bool any = mine && units_of(a, b) > 0;
   float M = -INFINITY, L = 0.0f;
   float4 o = make_float4(0, 0, 0, 0);
-  const int seen = a.len[b] - (a.steps - 1 - step);
-  if (n > 0) {
-    const long long first_item = n_before * p.pl.jobs_per_seq + job * n;
-    // the worker of item x: the last whose share begins at or before it
-    const int workers = workers_of(p, total);
-    const int w0 = (int)(((first_item + 1) * workers - 1) / total);
-    const int w1 = (int)(((first_item + n) * workers - 1) / total);
-    const long long slot0 = (long long)b * p.pl.jobs_per_seq + job;
-    for (int w = w0 + grp; w <= w1; w += GROUPS) {
-      const long long at = (slot0 + w) * (8 * NT) + row % (8 * NT);
-      const float2 ml = p.ml[at];
-      const float4 v = *reinterpret_cast<const float4*>(p.part + at * D + 4 * c4);
-      if (ml.y == 0.0f) continue;            // saw nothing
-      const float m = fmaxf(M, ml.x), f = ex2(M - m), e = ex2(ml.x - m);
-      L = L * f + ml.y * e;
-      o.x = o.x * f + v.x * e;
-      o.y = o.y * f + v.y * e;
-      o.z = o.z * f + v.z * e;
-      o.w = o.w * f + v.w * e;
-      M = m;
-    }
-  }
-  acc[threadIdx.x] = o;
-  stat[threadIdx.x] = make_float2(M, L);
-  __syncthreads();
-  if (grp != 0) return;
-  for (int k = 1; k < GROUPS; ++k) {
-    const float2 st = stat[k * LANES + c4];
-    const float4 v = acc[k * LANES + c4];
-    if (st.y == 0.0f) continue;
-    const float m = fmaxf(M, st.x), f = ex2(M - m), e = ex2(st.x - m);
-    L = L * f + st.y * e;
+  const auto add = [&](float m, float l, const float4& v) {
+    if (l == 0.0f) return;                     // saw nothing (a NaN sum counts)
+    const float to = fmaxf(M, m), f = ex2(M - to), e = ex2(m - to);
+    L = L * f + l * e;
     o.x = o.x * f + v.x * e;
     o.y = o.y * f + v.y * e;
     o.z = o.z * f + v.z * e;
     o.w = o.w * f + v.w * e;
-    M = m;
+    M = to;
+  };
+  if (any) {
+    const int2 span = p.span[job];
+    const Ranges own = ranges_of(span.x, span.y, p.pl.workers);
+    const long long at = ((long long)job + own.first) * (8 * NT) + row % (8 * NT);
+    const float2* ml = p.ml + at;
+    const float4* part = reinterpret_cast<const float4*>(p.part + at * D) + c4;
+    for (int i = grp; i < own.count; i += 4 * groups) {
+      float2 m[4];
+      float4 v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int x = i + k * groups;
+        m[k] = make_float2(0.0f, 0.0f);
+        if (x < own.count) {
+          m[k] = ml[(long long)x * (8 * NT)];
+          v[k] = part[(long long)x * (8 * NT) * (D / 4)];
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) add(m[k].x, m[k].y, v[k]);
+    }
   }
+  if (groups > 1) {
+    acc[threadIdx.x] = o;
+    stat[threadIdx.x] = make_float2(M, L);
+    __syncthreads();
+    if (grp == 0)
+      for (int k = 1; k < groups; ++k) add(stat[threadIdx.x + k * LANES].x, stat[threadIdx.x + k * LANES].y, acc[threadIdx.x + k * LANES]);
+  }
+  if (!mine || grp != 0) return;
   // no token seen: zeros; tokens seen whose weights are all zero (scores of -inf): NaN
-  const float inv = seen <= 0 || n == 0 ? 0.0f : 1.0f / L;
+  const bool sees = any && len - (a.steps - 1 - step) > 0;
+  const float inv = !sees ? 0.0f : L == 0.0f ? __uint_as_float(0x7fc00000u) : 1.0f / L;
   float r[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
-  if (seen > 0 && n > 0 && L == 0.0f) r[0] = r[1] = r[2] = r[3] = __uint_as_float(0x7fc00000u);
-  const long long tok = blockIdx.x;
   if (a.gate) {
-    const uint2 gt = *reinterpret_cast<const uint2*>(a.gate + tok * a.gate_st + h * a.gate_sh + 4 * c4);
     r[0] *= sigmoid(lo_f32(gt.x));
     r[1] *= sigmoid(hi_f32(gt.x));
     r[2] *= sigmoid(lo_f32(gt.y));
     r[3] *= sigmoid(hi_f32(gt.y));
   }
-  *reinterpret_cast<uint2*>(a.out + (tok * a.h_q + h) * D + 4 * c4) =
-      make_uint2(pack_bf16x2(r[0], r[1]), pack_bf16x2(r[2], r[3]));
+  *reinterpret_cast<uint2*>(a.out + out_row * D + 4 * c4) = make_uint2(pack_bf16x2(r[0], r[1]), pack_bf16x2(r[2], r[3]));
 }
 
 size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
@@ -701,8 +712,8 @@ cudaError_t launch_n(const AttnKv4Args& a, cudaStream_t stream, int sms) {
   p.pl.workers = ctas * C::WARPS;
   p.qscale = a.scale * 1.4426950408889634f;
   char* ws = static_cast<char*>(a.scratch);
-  p.before = reinterpret_cast<long long*>(ws);
-  ws += up256((size_t)(a.batch + 1) * sizeof(long long));
+  p.span = reinterpret_cast<int2*>(ws);
+  ws += up256((size_t)a.batch * p.pl.jobs_per_seq * sizeof(int2));
   const size_t rows = slots(a.batch, p.pl.jobs_per_seq) * 8 * NT;
   p.ml = reinterpret_cast<float2*>(ws);
   ws += up256(rows * sizeof(float2));
@@ -721,10 +732,15 @@ cudaError_t launch_n(const AttnKv4Args& a, cudaStream_t stream, int sms) {
   cfg.attrs = &overlap;
   cfg.numAttrs = 1;
   if ((e = cudaLaunchKernelEx(&cfg, kernel, p)) != cudaSuccess) return e;
-  cfg.gridDim = dim3(a.batch * a.steps, a.h_q);
+  // lane groups to a row: one for every four shares that a job has where all are alike
+  constexpr int LANES = D / 4 < 32 ? D / 4 : 32;
+  int groups = 1;
+  while (groups < kJoinThreads / LANES && (long long)groups * 4 * a.batch * p.pl.jobs_per_seq < p.pl.workers) groups *= 2;
+  const long long items = (long long)a.batch * a.steps * a.h_q * (D / 4 / LANES), per = kJoinThreads / LANES / groups;
+  cfg.gridDim = dim3((unsigned)((items + per - 1) / per));
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, attn_kv4_join<D, NT>, p);
+  return cudaLaunchKernelEx(&cfg, attn_kv4_join<D, NT>, p, groups);
 }
 
 template <int D>
@@ -737,7 +753,8 @@ cudaError_t launch_d(const AttnKv4Args& a, cudaStream_t stream, int sms) {
 size_t attn_kv4_scratch_bytes(int batch, int steps, int h_q, int h_kv, int d) {
   const int rows = steps * (h_q / h_kv), per = 8 * row_blocks(rows);
   const size_t n = slots(batch, h_kv * ((rows + per - 1) / per)) * per;
-  return up256((size_t)(batch + 1) * sizeof(long long)) + up256(n * sizeof(float2)) + up256(n * d * sizeof(float));
+  return up256((size_t)batch * (h_kv * ((rows + per - 1) / per)) * sizeof(int2)) + up256(n * sizeof(float2)) +
+         up256(n * d * sizeof(float));
 }
 
 cudaError_t launch_attn_kv4(const AttnKv4Args& p, cudaStream_t stream) {

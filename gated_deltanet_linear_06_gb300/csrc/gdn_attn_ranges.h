@@ -1,5 +1,5 @@
-// gdn_attn_ranges.h -- which of a job's ranges the join of gdn_attn_decode_shared
-// reads.  Plain C++, so that it is tested without a GPU.
+// gdn_attn_ranges.h -- which of a job's ranges the joins of gdn_attn_decode_shared
+// and gdn_attn_decode_kv4 read.  Plain C++, so that it is tested without a GPU.
 #pragma once
 
 #ifdef __CUDACC__
