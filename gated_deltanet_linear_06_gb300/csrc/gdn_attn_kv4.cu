@@ -1,8 +1,6 @@
 // gdn_attn_kv4.cu -- attention of a batch of sequences over the 4-bit paged cache.
 #include <math.h>
 
-#include <type_traits>
-
 #include "../../include/gdn.h"
 #include "gdn_attn_ranges.h"
 #include "gdn_kv4.cuh"
@@ -21,6 +19,7 @@ constexpr int kWide = 3;
 constexpr int kLeastV = -93;                       // scales are zero or at least 2^-93
 constexpr float kStored = 28.0f;                   // shares are stored with weights up to 2^(kTop - kStored)
 constexpr int kMinItems = 2;                       // units that a warp takes at least
+constexpr int kJobUnits = 4;                       // what a job costs besides its units
 constexpr int kMaxCtas = 160;                      // the workspace has room for
 constexpr int kMaxWarps = 16;
 
@@ -72,6 +71,9 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
   mma(d, a, b0, b1, d[0], d[1], d[2], d[3]);
 }
 
+__device__ __forceinline__ float lo_f32(uint32_t x) { return __uint_as_float(x << 16); }
+__device__ __forceinline__ float hi_f32(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
+
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t y;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -83,11 +85,19 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 // which the tensor cores take as it is).  The other operand or the end result makes up for
 // the power of two, and a product takes off the 8 that each code is too much.
 constexpr uint32_t kAt0 = 0x000f000fu, kAt4 = 0x00f000f0u, kAt2 = 0x003c003cu, kAt6 = 0x03c003c0u;
-constexpr uint32_t kLess8At0 = 0x80088008u, kLess8At4 = 0x80808080u;   // -8 at those places
+// -8 at those places
+constexpr uint32_t kLess8At0 = 0x80088008u, kLess8At4 = 0x80808080u, kLess8At2 = 0x80208020u, kLess8At6 = 0x82008200u;
 
 __device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {   // bf16 pairs; a NaN gives way
   const __nv_bfloat162 m = __hmax2(__habs2(reinterpret_cast<__nv_bfloat162&>(a)), __habs2(reinterpret_cast<__nv_bfloat162&>(b)));
   return reinterpret_cast<const uint32_t&>(m);
+}
+
+// A bf16 pair times a power of two (exact) as fp16.
+__device__ __forceinline__ uint32_t half_pair(uint32_t x, uint32_t up) {
+  uint32_t y;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(up));
+  return pack_f16x2(lo_f32(y), hi_f32(y));
 }
 
 __device__ __forceinline__ bool try_wait(uint64_t* bar, uint32_t parity) {
@@ -137,17 +147,18 @@ __device__ __forceinline__ void codes_at(uint32_t (&w0)[D / 32], uint32_t (&w1)[
   }
 }
 
-__device__ __forceinline__ float lo_f32(uint32_t x) { return __uint_as_float(x << 16); }
-__device__ __forceinline__ float hi_f32(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
 
-// Length of sequence b, in units; a length out of range counts as none.
+// Units of sequence b; a length out of range counts as none.
 __device__ __forceinline__ int units_of(const AttnKv4Args& a, int b) {
   const int n = a.len[b];
   return n > 0 && n <= (long long)a.width * a.page ? (n + kv4::kUnit - 1) / kv4::kUnit : 0;
 }
 
-// before[0 .. batch] in shared memory, by the whole CTA.
-__device__ void sum_units(const AttnKv4Args& a, long long* before, long long* warp_sums, bool report) {
+// What a job of n units costs, in units: kJobUnits for its rows in and out.
+__device__ __forceinline__ int cost_of(int n) { return n > 0 ? n + kJobUnits : 0; }
+
+// before[0 .. batch]: costs of a job of each sequence before, in shared memory, by the whole CTA.
+__device__ void sum_costs(const AttnKv4Args& a, long long* before, long long* warp_sums, bool report) {
   const int threads = blockDim.x, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int per = (a.batch + threads - 1) / threads, b0 = threadIdx.x * per;
   long long mine = 0;
@@ -155,7 +166,7 @@ __device__ void sum_units(const AttnKv4Args& a, long long* before, long long* wa
     if (b0 + i < a.batch) {
       const int n = a.len[b0 + i];
       if (report && (n < 0 || n > (long long)a.width * a.page)) record_status(a.status, GDN_ERR_DEVICE_BOUNDS);
-      mine += units_of(a, b0 + i);
+      mine += cost_of(units_of(a, b0 + i));
     }
   long long sum = mine;
 #pragma unroll
@@ -170,31 +181,34 @@ __device__ void sum_units(const AttnKv4Args& a, long long* before, long long* wa
   for (int i = 0; i < per; ++i)
     if (b0 + i < a.batch) {
       before[b0 + i] = at;
-      at += units_of(a, b0 + i);
+      at += cost_of(units_of(a, b0 + i));
       if (b0 + i == a.batch - 1) before[a.batch] = at;
     }
   __syncthreads();
 }
 
-// Warps that take part: one for every kMinItems items at most, so that none is empty.
+// Warps that take part: one for every kMinItems items at most, so that none has nothing.
 __device__ __forceinline__ int workers_of(const Kv4Params& p, long long total) {
   const long long n = (total + kMinItems - 1) / kMinItems;
   return n < p.pl.workers ? (int)n : p.pl.workers;
 }
 
-// Where an item (a unit of a job) lies.
+// A warp's place among the items: a job's kJobUnits and then its units, job after job.
 struct Item {
-  int b, job, u, n;          // sequence, job of it, unit, units of the sequence
+  int b, job, u, n;          // sequence, job of it, unit (below 0: before the first), units of the sequence
 };
 
-__device__ __forceinline__ void next_job(const Kv4Params& p, const long long* before, Item& it) {
+// The next job's start, given the items (from the end of this job on) that are left to the
+// warp; a job whose units begin past them is none.
+__device__ __forceinline__ void next_job(const Kv4Params& p, const long long* before, Item& it, long long& rest) {
   it.u = 0;
+  rest -= kJobUnits;
   if (++it.job < p.pl.jobs_per_seq) return;
   it.job = 0;
   do {
     ++it.b;
-    it.n = it.b < p.a.batch ? (int)(before[it.b + 1] - before[it.b]) : 0;
-  } while (it.n == 0 && it.b < p.a.batch);
+    it.n = it.b < p.a.batch ? (int)(before[it.b + 1] - before[it.b]) - kJobUnits : 0;
+  } while (it.n < 0 && it.b < p.a.batch);
 }
 
 template <int D, int NT>
@@ -214,7 +228,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) attn_kv4_kernel(Kv4
   if (lane == 0)
     for (int i = 0; i < C::STAGES; ++i) tc::mbar_init(bar + i, 1);
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  sum_units(a, before, warp_sums, blockIdx.x == 0);
+  sum_costs(a, before, warp_sums, blockIdx.x == 0);
 
   // This warp's items, and where the first one is.
   const long long total = before[a.batch] * p.pl.jobs_per_seq;
@@ -232,13 +246,19 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) attn_kv4_kernel(Kv4
         if (before[mid] * p.pl.jobs_per_seq <= x0) lo = mid; else hi = mid;
       }
       use.b = lo;
-      use.n = (int)(before[lo + 1] - before[lo]);
-      const long long rest = x0 - before[lo] * p.pl.jobs_per_seq;
-      use.job = (int)(rest / use.n);
-      use.u = (int)(rest - (long long)use.job * use.n);
+      const int cost = (int)(before[lo + 1] - before[lo]);
+      const long long at = x0 - before[lo] * p.pl.jobs_per_seq;
+      use.n = cost - kJobUnits;
+      use.job = (int)(at / cost);
+      use.u = (int)(at - (long long)use.job * cost) - kJobUnits;
+    }
+    long long rest = x1 - x0;                // units not yet met
+    if (use.u < 0) {                         // the share begins before the job's first unit
+      rest += use.u;
+      use.u = 0;
     }
     Item ask = use;
-    long long to_ask = x1 - x0;              // units not yet asked for
+    long long to_ask = rest;                 // units not yet asked for
     const int upp = a.page / kv4::kUnit;     // units of a page
     int entry = 0, entry_b = -1, entry_0 = 0;   // this lane's of 32 entries of a sequence's table
     int left = 0;                            // units of the page that `src` is in, from there on
@@ -310,11 +330,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) attn_kv4_kernel(Kv4
         --left;
       }
       put = put + 1 == C::STAGES ? 0 : put + 1;
-      if (ask.u == ask.n) next_job(p, before, ask);
+      if (ask.u == ask.n) next_job(p, before, ask, to_ask);
     };
     for (int i = 0; i < C::STAGES && to_ask > 0; ++i) request();
 
-    long long rest = x1 - x0;                // units not yet met
     while (rest > 0 && ok) {
       // one job's units, or this warp's share of them
       const int job = use.b * p.pl.jobs_per_seq + use.job;
@@ -340,41 +359,33 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) attn_kv4_kernel(Kv4
         const long long at = (long long)use.b * a.steps + row / p.pl.G;
         const uint16_t* from = a.q + (at * a.h_q + hk * p.pl.G + row % p.pl.G) * D + 8 * t;
         uint4 raw[R];
-        float most = 0.0f;
+        uint32_t most2 = 0;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           raw[r] = row < p.pl.R ? *reinterpret_cast<const uint4*>(from + 32 * r) : make_uint4(0, 0, 0, 0);
-          const uint32_t w[4] = {raw[r].x, raw[r].y, raw[r].z, raw[r].w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) most = fmaxf(most, fmaxf(fabsf(lo_f32(w[i])), fabsf(hi_f32(w[i]))));
+          most2 = max_abs2(max_abs2(max_abs2(most2, raw[r].x), raw[r].y), max_abs2(raw[r].z, raw[r].w));
         }
+        float most = fmaxf(lo_f32(most2), hi_f32(most2));
         most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
         most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
-        // 2^10 over the power of two in `most`, at most 2^126 (a row of nothing but tiny numbers)
-        const uint32_t ex = min(264 - min((int)(__float_as_uint(most) >> 23), 254), 253);
-        const float up = __uint_as_float(ex << 23), down = __uint_as_float((254 - ex) << 23);
+        // 2^10 over the power of two in `most`, at most 2^120 (a row of nothing but tiny numbers)
+        const uint32_t ex = min(264 - min((int)(__float_as_uint(most) >> 23), 254), 247);
+        const uint32_t up = ex << 7 | ex << 23, up16 = (ex + 4) << 7 | (ex + 4) << 23;   // bf16 pairs
+        const float down = __uint_as_float((254 - ex) << 23);
 #pragma unroll
         for (int i = 0; i < 2; ++i) scale[n][i] = p.qscale * 0x1p18f * __shfl_sync(0xffffffffu, down, (2 * t + i) * 4);
+        const uint32_t less8[4] = {kLess8At2, kLess8At2, kLess8At6, kLess8At6};
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-          const uint32_t w[4] = {raw[r].x, raw[r].y, raw[r].z, raw[r].w};
-          uint32_t h[4];
-          float sum = 0.0f;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float m = i % 2 == 0 ? 16.0f : 1.0f;
-            h[i] = pack_f16x2(lo_f32(w[i]) * up * m, hi_f32(w[i]) * up * m);
-            const float2 x = __half22float2(reinterpret_cast<const __half2&>(h[i]));
-            sum = fmaf(i % 2 == 0 ? -0x1p-19f : -0x1p-15f, x.x + x.y, sum);
-          }
-          sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-          sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-          const float sum0 = __shfl_sync(0xffffffffu, sum, 8 * t), sum1 = __shfl_sync(0xffffffffu, sum, 8 * t + 4);
-          const float4 sums = make_float4(sum0, sum1, sum0, sum1);
-          if constexpr (QREG) q[n][r] = make_uint4(h[0], h[1], h[2], h[3]);
-          else *reinterpret_cast<uint4*>(qs + (n * R + r) * 512 + lane * 16) = make_uint4(h[0], h[1], h[2], h[3]);
-          if constexpr (BREG) base[n][r] = sums;
-          else if (g == 0) bs[(n * R + r) * 4] = sums;
+          const uint4 h = make_uint4(half_pair(raw[r].x, up16), half_pair(raw[r].y, up), half_pair(raw[r].z, up16),
+                                     half_pair(raw[r].w, up));
+          float c[4];
+          mma(c, less8, h.x, h.y, 0.0f, 0.0f, 0.0f, 0.0f);
+          mma(c, less8, h.z, h.w);
+          if constexpr (QREG) q[n][r] = h;
+          else *reinterpret_cast<uint4*>(qs + (n * R + r) * 512 + lane * 16) = h;
+          if constexpr (BREG) base[n][r] = make_float4(c[0], c[1], c[2], c[3]);
+          else if (g == 0) bs[(n * R + r) * 4] = make_float4(c[0], c[1], c[2], c[3]);
         }
       }
       if constexpr (!BREG) __syncwarp();
@@ -390,6 +401,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) attn_kv4_kernel(Kv4
       float o[NT][R][2][4], ref[NT][2], sum[NT][2];
       int v = kLeastV;                       // 2^v: above every scale of V at the last update
       uint32_t fresh = (1u << (2 * NT)) - 1;   // this lane's rows that have not seen a score
+      uint32_t poison = 0;                   // their groups that are NaN, eight bits a row
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -402,9 +414,38 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) attn_kv4_kernel(Kv4
         sum[n][0] = sum[n][1] = 0.0f;
       }
 
-      // A stage of units from u on; at the edge some row does not see all of their tokens.
-      const auto meet = [&](int u, const uint8_t* st, uint32_t gone, auto at_edge) {
-        constexpr bool edge = decltype(at_edge)::value;
+      // Where not every row sees all of a stage's tokens: in tokens of no row (past the
+      // sequence, of another share, of a page that is not there) V's scales become zeros,
+      // whatever the cache holds.  So do scales that are not finite, for a row that does not see
+      // the token gives it a weight of zero, and its product with them would be NaN; groups of
+      // rows that do see it are noted and become NaN at the end.
+      const auto clean = [&](int u, uint8_t* st, uint32_t gone) {
+#pragma unroll 1
+        for (int i = 0; i < 2 * C::UNITS; ++i) {
+          const int token = u * kv4::kUnit + 8 * i + g;
+          uint8_t* at = st + i / 2 * C::UNIT + 16 * D + (g + i % 2 * 8) * (D / 8) + D / 16 + t % (R / 2) * 4;
+          uint32_t w = *reinterpret_cast<const uint32_t*>(at), odd = 0;
+          if ((w & 0x7f80u) == 0x7f80u) odd |= 1u, w &= 0xffff0000u;
+          if ((w & 0x7f800000u) == 0x7f800000u) odd |= 2u, w &= 0xffffu;
+          if (token >= past || gone >> (i / 2) & 1) w = odd = 0;
+          *reinterpret_cast<uint32_t*>(at) = w;
+          for (uint32_t lanes = __ballot_sync(0xffffffffu, odd != 0); lanes != 0; lanes &= lanes - 1) {
+            const int from = __ffs(lanes) - 1;
+            const int which = __shfl_sync(0xffffffffu, token, from);
+            const uint32_t groups = __shfl_sync(0xffffffffu, odd << (2 * (t % (R / 2))), from);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int k = 0; k < 2; ++k)
+                if (which <= last[n][k]) poison |= groups << (8 * (2 * n + k));
+          }
+        }
+        __syncwarp();
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // before the stage's next copy
+      };
+
+      // A stage of units from u on.
+      const auto meet = [&](int u, const uint8_t* st, uint32_t gone) {
         constexpr int NU = C::UNITS;
         const int j = u * kv4::kUnit + g;    // this lane's tokens: j + 16 k, j + 16 k + 8
         // scores: tokens g and g + 8 of each unit by rows 2 t, 2 t + 1
@@ -457,24 +498,25 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) attn_kv4_kernel(Kv4
         for (int k = 0; k < NU; ++k)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            uint32_t w = *reinterpret_cast<const uint32_t*>(st + k * C::UNIT + 16 * D + (g + 8 * h) * (D / 8) + D / 16 +
+            const uint32_t w = *reinterpret_cast<const uint32_t*>(st + k * C::UNIT + 16 * D + (g + 8 * h) * (D / 8) + D / 16 +
                                                             t % (R / 2) * 4);
-            if (edge && (j + 16 * k + 8 * h >= past || gone >> k & 1)) w = 0;   // whatever the cache holds there
             widest = max_abs2(widest, w);
           }
         const float wide = fmaxf(fmaxf(lo_f32(widest), hi_f32(widest)), 0.0f);   // (0 for NaN)
         bool over = fresh != 0 || (__float_as_int(wide) >> 23) >= v + kWide + 127;
         const float room = kTop + kGrow - (float)v;
 #pragma unroll
-        for (int k = 0; k < NU; ++k)
+        for (int k = 0; k < NU; ++k) {
+          const int at = gone >> k & 1 ? 0x7fffffff - 16 : j + 16 * k;
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               s[k][n][e] = fmaf(s[k][n][e], scale[n][e % 2], -ref[n][e % 2]);
-              if (edge && (j + 16 * k + e / 2 * 8 > last[n][e % 2] || gone >> k & 1)) s[k][n][e] = -INFINITY;
+              if (at + e / 2 * 8 > last[n][e % 2]) s[k][n][e] = -INFINITY;
               over = over || s[k][n][e] > room;
             }
+        }
         if (__any_sync(0xffffffffu, over)) {
           float w = wide;
 #pragma unroll
@@ -541,15 +583,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) attn_kv4_kernel(Kv4
                                       {x1 & kAt0, x1 & kAt4, y1 & kAt0, y1 & kAt4}};
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-              float e0 = s[k][n][0] * s0, e1 = s[k][n][1] * s0, e2 = s[k][n][2] * s1, e3 = s[k][n][3] * s1;
-              if constexpr (edge) {          // whatever the scale of a token that is not seen
-                const int at = gone >> k & 1 ? 0x7fffffff - 16 : j + 16 * k;
-                if (at > last[n][0]) e0 = 0.0f;
-                if (at > last[n][1]) e1 = 0.0f;
-                if (at + 8 > last[n][0]) e2 = 0.0f;
-                if (at + 8 > last[n][1]) e3 = 0.0f;
-              }
-              const uint32_t b0 = transpose8(pack_f16x2(e0, e1)), b1 = transpose8(pack_f16x2(e2, e3));
+              const uint32_t b0 = transpose8(pack_f16x2(s[k][n][0] * s0, s[k][n][1] * s0));
+              const uint32_t b1 = transpose8(pack_f16x2(s[k][n][2] * s1, s[k][n][3] * s1));
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
                 mma(o[n][r][i], less8, b0, b1);
@@ -565,14 +600,24 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) attn_kv4_kernel(Kv4
         if (!__all_sync(0xffffffffu, try_wait(bar + get, parity)))
           ok = __all_sync(0xffffffffu, tc::mbar_wait(bar + get, parity, kWaitClocks));
         if (!ok) break;
-        const uint8_t* st = ring + (warp * C::STAGES + get) * C::STAGE;
+        uint8_t* st = ring + (warp * C::STAGES + get) * C::STAGE;
         const uint32_t gone = bad >> (get * C::UNITS) & ((1u << C::UNITS) - 1);
-        if ((u + C::UNITS) * kv4::kUnit - 1 > all_see || gone != 0) meet(u, st, gone, std::true_type());
-        else meet(u, st, 0u, std::false_type());
+        if ((u + C::UNITS) * kv4::kUnit - 1 > all_see || gone != 0) clean(u, st, gone);
+        meet(u, st, gone);
         __syncwarp();
         get = get + 1 == C::STAGES ? 0 : get + 1;
         parity ^= get == 0;
         if (to_ask > 0) request();
+      }
+      if (__any_sync(0xffffffffu, poison != 0)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if (poison >> (16 * n + 8 * (e % 2) + r) & 1) o[n][r][0][e] = o[n][r][1][e] = __uint_as_float(0x7fc00000u);
+            }
       }
       // the share's sums into its slot, as with weights that do not go by V's scales
       const float stored = __uint_as_float((uint32_t)(v - (int)kStored + 127) << 23);
@@ -594,7 +639,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) attn_kv4_kernel(Kv4
       if (!ok) break;
       rest -= end - use.u;
       use.u = end;
-      if (end == use.n) next_job(p, before, use);
+      if (end == use.n) next_job(p, before, use, rest);
     }
     if (!ok) {                               // a copy did not come: wait for the others, then leave
       if (lane == 0) record_status(a.status, GDN_ERR_DEVICE_TIMEOUT);
