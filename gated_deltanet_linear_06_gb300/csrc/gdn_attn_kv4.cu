@@ -1,4 +1,5 @@
 // gdn_attn_kv4.cu -- attention of a batch of sequences over the 4-bit paged cache.
+#include <limits.h>
 #include <math.h>
 
 #include "../../include/gdn.h"
@@ -17,6 +18,7 @@ constexpr long long kWaitClocks = 2000000000LL;   // a second or so: a copy that
 constexpr float kTop = 8.0f, kGrow = 4.0f;
 constexpr int kWide = 3;
 constexpr int kLeastV = -93;                       // scales are zero or at least 2^-93
+constexpr int kTinyWeights = 60;                   // with a larger v, weights that count may be subnormal
 constexpr float kStored = 28.0f;                   // shares are stored with weights up to 2^(kTop - kStored)
 constexpr int kMinItems = 2;                       // units that a warp takes at least
 constexpr int kJobUnits = 4;                       // what a job costs besides its units
@@ -43,20 +45,25 @@ struct Kv4Params {
 template <int D, int NT>
 struct Cfg {
   static constexpr int R = D / 32;
-  static constexpr int UNITS = D == 256 && NT == 2 ? 1 : 2;   // met at once: a stage
+  static constexpr int UNITS = NT == 2 ? 256 / D : 512 / D < 4 ? 512 / D : 4;   // met at once: a stage
   static constexpr bool QREG = NT * R <= 8;          // q's operands in registers, else in shared memory
   static constexpr bool BREG = NT * R <= 2;          // and the sums of their channels
-  static constexpr int WARPS = D == 64 && NT == 1 ? 12 : 8;
+  static constexpr int WARPS = D == 64 && NT == 1 ? 12 : 8;   // (registers for 8 or 12; 10 left one scheduler with more)
   static constexpr int UNIT = kv4::unit_bytes(D), STAGE = UNITS * UNIT;
-  static constexpr int STAGES = D == 256 ? (NT == 1 ? 2 : 3) : (D == 128 ? 4 : 5);
+  static constexpr int STAGES = D == 256 && NT == 2 ? 3 : 2;
   static constexpr int QBYTES = QREG ? 0 : NT * R * 512, BBYTES = BREG ? 0 : NT * R * 64;   // a warp's
   static constexpr int SMEM = WARPS * (STAGES * STAGE + QBYTES + BBYTES);
   static_assert(SMEM <= 216 * 1024 && UNITS * STAGES <= 32, "shared memory, bits of `bad`");
 };
 
-__device__ __forceinline__ float ex2(float x) {
+__device__ __forceinline__ float ex2(float x) {   // results below 2^-126: zero
   float y;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));   // subnormal results count: scales of V may be huge
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float ex2_small(float x) {   // subnormal results too
+  float y;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
@@ -259,8 +266,11 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) attn_kv4_kernel(Kv4
     }
     Item ask = use;
     long long to_ask = rest;                 // units not yet asked for
-    const int upp = a.page / kv4::kUnit;     // units of a page
-    int entry = 0, entry_b = -1, entry_0 = 0;   // this lane's of 32 entries of a sequence's table
+    const int upp_log = 31 - __clz(a.page / kv4::kUnit), upp = 1 << upp_log;   // units of a page
+    const long long page_bytes = (long long)a.h_kv * upp * C::UNIT;
+    int entry = 0, entry_0 = INT_MIN;        // this lane's of 32 entries of the sequence's table
+    const auto head_of = [&]() { return a.cache + (long long)(ask.job / p.pl.blocks) * upp * C::UNIT; };
+    const uint8_t* head = head_of();         // page 0's units of the job's head
     int left = 0;                            // units of the page that `src` is in, from there on
     bool there = false;                      // is there such a page?
     const uint8_t* src = a.cache;
@@ -270,67 +280,56 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) attn_kv4_kernel(Kv4
     uint32_t parity = 0;
 
     const auto find_page = [&]() {
-      const int pg = ask.u / upp, at = ask.u - pg * upp;
-      if (ask.b != entry_b || pg - entry_0 >= 32 || pg < entry_0) {
-        entry_b = ask.b;
+      const int pg = ask.u >> upp_log, at = ask.u & (upp - 1);
+      if (pg < entry_0 || pg >= entry_0 + 32) {
         entry_0 = pg;
         entry = pg + lane < a.width ? a.table[(long long)ask.b * a.width + pg + lane] : -1;
       }
       const int page = __shfl_sync(0xffffffffu, entry, pg - entry_0);
-      there = page >= 0 && page < a.n_pages;
+      there = (unsigned)page < (unsigned)a.n_pages;
       if (!there && lane == 0) record_status(a.status, GDN_ERR_DEVICE_BOUNDS);
       left = min(upp - at, ask.n - ask.u);
-      src = a.cache + (((long long)page * a.h_kv + ask.job / p.pl.blocks) * upp + at) * C::UNIT;
+      src = head + page * page_bytes + at * C::UNIT;
     };
-    const auto copy = [&](int unit, int bytes) {
-      asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                       stages + put * C::STAGE + unit * C::UNIT),
-                   "l"(src), "r"(bytes), "r"(tc::smem_u32(bar + put))
-                   : "memory");
-    };
-    // One more stage: of one job's units as many as it holds, in one copy where they are of
-    // one page.
+    // One more stage: of one job's units as many as it holds, one copy for each page.
     const auto request = [&]() {
       int units = min(C::UNITS, ask.n - ask.u);
       if (units > to_ask) units = (int)to_ask;
       to_ask -= units;
-      // (armed before the first copy, with what there will be)
-      if (left == 0) find_page();
-      const int first = min(left, units);
-      int bytes = there ? first * C::UNIT : 0;
       bad &= ~(((1u << C::UNITS) - 1) << (put * C::UNITS));
-      if (!there) bad |= ((1u << first) - 1) << (put * C::UNITS);
-      if (C::UNITS == 1 || first == units) {
-        if (lane == 0) {
-          asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(tc::smem_u32(bar + put)), "r"(bytes)
-                       : "memory");
-          if (there) copy(0, bytes);
+      int done = 0;
+#pragma unroll 1
+      while (true) {
+        if (left == 0) find_page();
+        const int run = min(left, units - done);
+        if (there) {
+          // (the barrier's turn does not end before the arrival below)
+          if (lane == 0) {
+            asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(tc::smem_u32(bar + put)),
+                         "r"(run * C::UNIT)
+                         : "memory");
+            asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                             stages + put * C::STAGE + done * C::UNIT),
+                         "l"(src), "r"(run * C::UNIT), "r"(tc::smem_u32(bar + put))
+                         : "memory");
+          }
+        } else {
+          bad |= ((1u << run) - 1) << (put * C::UNITS + done);
         }
-        src += first * C::UNIT;
-        ask.u += first;
-        left -= first;
-      } else {                               // the second unit is another page's
-        const uint8_t* src0 = src;
-        const bool there0 = there;
-        ++ask.u;
-        find_page();
-        if (!there) bad |= 2u << (put * C::UNITS);
-        if (lane == 0) {
-          asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(tc::smem_u32(bar + put)),
-                       "r"(bytes + (there ? C::UNIT : 0))
-                       : "memory");
-          if (there) copy(1, C::UNIT);
-          const uint8_t* src1 = src;
-          src = src0;
-          if (there0) copy(0, C::UNIT);
-          src = src1;
-        }
-        src += C::UNIT;
-        ++ask.u;
-        --left;
+        src += run * C::UNIT;
+        left -= run;
+        done += run;
+        ask.u += run;
+        if (done == units) break;
       }
+      if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(tc::smem_u32(bar + put)) : "memory");
       put = put + 1 == C::STAGES ? 0 : put + 1;
-      if (ask.u == ask.n) next_job(p, before, ask, to_ask);
+      if (ask.u == ask.n) {
+        const int b = ask.b;
+        next_job(p, before, ask, to_ask);
+        head = head_of();
+        if (ask.b != b) entry_0 = INT_MIN;
+      }
     };
     for (int i = 0; i < C::STAGES && to_ask > 0; ++i) request();
 
@@ -363,11 +362,13 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) attn_kv4_kernel(Kv4
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           raw[r] = row < p.pl.R ? *reinterpret_cast<const uint4*>(from + 32 * r) : make_uint4(0, 0, 0, 0);
-          most2 = max_abs2(max_abs2(max_abs2(most2, raw[r].x), raw[r].y), max_abs2(raw[r].z, raw[r].w));
+          most2 = __vmaxu2(__vmaxu2(most2, raw[r].x & 0x7fff7fffu), raw[r].y & 0x7fff7fffu);
+          most2 = __vmaxu2(__vmaxu2(most2, raw[r].z & 0x7fff7fffu), raw[r].w & 0x7fff7fffu);
         }
-        float most = fmaxf(lo_f32(most2), hi_f32(most2));
-        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
-        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+        most2 = max(most2 & 0xffffu, most2 >> 16);     // (an infinity or a NaN: 0x7f80 or above)
+        most2 = max(most2, __shfl_xor_sync(0xffffffffu, most2, 1));
+        most2 = max(most2, __shfl_xor_sync(0xffffffffu, most2, 2));
+        const float most = __uint_as_float(most2 << 16);
         // 2^10 over the power of two in `most`, at most 2^120 (a row of nothing but tiny numbers)
         const uint32_t ex = min(264 - min((int)(__float_as_uint(most) >> 23), 254), 247);
         const uint32_t up = ex << 7 | ex << 23, up16 = (ex + 4) << 7 | (ex + 4) << 23;   // bf16 pairs
@@ -445,7 +446,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) attn_kv4_kernel(Kv4
       };
 
       // A stage of units from u on.
-      const auto meet = [&](int u, const uint8_t* st, uint32_t gone) {
+      const auto meet = [&](int u, const uint8_t* st, uint32_t gone, bool edge) {
         constexpr int NU = C::UNITS;
         const int j = u * kv4::kUnit + g;    // this lane's tokens: j + 16 k, j + 16 k + 8
         // scores: tokens g and g + 8 of each unit by rows 2 t, 2 t + 1
@@ -506,17 +507,28 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) attn_kv4_kernel(Kv4
         bool over = fresh != 0 || (__float_as_int(wide) >> 23) >= v + kWide + 127;
         const float room = kTop + kGrow - (float)v;
 #pragma unroll
-        for (int k = 0; k < NU; ++k) {
-          const int at = gone >> k & 1 ? 0x7fffffff - 16 : j + 16 * k;
+        for (int k = 0; k < NU; ++k)
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              s[k][n][e] = fmaf(s[k][n][e], scale[n][e % 2], -ref[n][e % 2]);
-              if (at + e / 2 * 8 > last[n][e % 2]) s[k][n][e] = -INFINITY;
-              over = over || s[k][n][e] > room;
-            }
+            for (int e = 0; e < 4; ++e) s[k][n][e] = fmaf(s[k][n][e], scale[n][e % 2], -ref[n][e % 2]);
+        if (edge) {
+#pragma unroll
+          for (int k = 0; k < NU; ++k) {
+            const int at = gone >> k & 1 ? 0x7fffffff - 16 : j + 16 * k;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (at + e / 2 * 8 > last[n][e % 2]) s[k][n][e] = -INFINITY;
+          }
         }
+#pragma unroll
+        for (int k = 0; k < NU; ++k)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) over = over || s[k][n][e] > room;
         if (__any_sync(0xffffffffu, over)) {
           float w = wide;
 #pragma unroll
@@ -556,15 +568,27 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) attn_kv4_kernel(Kv4
             }
           v = v1;
         }
+        if (v > kTinyWeights) {              // V's scales are huge, and weights tiny
+#pragma unroll
+          for (int k = 0; k < NU; ++k)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) s[k][n][e] = ex2_small(s[k][n][e]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < NU; ++k)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) s[k][n][e] = ex2(s[k][n][e]);
+        }
 #pragma unroll
         for (int k = 0; k < NU; ++k)
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              s[k][n][e] = ex2(s[k][n][e]);
-              sum[n][e % 2] += s[k][n][e];
-            }
+            for (int e = 0; e < 4; ++e) sum[n][e % 2] += s[k][n][e];
         // outputs: channels by rows, over the 16 tokens of each unit
         const uint32_t less8[4] = {kLess8At0, kLess8At4, kLess8At0, kLess8At4};
 #pragma unroll
@@ -602,8 +626,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) attn_kv4_kernel(Kv4
         if (!ok) break;
         uint8_t* st = ring + (warp * C::STAGES + get) * C::STAGE;
         const uint32_t gone = bad >> (get * C::UNITS) & ((1u << C::UNITS) - 1);
-        if ((u + C::UNITS) * kv4::kUnit - 1 > all_see || gone != 0) clean(u, st, gone);
-        meet(u, st, gone);
+        const bool edge = (u + C::UNITS) * kv4::kUnit - 1 > all_see || gone != 0;
+        if (edge) clean(u, st, gone);
+        meet(u, st, gone, edge);
         __syncwarp();
         get = get + 1 == C::STAGES ? 0 : get + 1;
         parity ^= get == 0;
