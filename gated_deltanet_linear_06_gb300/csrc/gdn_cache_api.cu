@@ -17,6 +17,12 @@ bool maybe16(const void* p) { return aligned(p, 16); }
 
 bool page_size(int page) { return page == 16 || page == 32 || page == 64 || page == 128 || page == 256; }
 
+int log2_of(int page) {
+  int n = 0;
+  while (1 << n < page) ++n;
+  return n;
+}
+
 // What these calls take of the attention dimensions: heads, head size, scale.
 gdn_status check_dims(const gdn_attn_dims* d) {
   if (!d || d->h_q <= 0 || d->h_kv <= 0 || d->h_q % d->h_kv != 0 || d->d <= 0 || !isfinite(d->scale) ||
@@ -133,7 +139,7 @@ gdn_status gdn_kv4_store(const gdn_attn_dims* dims, int page, long long n_pages,
   p.cache_rows = n_pages * page;
   p.h_kv = dims->h_kv;
   p.d = dims->d;
-  p.page = page;
+  p.page_log = log2_of(page);
   return gdn::launch_kv4_store(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
@@ -162,7 +168,7 @@ gdn_status gdn_kv4_load(const gdn_attn_dims* dims, int page, long long n_pages, 
   p.cache_rows = n_pages * page;
   p.h_kv = dims->h_kv;
   p.d = dims->d;
-  p.page = page;
+  p.page_log = log2_of(page);
   p.out_f32 = out_dtype == GDN_DTYPE_F32;
   return gdn::launch_kv4_load(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }

@@ -19,15 +19,6 @@ namespace {
 
 constexpr int kKv4Warps = 8;
 
-__device__ __forceinline__ void unpack8(uint4 raw, float (&x)[8]) {
-  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
-}
-
 // One warp's share of a call: tokens first .. first + 15 of the list (those in range),
 // head, K or V, vector.
 struct Share {
@@ -37,19 +28,18 @@ struct Share {
 };
 
 template <int D>
-__device__ __forceinline__ bool share_of(const Kv4RowsArgs& p, long long item, Share& s) {
+__device__ __forceinline__ bool share_of(const Kv4RowsArgs& p, unsigned item, Share& s) {
   constexpr int NV = D / 64;
-  const int kinds = (p.k != nullptr) + (p.v != nullptr);
-  const int per = p.h_kv * kinds * NV;
-  const long long block = item / per;
-  int rest = (int)(item - block * per);
+  const unsigned kinds = (p.k != nullptr) + (p.v != nullptr);
+  const unsigned per = p.h_kv * kinds * NV, block = item / per;
+  unsigned rest = item - block * per;
   s.vec = rest % NV;
   rest /= NV;
   s.is_v = p.k == nullptr || rest % kinds == 1;
   s.head = rest / kinds;
   // sixteens that end with the first token's unit, where there is more than one
   const int lead = p.slot && p.tokens > kv4::kUnit ? max(p.slot[0], 0) % kv4::kUnit : 0;
-  s.first = block * kv4::kUnit - lead;
+  s.first = (long long)block * kv4::kUnit - lead;
   return s.first < p.tokens;
 }
 
@@ -66,52 +56,56 @@ __device__ __forceinline__ int row_of(const Kv4RowsArgs& p, long long t) {
 // The unit of cache row r (>= 0) for a head.
 template <int D>
 __device__ __forceinline__ uint8_t* unit_at(const Kv4RowsArgs& p, int r, int head) {
-  const int page = r / p.page, at = (r - page * p.page) / kv4::kUnit;
-  return p.cache + (((long long)page * p.h_kv + head) * (p.page / kv4::kUnit) + at) * kv4::unit_bytes(D);
+  const int upp_log = p.page_log - 4;   // units of a page
+  const long long page = r >> p.page_log;
+  return p.cache + (((page * p.h_kv + head) << upp_log) + ((r >> 4) & ((1 << upp_log) - 1))) * kv4::unit_bytes(D);
 }
+
+// A group's scale from a lane's numbers (N words of bf16 pairs), the group's lanes FROM .. TO
+// apart.
+template <int N, int FROM, int TO>
+__device__ __forceinline__ float scale_of(const uint32_t (&w)[N]) {
+  uint32_t mags = 0, tops = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    mags = __vmaxu2(mags, w[i] & 0x7fff7fffu);
+    tops = __vmaxs2(tops, w[i]);             // (negative numbers' bits are below 0)
+  }
+  uint32_t ex = kv4::extremes(mags, tops);
+#pragma unroll
+  for (int m = FROM; m <= TO; m <<= 1) ex = __vmaxu2(ex, __shfl_xor_sync(0xffffffffu, ex, m));
+  return kv4::group_scale(ex);
+}
+
+__device__ __forceinline__ float lo_f32(uint32_t x) { return __uint_as_float(x << 16); }
+__device__ __forceinline__ float hi_f32(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
 
 // Codes of a group's eight channels (of lane t of four) as K's word, and the group's scale.
 __device__ __forceinline__ uint32_t k_word(uint4 raw, float& s) {
-  float x[8], hi, lo;
-  unpack8(raw, x);
-  hi = lo = x[0];
-  bool finite = isfinite(x[0]);
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+  s = scale_of<4, 1, 2>(w);
+  const float r = kv4::inverse(s);
+  uint32_t c = 0;                              // nibble 7 first: channels 7, 5, 3, 1, 6, 4, 2, 0
 #pragma unroll
-  for (int i = 1; i < 8; ++i) {
-    hi = fmaxf(hi, x[i]);
-    lo = fminf(lo, x[i]);
-    finite = finite && isfinite(x[i]);
-  }
+  for (int i = 3; i >= 0; --i) c = c * 16 + kv4::code_bits(hi_f32(w[i]), s, r);
 #pragma unroll
-  for (int m = 1; m <= 2; m <<= 1) {
-    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, m));
-    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, m));
-    finite = __shfl_xor_sync(0xffffffffu, (int)finite, m) && finite;
-  }
-  s = kv4::group_scale(hi, lo, finite);
-  uint32_t w = 0;
-#pragma unroll
-  for (int o = 0; o < 8; ++o) w |= kv4::code_of(x[o], s) << (4 * (o / 2 + 4 * (o % 2)));
-  return __funnelshift_l(w, w, 3);
+  for (int i = 3; i >= 0; --i) c = c * 16 + kv4::code_bits(lo_f32(w[i]), s, r);
+  c -= kv4::kCodeBase * 0x11111111u;
+  return s == s ? __funnelshift_l(c, c, 3) : 0x44444444u;   // of a NaN scale 8s, as of zeros
 }
 
 // Codes of a group's four channels (of lane group g of eight) as half a word of V.
 __device__ __forceinline__ uint32_t v_half(uint2 raw, float& s) {
-  const float x[4] = {__uint_as_float(raw.x << 16), __uint_as_float(raw.x & 0xffff0000u),
-                      __uint_as_float(raw.y << 16), __uint_as_float(raw.y & 0xffff0000u)};
-  float hi = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), lo = fminf(fminf(x[0], x[1]), fminf(x[2], x[3]));
-  bool finite = isfinite(x[0]) && isfinite(x[1]) && isfinite(x[2]) && isfinite(x[3]);
+  const uint32_t w[2] = {raw.x, raw.y};
+  s = scale_of<2, 4, 16>(w);
+  const float r = kv4::inverse(s);
+  uint32_t c = 0;
 #pragma unroll
-  for (int m = 4; m <= 16; m <<= 1) {
-    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, m));
-    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, m));
-    finite = __shfl_xor_sync(0xffffffffu, (int)finite, m) && finite;
+  for (int i = 1; i >= 0; --i) {
+    c = c * 16 + kv4::code_bits(hi_f32(w[i]), s, r);
+    c = c * 16 + kv4::code_bits(lo_f32(w[i]), s, r);
   }
-  s = kv4::group_scale(hi, lo, finite);
-  uint32_t w = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) w |= kv4::code_of(x[i], s) << (4 * i);
-  return w;
+  return s == s ? c - kv4::kCodeBase * 0x1111u : 0x8888u;
 }
 
 // Two scales as bf16, which they are exactly (a NaN keeps its bits).
@@ -125,180 +119,258 @@ __device__ __forceinline__ int scale_at(int j, bool is_v, int group) {
   return 16 * D + (j * (D / 16) + (is_v ? D / 32 : 0) + group) * 2;
 }
 
+// Whether the rows of V's two (at d = 64 four) tokens per lane, the warp's sixteen together,
+// are one unit in order; its first row in `start`.
+template <int NH>
+__device__ __forceinline__ bool one_unit(const int (&row)[NH][2], int j0, int& start) {
+  bool run = true;
+  start = __shfl_sync(0xffffffffu, row[0][0] - j0, 0);
+#pragma unroll
+  for (int h = 0; h < NH; ++h)
+#pragma unroll
+    for (int par = 0; par < 2; ++par) run = run && row[h][par] >= 0 && row[h][par] - (j0 + 8 * h + par) == start;
+  return __all_sync(0xffffffffu, run) && start % kv4::kUnit == 0;
+}
+
 template <int D>
-__global__ void __launch_bounds__(kKv4Warps * 32) kv4_store_kernel(Kv4RowsArgs p, long long items) {
-  constexpr int R = D / 32;
+__global__ void __launch_bounds__(kKv4Warps * 32) kv4_store_kernel(Kv4RowsArgs p, unsigned items) {
+  constexpr int R = D / 32, NH = R == 2 ? 2 : 1;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x % 32;
-  const long long item = (long long)blockIdx.x * kKv4Warps + threadIdx.x / 32;
+  const unsigned item = blockIdx.x * kKv4Warps + threadIdx.x / 32;
   Share sh;
   if (item >= items || !share_of<D>(p, item, sh)) return;
+  const int g0 = 4 * sh.vec % R;               // the vector's first group
   if (!sh.is_v) {
-    const int t = lane % 4;
+    // word 4 vec + i: of the token at w / R * 8 + lane / 4, group w % R
+    const int t = lane % 4, j0 = 4 * sh.vec / R * 8 + lane / 4;
+    const uint16_t* src = p.k + sh.head * p.k_sh + 8 * t;
     uint4 raw[4];
-    int row[2] = {-1, -1};
+    int row[NH];
+#pragma unroll
+    for (int h = 0; h < NH; ++h) row[h] = row_of(p, sh.first + j0 + 8 * h);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      // word 4 vec + i: of the token at w / R * 8 + lane / 4, group w % R
-      const int w = 4 * sh.vec + i, j = w / R * 8 + lane / 4;
-      const long long tok = sh.first + j;
-      if (i == 0 || (R == 2 && i == 2)) row[i / 2] = row_of(p, tok);
+      const int h = R == 2 ? i / 2 : 0;
+      const long long tok = sh.first + j0 + 8 * h;
       raw[i] = make_uint4(0, 0, 0, 0);
-      if (row[R == 2 ? i / 2 : 0] >= 0)
-        raw[i] = *reinterpret_cast<const uint4*>(p.k + tok * p.k_st + sh.head * p.k_sh + (w % R) * 32 + 8 * t);
+      if (tok >= 0 && tok < p.tokens) raw[i] = *reinterpret_cast<const uint4*>(src + tok * p.k_st + (R == 2 ? i % 2 : g0 + i) * 32);
     }
     uint32_t word[4];
     float s[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) word[i] = k_word(raw[i], s[i]);
-    if constexpr (R >= 4) {
-      if (row[0] < 0) return;
-      uint8_t* u = unit_at<D>(p, row[0], sh.head);
-      const int j = row[0] % kv4::kUnit, g0 = 4 * sh.vec % R;
-      const int vec = (j / 8 * R + g0) / 4;
-      *reinterpret_cast<uint4*>(u + 512 * vec + 16 * ((j % 8) * 4 + t)) =
-          make_uint4(word[0], word[1], word[2], word[3]);
-      if (t == 0)
-        *reinterpret_cast<uint2*>(u + scale_at<D>(j, false, g0)) =
-            make_uint2(scales2(s[0], s[1]), scales2(s[2], s[3]));
-    } else {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (row[h] < 0) continue;
-        uint8_t* u = unit_at<D>(p, row[h], sh.head);
-        const int j = row[h] % kv4::kUnit;
+    for (int h = 0; h < NH; ++h) {
+      if (row[h] < 0) continue;
+      uint8_t* u = unit_at<D>(p, row[h], sh.head);
+      const int j = row[h] % kv4::kUnit;
+      if constexpr (R >= 4) {
+        *reinterpret_cast<uint4*>(u + 512 * ((j / 8 * R + g0) / 4) + 16 * ((j % 8) * 4 + t)) =
+            make_uint4(word[0], word[1], word[2], word[3]);
+        if (t == 0) *reinterpret_cast<uint2*>(u + scale_at<D>(j, false, g0)) = make_uint2(scales2(s[0], s[1]), scales2(s[2], s[3]));
+      } else {
         *reinterpret_cast<uint2*>(u + 16 * ((j % 8) * 4 + t) + j / 8 * 8) = make_uint2(word[2 * h], word[2 * h + 1]);
         if (t == 0) *reinterpret_cast<uint32_t*>(u + scale_at<D>(j, false, 0)) = scales2(s[2 * h], s[2 * h + 1]);
       }
     }
   } else {
-    const int g = lane / 4, t = lane % 4;
-    // rows of the two tokens of each half that this vector takes from
-    constexpr int NH = R == 2 ? 2 : 1;
+    const int g = lane / 4, j0 = 4 * sh.vec / R * 8 + 2 * (lane % 4);
+    const uint16_t* src = p.v + sh.head * p.v_sh + 4 * g;
     int row[NH][2];
+#pragma unroll
+    for (int h = 0; h < NH; ++h)
+#pragma unroll
+      for (int par = 0; par < 2; ++par) row[h][par] = row_of(p, sh.first + j0 + 8 * h + par);
     uint2 raw[4][2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int w = 4 * sh.vec + i;
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int par = 0; par < 2; ++par) {
-        const long long tok = sh.first + w / R * 8 + 2 * t + par;
-        int& r = row[R == 2 ? i / 2 : 0][par];
-        if (i == 0 || (R == 2 && i == 2)) r = row_of(p, tok);
+        const long long tok = sh.first + j0 + (R == 2 ? i / 2 * 8 : 0) + par;
         raw[i][par] = make_uint2(0, 0);
-        if (r >= 0)
-          raw[i][par] = *reinterpret_cast<const uint2*>(p.v + tok * p.v_st + sh.head * p.v_sh + (w % R) * 32 + 4 * g);
+        if (tok >= 0 && tok < p.tokens)
+          raw[i][par] = *reinterpret_cast<const uint2*>(src + tok * p.v_st + (R == 2 ? i % 2 : g0 + i) * 32);
       }
-    }
     uint32_t half[4][2];
     float s[4][2];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int par = 0; par < 2; ++par) half[i][par] = v_half(raw[i][par], s[i][par]);
-    // a unit of its own: every token where the first one's place says
-    const int w0 = 4 * sh.vec, j0 = w0 / R * 8 + 2 * t;
-    bool run = true;
-    int start = 0;
+    int start;
+    const bool run = one_unit(row, j0, start);
+    if (run)
+      *reinterpret_cast<uint4*>(unit_at<D>(p, start, sh.head) + 8 * D + 512 * sh.vec + 16 * lane) =
+          make_uint4(half[0][0] | half[0][1] << 16, half[1][0] | half[1][1] << 16, half[2][0] | half[2][1] << 16,
+                     half[3][0] | half[3][1] << 16);
+    if (run && g != 0) return;
 #pragma unroll
     for (int h = 0; h < NH; ++h)
 #pragma unroll
       for (int par = 0; par < 2; ++par) {
-        const int at = row[h][par] - (j0 + 8 * h + par);
-        if (h == 0 && par == 0) start = __shfl_sync(0xffffffffu, at, 0);
-        run = run && row[h][par] >= 0 && at == start;
-      }
-    run = __all_sync(0xffffffffu, run) && start % kv4::kUnit == 0;
-    if (run) {
-      uint8_t* u = unit_at<D>(p, start, sh.head);
-      *reinterpret_cast<uint4*>(u + 8 * D + 512 * sh.vec + 16 * lane) =
-          make_uint4(half[0][0] | half[0][1] << 16, half[1][0] | half[1][1] << 16, half[2][0] | half[2][1] << 16,
-                     half[3][0] | half[3][1] << 16);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int par = 0; par < 2; ++par) {
-        const int r = row[R == 2 ? i / 2 : 0][par];
+        const int r = row[h][par], j = r % kv4::kUnit;
         if (r < 0) continue;
         uint8_t* u = unit_at<D>(p, r, sh.head);
-        const int j = r % kv4::kUnit, grp = (4 * sh.vec + i) % R, w = j / 8 * R + grp;
-        if (!run)
-          *reinterpret_cast<uint16_t*>(u + 8 * D + 512 * (w / 4) + 16 * (4 * g + j % 8 / 2) + 4 * (w % 4) + 2 * (j % 2)) =
-              (uint16_t)half[i][par];
-        if (g == 0) *reinterpret_cast<uint16_t*>(u + scale_at<D>(j, true, grp)) = (uint16_t)(__float_as_uint(s[i][par]) >> 16);
+        if (!run) {
+          // word j / 8 * R + group of lane 4 g + j % 8 / 2, half j % 2
+          uint16_t* at = reinterpret_cast<uint16_t*>(u + 8 * D + 16 * (4 * g + j % 8 / 2) + 2 * (j % 2));
+#pragma unroll
+          for (int i = 0; i < 4 / NH; ++i) {
+            const int w = j / 8 * R + (R == 2 ? i : g0 + i);
+            at[256 * (w / 4) + 2 * (w % 4)] = (uint16_t)half[NH == 2 ? 2 * h + i : i][par];
+          }
+        }
+        if (g == 0) {
+          if constexpr (R >= 4)
+            *reinterpret_cast<uint2*>(u + scale_at<D>(j, true, g0)) =
+                make_uint2(scales2(s[0][par], s[1][par]), scales2(s[2][par], s[3][par]));
+          else
+            *reinterpret_cast<uint32_t*>(u + scale_at<D>(j, true, 0)) = scales2(s[2 * h][par], s[2 * h + 1][par]);
+        }
       }
   }
 }
 
-// n values (4 or 8) to bf16 or fp32.
-template <int N, bool F32>
-__device__ __forceinline__ void put(void* out, long long at, const float (&x)[N]) {
-  if constexpr (F32) {
-    float* o = static_cast<float*>(out) + at;
-#pragma unroll
-    for (int i = 0; i < N; i += 4) *reinterpret_cast<float4*>(o + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
-  } else {
-    uint16_t* o = static_cast<uint16_t*>(out) + at;
-    if constexpr (N == 8)
-      *reinterpret_cast<uint4*>(o) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                                                pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
-    else
-      *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
-  }
+// Two codes (bits 0..3 and 16..19) times a scale: code - 8 as bf16 pairs, then either the
+// product rounded once to bf16 or the exact one in fp32.
+__device__ __forceinline__ uint32_t less8(uint32_t x) {
+  uint32_t y = (x & 0x000f000fu) | 0x43004300u;               // 128 + code
+  asm("sub.rn.bf16x2 %0, %0, %1;" : "+r"(y) : "r"(0x43084308u));
+  return y;
+}
+__device__ __forceinline__ uint32_t times(uint32_t x, uint32_t s2) {
+  uint32_t y;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(s2));
+  return y;
+}
+__device__ __forceinline__ float2 times_f32(uint32_t x, float s) {
+  return make_float2(__uint_as_float(x << 16) * s, __uint_as_float(x & 0xffff0000u) * s);
 }
 
-__device__ __forceinline__ float scale_in(const uint8_t* at) {
-  return bf16_to_f32(*reinterpret_cast<const uint16_t*>(at));
+// N pairs of one row times their scale (bf16 bits) to out + at.
+template <int N, bool F32>
+__device__ __forceinline__ void put(void* out, long long at, const uint32_t (&x)[N], uint32_t scale) {
+  if constexpr (F32) {
+    float* o = static_cast<float*>(out) + at;
+    const float s = __uint_as_float(scale << 16);
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      const float2 a = times_f32(x[i], s), b = times_f32(x[i + 1], s);
+      *reinterpret_cast<float4*>(o + 2 * i) = make_float4(a.x, a.y, b.x, b.y);
+    }
+  } else {
+    uint16_t* o = static_cast<uint16_t*>(out) + at;
+    const uint32_t s2 = scale | scale << 16;
+    if constexpr (N == 4)
+      *reinterpret_cast<uint4*>(o) = make_uint4(times(x[0], s2), times(x[1], s2), times(x[2], s2), times(x[3], s2));
+    else
+      *reinterpret_cast<uint2*>(o) = make_uint2(times(x[0], s2), times(x[1], s2));
+  }
 }
 
 template <int D, bool F32>
-__global__ void __launch_bounds__(kKv4Warps * 32) kv4_load_kernel(Kv4RowsArgs p, long long items) {
-  constexpr int R = D / 32;
+__global__ void __launch_bounds__(kKv4Warps * 32) kv4_load_kernel(Kv4RowsArgs p, unsigned items) {
+  constexpr int R = D / 32, NH = R == 2 ? 2 : 1, NG = 4 / NH;   // groups of a token in a vector
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x % 32;
-  const long long item = (long long)blockIdx.x * kKv4Warps + threadIdx.x / 32;
+  const unsigned item = blockIdx.x * kKv4Warps + threadIdx.x / 32;
   Share sh;
   if (item >= items || !share_of<D>(p, item, sh)) return;
+  const int g0 = 4 * sh.vec % R;
+  if (!sh.is_v) {
+    const int t = lane % 4, j0 = 4 * sh.vec / R * 8 + lane / 4;
+    uint32_t word[NH][NG], sc[NH][NG / 2];
+    bool there[NH];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int w0 = 4 * sh.vec + i, grp = w0 % R;
-    if (!sh.is_v) {
-      const int t = lane % 4;
-      const long long tok = sh.first + w0 / R * 8 + lane / 4;
-      if (tok < 0 || tok >= p.tokens) continue;
-      const int r = row_of(p, tok);
-      float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-      if (r >= 0) {
-        const uint8_t* u = unit_at<D>(p, r, sh.head);
-        const int j = r % kv4::kUnit, w = j / 8 * R + grp;
-        uint32_t c = *reinterpret_cast<const uint32_t*>(u + 512 * (w / 4) + 16 * ((j % 8) * 4 + t) + 4 * (w % 4));
-        const float s = scale_in(u + scale_at<D>(j, false, grp));
-        c = __funnelshift_r(c, c, 3);
+    for (int h = 0; h < NH; ++h) {
+      const int r = row_of(p, sh.first + j0 + 8 * h);
+      there[h] = r >= 0;
 #pragma unroll
-        for (int o = 0; o < 8; ++o) x[o] = s * (float)((int)(c >> (4 * (o / 2 + 4 * (o % 2))) & 15) - 8);
-      }
-      put<8, F32>(p.k_out, (tok * p.h_kv + sh.head) * D + grp * 32 + 8 * t, x);
-    } else {
-      const int g = lane / 4;
-#pragma unroll
-      for (int par = 0; par < 2; ++par) {
-        const long long tok = sh.first + w0 / R * 8 + 2 * (lane % 4) + par;
-        if (tok < 0 || tok >= p.tokens) continue;
-        const int r = row_of(p, tok);
-        float x[4] = {0, 0, 0, 0};
-        if (r >= 0) {
-          const uint8_t* u = unit_at<D>(p, r, sh.head);
-          const int j = r % kv4::kUnit, w = j / 8 * R + grp;
-          const uint32_t c = *reinterpret_cast<const uint16_t*>(u + 8 * D + 512 * (w / 4) + 16 * (4 * g + j % 8 / 2) +
-                                                                4 * (w % 4) + 2 * (j % 2));
-          const float s = scale_in(u + scale_at<D>(j, true, grp));
-#pragma unroll
-          for (int i2 = 0; i2 < 4; ++i2) x[i2] = s * (float)((int)(c >> (4 * i2) & 15) - 8);
-        }
-        put<4, F32>(p.v_out, (tok * p.h_kv + sh.head) * D + grp * 32 + 4 * g, x);
+      for (int i = 0; i < NG; ++i) word[h][i] = sc[h][i / 2] = 0;   // (a scale of zero: zeros)
+      if (r < 0) continue;
+      const uint8_t* u = unit_at<D>(p, r, sh.head);
+      const int j = r % kv4::kUnit;
+      const uint8_t* at = u + 512 * ((j / 8 * R + g0) / 4) + 16 * ((j % 8) * 4 + t) + (j / 8 * R + g0) % 4 * 4;
+      if constexpr (NG == 4) {
+        const uint4 w = *reinterpret_cast<const uint4*>(at);
+        word[h][0] = w.x, word[h][1] = w.y, word[h][2] = w.z, word[h][3] = w.w;
+        const uint2 s = *reinterpret_cast<const uint2*>(u + scale_at<D>(j, false, g0));
+        sc[h][0] = s.x, sc[h][1] = s.y;
+      } else {
+        const uint2 w = *reinterpret_cast<const uint2*>(at);
+        word[h][0] = w.x, word[h][1] = w.y;
+        sc[h][0] = *reinterpret_cast<const uint32_t*>(u + scale_at<D>(j, false, 0));
       }
     }
+#pragma unroll
+    for (int h = 0; h < NH; ++h) {
+      const long long tok = sh.first + j0 + 8 * h;
+      if (tok < 0 || tok >= p.tokens) continue;
+#pragma unroll
+      for (int i = 0; i < NG; ++i) {
+        const uint32_t c = __funnelshift_r(word[h][i], word[h][i], 3), s = sc[h][i / 2] >> (16 * (i % 2)) & 0xffffu;
+        uint32_t x[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[k] = there[h] ? less8(c >> (4 * k)) : 0;
+        put<4, F32>(p.k_out, (tok * p.h_kv + sh.head) * D + (g0 + i) * 32 + 8 * t, x, s);
+      }
+    }
+  } else {
+    const int g = lane / 4, j0 = 4 * sh.vec / R * 8 + 2 * (lane % 4);
+    int row[NH][2];
+#pragma unroll
+    for (int h = 0; h < NH; ++h)
+#pragma unroll
+      for (int par = 0; par < 2; ++par) row[h][par] = row_of(p, sh.first + j0 + 8 * h + par);
+    uint32_t half[4][2], sc[NH][2][NG / 2];
+    int start;
+    const bool run = one_unit(row, j0, start);
+    if (run) {
+      const uint4 w = *reinterpret_cast<const uint4*>(unit_at<D>(p, start, sh.head) + 8 * D + 512 * sh.vec + 16 * lane);
+      const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) half[i][0] = x[i] & 0xffffu, half[i][1] = x[i] >> 16;
+    }
+#pragma unroll
+    for (int h = 0; h < NH; ++h)
+#pragma unroll
+      for (int par = 0; par < 2; ++par) {
+        const int r = row[h][par], j = r % kv4::kUnit;
+#pragma unroll
+        for (int i = 0; i < NG / 2; ++i) sc[h][par][i] = 0;
+        if (r < 0) continue;
+        const uint8_t* u = unit_at<D>(p, r, sh.head);
+        if (!run) {
+          const uint16_t* at = reinterpret_cast<const uint16_t*>(u + 8 * D + 16 * (4 * g + j % 8 / 2) + 2 * (j % 2));
+#pragma unroll
+          for (int i = 0; i < NG; ++i) {
+            const int w = j / 8 * R + (R == 2 ? i : g0 + i);
+            half[NH == 2 ? 2 * h + i : i][par] = at[256 * (w / 4) + 2 * (w % 4)];
+          }
+        }
+        if constexpr (NG == 4) {
+          const uint2 s = *reinterpret_cast<const uint2*>(u + scale_at<D>(j, true, g0));
+          sc[h][par][0] = s.x, sc[h][par][1] = s.y;
+        } else {
+          sc[h][par][0] = *reinterpret_cast<const uint32_t*>(u + scale_at<D>(j, true, 0));
+        }
+      }
+#pragma unroll
+    for (int h = 0; h < NH; ++h)
+#pragma unroll
+      for (int par = 0; par < 2; ++par) {
+        const long long tok = sh.first + j0 + 8 * h + par;
+        if (tok < 0 || tok >= p.tokens) continue;
+        const bool there = row[h][par] >= 0;
+#pragma unroll
+        for (int i = 0; i < NG; ++i) {
+          const uint32_t c = half[NH == 2 ? 2 * h + i : i][par], s = sc[h][par][i / 2] >> (16 * (i % 2)) & 0xffffu;
+          const uint32_t d = c >> 8;           // channels 0, 1 and 2, 3: the second nibble to bit 16
+          const uint32_t x[2] = {there ? less8(c | c << 12) : 0, there ? less8(d | d << 12) : 0};
+          put<2, F32>(p.v_out, (tok * p.h_kv + sh.head) * D + (g0 + i) * 32 + 4 * g, x, s);
+        }
+      }
   }
 }
 
@@ -309,7 +381,7 @@ cudaError_t launch_d(const Kv4RowsArgs& p, bool load, cudaStream_t stream) {
   const long long blocks16 = (p.tokens + kv4::kUnit - 1) / kv4::kUnit + (p.slot && p.tokens > kv4::kUnit ? 1 : 0);
   const long long items = blocks16 * p.h_kv * kinds * (D / 64);
   const long long grid = (items + kKv4Warps - 1) / kKv4Warps;
-  if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
+  if (grid > 0x7fffffffLL || items > 0xffffffffLL) return cudaErrorInvalidValue;
   cudaLaunchAttribute overlap;
   overlap.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   overlap.val.programmaticStreamSerializationAllowed = 1;
@@ -319,8 +391,8 @@ cudaError_t launch_d(const Kv4RowsArgs& p, bool load, cudaStream_t stream) {
   cfg.stream = stream;
   cfg.attrs = &overlap;
   cfg.numAttrs = 1;
-  if (!load) return cudaLaunchKernelEx(&cfg, kv4_store_kernel<D>, p, items);
-  return cudaLaunchKernelEx(&cfg, p.out_f32 ? kv4_load_kernel<D, true> : kv4_load_kernel<D, false>, p, items);
+  if (!load) return cudaLaunchKernelEx(&cfg, kv4_store_kernel<D>, p, (unsigned)items);
+  return cudaLaunchKernelEx(&cfg, p.out_f32 ? kv4_load_kernel<D, true> : kv4_load_kernel<D, false>, p, (unsigned)items);
 }
 
 cudaError_t launch_rows(const Kv4RowsArgs& p, bool load, cudaStream_t stream) {

@@ -26,19 +26,39 @@ __host__ __device__ constexpr int unit_bytes(int d) { return 18 * d; }
 // product of a scale with a softmax weight, comes near fp32's smallest numbers.
 constexpr float kTiny = 8.077935669463161e-28f;   // 2^-90
 
-// Scale of a group with the given extremes: -m / 8, m of largest magnitude, the positive
-// one of two alike; exact in bf16, as m is.
-__device__ __forceinline__ float group_scale(float hi, float lo, bool finite) {
-  const float m = hi >= -lo ? hi : lo;
-  if (!finite) return __uint_as_float(0x7fc00000u);
-  return fabsf(m) < kTiny ? 0.0f : m * -0.125f;
+// Extremes of numbers as bf16 pairs, both as their bits: the largest magnitude in the low
+// half, the largest number (0 where none is positive) in the high half.  Bits of magnitudes
+// are in the numbers' order, an infinity and NaN above all.
+__device__ __forceinline__ uint32_t extremes(uint32_t mags, uint32_t tops) {
+  const uint32_t m = max(mags & 0xffffu, mags >> 16), t = max(tops & 0xffffu, tops >> 16);
+  return m | t << 16;
 }
 
-// Code 0 .. 15 of x.  x / s is 8 significant bits over 8, at least 2^-17 of itself away
-// from a half-integer that it does not equal, so the division's rounding moves no code.
-__device__ __forceinline__ uint32_t code_of(float x, float s) {
-  if (!(fabsf(s) > 0.0f)) return 8;   // zeros, and NaN scales
-  return (uint32_t)(__float2int_rn(fminf(fmaxf(__fdiv_rn(x, s), -8.0f), 7.0f)) + 8);
+// Scale of a group with these extremes: -m / 8, m of largest magnitude, the positive one of
+// two alike; exact in bf16, as m is.
+__device__ __forceinline__ float group_scale(uint32_t extremes) {
+  const uint32_t mag = extremes & 0xffffu;
+  if (mag >= 0x7f80u) return __uint_as_float(0x7fc00000u);
+  const float m = __uint_as_float(mag << 16);
+  return m < kTiny ? 0.0f : extremes >> 16 == mag ? m * -0.125f : m * 0.125f;
+}
+
+// Code of x plus kCodeBase, modulo 2^32, with r = 1 / s (a few steps off at most).  The
+// quotient x r is corrected by its remainder, which leaves it exact wherever x / s can be
+// told in 24 bits, so also where it is half-way between two codes; elsewhere x / s, 8
+// significant bits over 8, is at least 2^-17 of itself away from half-way.  No quotient is
+// below -8, and adding 1.5 2^23 rounds to a whole number, ties to even.
+constexpr uint32_t kCodeBase = 0x4b400000u;
+__device__ __forceinline__ uint32_t code_bits(float x, float s, float r) {
+  const float q = x * r;
+  return __float_as_uint(fminf(fmaf(fmaf(-q, s, x), r, q), 7.0f) + (12582912.0f + 8.0f));
+}
+
+// 1 / s for code_bits; of a group without a scale (zeros) one that makes every code 8.
+__device__ __forceinline__ float inverse(float s) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+  return s == 0.0f ? 0.0f : r;
 }
 
 }  // namespace kv4

@@ -182,7 +182,7 @@ struct Kv4RowsArgs {
   void *k_out, *v_out;
   int32_t* status;
   long long tokens, cache_rows;
-  int h_kv, d, page;
+  int h_kv, d, page_log;   // page: 2^page_log rows
   bool out_f32;
 };
 cudaError_t launch_kv4_store(const Kv4RowsArgs& p, cudaStream_t stream);
