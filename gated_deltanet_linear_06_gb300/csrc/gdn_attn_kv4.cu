@@ -362,8 +362,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) attn_kv4_kernel(Kv4
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           raw[r] = row < p.pl.R ? *reinterpret_cast<const uint4*>(from + 32 * r) : make_uint4(0, 0, 0, 0);
-          most2 = __vmaxu2(__vmaxu2(most2, raw[r].x & 0x7fff7fffu), raw[r].y & 0x7fff7fffu);
-          most2 = __vmaxu2(__vmaxu2(most2, raw[r].z & 0x7fff7fffu), raw[r].w & 0x7fff7fffu);
+          most2 = max_u16x2(max_u16x2(most2, raw[r].x & 0x7fff7fffu), raw[r].y & 0x7fff7fffu);
+          most2 = max_u16x2(max_u16x2(most2, raw[r].z & 0x7fff7fffu), raw[r].w & 0x7fff7fffu);
         }
         most2 = max(most2 & 0xffffu, most2 >> 16);     // (an infinity or a NaN: 0x7f80 or above)
         most2 = max(most2, __shfl_xor_sync(0xffffffffu, most2, 1));

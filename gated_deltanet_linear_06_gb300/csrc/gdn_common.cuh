@@ -36,6 +36,18 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return r;
 }
 
+// Larger ones of two pairs of 16-bit numbers, without and with sign.
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t max_s16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.s16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 // a and b rounded to bf16 (returned as fp32), with one packed conversion.
 __device__ __forceinline__ void round_bf16x2(float a, float b, float& ra, float& rb) {
   const uint32_t r = pack_bf16x2(a, b);

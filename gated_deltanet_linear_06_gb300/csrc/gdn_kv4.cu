@@ -28,12 +28,12 @@ struct Share {
 };
 
 template <int D>
-__device__ __forceinline__ bool share_of(const Kv4RowsArgs& p, unsigned item, Share& s) {
-  constexpr int NV = D / 64;
+__device__ __forceinline__ bool share_of(const Kv4RowsArgs& p, unsigned item, int vectors, Share& s) {
+  const int NV = D / 64 / vectors;
   const unsigned kinds = (p.k != nullptr) + (p.v != nullptr);
   const unsigned per = p.h_kv * kinds * NV, block = item / per;
   unsigned rest = item - block * per;
-  s.vec = rest % NV;
+  s.vec = rest % NV * vectors;
   rest /= NV;
   s.is_v = p.k == nullptr || rest % kinds == 1;
   s.head = rest / kinds;
@@ -68,44 +68,33 @@ __device__ __forceinline__ float scale_of(const uint32_t (&w)[N]) {
   uint32_t mags = 0, tops = 0;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    mags = __vmaxu2(mags, w[i] & 0x7fff7fffu);
-    tops = __vmaxs2(tops, w[i]);             // (negative numbers' bits are below 0)
+    mags = max_u16x2(mags, w[i] & 0x7fff7fffu);
+    tops = max_s16x2(tops, w[i]);             // (negative numbers' bits are below 0)
   }
   uint32_t ex = kv4::extremes(mags, tops);
 #pragma unroll
-  for (int m = FROM; m <= TO; m <<= 1) ex = __vmaxu2(ex, __shfl_xor_sync(0xffffffffu, ex, m));
+  for (int m = FROM; m <= TO; m <<= 1) ex = max_u16x2(ex, __shfl_xor_sync(0xffffffffu, ex, m));
   return kv4::group_scale(ex);
 }
 
 __device__ __forceinline__ float lo_f32(uint32_t x) { return __uint_as_float(x << 16); }
 __device__ __forceinline__ float hi_f32(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
 
-// Codes of a group's eight channels (of lane t of four) as K's word, and the group's scale.
-__device__ __forceinline__ uint32_t k_word(uint4 raw, float& s) {
+// Codes of a group's eight channels (of lane t of four), and the group's scale: as K's word,
+// or in their order, the first four and the last four a half of V's words each.
+template <bool V>
+__device__ __forceinline__ uint32_t codes_of(uint4 raw, float& s) {
   const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
   s = scale_of<4, 1, 2>(w);
   const float r = kv4::inverse(s);
-  uint32_t c = 0;                              // nibble 7 first: channels 7, 5, 3, 1, 6, 4, 2, 0
+  uint32_t c = 0;                              // the highest nibble first; K: channels 7 5 3 1 6 4 2 0
 #pragma unroll
-  for (int i = 3; i >= 0; --i) c = c * 16 + kv4::code_bits(hi_f32(w[i]), s, r);
-#pragma unroll
-  for (int i = 3; i >= 0; --i) c = c * 16 + kv4::code_bits(lo_f32(w[i]), s, r);
-  c -= kv4::kCodeBase * 0x11111111u;
-  return s == s ? __funnelshift_l(c, c, 3) : 0x44444444u;   // of a NaN scale 8s, as of zeros
-}
-
-// Codes of a group's four channels (of lane group g of eight) as half a word of V.
-__device__ __forceinline__ uint32_t v_half(uint2 raw, float& s) {
-  const uint32_t w[2] = {raw.x, raw.y};
-  s = scale_of<2, 4, 16>(w);
-  const float r = kv4::inverse(s);
-  uint32_t c = 0;
-#pragma unroll
-  for (int i = 1; i >= 0; --i) {
-    c = c * 16 + kv4::code_bits(hi_f32(w[i]), s, r);
-    c = c * 16 + kv4::code_bits(lo_f32(w[i]), s, r);
+  for (int k = 7; k >= 0; --k) {
+    const int o = V ? k : k < 4 ? 2 * k : 2 * k - 7;
+    c = c * 16 + kv4::code_bits(o % 2 ? hi_f32(w[o / 2]) : lo_f32(w[o / 2]), s, r);
   }
-  return s == s ? c - kv4::kCodeBase * 0x1111u : 0x8888u;
+  c = s == s ? c - kv4::kCodeBase * 0x11111111u : 0x88888888u;   // of a NaN scale 8s, as of zeros
+  return V ? c : __funnelshift_l(c, c, 3);
 }
 
 // Two scales as bf16, which they are exactly (a NaN keeps its bits).
@@ -132,103 +121,94 @@ __device__ __forceinline__ bool one_unit(const int (&row)[NH][2], int j0, int& s
   return __all_sync(0xffffffffu, run) && start % kv4::kUnit == 0;
 }
 
+// Words 4 vec .. 4 vec + 3 of 16 tokens' K or V, a warp: lane 4 j + t reads channels 8 t ..
+// 8 t + 7 of token j (and, at d = 64, of token j + 8) in four groups.  That is K's vector as it
+// stands; V's wants two tokens' four channels, which two lanes hand over.
+template <int D, bool V>
+__device__ __forceinline__ void store_vector(const uint16_t* const (&src)[D == 64 ? 2 : 1], uint8_t* const (&unit)[D == 64 ? 2 : 1],
+                                             const int (&row)[D == 64 ? 2 : 1], uint8_t* run, int vec) {
+  constexpr int R = D / 32, NH = R == 2 ? 2 : 1, NG = 4 / NH;
+  const int lane = threadIdx.x % 32, t = lane % 4, g0 = 4 * vec % R;
+  uint4 raw[4];
+#pragma unroll
+  for (int h = 0; h < NH; ++h)
+#pragma unroll
+    for (int i = 0; i < NG; ++i) {
+      raw[h * NG + i] = make_uint4(0, 0, 0, 0);
+      if (src[h]) raw[h * NG + i] = *reinterpret_cast<const uint4*>(src[h] + (g0 + i) * 32);
+    }
+  uint32_t c[4];
+  float s[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c[i] = codes_of<V>(raw[i], s[i]);
+  if (V && run) {
+    const int g = lane / 4, from = 8 * t + g / 2;   // token 2 t's lane with channels 4 g .. 4 g + 3
+    const uint32_t pick = g % 2 ? 0x7632 : 0x5410;
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w[i] = __byte_perm(__shfl_sync(0xffffffffu, c[i], from), __shfl_sync(0xffffffffu, c[i], from + 4), pick);
+    *reinterpret_cast<uint4*>(run + 8 * D + 512 * vec + 16 * lane) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+#pragma unroll
+  for (int h = 0; h < NH; ++h) {
+    if (!unit[h]) continue;
+    const int j = row[h] % kv4::kUnit, w0 = j / 8 * R + g0;
+    if constexpr (!V) {
+      uint8_t* at = unit[h] + 512 * (w0 / 4) + 16 * (j % 8 * 4 + t) + w0 % 4 * 4;
+      if constexpr (NG == 4) *reinterpret_cast<uint4*>(at) = make_uint4(c[0], c[1], c[2], c[3]);
+      else *reinterpret_cast<uint2*>(at) = make_uint2(c[2 * h], c[2 * h + 1]);
+    } else if (!run) {
+      // halves j % 2 of lanes 4 g + j % 8 / 2, g = 2 t and 2 t + 1
+#pragma unroll
+      for (int i = 0; i < NG; ++i) {
+        const int w = w0 + i;
+        uint8_t* at = unit[h] + 8 * D + 512 * (w / 4) + 16 * (8 * t + j % 8 / 2) + w % 4 * 4 + j % 2 * 2;
+        *reinterpret_cast<uint16_t*>(at) = (uint16_t)c[h * NG + i];
+        *reinterpret_cast<uint16_t*>(at + 64) = (uint16_t)(c[h * NG + i] >> 16);
+      }
+    }
+    if (t == 0) {
+      uint8_t* at = unit[h] + scale_at<D>(j, V, g0);
+      if constexpr (NG == 4) *reinterpret_cast<uint2*>(at) = make_uint2(scales2(s[0], s[1]), scales2(s[2], s[3]));
+      else *reinterpret_cast<uint32_t*>(at) = scales2(s[2 * h], s[2 * h + 1]);
+    }
+  }
+}
+
+// A warp takes `vectors` vectors of its 16 tokens, all of a half's rows where there is work for
+// every warp of the GPU even so.
 template <int D>
-__global__ void __launch_bounds__(kKv4Warps * 32) kv4_store_kernel(Kv4RowsArgs p, unsigned items) {
-  constexpr int R = D / 32, NH = R == 2 ? 2 : 1;
+__global__ void __launch_bounds__(kKv4Warps * 32) kv4_store_kernel(Kv4RowsArgs p, unsigned items, int vectors) {
+  constexpr int NH = D == 64 ? 2 : 1, PER_HALF = D / 128 > 0 ? D / 128 : 1;   // vectors of eight tokens
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x % 32;
   const unsigned item = blockIdx.x * kKv4Warps + threadIdx.x / 32;
   Share sh;
-  if (item >= items || !share_of<D>(p, item, sh)) return;
-  const int g0 = 4 * sh.vec % R;               // the vector's first group
-  if (!sh.is_v) {
-    // word 4 vec + i: of the token at w / R * 8 + lane / 4, group w % R
-    const int t = lane % 4, j0 = 4 * sh.vec / R * 8 + lane / 4;
-    const uint16_t* src = p.k + sh.head * p.k_sh + 8 * t;
-    uint4 raw[4];
-    int row[NH];
+  if (item >= items || !share_of<D>(p, item, vectors, sh)) return;
+  const int j0 = D == 64 ? lane / 4 : sh.vec / PER_HALF * 8 + lane / 4;
+  const uint16_t* const from = (sh.is_v ? p.v + sh.head * p.v_sh : p.k + sh.head * p.k_sh) + lane % 4 * 8;
+  const long long stride = sh.is_v ? p.v_st : p.k_st;
+  const uint16_t* src[NH];
+  uint8_t* unit[NH];
+  int row[NH];
+  bool ordered = true;
 #pragma unroll
-    for (int h = 0; h < NH; ++h) row[h] = row_of(p, sh.first + j0 + 8 * h);
+  for (int h = 0; h < NH; ++h) {
+    const long long tok = sh.first + j0 + 8 * h;
+    row[h] = row_of(p, tok);
+    src[h] = tok >= 0 && tok < p.tokens ? from + tok * stride : nullptr;
+    unit[h] = row[h] >= 0 ? unit_at<D>(p, row[h], sh.head) : nullptr;
+  }
+  // V's tokens one unit (half of one, above d = 64), each where its place in the list says?
+  const int start = __shfl_sync(0xffffffffu, row[0] - j0, 0);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int h = R == 2 ? i / 2 : 0;
-      const long long tok = sh.first + j0 + 8 * h;
-      raw[i] = make_uint4(0, 0, 0, 0);
-      if (tok >= 0 && tok < p.tokens) raw[i] = *reinterpret_cast<const uint4*>(src + tok * p.k_st + (R == 2 ? i % 2 : g0 + i) * 32);
-    }
-    uint32_t word[4];
-    float s[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) word[i] = k_word(raw[i], s[i]);
-#pragma unroll
-    for (int h = 0; h < NH; ++h) {
-      if (row[h] < 0) continue;
-      uint8_t* u = unit_at<D>(p, row[h], sh.head);
-      const int j = row[h] % kv4::kUnit;
-      if constexpr (R >= 4) {
-        *reinterpret_cast<uint4*>(u + 512 * ((j / 8 * R + g0) / 4) + 16 * ((j % 8) * 4 + t)) =
-            make_uint4(word[0], word[1], word[2], word[3]);
-        if (t == 0) *reinterpret_cast<uint2*>(u + scale_at<D>(j, false, g0)) = make_uint2(scales2(s[0], s[1]), scales2(s[2], s[3]));
-      } else {
-        *reinterpret_cast<uint2*>(u + 16 * ((j % 8) * 4 + t) + j / 8 * 8) = make_uint2(word[2 * h], word[2 * h + 1]);
-        if (t == 0) *reinterpret_cast<uint32_t*>(u + scale_at<D>(j, false, 0)) = scales2(s[2 * h], s[2 * h + 1]);
-      }
-    }
-  } else {
-    const int g = lane / 4, j0 = 4 * sh.vec / R * 8 + 2 * (lane % 4);
-    const uint16_t* src = p.v + sh.head * p.v_sh + 4 * g;
-    int row[NH][2];
-#pragma unroll
-    for (int h = 0; h < NH; ++h)
-#pragma unroll
-      for (int par = 0; par < 2; ++par) row[h][par] = row_of(p, sh.first + j0 + 8 * h + par);
-    uint2 raw[4][2];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int par = 0; par < 2; ++par) {
-        const long long tok = sh.first + j0 + (R == 2 ? i / 2 * 8 : 0) + par;
-        raw[i][par] = make_uint2(0, 0);
-        if (tok >= 0 && tok < p.tokens)
-          raw[i][par] = *reinterpret_cast<const uint2*>(src + tok * p.v_st + (R == 2 ? i % 2 : g0 + i) * 32);
-      }
-    uint32_t half[4][2];
-    float s[4][2];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int par = 0; par < 2; ++par) half[i][par] = v_half(raw[i][par], s[i][par]);
-    int start;
-    const bool run = one_unit(row, j0, start);
-    if (run)
-      *reinterpret_cast<uint4*>(unit_at<D>(p, start, sh.head) + 8 * D + 512 * sh.vec + 16 * lane) =
-          make_uint4(half[0][0] | half[0][1] << 16, half[1][0] | half[1][1] << 16, half[2][0] | half[2][1] << 16,
-                     half[3][0] | half[3][1] << 16);
-    if (run && g != 0) return;
-#pragma unroll
-    for (int h = 0; h < NH; ++h)
-#pragma unroll
-      for (int par = 0; par < 2; ++par) {
-        const int r = row[h][par], j = r % kv4::kUnit;
-        if (r < 0) continue;
-        uint8_t* u = unit_at<D>(p, r, sh.head);
-        if (!run) {
-          // word j / 8 * R + group of lane 4 g + j % 8 / 2, half j % 2
-          uint16_t* at = reinterpret_cast<uint16_t*>(u + 8 * D + 16 * (4 * g + j % 8 / 2) + 2 * (j % 2));
-#pragma unroll
-          for (int i = 0; i < 4 / NH; ++i) {
-            const int w = j / 8 * R + (R == 2 ? i : g0 + i);
-            at[256 * (w / 4) + 2 * (w % 4)] = (uint16_t)half[NH == 2 ? 2 * h + i : i][par];
-          }
-        }
-        if (g == 0) {
-          if constexpr (R >= 4)
-            *reinterpret_cast<uint2*>(u + scale_at<D>(j, true, g0)) =
-                make_uint2(scales2(s[0][par], s[1][par]), scales2(s[2][par], s[3][par]));
-          else
-            *reinterpret_cast<uint32_t*>(u + scale_at<D>(j, true, 0)) = scales2(s[2 * h][par], s[2 * h + 1][par]);
-        }
-      }
+  for (int h = 0; h < NH; ++h) ordered = ordered && row[h] >= 0 && row[h] - (j0 + 8 * h) == start;
+  uint8_t* run = nullptr;
+  if (__all_sync(0xffffffffu, ordered) && start % kv4::kUnit == 0) run = unit[0];   // (every lane's the same)
+  for (int v = sh.vec; v < sh.vec + vectors; ++v) {
+    if (sh.is_v) store_vector<D, true>(src, unit, row, run, v);
+    else store_vector<D, false>(src, unit, row, nullptr, v);
   }
 }
 
@@ -276,7 +256,7 @@ __global__ void __launch_bounds__(kKv4Warps * 32) kv4_load_kernel(Kv4RowsArgs p,
   const int lane = threadIdx.x % 32;
   const unsigned item = blockIdx.x * kKv4Warps + threadIdx.x / 32;
   Share sh;
-  if (item >= items || !share_of<D>(p, item, sh)) return;
+  if (item >= items || !share_of<D>(p, item, 1, sh)) return;
   const int g0 = 4 * sh.vec % R;
   if (!sh.is_v) {
     const int t = lane % 4, j0 = 4 * sh.vec / R * 8 + lane / 4;
@@ -375,11 +355,14 @@ __global__ void __launch_bounds__(kKv4Warps * 32) kv4_load_kernel(Kv4RowsArgs p,
 }
 
 template <int D>
-cudaError_t launch_d(const Kv4RowsArgs& p, bool load, cudaStream_t stream) {
+cudaError_t launch_d(const Kv4RowsArgs& p, bool load, cudaStream_t stream, int sms) {
   const int kinds = (p.k != nullptr) + (p.v != nullptr);
   // one sixteen more than the tokens fill: the first may be part of one
   const long long blocks16 = (p.tokens + kv4::kUnit - 1) / kv4::kUnit + (p.slot && p.tokens > kv4::kUnit ? 1 : 0);
-  const long long items = blocks16 * p.h_kv * kinds * (D / 64);
+  long long items = blocks16 * p.h_kv * kinds * (D / 64);
+  // d = 256 has two vectors to eight tokens' rows: a warp takes both once each SM has 32 warps
+  const int vectors = !load && D == 256 && items >= 64LL * sms ? 2 : 1;
+  items /= vectors;
   const long long grid = (items + kKv4Warps - 1) / kKv4Warps;
   if (grid > 0x7fffffffLL || items > 0xffffffffLL) return cudaErrorInvalidValue;
   cudaLaunchAttribute overlap;
@@ -391,15 +374,19 @@ cudaError_t launch_d(const Kv4RowsArgs& p, bool load, cudaStream_t stream) {
   cfg.stream = stream;
   cfg.attrs = &overlap;
   cfg.numAttrs = 1;
-  if (!load) return cudaLaunchKernelEx(&cfg, kv4_store_kernel<D>, p, (unsigned)items);
+  if (!load) return cudaLaunchKernelEx(&cfg, kv4_store_kernel<D>, p, (unsigned)items, vectors);
   return cudaLaunchKernelEx(&cfg, p.out_f32 ? kv4_load_kernel<D, true> : kv4_load_kernel<D, false>, p, (unsigned)items);
 }
 
 cudaError_t launch_rows(const Kv4RowsArgs& p, bool load, cudaStream_t stream) {
+  int dev = 0, sms = 0;
+  cudaError_t e;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+  if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
   switch (p.d) {
-    case 64: return launch_d<64>(p, load, stream);
-    case 128: return launch_d<128>(p, load, stream);
-    case 256: return launch_d<256>(p, load, stream);
+    case 64: return launch_d<64>(p, load, stream, sms);
+    case 128: return launch_d<128>(p, load, stream, sms);
+    case 256: return launch_d<256>(p, load, stream, sms);
   }
   return cudaErrorInvalidValue;
 }
