@@ -122,6 +122,8 @@ _P = ctypes.c_void_p
 def lib() -> ctypes.CDLL:
     """The loaded libgdn.so (raises if it was never built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):

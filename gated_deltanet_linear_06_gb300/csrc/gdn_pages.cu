@@ -13,6 +13,8 @@
 // Bytes then.  Whole pages move by a second kernel over the whole GPU, a warp 4 KB at a time
 // with eight 16-byte loads in flight per lane before the first store; it finds how many
 // there are in the workspace, and also changes the tables where there is much of them.
+#include <limits.h>
+
 #include "../../include/gdn.h"
 #include "gdn_common.cuh"
 #include "gdn_launch.h"
@@ -68,30 +70,34 @@ __device__ __forceinline__ void store_to(int* at, uint32_t rank, int v) {
 }
 
 template <typename T>
-__device__ __forceinline__ T block_scan(T v, T* warp_sums, T& total) {   // exclusive
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  T s = v;
+__device__ __forceinline__ T warp_scan(T v) {   // inclusive
 #pragma unroll
   for (int m = 1; m < 32; m <<= 1) {
-    const T o = __shfl_up_sync(0xffffffffu, s, m);
-    if (lane >= m) s += o;
+    const T o = __shfl_up_sync(0xffffffffu, v, m);
+    if (threadIdx.x % 32 >= m) v += o;
   }
+  return v;
+}
+
+// What the threads before this one have in all, and the CTA's total.
+template <typename T>
+__device__ __forceinline__ T block_scan(T v, T* warp_sums, T& total) {
+  static_assert(kPlanWarps == 32, "the warps' sums are one to a lane");
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const T s = warp_scan(v);
   __syncthreads();                          // the sums of a scan before may still be read
   if (lane == 31) warp_sums[warp] = s;
   __syncthreads();
-  T before = 0, all = 0;
-  for (int w = 0; w < kPlanWarps; ++w) {
-    before += w < warp ? warp_sums[w] : 0;
-    all += warp_sums[w];
-  }
-  total = all;
-  return before + s - v;
+  const T all = warp_scan(warp_sums[lane]);
+  total = __shfl_sync(0xffffffffu, all, 31);
+  const T before = __shfl_sync(0xffffffffu, all, warp == 0 ? 0 : warp - 1);
+  return (warp == 0 ? 0 : before) + s - v;
 }
 
 struct Shared {
   uint32_t seen[GDN_PAGES_MAX_SEQS / 32];
-  long long warp_sums[kPlanWarps];
-  int tile_sums[kPlanWarps];
+  long long need_sums[kPlanWarps];
+  int free_sums[kPlanWarps];
   int found[2][kCluster];
 };
 
@@ -105,29 +111,37 @@ __device__ __forceinline__ int4 counts(const PagePool& p, int i) {
   return c;
 }
 
-// The lowest `need` free pages into list[], by the whole cluster.  Returns false where
-// there are not as many.  Its last barrier makes the list visible to the cluster.
-__device__ bool find_free(const PagePool& p, long long need, int32_t* list, Shared& sh) {
+// Which of this thread's eight pages of a tile (65536 pages, over the cluster) are free.
+__device__ __forceinline__ uint32_t free_pages(const PagePool& p, int tile) {
+  const int at = tile + ((int)cluster_rank() * kPlanThreads + (int)threadIdx.x) * 2;
+  const int4 c = counts(p, at), d = counts(p, at + 1);
+  return (c.x <= 0) | (c.y <= 0) << 1 | (c.z <= 0) << 2 | (c.w <= 0) << 3 | (d.x <= 0) << 4 | (d.y <= 0) << 5 |
+         (d.z <= 0) << 6 | (d.w <= 0) << 7;
+}
+constexpr int kTileGroups = kCluster * kPlanThreads * 2;   // groups of four pages of a tile
+
+// The lowest `need` free pages into list[], by the whole cluster.  Of the first tile the
+// caller has this thread's pages in `mask`, the free ones in the threads before it in `before`
+// and the CTA's in `total`.  Returns false where there are not as many.  The last barrier
+// makes the list visible to the cluster.
+__device__ bool find_free(const PagePool& p, long long need, uint32_t mask, int before, int total, int32_t* list,
+                          Shared& sh) {
   const int rank = (int)cluster_rank();
   long long have = 0;
-  for (int tile = 0, turn = 0; have < need && (long long)tile * 4 < p.n_pages;
-       tile += kCluster * kPlanThreads * 2, turn ^= 1) {
-    const int at = tile + (rank * kPlanThreads + (int)threadIdx.x) * 2;
-    const int4 c = counts(p, at), d = counts(p, at + 1);
-    const uint32_t mask = (c.x <= 0) | (c.y <= 0) << 1 | (c.z <= 0) << 2 | (c.w <= 0) << 3 | (d.x <= 0) << 4 |
-                          (d.y <= 0) << 5 | (d.z <= 0) << 6 | (d.w <= 0) << 7;
-    int total;
-    int mine = block_scan(__popc(mask), sh.tile_sums, total);
+  for (int tile = 0, turn = 0; have < need && (long long)tile * 4 < p.n_pages; tile += kTileGroups, turn ^= 1) {
+    if (tile > 0) {
+      mask = free_pages(p, tile);
+      before = block_scan(__popc(mask), sh.free_sums, total);
+    }
     if (threadIdx.x < kCluster) store_to(&sh.found[turn][rank], threadIdx.x, total);
     cluster_sync();
-    long long before = have;
+    long long at = have + before;
     for (int r = 0; r < kCluster; ++r) {
-      before += r < rank ? sh.found[turn][r] : 0;
+      at += r < rank ? sh.found[turn][r] : 0;
       have += sh.found[turn][r];
     }
-    before += mine;
-    for (uint32_t m = mask; m != 0; m &= m - 1, ++before)
-      if (before < need) list[before] = 4 * at + __ffs(m) - 1;
+    const int first = 4 * (tile + (rank * kPlanThreads + (int)threadIdx.x) * 2);
+    for (uint32_t m = mask; m != 0 && at < need; m &= m - 1, ++at) list[at] = first + __ffs(m) - 1;
   }
   cluster_sync();
   return have >= need;
@@ -180,7 +194,9 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
   const int rank = (int)cluster_rank(), thread = rank * kPlanThreads + (int)threadIdx.x;
   for (int i = threadIdx.x; i < GDN_PAGES_MAX_SEQS / 32; i += kPlanThreads) sh.seen[i] = 0;
   __syncthreads();
-  // the list, by every CTA
+  // the list, by every CTA, and under its loads those of the pool's first tile (of a trim or a
+  // free, which hardly ever or never need a page, only where they do)
+  uint32_t mask = OP == kExtend || OP == kFork ? free_pages(p, 0) : 0;
   const int per = (a.n + kPlanThreads - 1) / kPlanThreads, i0 = threadIdx.x * per;
   long long mine = 0;
   bool good = true;
@@ -191,7 +207,9 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
     mine += need;
   }
   long long total;
-  long long at = block_scan(mine, sh.warp_sums, total);
+  long long at = block_scan(mine, sh.need_sums, total);
+  int here;
+  const int before = block_scan(__popc(mask), sh.free_sums, here);
   for (int i = i0; i < min(i0 + per, a.n); ++i) {
     const int need = off[i];
     off[i] = (int)at;
@@ -201,15 +219,23 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
   bool ok = __syncthreads_and(good) && total <= p.n_pages;
   cluster_wait();
   // (every CTA came to the same ok; the barrier in find_free is the one between looking and changing)
-  ok = find_free(p, ok ? total : 0, a.dest, sh) && ok;
+  if (!ok) total = 0;
+  if ((OP == kTrim || OP == kFree) && total > 0) {
+    mask = free_pages(p, 0);
+    const int mine_before = block_scan(__popc(mask), sh.free_sums, here);
+    ok = find_free(p, total, mask, mine_before, here, a.dest, sh);
+  } else {
+    ok = find_free(p, total, mask, before, here, a.dest, sh) && ok;
+  }
   if (!ok) {
     if (thread == 0) record_status(a.status, GDN_ERR_DEVICE_BOUNDS);
     if (thread == 0 && OP != kExtend && OP != kFree) a.head->moves = a.head->pairs = 0;
     if (OP == kExtend)
       for (long long x = thread; x < (long long)a.n * a.steps; x += kCluster * kPlanThreads) a.slot[x] = -1;
   } else if (OP == kExtend) {
-    for (long long x = thread; x < (long long)a.n * a.steps; x += kCluster * kPlanThreads) {
-      const int i = (int)(x / a.steps), st = (int)(x - (long long)i * a.steps);
+    const long long slots = (long long)a.n * a.steps;
+    for (long long x = thread; x < slots; x += kCluster * kPlanThreads) {
+      const int i = slots <= INT_MAX ? (int)x / a.steps : (int)(x / a.steps), st = (int)(x - (long long)i * a.steps);
       const int s = a.seq ? a.seq[i] : i, c = a.arg ? a.arg[i] : a.steps, len = len0[i];
       int32_t* row = p.table + (long long)s * p.width;
       if (st == 0) p.len[s] = len + c;
@@ -291,7 +317,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
   int n = 0;
   for (int i = lo + threadIdx.x; i < hi; i += kPlanThreads) n += __popc(used(i));
   int total;
-  block_scan(n, sh.tile_sums, total);
+  block_scan(n, sh.free_sums, total);
   cluster_wait();
   if (threadIdx.x < kCluster) store_to(&sh.found[0][rank], threadIdx.x, total);
   cluster_sync();
@@ -308,7 +334,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
     const uint32_t below = 4LL * i + 3 < live ? 15u : 4LL * i >= live ? 0u : (1u << (live - 4 * i)) - 1;
     n += __popc(~used(i) & below);
   }
-  block_scan(n, sh.tile_sums, total);
+  block_scan(n, sh.free_sums, total);
   if (threadIdx.x < kCluster) store_to(&sh.found[1][rank], threadIdx.x, total);
   cluster_sync();
   int holes = 0;
@@ -316,7 +342,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
   for (int tile = lo; tile < hi; tile += kPlanThreads) {
     const int i = tile + (int)threadIdx.x;
     const uint32_t u = i < hi ? used(i) : 0;
-    int in_use = before + block_scan(__popc(u), sh.tile_sums, total);
+    int in_use = before + block_scan(__popc(u), sh.free_sums, total);
     before += total;
     if (i < hi) {
 #pragma unroll
@@ -424,10 +450,10 @@ __device__ __forceinline__ void move_pages(const MoveParams& v) {
     uint4 r[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k)
-      if (at + k * 512 < bytes) r[k] = __ldcs(reinterpret_cast<const uint4*>(s + at + k * 512));
+      if (at + k * 512 < bytes) r[k] = *reinterpret_cast<const uint4*>(s + at + k * 512);
 #pragma unroll
     for (int k = 0; k < 8; ++k)
-      if (at + k * 512 < bytes) __stcs(reinterpret_cast<uint4*>(d + at + k * 512), r[k]);
+      if (at + k * 512 < bytes) *reinterpret_cast<uint4*>(d + at + k * 512) = r[k];
   }
 }
 
@@ -475,9 +501,11 @@ struct Launch {
 template <Op OP>
 cudaError_t launch_plan(const PoolParams& a, cudaStream_t stream) {
   const size_t smem = (2 * (size_t)a.n + 1) * sizeof(int);
-  const cudaError_t e =
-      cudaFuncSetAttribute(pages_plan_kernel<OP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (2 * GDN_PAGES_MAX_LIST + 1) * 4);
-  if (e != cudaSuccess) return e;
+  if (smem + sizeof(Shared) > 48 * 1024) {   // more than a kernel may have unasked
+    const cudaError_t e = cudaFuncSetAttribute(pages_plan_kernel<OP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (2 * GDN_PAGES_MAX_LIST + 1) * (int)sizeof(int));
+    if (e != cudaSuccess) return e;
+  }
   Launch l(kCluster, kPlanThreads, smem, stream);
   return cudaLaunchKernelEx(&l.cfg, pages_plan_kernel<OP>, a);
 }
@@ -493,8 +521,10 @@ cudaError_t launch_moves(const PoolParams& a, const MoveParams& v, long long mos
   int sms;
   const cudaError_t e = sm_count(sms);
   if (e != cudaSuccess) return e;
-  // enough warps for every piece there can be, up to all that fit on the GPU
-  const long long want = (most + kMoveWarps - 1) / kMoveWarps, fit = (long long)sms * 8;
+  // Enough warps for every piece there can be, up to sixteen times as many as fit on the GPU:
+  // 2000 pages of 12 caches of 36 KB took 242 us with twice as many, whose shares end far
+  // apart, and 226 so (9700 CTAs without anything to do cost 1 us).
+  const long long want = (most + kMoveWarps - 1) / kMoveWarps, fit = (long long)sms * 64;
   Launch l((unsigned)(want < 1 ? 1 : want < fit ? want : fit), kMoveWarps * 32, 0, stream);
   return cudaLaunchKernelEx(&l.cfg, pages_move_kernel<ROWS>, a, v);
 }
