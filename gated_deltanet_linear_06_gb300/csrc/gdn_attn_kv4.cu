@@ -20,8 +20,6 @@ constexpr int kWide = 3;
 constexpr int kLeastV = -93;                       // scales are zero or at least 2^-93
 constexpr int kTinyWeights = 60;                   // with a larger v, weights that count may be subnormal
 constexpr float kStored = 28.0f;                   // shares are stored with weights up to 2^(kTop - kStored)
-constexpr int kMinItems = 2;                       // units that a warp takes at least
-constexpr int kJobUnits = 4;                       // what a job costs besides its units
 constexpr int kMaxCtas = 160;                      // the workspace has room for
 constexpr int kMaxWarps = 16;
 
@@ -46,6 +44,10 @@ template <int D, int NT>
 struct Cfg {
   static constexpr int R = D / 32;
   static constexpr int UNITS = NT == 2 ? 256 / D : 512 / D < 4 ? 512 / D : 4;   // met at once: a stage
+  // What a job costs besides its units (its rows in and out), in stages, some 640 / D units: 96
+  // sequences of up to 2900 tokens of d = 64 took 40 us with 2 units, 34 with 4 and 28 with 8;
+  // 256 of up to 8000 of d = 256 took 126 with 8 and 122.5 with 2.
+  static constexpr int JOB = 640 / D > UNITS ? 640 / D / UNITS : 1;
   static constexpr bool QREG = NT * R <= 8;          // q's operands in registers, else in shared memory
   static constexpr bool BREG = NT * R <= 2;          // and the sums of their channels
   static constexpr int WARPS = D == 64 && NT == 1 ? 12 : 8;   // (registers for 8 or 12; 10 left one scheduler with more)
@@ -161,10 +163,11 @@ __device__ __forceinline__ int units_of(const AttnKv4Args& a, int b) {
   return n > 0 && n <= (long long)a.width * a.page ? (n + kv4::kUnit - 1) / kv4::kUnit : 0;
 }
 
-// What a job of n units costs, in units: kJobUnits for its rows in and out.
-__device__ __forceinline__ int cost_of(int n) { return n > 0 ? n + kJobUnits : 0; }
+// What a job of n units costs, in stages of `units`: `job` for its rows in and out.
+__device__ __forceinline__ int cost_of(int n, int units, int job) { return n > 0 ? (n + units - 1) / units + job : 0; }
 
 // before[0 .. batch]: costs of a job of each sequence before, in shared memory, by the whole CTA.
+template <int UNITS, int JOB>
 __device__ void sum_costs(const AttnKv4Args& a, long long* before, long long* warp_sums, bool report) {
   const int threads = blockDim.x, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int per = (a.batch + threads - 1) / threads, b0 = threadIdx.x * per;
@@ -173,7 +176,7 @@ __device__ void sum_costs(const AttnKv4Args& a, long long* before, long long* wa
     if (b0 + i < a.batch) {
       const int n = a.len[b0 + i];
       if (report && (n < 0 || n > (long long)a.width * a.page)) record_status(a.status, GDN_ERR_DEVICE_BOUNDS);
-      mine += cost_of(units_of(a, b0 + i));
+      mine += cost_of(units_of(a, b0 + i), UNITS, JOB);
     }
   long long sum = mine;
 #pragma unroll
@@ -188,33 +191,28 @@ __device__ void sum_costs(const AttnKv4Args& a, long long* before, long long* wa
   for (int i = 0; i < per; ++i)
     if (b0 + i < a.batch) {
       before[b0 + i] = at;
-      at += cost_of(units_of(a, b0 + i));
+      at += cost_of(units_of(a, b0 + i), UNITS, JOB);
       if (b0 + i == a.batch - 1) before[a.batch] = at;
     }
   __syncthreads();
 }
 
-// Warps that take part: one for every kMinItems items at most, so that none has nothing.
-__device__ __forceinline__ int workers_of(const Kv4Params& p, long long total) {
-  const long long n = (total + kMinItems - 1) / kMinItems;
-  return n < p.pl.workers ? (int)n : p.pl.workers;
-}
-
-// A warp's place among the items: a job's kJobUnits and then its units, job after job.
+// A warp's place among the items: what a job costs besides, then its stages, job after job.
 struct Item {
-  int b, job, u, n;          // sequence, job of it, unit (below 0: before the first), units of the sequence
+  int b, job, s, n;          // sequence, job of it, stage (below 0: before the first), stages
 };
 
 // The next job's start, given the items (from the end of this job on) that are left to the
-// warp; a job whose units begin past them is none.
+// warp; a job whose stages begin past them is none.
+template <int JOB>
 __device__ __forceinline__ void next_job(const Kv4Params& p, const long long* before, Item& it, long long& rest) {
-  it.u = 0;
-  rest -= kJobUnits;
+  it.s = 0;
+  rest -= JOB;
   if (++it.job < p.pl.jobs_per_seq) return;
   it.job = 0;
   do {
     ++it.b;
-    it.n = it.b < p.a.batch ? (int)(before[it.b + 1] - before[it.b]) - kJobUnits : 0;
+    it.n = it.b < p.a.batch ? (int)(before[it.b + 1] - before[it.b]) - JOB : 0;
   } while (it.n < 0 && it.b < p.a.batch);
 }
 
@@ -235,12 +233,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) attn_kv4_kernel(Kv4
   if (lane == 0)
     for (int i = 0; i < C::STAGES; ++i) tc::mbar_init(bar + i, 1);
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  sum_costs(a, before, warp_sums, blockIdx.x == 0);
+  sum_costs<C::UNITS, C::JOB>(a, before, warp_sums, blockIdx.x == 0);
 
   // This warp's items, and where the first one is.
   const long long total = before[a.batch] * p.pl.jobs_per_seq;
   const int worker = warp * gridDim.x + blockIdx.x;   // few workers: on many SMs
-  const int workers = workers_of(p, total);
+  const int workers = total < p.pl.workers ? (int)total : p.pl.workers;   // (none without an item)
   const long long x0 = worker < workers ? total * worker / workers : 0;
   const long long x1 = worker < workers ? total * (worker + 1) / workers : 0;
   bool ok = true;
@@ -255,17 +253,18 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) attn_kv4_kernel(Kv4
       use.b = lo;
       const int cost = (int)(before[lo + 1] - before[lo]);
       const long long at = x0 - before[lo] * p.pl.jobs_per_seq;
-      use.n = cost - kJobUnits;
+      use.n = cost - C::JOB;
       use.job = (int)(at / cost);
-      use.u = (int)(at - (long long)use.job * cost) - kJobUnits;
+      use.s = (int)(at - (long long)use.job * cost) - C::JOB;
     }
-    long long rest = x1 - x0;                // units not yet met
-    if (use.u < 0) {                         // the share begins before the job's first unit
-      rest += use.u;
-      use.u = 0;
+    long long rest = x1 - x0;                // stages not yet met
+    if (use.s < 0) {                         // the share begins before the job's first stage
+      rest += use.s;
+      use.s = 0;
     }
     Item ask = use;
-    long long to_ask = rest;                 // units not yet asked for
+    long long to_ask = rest;                 // stages not yet asked for
+    int ask_len = units_of(a, ask.b), ask_u = ask.s * C::UNITS;   // the sequence's units, the next one
     const int upp_log = 31 - __clz(a.page / kv4::kUnit), upp = 1 << upp_log;   // units of a page
     const long long page_bytes = (long long)a.h_kv * upp * C::UNIT;
     int entry = 0, entry_0 = INT_MIN;        // this lane's of 32 entries of the sequence's table
@@ -280,7 +279,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) attn_kv4_kernel(Kv4
     uint32_t parity = 0;
 
     const auto find_page = [&]() {
-      const int pg = ask.u >> upp_log, at = ask.u & (upp - 1);
+      const int pg = ask_u >> upp_log, at = ask_u & (upp - 1);
       if (pg < entry_0 || pg >= entry_0 + 32) {
         entry_0 = pg;
         entry = pg + lane < a.width ? a.table[(long long)ask.b * a.width + pg + lane] : -1;
@@ -288,14 +287,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) attn_kv4_kernel(Kv4
       const int page = __shfl_sync(0xffffffffu, entry, pg - entry_0);
       there = (unsigned)page < (unsigned)a.n_pages;
       if (!there && lane == 0) record_status(a.status, GDN_ERR_DEVICE_BOUNDS);
-      left = min(upp - at, ask.n - ask.u);
+      left = min(upp - at, ask_len - ask_u);
       src = head + page * page_bytes + at * C::UNIT;
     };
-    // One more stage: of one job's units as many as it holds, one copy for each page.
+    // One more stage, one copy for each page.
     const auto request = [&]() {
-      int units = min(C::UNITS, ask.n - ask.u);
-      if (units > to_ask) units = (int)to_ask;
-      to_ask -= units;
+      const int units = min(C::UNITS, ask_len - ask_u);
       bad &= ~(((1u << C::UNITS) - 1) << (put * C::UNITS));
       int done = 0;
 #pragma unroll 1
@@ -319,16 +316,21 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) attn_kv4_kernel(Kv4
         src += run * C::UNIT;
         left -= run;
         done += run;
-        ask.u += run;
+        ask_u += run;
         if (done == units) break;
       }
       if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(tc::smem_u32(bar + put)) : "memory");
       put = put + 1 == C::STAGES ? 0 : put + 1;
-      if (ask.u == ask.n) {
+      --to_ask;
+      if (++ask.s == ask.n) {
         const int b = ask.b;
-        next_job(p, before, ask, to_ask);
+        next_job<C::JOB>(p, before, ask, to_ask);
         head = head_of();
-        if (ask.b != b) entry_0 = INT_MIN;
+        ask_u = 0;
+        if (ask.b != b) {
+          entry_0 = INT_MIN;
+          if (to_ask > 0) ask_len = units_of(a, ask.b);
+        }
       }
     };
     for (int i = 0; i < C::STAGES && to_ask > 0; ++i) request();
@@ -339,8 +341,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) attn_kv4_kernel(Kv4
       const long long slot = (long long)job + worker;
       const int hk = use.job / p.pl.blocks, row0 = use.job % p.pl.blocks * (8 * NT);
       const int len = a.len[use.b];
-      const int end = use.n - use.u < rest ? use.n : use.u + (int)rest;
-      if (lane == 0 && use.u == 0) p.span[job].x = worker;
+      const int end = use.n - use.s < rest ? use.n : use.s + (int)rest;
+      if (lane == 0 && use.s == 0) p.span[job].x = worker;
       if (lane == 0 && end == use.n) p.span[job].y = worker;
 
       // q as the second operand: row g of a block of 8, a group's channels 8 t .. 8 t + 7, as
@@ -396,9 +398,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) attn_kv4_kernel(Kv4
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          last[n][i] = min(len - a.steps + min((row0 + 8 * n + 2 * t + i) / p.pl.G, a.steps - 1), end * kv4::kUnit - 1);
-      const int past = min(len, end * kv4::kUnit);   // tokens from here on are no row's, or another share's
-      const int all_see = min(len - a.steps, end * kv4::kUnit - 1);   // up to here every row's
+          last[n][i] = len - a.steps + min((row0 + 8 * n + 2 * t + i) / p.pl.G, a.steps - 1);
+      const int all_see = len - a.steps;     // tokens up to this one are every row's
       float o[NT][R][2][4], ref[NT][2], sum[NT][2];
       int v = kLeastV;                       // 2^v: above every scale of V at the last update
       uint32_t fresh = (1u << (2 * NT)) - 1;   // this lane's rows that have not seen a score
@@ -416,7 +417,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) attn_kv4_kernel(Kv4
       }
 
       // Where not every row sees all of a stage's tokens: in tokens of no row (past the
-      // sequence, of another share, of a page that is not there) V's scales become zeros,
+      // sequence, of a page that is not there) V's scales become zeros,
       // whatever the cache holds.  So do scales that are not finite, for a row that does not see
       // the token gives it a weight of zero, and its product with them would be NaN; groups of
       // rows that do see it are noted and become NaN at the end.
@@ -428,7 +429,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) attn_kv4_kernel(Kv4
           uint32_t w = *reinterpret_cast<const uint32_t*>(at), odd = 0;
           if ((w & 0x7f80u) == 0x7f80u) odd |= 1u, w &= 0xffff0000u;
           if ((w & 0x7f800000u) == 0x7f800000u) odd |= 2u, w &= 0xffffu;
-          if (token >= past || gone >> (i / 2) & 1) w = odd = 0;
+          if (token >= len || gone >> (i / 2) & 1) w = odd = 0;
           *reinterpret_cast<uint32_t*>(at) = w;
           for (uint32_t lanes = __ballot_sync(0xffffffffu, odd != 0); lanes != 0; lanes &= lanes - 1) {
             const int from = __ffs(lanes) - 1;
@@ -620,7 +621,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) attn_kv4_kernel(Kv4
       };
 
 #pragma unroll 1
-      for (int u = use.u; u < end; u += C::UNITS) {
+      for (int s = use.s; s < end; ++s) {
+        const int u = s * C::UNITS;
         if (!__all_sync(0xffffffffu, try_wait(bar + get, parity)))
           ok = __all_sync(0xffffffffu, tc::mbar_wait(bar + get, parity, kWaitClocks));
         if (!ok) break;
@@ -662,9 +664,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) attn_kv4_kernel(Kv4
                             o[n][r][1][i] * 0x1p24f * stored, o[n][r][1][2 + i] * 0x1p20f * stored);
         }
       if (!ok) break;
-      rest -= end - use.u;
-      use.u = end;
-      if (end == use.n) next_job(p, before, use, rest);
+      rest -= end - use.s;
+      use.s = end;
+      if (end == use.n) next_job<C::JOB>(p, before, use, rest);
     }
     if (!ok) {                               // a copy did not come: wait for the others, then leave
       if (lane == 0) record_status(a.status, GDN_ERR_DEVICE_TIMEOUT);
