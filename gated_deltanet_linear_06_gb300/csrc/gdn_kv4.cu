@@ -135,7 +135,7 @@ __device__ __forceinline__ void store_vector(const uint16_t* const (&src)[D == 6
 #pragma unroll
     for (int i = 0; i < NG; ++i) {
       raw[h * NG + i] = make_uint4(0, 0, 0, 0);
-      if (src[h]) raw[h * NG + i] = *reinterpret_cast<const uint4*>(src[h] + (g0 + i) * 32);
+      if (src[h]) raw[h * NG + i] = __ldcs(reinterpret_cast<const uint4*>(src[h] + (g0 + i) * 32));
     }
   uint32_t c[4];
   float s[4];
