@@ -17,7 +17,7 @@
 
 namespace {
 
-constexpr int kVersion = 400;  // 0.4.0: the attention layer's and the expert layer's operators
+constexpr int kVersion = 500;  // 0.5.0: the 4-bit cache and the pages' pool
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 

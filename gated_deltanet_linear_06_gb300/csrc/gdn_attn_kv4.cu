@@ -1,4 +1,54 @@
-// gdn_attn_kv4.cu -- attention of a batch of sequences over the 4-bit paged cache.
+// gdn_attn_kv4.cu -- attention of a batch of sequences over the 4-bit paged cache
+// (mma.sync tensor-core products that take the codes as they are stored).
+//
+// Mathematics.  A row r = (step, query head) of a sequence wants o = sum_j w_j v_j / sum_j w_j,
+// w_j = 2^(s_j - ref), s_j = scale log2(e) q.k_j, for any ref.  With k_jc = a_jg c_jc, codes c and a
+// scale a per token and group g of 32 channels,
+//   s_j = sum_g a_jg (sum_{c in g} c_jc q_c),   o_c = sum_j c_jc (w_j b_jg),
+// so the codes are multiplied as whole numbers, K's scales meet the products' sums in fp32
+// and V's meet the weights before their one rounding, to fp16.
+//
+// What bounds it.  4.5 bits a value: at the memory's rate an SM gets 46 values a clock, and
+// what it can do for each of them decides.  Taking a nibble out costs an instruction for two
+// values whatever one does; so everything else is kept from costing any:
+//   - the codes lie as the operands' fragments do, so a lane's words come by 16-byte loads and no
+//     lane hands anything to another;
+//   - four bits masked out of a word are an fp16 number already (see kAt0 below): no
+//     conversion, no offset to subtract, at most one shift for two masks;
+//   - the 8 by which the stored codes are too large is taken off by the tensor cores: for K as
+//     the value that the sum starts from, for V by a product with a constant (taking it off the
+//     values was eight instructions for every one of those);
+//   - rows (8 at a time: a group's query heads, or several steps' of them) are the products' N,
+//     tokens or channels their M, so few rows waste nothing.
+// tcgen05 takes its operands from shared memory, where each value would have to be written as
+// 16 bits first, four times what is read: more than the 128 bytes a clock there.  Scales per
+// (token, group) bar its 4-bit kinds, whose scales run along the other dimension for V.
+// (fp8 products would need half the masks, but mma.sync's are converted to fp16 here: 40 clocks
+// a product with fresh operands where fp16's takes 13.)
+//
+// Split.  A job is a (sequence, kv head, 8 or 16 rows).  All jobs' stages (64 tokens of d = 64 or
+// 128, 32 of 256) are laid end to end, with something for each job's fixed cost, and every warp
+// of a grid of one CTA an SM takes an equal share: one long sequence fills the GPU as well as
+// many short ones do.  Warps share nothing but the sums of the lengths at the start; each has
+// its own ring of two stages, filled by bulk copies (a page's units of a head are contiguous)
+// while the other is met.  A share ends where it ends; a second launch joins a job's shares.
+// Shares follow from the lengths alone, so equal calls add in equal order, and they are found
+// on the device, so a captured call stays valid while the lengths grow.
+//
+// Softmax.  ref moves only when a score passes it by kGrow binary orders or a scale of V by
+// kWide; else a stage costs a vote.  Weights times scales stay below 2^15, fp16's range, at any
+// scale of V (ref goes by it), and 30 binary orders below the largest are still in range.
+//
+// Measured, both launches, of the bytes that the cache holds for the tokens: 256 sequences of 100
+// to 8000 tokens (16 query heads, 2 kv heads, d = 256) 123 us, 4.9 TB/s; one of 131072 (32, 8,
+// 128) 42 us, 3.6 TB/s; 64 of 6001 (32, 8, 128) 94 us, 4.7 TB/s, in pages of 16 120 us; 96 of 1 to
+// 2900 (64, 8, 64) 27 us, 3.0 TB/s; 17 of 4 to 6001 with 4 steps (32, 8, 128, pages of 16) 34 us,
+// 1.8 TB/s; one of 833 9 us, latency (the lengths 0.8, first copy asked for 1.3, its rows and the
+// data 1, a stage 1.4, the share written 0.5, join 2).  Per unit of 16 tokens at d = 256: 264
+// clocks of an SM, for 535 instructions (272 of the integer pipe, which starts one every other
+// clock and scheduler: 136) and 48 products (96).  Masks, products and the fp32 arithmetic
+// between them contend for the same registers' ports: leaving out a sixth of any of them saved
+// a tenth at most.
 #include <limits.h>
 #include <math.h>
 

@@ -1,15 +1,20 @@
 // gdn_kv4.cu -- rows of k and v into the 4-bit cache (gdn_kv4_store) and back out of it
 // (gdn_kv4_load).
 //
-// Both are streams: a row is read once and written once, and what little arithmetic
-// there is (a group's extremes, 32 divisions) hides under them.  The work is cut the
-// way the cache's vectors lie: a warp takes 16 tokens of the list, one head, K or V and
-// one 16-byte vector per lane, so each lane makes (or takes apart) whole vectors: of K
-// four groups' eight channels of one token, whichever unit the token goes to; of V two
-// tokens' four channels of four groups, which are one vector only where the 16 tokens
-// are a unit.  Elsewhere (a decode step's rows, one of each sequence) V's pieces are two
-// bytes each.  When the list runs through units it need not begin with one: the tokens
-// are taken in sixteens that end where the first token's unit does.
+// Both are streams: a row is read once and written once.  The work is cut the way the cache's
+// vectors lie.  A warp of a store takes sixteen tokens of the list, one head, K or V and a
+// 16-byte vector per lane: four lanes read 32 channels of a token, find the group's scale
+// between them and make K's vector as it stands; V's vectors hold two tokens' channels and are
+// put together between lanes where the tokens are a unit's in order.  Elsewhere (a decode
+// step's rows, one of each sequence) V's pieces are two bytes each.  A list that runs through
+// units need not begin with one: the tokens are taken in sixteens that end where the first
+// token's unit does.
+//
+// A store is bound by its instructions, some 17 a value (of which 7 for the quotient, its
+// rounding and its place); without divisions and with extremes as packed 16-bit numbers they
+// are half of what they were.  Measured, 32768 rows of 2 heads of 256: store 24 us (3.6 TB/s of
+// 67 MB read and 19 MB written), load as bf16 15 us (5.8 TB/s).  256 rows of as many
+// sequences: 5 us each, latency.
 #include "../../include/gdn.h"
 #include "gdn_kv4.cuh"
 #include "gdn_launch.h"

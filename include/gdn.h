@@ -43,6 +43,7 @@
  *     a call's launches; the outputs and states are then undefined.
  *   - All device pointers must be 16-byte aligned.  Tensors are dense and
  *     row-major in the shapes given below.
+ *   - A workspace serves one call at a time: calls that may run at once need one each.
  *   - Some calls are several kernels, which may begin while the one before them in
  *     the same call still runs; work enqueued before the call is complete when its
  *     first kernel begins, and the call is when its last one ends.
@@ -704,8 +705,8 @@ gdn_status gdn_kv4_load(const gdn_attn_dims* dims, int page, long long n_pages, 
  * Each softmax weight times its token's scale is rounded to fp16 (at a power of two that
  * keeps it in range) before it meets the codes, which moves out by at most 2^-11 sum p |v|
  * besides its own rounding; everything else is fp32, with steps of the largest magnitude M
- * in a value's group where values cancel (2^-17 sum p M).  Magnitudes of k are to be below
- * 2^100.  Equal calls give equal bits; the order
+ * in a value's group where values cancel (2^-17 sum p M).  Magnitudes of q are to be below
+ * 2^108.  Equal calls give equal bits; the order
  * of a row's sums, and with it the last bits, depends on the batch, the lengths and the
  * GPU's SM count.
  */
