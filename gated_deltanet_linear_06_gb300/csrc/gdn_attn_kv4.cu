@@ -315,62 +315,44 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) attn_kv4_kernel(Kv4
     Item ask = use;
     long long to_ask = rest;                 // stages not yet asked for
     int ask_len = units_of(a, ask.b), ask_u = ask.s * C::UNITS;   // the sequence's units, the next one
-    const int upp_log = 31 - __clz(a.page / kv4::kUnit), upp = 1 << upp_log;   // units of a page
-    const long long page_bytes = (long long)a.h_kv * upp * C::UNIT;
+    const int upp_log = 31 - __clz(a.page / kv4::kUnit);   // units of a page
+    const long long page_bytes = (long long)a.h_kv * C::UNIT << upp_log;
     int entry = 0, entry_0 = INT_MIN;        // this lane's of 32 entries of the sequence's table
-    const auto head_of = [&]() { return a.cache + (long long)(ask.job / p.pl.blocks) * upp * C::UNIT; };
+    const auto head_of = [&]() { return a.cache + ((long long)(ask.job / p.pl.blocks) * C::UNIT << upp_log); };
     const uint8_t* head = head_of();         // page 0's units of the job's head
-    int left = 0;                            // units of the page that `src` is in, from there on
-    bool there = false;                      // is there such a page?
-    const uint8_t* src = a.cache;
     uint32_t bad = 0;                        // units of the stages whose page there is not
     const uint32_t stages = tc::smem_u32(ring) + warp * C::STAGES * C::STAGE;
     int put = 0, get = 0;
     uint32_t parity = 0;
 
-    const auto find_page = [&]() {
-      const int pg = ask_u >> upp_log, at = ask_u & (upp - 1);
-      if (pg < entry_0 || pg >= entry_0 + 32) {
-        entry_0 = pg;
-        entry = pg + lane < a.width ? a.table[(long long)ask.b * a.width + pg + lane] : -1;
-      }
-      const int page = __shfl_sync(0xffffffffu, entry, pg - entry_0);
-      there = (unsigned)page < (unsigned)a.n_pages;
-      if (!there && lane == 0) record_status(a.status, GDN_ERR_DEVICE_BOUNDS);
-      left = min(upp - at, ask_len - ask_u);
-      src = head + page * page_bytes + at * C::UNIT;
-    };
-    // One more stage, one copy for each page.
+    // One more stage: a lane for each unit, or where a page holds a whole stage one for all.
     const auto request = [&]() {
       const int units = min(C::UNITS, ask_len - ask_u);
-      bad &= ~(((1u << C::UNITS) - 1) << (put * C::UNITS));
-      int done = 0;
-#pragma unroll 1
-      while (true) {
-        if (left == 0) find_page();
-        const int run = min(left, units - done);
-        if (there) {
-          // (the barrier's turn does not end before the arrival below)
-          if (lane == 0) {
-            asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(tc::smem_u32(bar + put)),
-                         "r"(run * C::UNIT)
-                         : "memory");
-            asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                             stages + put * C::STAGE + done * C::UNIT),
-                         "l"(src), "r"(run * C::UNIT), "r"(tc::smem_u32(bar + put))
-                         : "memory");
-          }
-        } else {
-          bad |= ((1u << run) - 1) << (put * C::UNITS + done);
-        }
-        src += run * C::UNIT;
-        left -= run;
-        done += run;
-        ask_u += run;
-        if (done == units) break;
+      const int page_0 = ask_u >> upp_log, mine = ask_u + lane;
+      if (page_0 < entry_0 || page_0 + C::UNITS > entry_0 + 32) {
+        entry_0 = page_0;
+        entry = page_0 + lane < a.width ? a.table[(long long)ask.b * a.width + page_0 + lane] : -1;
       }
-      if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(tc::smem_u32(bar + put)) : "memory");
+      const int page = __shfl_sync(0xffffffffu, entry, (mine >> upp_log) - entry_0);
+      const bool there = (unsigned)page < (unsigned)a.n_pages;
+      if (lane < units && !there) record_status(a.status, GDN_ERR_DEVICE_BOUNDS);
+      const uint32_t found = __ballot_sync(0xffffffffu, lane < units && there);
+      const bool whole = 1 << upp_log >= C::UNITS;
+      bad &= ~(((1u << C::UNITS) - 1) << (put * C::UNITS));
+      bad |= (((1u << units) - 1) & ~found) << (put * C::UNITS);
+      const uint32_t b = tc::smem_u32(bar + put);
+      if (lane == 0)
+        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(b), "r"(__popc(found) * C::UNIT)
+                     : "memory");
+      if (lane < units && there && (!whole || lane == 0)) {
+        const uint8_t* src = head + page * page_bytes + (mine & ((1 << upp_log) - 1)) * C::UNIT;
+        asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                         stages + put * C::STAGE + lane * C::UNIT),
+                     "l"(src), "r"(whole ? units * C::UNIT : C::UNIT), "r"(b)
+                     : "memory");
+      }
       put = put + 1 == C::STAGES ? 0 : put + 1;
+      ask_u += units;
       --to_ask;
       if (++ask.s == ask.n) {
         const int b = ask.b;
