@@ -40,15 +40,16 @@
 // scale of V (ref goes by it), and 30 binary orders below the largest are still in range.
 //
 // Measured, both launches, of the bytes that the cache holds for the tokens: 256 sequences of 100
-// to 8000 tokens (16 query heads, 2 kv heads, d = 256) 123 us, 4.9 TB/s; one of 131072 (32, 8,
-// 128) 42 us, 3.6 TB/s; 64 of 6001 (32, 8, 128) 94 us, 4.7 TB/s, in pages of 16 120 us; 96 of 1 to
-// 2900 (64, 8, 64) 27 us, 3.0 TB/s; 17 of 4 to 6001 with 4 steps (32, 8, 128, pages of 16) 34 us,
+// to 8000 tokens (16 query heads, 2 kv heads, d = 256) 120 us, 5.0 TB/s; one of 131072 (32, 8,
+// 128) 41 us, 3.7 TB/s; 64 of 6001 (32, 8, 128) 92 us, 4.8 TB/s, in pages of 16 97 us; 96 of 1 to
+// 2900 (64, 8, 64) 28 us, 2.9 TB/s; 17 of 4 to 6001 with 4 steps (32, 8, 128, pages of 16) 33 us,
 // 1.8 TB/s; one of 833 9 us, latency (the lengths 0.8, first copy asked for 1.3, its rows and the
-// data 1, a stage 1.4, the share written 0.5, join 2).  Per unit of 16 tokens at d = 256: 264
-// clocks of an SM, for 535 instructions (272 of the integer pipe, which starts one every other
-// clock and scheduler: 136) and 48 products (96).  Masks, products and the fp32 arithmetic
-// between them contend for the same registers' ports: leaving out a sixth of any of them saved
-// a tenth at most.
+// data 1, a stage 1.4, the share written 0.5, join 2).  Per unit of 16 tokens at d = 256: 260
+// clocks of an SM, for 530 instructions (270 of the integer pipe, which starts one every other
+// clock and scheduler: 135) and 48 products (96).  Masks, products and the fp32 arithmetic
+// between them contend for the same issue slots and registers' ports: a timing without the
+// products that take off the 8s was 6 % shorter, one without the multiplications by V's scales
+// 6 %, without V's masks 2 %, with a third more warps none.
 #include <limits.h>
 #include <math.h>
 
