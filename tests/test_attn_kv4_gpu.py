@@ -190,6 +190,78 @@ def test_values_at_the_ends_of_bf16():
         check(x)
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_scales_of_values_that_differ_by_many_orders(d):
+    # tokens' values from 2^-60 to 2^60, small ones first and then in any order; an output is
+    # held against the largest magnitudes that reach it
+    for order in (False, True):
+        x = build(2, 1, 8, 1, d, 32, [700, 333], seed=15, gate=False)
+        g = torch.Generator().manual_seed(d)
+        e = torch.linspace(-60, 60, 1033)[torch.randperm(1033, generator=g) if order else torch.arange(1033)]
+        v = torch.randn(1033, 1, d, generator=g) * torch.exp2(e)[:, None, None]
+        gdn.gdn_kv4_store(x["dims"], None, v.to(BF).to(DEV), x["cache"], slot=x["slot"].to(DEV))
+        check(x)
+
+
+def test_groups_that_differ_by_many_orders():
+    # a token's groups of channels from 2^-9 to 2^9: each output against its own group's size,
+    # except that a weight times a scale below 2^-14 of fp16's top loses bits below 2^-24
+    x = build(1, 1, 8, 1, 256, 32, [500], seed=16, gate=False)
+    v = torch.randn(500, 1, 8, 32, generator=torch.Generator().manual_seed(3))
+    v = (v * torch.exp2(torch.linspace(-9, 9, 8))[:, None]).flatten(-2)
+    gdn.gdn_kv4_store(x["dims"], None, v.to(BF).to(DEV), x["cache"], slot=x["slot"].to(DEV))
+    check(x)
+
+
+@pytest.mark.parametrize("S", [1, 3])
+def test_rows_of_any_size(S):
+    # rows of q of zeros, of subnormal and of huge numbers, with keys that keep the scores ordinary
+    x = build(3, S, 8, 1, 128, 32, [100, 65, 40], seed=17, gate=False)
+    size = torch.tensor([0.0, 2.0 ** -126, 2.0 ** -130, 2.0 ** -60, 1.0, 2.0 ** -20, 3.0, 2.0 ** 6], device=DEV)
+    x["q"] = (x["q"].float() * size[:, None]).to(BF).contiguous()
+    check(x)
+    for up in (100, -100):                     # (q below 2^108)
+        y = build(1, S, 8, 1, 128, 32, [100], seed=18, gate=False)
+        y["q"] = (y["q"].float() * 2.0 ** up).to(BF)
+        # keys of 2^-88 at the least are held
+        k = torch.randn(100, 1, 128, generator=torch.Generator().manual_seed(4)) * 2.0 ** (-86 if up > 0 else 100)
+        gdn.gdn_kv4_store(y["dims"], k.to(BF).to(DEV), None, y["cache"], slot=y["slot"].to(DEV))
+        y["dims"].scale = 2.0 ** (-17 if up > 0 else -4)
+        check(y, y["dims"].scale)
+
+
+def test_channels_of_a_row_that_differ_by_many_orders():
+    # the largest channel meets keys of zero: the scores hang on the small ones
+    x = build(1, 1, 8, 1, 128, 32, [300], seed=19, gate=False)
+    x["q"][..., 7] = 4096.0
+    k = torch.randn(300, 1, 128, generator=torch.Generator().manual_seed(5))
+    k[..., :32] = 0
+    gdn.gdn_kv4_store(x["dims"], k.to(BF).to(DEV), None, x["cache"], slot=x["slot"].to(DEV))
+    check(x)
+
+
+def test_a_nan_in_the_middle_reaches_every_row_that_sees_it():
+    x = build(2, 2, 8, 2, 128, 16, [400, 90], seed=20, gate=False)
+    clean = call(x)
+    at = x["slot"][[200]].to(DEV)
+    bad = torch.ones(1, 2, 128, dtype=BF, device=DEV)
+    bad[0, 1, 70] = float("nan")
+    gdn.gdn_kv4_store(x["dims"], None, bad, x["cache"], slot=at)     # a group of V of one head
+    got = call(x)
+    nan = torch.isnan(got)
+    assert nan[0, :, 4:, 64:96].all() and not nan[0, :, :4].any() and not nan[0, :, 4:, :64].any()
+    assert not nan[0, :, 4:, 96:].any() and torch.equal(got[1], clean[1])
+    gdn.gdn_kv4_store(x["dims"], bad, None, x["cache"], slot=at)     # and of K
+    got = call(x)
+    assert torch.isnan(got[0, :, 4:]).all() and not torch.isnan(got[0, :, :4]).any() and torch.equal(got[1], clean[1])
+
+
+@pytest.mark.parametrize("d,hq,hk,S", [(256, 32, 2, 4), (256, 16, 2, 8), (128, 40, 8, 2), (64, 64, 1, 2)])
+def test_many_rows_over_many_jobs(d, hq, hk, S):
+    g = torch.Generator().manual_seed(d)
+    check(build(24, S, hq, hk, d, 16, torch.randint(0, 900, (24,), generator=g).tolist(), seed=21))
+
+
 def test_infinite_scores_follow_the_formula():
     x = build(1, 1, 1, 1, 64, 16, [20], seed=10, gate=False)
     x["q"][0, 0, 0, 3] = float("inf")
