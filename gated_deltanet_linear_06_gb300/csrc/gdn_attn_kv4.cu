@@ -714,18 +714,18 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) attn_kv4_kernel(Kv4
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-constexpr int kJoinThreads = 256;
+constexpr int kJoinThreads = 256, kMaxJoinThreads = 1024;
 
 // Joins the shares of each row: 2^(ref_i - M) of each, over the sum of the sums.  A CTA
-// takes kJoinThreads / LANES / groups rows (of up to 128 channels), `groups` lane groups to a
-// row, each every groups-th share with four shares' loads in flight.
+// takes threads / LANES / groups rows (of up to 128 channels), `groups` (a power of two) lane
+// groups to a row, each every groups-th share with four shares' loads in flight.
 template <int D, int NT>
-__global__ void __launch_bounds__(kJoinThreads) attn_kv4_join(Kv4Params p, int groups) {
+__global__ void __launch_bounds__(kMaxJoinThreads) attn_kv4_join(Kv4Params p, int groups) {
   constexpr int LANES = D / 4 < 32 ? D / 4 : 32, CHUNKS = D / 4 / LANES;
-  __shared__ float4 acc[kJoinThreads];
-  __shared__ float2 stat[kJoinThreads];
+  __shared__ float4 acc[kMaxJoinThreads];
+  __shared__ float2 stat[kMaxJoinThreads];
   const AttnKv4Args& a = p.a;
-  const int per = kJoinThreads / LANES / groups;   // rows of a CTA
+  const int per = blockDim.x / LANES / groups;   // rows of a CTA
   const int set = threadIdx.x / LANES, grp = set % groups;
   const long long item = (long long)blockIdx.x * per + set / groups, items = (long long)a.batch * a.steps * a.h_q * CHUNKS;
   const bool mine = item < items;
@@ -775,12 +775,13 @@ __global__ void __launch_bounds__(kJoinThreads) attn_kv4_join(Kv4Params p, int g
       for (int k = 0; k < 4; ++k) add(m[k].x, m[k].y, v[k]);
     }
   }
-  if (groups > 1) {
-    acc[threadIdx.x] = o;
-    stat[threadIdx.x] = make_float2(M, L);
+  for (int half = groups / 2; half > 0; half /= 2) {   // halves of the groups hand over to the others
+    if (grp >= half && grp < 2 * half) {
+      acc[threadIdx.x] = o;
+      stat[threadIdx.x] = make_float2(M, L);
+    }
     __syncthreads();
-    if (grp == 0)
-      for (int k = 1; k < groups; ++k) add(stat[threadIdx.x + k * LANES].x, stat[threadIdx.x + k * LANES].y, acc[threadIdx.x + k * LANES]);
+    if (grp < half) add(stat[threadIdx.x + half * LANES].x, stat[threadIdx.x + half * LANES].y, acc[threadIdx.x + half * LANES]);
   }
   if (!mine || grp != 0) return;
   // no token seen: zeros; tokens seen whose weights are all zero (scores of -inf): NaN
@@ -837,13 +838,19 @@ cudaError_t launch_n(const AttnKv4Args& a, cudaStream_t stream, int sms) {
   cfg.attrs = &overlap;
   cfg.numAttrs = 1;
   if ((e = cudaLaunchKernelEx(&cfg, kernel, p)) != cudaSuccess) return e;
-  // lane groups to a row: one for every four shares that a job has where all are alike
+  // Lane groups to a row: one for every four shares that a job can have where all are alike; larger
+  // CTAs where there are few rows with many shares (four sequences of up to 4000 10.6 us for 12.3;
+  // with few shares they only start later, one of 833 9.3 for 8.7).
   constexpr int LANES = D / 4 < 32 ? D / 4 : 32;
+  const long long items = (long long)a.batch * a.steps * a.h_q * (D / 4 / LANES);
+  const long long stages = ((long long)a.width * a.page / kv4::kUnit + C::UNITS - 1) / C::UNITS;
+  const long long even = p.pl.workers / ((long long)a.batch * p.pl.jobs_per_seq) + 1, shares = stages < even ? stages : even;
+  const int threads = items < sms && shares > 4 * kJoinThreads / LANES ? kMaxJoinThreads : kJoinThreads;
   int groups = 1;
-  while (groups < kJoinThreads / LANES && (long long)groups * 4 * a.batch * p.pl.jobs_per_seq < p.pl.workers) groups *= 2;
-  const long long items = (long long)a.batch * a.steps * a.h_q * (D / 4 / LANES), per = kJoinThreads / LANES / groups;
+  while (groups < threads / LANES && 4 * groups < shares) groups *= 2;
+  const long long per = threads / LANES / groups;
   cfg.gridDim = dim3((unsigned)((items + per - 1) / per));
-  cfg.blockDim = dim3(kJoinThreads);
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, attn_kv4_join<D, NT>, p, groups);
 }
