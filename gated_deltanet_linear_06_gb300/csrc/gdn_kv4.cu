@@ -10,10 +10,10 @@
 // units need not begin with one: the tokens are taken in sixteens that end where the first
 // token's unit does.
 //
-// A store is bound by its instructions, some 17 a value (of which 7 for the quotient, its
+// A store is bound by its instructions, some 16 a value (of which 5 for the quotient, its
 // rounding and its place); without divisions and with extremes as packed 16-bit numbers they
-// are half of what they were.  Measured, 32768 rows of 2 heads of 256: store 24 us (3.6 TB/s of
-// 67 MB read and 19 MB written), load as bf16 15 us (5.8 TB/s).  256 rows of as many
+// are less than half of what they were.  Measured, 32768 rows of 2 heads of 256: store 20.7 us
+// (4.2 TB/s of 67 MB read and 19 MB written), load as bf16 15 us (5.8 TB/s).  256 rows of as many
 // sequences: 5 us each, latency.
 #include "../../include/gdn.h"
 #include "gdn_kv4.cuh"
@@ -96,7 +96,7 @@ __device__ __forceinline__ uint32_t codes_of(uint4 raw, float& s) {
 #pragma unroll
   for (int k = 7; k >= 0; --k) {
     const int o = V ? k : k < 4 ? 2 * k : 2 * k - 7;
-    c = c * 16 + kv4::code_bits(o % 2 ? hi_f32(w[o / 2]) : lo_f32(w[o / 2]), s, r);
+    c = c * 16 + kv4::code_bits(o % 2 ? hi_f32(w[o / 2]) : lo_f32(w[o / 2]), r);
   }
   c = s == s ? c - kv4::kCodeBase * 0x11111111u : 0x88888888u;   // of a NaN scale 8s, as of zeros
   return V ? c : __funnelshift_l(c, c, 3);

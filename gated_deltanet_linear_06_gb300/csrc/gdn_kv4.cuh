@@ -43,15 +43,17 @@ __device__ __forceinline__ float group_scale(uint32_t extremes) {
   return m < kTiny ? 0.0f : extremes >> 16 == mag ? m * -0.125f : m * 0.125f;
 }
 
-// Code of x plus kCodeBase, modulo 2^32, with r = 1 / s (a few steps off at most).  The
-// quotient x r is corrected by its remainder, which leaves it exact wherever x / s can be
-// told in 24 bits, so also where it is half-way between two codes; elsewhere x / s, 8
-// significant bits over 8, is at least 2^-17 of itself away from half-way.  No quotient is
-// below -8, and adding 1.5 2^23 rounds to a whole number, ties to even.
+// Code of x plus kCodeBase, modulo 2^32, with r = 1 / s (a few steps off at most): x r to a
+// multiple of 2^-13 (the step of numbers around 1536), then to a whole number, ties to even both.
+// With significands X and M of x and of the group's extreme (8 bits each) and e >= 0 their
+// exponents' distance, |x / s| = 8 X / (2^e M) is at least 1 / (2^(e+1) M) from a half-integer that
+// it does not equal, and near one e <= 4 (as 8 X / (2^e M) is about 1/2 at the least): more than
+// 2^-13, which half a step of 2^-13 and r's error do not bridge; and where it equals one, both
+// leave it there.  No quotient is below -8.
 constexpr uint32_t kCodeBase = 0x4b400000u;
-__device__ __forceinline__ uint32_t code_bits(float x, float s, float r) {
-  const float q = x * r;
-  return __float_as_uint(fminf(fmaf(fmaf(-q, s, x), r, q), 7.0f) + (12582912.0f + 8.0f));
+__device__ __forceinline__ uint32_t code_bits(float x, float r) {
+  const float q = fminf(fmaf(x, r, 1536.0f), 1536.0f + 7.0f);
+  return __float_as_uint(q + (12582912.0f + 8.0f - 1536.0f));
 }
 
 // 1 / s for code_bits; of a group without a scale (zeros) one that makes every code 8.
