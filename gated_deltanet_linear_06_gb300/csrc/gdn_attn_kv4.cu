@@ -140,13 +140,14 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   return y;
 }
 
-// Codes as fp16 values, two in a word: four bits anywhere among the ten of a significand,
-// under an exponent of zero, are that code times 2^(place - 24), exactly (a subnormal number,
-// which the tensor cores take as it is).  The other operand or the end result makes up for
-// the power of two, and a product takes off the 8 that each code is too much.
-constexpr uint32_t kAt0 = 0x000f000fu, kAt4 = 0x00f000f0u, kAt2 = 0x003c003cu, kAt6 = 0x03c003c0u;
+// Codes as fp16 values, two in a word: four bits anywhere among the lowest eleven, under zeros,
+// are that code times 2^(place - 24), exactly (a subnormal number, which the tensor cores take
+// as it is, or one of the least exponent, whose steps are the same).  The other operand or the
+// end result makes up for the power of two, and a product takes off the 8 that each code is
+// too much.  K's words lie so that two of their four pairs need no shift; V's too.
+constexpr uint32_t kAt0 = 0x000f000fu, kAt4 = 0x00f000f0u, kAt3 = 0x00780078u, kAt7 = 0x07800780u;
 // -8 at those places
-constexpr uint32_t kLess8At0 = 0x80088008u, kLess8At4 = 0x80808080u, kLess8At2 = 0x80208020u, kLess8At6 = 0x82008200u;
+constexpr uint32_t kLess8At0 = 0x80088008u, kLess8At4 = 0x80808080u, kLess8At3 = 0x80408040u, kLess8At7 = 0x84008400u;
 
 __device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {   // bf16 pairs; a NaN gives way
   const __nv_bfloat162 m = __hmax2(__habs2(reinterpret_cast<__nv_bfloat162&>(a)), __habs2(reinterpret_cast<__nv_bfloat162&>(b)));
@@ -379,8 +380,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) attn_kv4_kernel(Kv4
       if (lane == 0 && end == use.n) p.span[job].y = worker;
 
       // q as the second operand: row g of a block of 8, a group's channels 8 t .. 8 t + 7, as
-      // fp16 with the row's largest value between 2^10 and 2^11 (what that rounds is below
-      // 2^-34 of it); channels that meet codes at place 2 16 times that.  base: what the 8s
+      // fp16 with the row's largest value between 2^9 and 2^10 (what that rounds is at most
+      // 2^-34 of it); channels that meet codes at place 3 16 times that.  base: what the 8s
       // add to rows 2 t and 2 t + 1, taken off.
       uint4 q[QREG ? NT : 1][QREG ? R : 1];
       float4 base[BREG ? NT : 1][BREG ? R : 1];
@@ -404,13 +405,13 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) attn_kv4_kernel(Kv4
         most2 = max(most2, __shfl_xor_sync(0xffffffffu, most2, 1));
         most2 = max(most2, __shfl_xor_sync(0xffffffffu, most2, 2));
         const float most = __uint_as_float(most2 << 16);
-        // 2^10 over the power of two in `most`, at most 2^120 (a row of nothing but tiny numbers)
-        const uint32_t ex = min(264 - min((int)(__float_as_uint(most) >> 23), 254), 247);
+        // 2^9 over the power of two in `most`, at most 2^120 (a row of nothing but tiny numbers)
+        const uint32_t ex = min(263 - min((int)(__float_as_uint(most) >> 23), 254), 247);
         const uint32_t up = ex << 7 | ex << 23, up16 = (ex + 4) << 7 | (ex + 4) << 23;   // bf16 pairs
         const float down = __uint_as_float((254 - ex) << 23);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) scale[n][i] = p.qscale * 0x1p18f * __shfl_sync(0xffffffffu, down, (2 * t + i) * 4);
-        const uint32_t less8[4] = {kLess8At2, kLess8At2, kLess8At6, kLess8At6};
+        for (int i = 0; i < 2; ++i) scale[n][i] = p.qscale * 0x1p17f * __shfl_sync(0xffffffffu, down, (2 * t + i) * 4);
+        const uint32_t less8[4] = {kLess8At3, kLess8At3, kLess8At7, kLess8At7};
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           const uint4 h = make_uint4(half_pair(raw[r].x, up16), half_pair(raw[r].y, up), half_pair(raw[r].z, up16),
@@ -498,15 +499,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) attn_kv4_kernel(Kv4
             for (int e = 0; e < 4; ++e) s[k][n][e] = 0.0f;
 #pragma unroll
           for (int r = 0; r < R; ++r) {
-            uint32_t f[2][4];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const uint32_t x = __funnelshift_r(w0[r], w0[r], 1 + 8 * i), y = __funnelshift_r(w1[r], w1[r], 1 + 8 * i);
-              f[i][0] = x & kAt2;
-              f[i][1] = y & kAt2;
-              f[i][2] = x & kAt6;
-              f[i][3] = y & kAt6;
-            }
+            const uint32_t x1 = __funnelshift_r(w0[r], w0[r], 8), y1 = __funnelshift_r(w1[r], w1[r], 8);
+            const uint32_t f[2][4] = {{w0[r] & kAt3, w1[r] & kAt3, w0[r] & kAt7, w1[r] & kAt7},
+                                      {x1 & kAt3, y1 & kAt3, x1 & kAt7, y1 & kAt7}};
             const float s0 = r % 2 ? hi_f32(ks[0][r / 2]) : lo_f32(ks[0][r / 2]);
             const float s1 = r % 2 ? hi_f32(ks[1][r / 2]) : lo_f32(ks[1][r / 2]);
 #pragma unroll
