@@ -100,11 +100,11 @@ struct Cfg {
   // 256 of up to 8000 of d = 256 took 126 with 8 and 122.5 with 2.
   static constexpr int JOB = 640 / D > UNITS ? 640 / D / UNITS : 1;
   static constexpr bool QREG = NT * R <= 8;          // q's operands in registers, else in shared memory
-  static constexpr bool BREG = NT * R <= 2;          // and the sums of their channels
+  static constexpr bool BREG = R <= 2;               // and the sums of their channels
   static constexpr int WARPS = D == 64 && NT == 1 ? 12 : 8;   // (registers for 8 or 12; 10 left one scheduler with more)
   static constexpr int UNIT = kv4::unit_bytes(D), STAGE = UNITS * UNIT;
   static constexpr int STAGES = D == 256 && NT == 2 ? 3 : 2;
-  static constexpr int QBYTES = QREG ? 0 : NT * R * 512, BBYTES = BREG ? 0 : NT * R * 64;   // a warp's
+  static constexpr int QBYTES = QREG ? 0 : NT * R * 512, BBYTES = BREG ? 0 : R * 64;   // a warp's
   static constexpr int SMEM = WARPS * (STAGES * STAGE + QBYTES + BBYTES);
   static_assert(SMEM <= 216 * 1024 && UNITS * STAGES <= 32, "shared memory, bits of `bad`");
 };
@@ -190,21 +190,22 @@ __device__ __forceinline__ void words_at(uint32_t (&w)[W], const uint8_t* p) {
   }
 }
 
-// A lane's words of K's or V's codes of a unit: of both halves of its tokens, per group.
 template <int D>
-__device__ __forceinline__ void codes_at(uint32_t (&w0)[D / 32], uint32_t (&w1)[D / 32], const uint8_t* p, int lane) {
+constexpr int kSet = D / 32 < 4 ? D / 32 : 4;   // groups whose words come together
+
+// A lane's words of K's or V's codes of a unit: of both halves of its tokens, for a set of groups.
+template <int D>
+__device__ __forceinline__ void codes_at(uint32_t (&w0)[kSet<D>], uint32_t (&w1)[kSet<D>], const uint8_t* p, int lane,
+                                         int set) {
   constexpr int NV = D / 64;
   const uint4* v = reinterpret_cast<const uint4*>(p) + lane;
   if constexpr (NV == 1) {
     const uint4 x = v[0];
     w0[0] = x.x, w0[1] = x.y, w1[0] = x.z, w1[1] = x.w;
   } else {
-#pragma unroll
-    for (int i = 0; i < NV / 2; ++i) {
-      const uint4 x = v[i * 32], y = v[(i + NV / 2) * 32];
-      w0[4 * i] = x.x, w0[4 * i + 1] = x.y, w0[4 * i + 2] = x.z, w0[4 * i + 3] = x.w;
-      w1[4 * i] = y.x, w1[4 * i + 1] = y.y, w1[4 * i + 2] = y.z, w1[4 * i + 3] = y.w;
-    }
+    const uint4 x = v[set * 32], y = v[(set + NV / 2) * 32];
+    w0[0] = x.x, w0[1] = x.y, w0[2] = x.z, w0[3] = x.w;
+    w1[0] = y.x, w1[1] = y.y, w1[2] = y.z, w1[3] = y.w;
   }
 }
 
@@ -273,12 +274,22 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) attn_kv4_kernel(Kv4
   using C = Cfg<D, NT>;
   constexpr int R = C::R;                    // groups
   constexpr bool QREG = C::QREG, BREG = C::BREG;
+  // 8 rows are the products' N: a lane has tokens g, g + 8 of a unit and rows 2 t, 2 t + 1 (element
+  // e of a product: token g + 8 (e / 2), row 2 t + e % 2).  16 are their M: it has tokens 2 t,
+  // 2 t + 1 (of half x) and rows g, g + 8 (e / 2), the weights come out as the next products
+  // want them, and the 8s of all of a group's channels take one product instead of two for
+  // every 8 rows.
+  constexpr bool WIDE = NT == 2;
+  constexpr int LANES_0 = WIDE ? 1 : 4, LANES_1 = WIDE ? 2 : 16;   // lane bits that tell tokens, not rows, apart
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ long long before[GDN_ATTN_MAX_BATCH + 1];
   __shared__ long long warp_sums[kMaxWarps];
   __shared__ uint64_t full[C::WARPS * C::STAGES];
   const AttnKv4Args& a = p.a;
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g = lane / 4, t = lane % 4;
+
+  const auto row_of = [](int e) { return WIDE ? e / 2 : e % 2; };
+  const auto token_of = [&](int x, int e) { return WIDE ? 8 * x + 2 * t + e % 2 : g + e / 2 * 8; };
 
   asm volatile("griddepcontrol.wait;" ::: "memory");
   uint64_t* bar = full + warp * C::STAGES;
@@ -379,15 +390,15 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) attn_kv4_kernel(Kv4
       if (lane == 0 && use.s == 0) p.span[job].x = worker;
       if (lane == 0 && end == use.n) p.span[job].y = worker;
 
-      // q as the second operand: row g of a block of 8, a group's channels 8 t .. 8 t + 7, as
+      // q as an operand: row g of a block of 8, a group's channels 8 t .. 8 t + 7, as
       // fp16 with the row's largest value between 2^9 and 2^10 (what that rounds is at most
       // 2^-34 of it); channels that meet codes at place 3 16 times that.  base: what the 8s
-      // add to rows 2 t and 2 t + 1, taken off.
+      // add to this lane's two rows, taken off.
       uint4 q[QREG ? NT : 1][QREG ? R : 1];
-      float4 base[BREG ? NT : 1][BREG ? R : 1];
+      float2 base[BREG ? R : 1];
       uint8_t* const qs = ring + C::WARPS * C::STAGES * C::STAGE + warp * (C::QBYTES + C::BBYTES);
-      float4* const bs = reinterpret_cast<float4*>(qs + C::QBYTES) + t;
-      float scale[NT][2];                    // of the scores of rows 2 t and 2 t + 1
+      float2* const bs = reinterpret_cast<float2*>(qs + C::QBYTES) + (WIDE ? g : t);
+      float scale[2];                        // of this lane's rows' scores
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const int row = row0 + 8 * n + g;
@@ -408,47 +419,61 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) attn_kv4_kernel(Kv4
         // 2^9 over the power of two in `most`, at most 2^120 (a row of nothing but tiny numbers)
         const uint32_t ex = min(263 - min((int)(__float_as_uint(most) >> 23), 254), 247);
         const uint32_t up = ex << 7 | ex << 23, up16 = (ex + 4) << 7 | (ex + 4) << 23;   // bf16 pairs
-        const float down = __uint_as_float((254 - ex) << 23);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) scale[n][i] = p.qscale * 0x1p17f * __shfl_sync(0xffffffffu, down, (2 * t + i) * 4);
-        const uint32_t less8[4] = {kLess8At3, kLess8At3, kLess8At7, kLess8At7};
+        const float down = p.qscale * 0x1p17f * __uint_as_float((254 - ex) << 23);
+        if constexpr (WIDE) {
+          scale[n] = down;
+        } else {
+          scale[0] = __shfl_sync(0xffffffffu, down, 8 * t);
+          scale[1] = __shfl_sync(0xffffffffu, down, 8 * t + 4);
+        }
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           const uint4 h = make_uint4(half_pair(raw[r].x, up16), half_pair(raw[r].y, up), half_pair(raw[r].z, up16),
                                      half_pair(raw[r].w, up));
-          float c[4];
-          mma(c, less8, h.x, h.y, 0.0f, 0.0f, 0.0f, 0.0f);
-          mma(c, less8, h.z, h.w);
           if constexpr (QREG) q[n][r] = h;
           else *reinterpret_cast<uint4*>(qs + (n * R + r) * 512 + lane * 16) = h;
-          if constexpr (BREG) base[n][r] = make_float4(c[0], c[1], c[2], c[3]);
-          else if (g == 0) bs[(n * R + r) * 4] = make_float4(c[0], c[1], c[2], c[3]);
         }
       }
+      const auto q_at = [&](int n, int r) {
+        if constexpr (QREG) return q[n][r];
+        else return *reinterpret_cast<const uint4*>(qs + (n * R + r) * 512 + lane * 16);
+      };
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const uint4 x = q_at(0, r), y = q_at(NT - 1, r);   // (a lane reads what it wrote)
+        float c[4];
+        float2 sums;
+        if constexpr (WIDE) {
+          const uint32_t a0[4] = {x.x, y.x, x.y, y.y}, a1[4] = {x.z, y.z, x.w, y.w};
+          mma(c, a0, kLess8At3, kLess8At7, 0.0f, 0.0f, 0.0f, 0.0f);
+          mma(c, a1, kLess8At3, kLess8At7);
+          sums = make_float2(c[0], c[2]);
+        } else {
+          const uint32_t less8[4] = {kLess8At3, kLess8At3, kLess8At7, kLess8At7};
+          mma(c, less8, x.x, x.y, 0.0f, 0.0f, 0.0f, 0.0f);
+          mma(c, less8, x.z, x.w);
+          sums = make_float2(c[0], c[1]);
+        }
+        if constexpr (BREG) base[r] = sums;
+        else if ((WIDE ? t : g) == 0) bs[r * 8] = sums;
+      }
       if constexpr (!BREG) __syncwarp();
-      // the last token that rows 2 t and 2 t + 1 of each block see
-      int last[NT][2];
+      // the last token that this lane's rows see
+      int last[2];
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          last[n][i] = len - a.steps + min((row0 + 8 * n + 2 * t + i) / p.pl.G, a.steps - 1);
+      for (int i = 0; i < 2; ++i)
+        last[i] = len - a.steps + min((row0 + (WIDE ? 8 * i + g : 2 * t + i)) / p.pl.G, a.steps - 1);
       const int all_see = len - a.steps;     // tokens up to this one are every row's
-      float o[NT][R][2][4], ref[NT][2], sum[NT][2];
+      float o[R][2 * NT][4], ref[2] = {0.0f, 0.0f}, sum[2] = {0.0f, 0.0f};
       int v = kLeastV;                       // 2^v: above every scale of V at the last update
-      uint32_t fresh = (1u << (2 * NT)) - 1;   // this lane's rows that have not seen a score
+      uint32_t fresh = 3;                    // this lane's rows that have not seen a score
       uint32_t poison = 0;                   // their groups that are NaN, eight bits a row
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
+      for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int r = 0; r < R; ++r)
+        for (int x = 0; x < 2 * NT; ++x)
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[n][r][i][e] = 0.0f;
-        ref[n][0] = ref[n][1] = 0.0f;
-        sum[n][0] = sum[n][1] = 0.0f;
-      }
+          for (int e = 0; e < 4; ++e) o[r][x][e] = 0.0f;
 
       // Where not every row sees all of a stage's tokens: in tokens of no row (past the
       // sequence, of a page that is not there) V's scales become zeros,
@@ -470,10 +495,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) attn_kv4_kernel(Kv4
             const int which = __shfl_sync(0xffffffffu, token, from);
             const uint32_t groups = __shfl_sync(0xffffffffu, odd << (2 * (t % (R / 2))), from);
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-              for (int k = 0; k < 2; ++k)
-                if (which <= last[n][k]) poison |= groups << (8 * (2 * n + k));
+            for (int k = 0; k < 2; ++k)
+              if (which <= last[k]) poison |= groups << (8 * k);
           }
         }
         __syncwarp();
@@ -483,46 +506,58 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) attn_kv4_kernel(Kv4
       // A stage of units from u on.
       const auto meet = [&](int u, const uint8_t* st, uint32_t gone, bool edge) {
         constexpr int NU = C::UNITS;
-        const int j = u * kv4::kUnit + g;    // this lane's tokens: j + 16 k, j + 16 k + 8
-        // scores: tokens g and g + 8 of each unit by rows 2 t, 2 t + 1
-        float s[NU][NT][4];
+        constexpr int SET = kSet<D>, TOKS = WIDE ? 4 : 2;   // tokens of a unit that a lane has
+        // the scales of this lane's i-th token of a unit, K's
+        const auto scales = [&](int k, int i) {
+          return st + k * C::UNIT + 16 * D + (WIDE ? 2 * t + i % 2 + i / 2 * 8 : g + 8 * i) * (D / 8);
+        };
+        float s[NU][NT][4];                  // scores: token_of(x, e) of each unit, row row_of(e)
 #pragma unroll
         for (int k = 0; k < NU; ++k) {
-          uint32_t ks[2][R / 2];             // scales of tokens g and g + 8, two groups a word
+          uint32_t ks[TOKS][R / 2];          // two groups a word
 #pragma unroll
-          for (int h = 0; h < 2; ++h) words_at<R / 2>(ks[h], st + k * C::UNIT + 16 * D + (g + 8 * h) * (D / 8));
-          uint32_t w0[R], w1[R];
-          codes_at<D>(w0, w1, st + k * C::UNIT, lane);
+          for (int i = 0; i < TOKS; ++i) words_at<R / 2>(ks[i], scales(k, i));
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
+          for (int x = 0; x < NT; ++x)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[k][n][e] = 0.0f;
+            for (int e = 0; e < 4; ++e) s[k][x][e] = 0.0f;
 #pragma unroll
-          for (int r = 0; r < R; ++r) {
-            const uint32_t x1 = __funnelshift_r(w0[r], w0[r], 8), y1 = __funnelshift_r(w1[r], w1[r], 8);
-            const uint32_t f[2][4] = {{w0[r] & kAt3, w1[r] & kAt3, w0[r] & kAt7, w1[r] & kAt7},
-                                      {x1 & kAt3, y1 & kAt3, x1 & kAt7, y1 & kAt7}};
-            const float s0 = r % 2 ? hi_f32(ks[0][r / 2]) : lo_f32(ks[0][r / 2]);
-            const float s1 = r % 2 ? hi_f32(ks[1][r / 2]) : lo_f32(ks[1][r / 2]);
+          for (int set = 0; set < R / SET; ++set) {
+            uint32_t w0[SET], w1[SET];
+            codes_at<D>(w0, w1, st + k * C::UNIT, lane, set);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              uint4 qq;
-              float4 bb;
-              if constexpr (QREG) qq = q[n][r];
-              else qq = *reinterpret_cast<const uint4*>(qs + (n * R + r) * 512 + lane * 16);
-              if constexpr (BREG) bb = base[n][r];
-              else bb = bs[(n * R + r) * 4];
-              float c[4];
-              mma(c, f[0], qq.x, qq.y, bb.x, bb.y, bb.z, bb.w);
-              mma(c, f[1], qq.z, qq.w);
-              s[k][n][0] = fmaf(c[0], s0, s[k][n][0]);
-              s[k][n][1] = fmaf(c[1], s0, s[k][n][1]);
-              s[k][n][2] = fmaf(c[2], s1, s[k][n][2]);
-              s[k][n][3] = fmaf(c[3], s1, s[k][n][3]);
+            for (int rr = 0; rr < SET; ++rr) {
+              const int r = set * SET + rr;
+              const uint32_t x1 = __funnelshift_r(w0[rr], w0[rr], 8), y1 = __funnelshift_r(w1[rr], w1[rr], 8);
+              float sc[TOKS];
+#pragma unroll
+              for (int i = 0; i < TOKS; ++i) sc[i] = r % 2 ? hi_f32(ks[i][r / 2]) : lo_f32(ks[i][r / 2]);
+              const uint4 qx = q_at(0, r);
+              float2 bb;
+              if constexpr (BREG) bb = base[r];
+              else bb = bs[r * 8];
+              float c[NT][4];
+              if constexpr (WIDE) {          // rows by tokens
+                const uint4 qy = q_at(1, r);
+                const uint32_t a0[4] = {qx.x, qy.x, qx.y, qy.y}, a1[4] = {qx.z, qy.z, qx.w, qy.w};
+                mma(c[0], a0, w0[rr] & kAt3, w0[rr] & kAt7, bb.x, bb.x, bb.y, bb.y);
+                mma(c[1], a0, w1[rr] & kAt3, w1[rr] & kAt7, bb.x, bb.x, bb.y, bb.y);
+                mma(c[0], a1, x1 & kAt3, x1 & kAt7);
+                mma(c[1], a1, y1 & kAt3, y1 & kAt7);
+              } else {                       // tokens by rows
+                const uint32_t f0[4] = {w0[rr] & kAt3, w1[rr] & kAt3, w0[rr] & kAt7, w1[rr] & kAt7};
+                const uint32_t f1[4] = {x1 & kAt3, y1 & kAt3, x1 & kAt7, y1 & kAt7};
+                mma(c[0], f0, qx.x, qx.y, bb.x, bb.y, bb.x, bb.y);
+                mma(c[0], f1, qx.z, qx.w);
+              }
+#pragma unroll
+              for (int x = 0; x < NT; ++x)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[k][x][e] = fmaf(c[x][e], sc[WIDE ? 2 * x + e % 2 : e / 2], s[k][x][e]);
             }
           }
         }
-        // the widest scale of V: a lane looks at one word of each of its tokens
+        // the widest scale of V: a lane looks at one word of each of two tokens
         uint32_t widest = 0;
 #pragma unroll
         for (int k = 0; k < NU; ++k)
@@ -538,110 +573,148 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) attn_kv4_kernel(Kv4
 #pragma unroll
         for (int k = 0; k < NU; ++k)
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
+          for (int x = 0; x < NT; ++x)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[k][n][e] = fmaf(s[k][n][e], scale[n][e % 2], -ref[n][e % 2]);
+            for (int e = 0; e < 4; ++e) s[k][x][e] = fmaf(s[k][x][e], scale[row_of(e)], -ref[row_of(e)]);
         if (edge) {
 #pragma unroll
           for (int k = 0; k < NU; ++k) {
-            const int at = gone >> k & 1 ? 0x7fffffff - 16 : j + 16 * k;
+            const int at = gone >> k & 1 ? 0x7fffffff - 16 : (u + k) * kv4::kUnit;
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int x = 0; x < NT; ++x)
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                if (at + e / 2 * 8 > last[n][e % 2]) s[k][n][e] = -INFINITY;
+                if (at + token_of(x, e) > last[row_of(e)]) s[k][x][e] = -INFINITY;
           }
         }
 #pragma unroll
         for (int k = 0; k < NU; ++k)
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
+          for (int x = 0; x < NT; ++x)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) over = over || s[k][n][e] > room;
+            for (int e = 0; e < 4; ++e) over = over || s[k][x][e] > room;
         if (__any_sync(0xffffffffu, over)) {
           float w = wide;
 #pragma unroll
           for (int k = 1; k <= 16; k <<= 1) w = fmaxf(w, __shfl_xor_sync(0xffffffffu, w, k));
           const int v1 = min(max(v, (__float_as_int(w) >> 23) - 126), 126);
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
+          for (int i = 0; i < 2; ++i) {
+            // largest score, less ref: of these units and of those before
+            float m = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              // largest score, less ref: of these units and of those before
-              float m = -INFINITY;
+            for (int k = 0; k < NU; ++k)
 #pragma unroll
-              for (int k = 0; k < NU; ++k) m = fmaxf(m, fmaxf(s[k][n][i], s[k][n][2 + i]));
+              for (int x = 0; x < NT; ++x)
 #pragma unroll
-              for (int k = 4; k <= 16; k <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
-              const bool first = fresh >> (2 * n + i) & 1;
-              if (!first) m = fmaxf(m, kTop - (float)v);
-              const float to = ref[n][i] + (m - (kTop - (float)v1)), by = ref[n][i] - to;
-              if (by != 0.0f && m != -INFINITY) {
-                const float f = first ? 1.0f : ex2(by);
-                ref[n][i] = to;
-                sum[n][i] *= f;
+                for (int e = 0; e < 4; ++e)
+                  if (row_of(e) == i) m = fmaxf(m, s[k][x][e]);
 #pragma unroll
-                for (int k = 0; k < NU; ++k) {
-                  s[k][n][i] += by;
-                  s[k][n][2 + i] += by;
+            for (int k = LANES_0; k <= LANES_1; k <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
+            const bool first = fresh >> i & 1;
+            if (!first) m = fmaxf(m, kTop - (float)v);
+            const float to = ref[i] + (m - (kTop - (float)v1)), by = ref[i] - to;
+            if (by != 0.0f && m != -INFINITY) {
+              const float f = first ? 1.0f : ex2(by);
+              ref[i] = to;
+              sum[i] *= f;
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (row_of(e) == i) {
+#pragma unroll
+                  for (int k = 0; k < NU; ++k)
+#pragma unroll
+                    for (int x = 0; x < NT; ++x) s[k][x][e] += by;
+#pragma unroll
+                  for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (int x = 0; x < 2 * NT; ++x) o[r][x][e] *= f;
                 }
-#pragma unroll
-                for (int r = 0; r < R; ++r)
-#pragma unroll
-                  for (int k = 0; k < 2; ++k) {
-                    o[n][r][k][i] *= f;
-                    o[n][r][k][2 + i] *= f;
-                  }
-              }
-              if (m != -INFINITY) fresh &= ~(1u << (2 * n + i));
             }
+            if (m != -INFINITY) fresh &= ~(1u << i);
+          }
           v = v1;
         }
         if (v > kTinyWeights) {              // V's scales are huge, and weights tiny
 #pragma unroll
           for (int k = 0; k < NU; ++k)
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int x = 0; x < NT; ++x)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) s[k][n][e] = ex2_small(s[k][n][e]);
+              for (int e = 0; e < 4; ++e) s[k][x][e] = ex2_small(s[k][x][e]);
         } else {
 #pragma unroll
           for (int k = 0; k < NU; ++k)
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int x = 0; x < NT; ++x)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) s[k][n][e] = ex2(s[k][n][e]);
+              for (int e = 0; e < 4; ++e) s[k][x][e] = ex2(s[k][x][e]);
         }
 #pragma unroll
         for (int k = 0; k < NU; ++k)
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
+          for (int x = 0; x < NT; ++x)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sum[n][e % 2] += s[k][n][e];
-        // outputs: channels by rows, over the 16 tokens of each unit
+            for (int e = 0; e < 4; ++e) sum[row_of(e)] += s[k][x][e];
+        // outputs, over the 16 tokens of each unit: a pair of units' 8s first, a sum for all of a
+        // group's channels, then their codes
+        constexpr int PAIR = NU < 2 ? NU : 2;
         const uint32_t less8[4] = {kLess8At0, kLess8At4, kLess8At0, kLess8At4};
+        const uint32_t less8n = g % 2 ? kLess8At4 : kLess8At0;
 #pragma unroll
-        for (int k = 0; k < NU; ++k) {
-          uint32_t vs[2][R / 2];
+        for (int k0 = 0; k0 < NU; k0 += PAIR) {
+          uint32_t vs[PAIR][TOKS][R / 2];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) words_at<R / 2>(vs[h], st + k * C::UNIT + 16 * D + (g + 8 * h) * (D / 8) + D / 16);
-          uint32_t w0[R], w1[R];
-          codes_at<D>(w0, w1, st + k * C::UNIT + 8 * D, lane);
+          for (int k = 0; k < PAIR; ++k)
 #pragma unroll
-          for (int r = 0; r < R; ++r) {
-            const float s0 = r % 2 ? hi_f32(vs[0][r / 2]) : lo_f32(vs[0][r / 2]);
-            const float s1 = r % 2 ? hi_f32(vs[1][r / 2]) : lo_f32(vs[1][r / 2]);
-            const uint32_t x1 = w0[r] >> 8, y1 = w1[r] >> 8;
-            const uint32_t f[2][4] = {{w0[r] & kAt0, w0[r] & kAt4, w1[r] & kAt0, w1[r] & kAt4},
-                                      {x1 & kAt0, x1 & kAt4, y1 & kAt0, y1 & kAt4}};
+            for (int i = 0; i < TOKS; ++i) words_at<R / 2>(vs[k][i], scales(k0 + k, i) + D / 16);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              const uint32_t b0 = transpose8(pack_f16x2(s[k][n][0] * s0, s[k][n][1] * s0));
-              const uint32_t b1 = transpose8(pack_f16x2(s[k][n][2] * s1, s[k][n][3] * s1));
+          for (int set = 0; set < R / SET; ++set) {
+            uint32_t w0[PAIR][SET], w1[PAIR][SET];
 #pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                mma(o[n][r][i], less8, b0, b1);
-                mma(o[n][r][i], f[i], b0, b1);
+            for (int k = 0; k < PAIR; ++k) codes_at<D>(w0[k], w1[k], st + (k0 + k) * C::UNIT + 8 * D, lane, set);
+#pragma unroll
+            for (int rr = 0; rr < SET; ++rr) {
+              const int r = set * SET + rr;
+              uint32_t w[PAIR][2 * NT];      // weights times scales, as an operand
+              float off[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+              for (int k = 0; k < PAIR; ++k) {
+                float sc[TOKS];
+#pragma unroll
+                for (int i = 0; i < TOKS; ++i) sc[i] = r % 2 ? hi_f32(vs[k][i][r / 2]) : lo_f32(vs[k][i][r / 2]);
+                const auto& y = s[k0 + k];
+                if constexpr (WIDE) {
+#pragma unroll
+                  for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                      w[k][2 * x + i] = pack_f16x2(y[x][2 * i] * sc[2 * x], y[x][2 * i + 1] * sc[2 * x + 1]);
+                  mma(off, w[k], less8n, less8n);
+                } else {
+                  w[k][0] = transpose8(pack_f16x2(y[0][0] * sc[0], y[0][1] * sc[0]));
+                  w[k][1] = transpose8(pack_f16x2(y[0][2] * sc[1], y[0][3] * sc[1]));
+                  mma(off, less8, w[k][0], w[k][1]);
+                }
+              }
+#pragma unroll
+              for (int x = 0; x < 2 * NT; ++x)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[r][x][e] += off[WIDE ? e / 2 * 2 + x % 2 : e];
+#pragma unroll
+              for (int k = 0; k < PAIR; ++k) {
+                const uint32_t x0 = w0[k][rr], y0 = w1[k][rr], x1 = x0 >> 8, y1 = y0 >> 8;
+                if constexpr (WIDE) {        // rows by channels
+                  mma(o[r][0], w[k], x0 & kAt0, y0 & kAt0);
+                  mma(o[r][1], w[k], x0 & kAt4, y0 & kAt4);
+                  mma(o[r][2], w[k], x1 & kAt0, y1 & kAt0);
+                  mma(o[r][3], w[k], x1 & kAt4, y1 & kAt4);
+                } else {                     // channels by rows
+                  const uint32_t f0[4] = {x0 & kAt0, x0 & kAt4, y0 & kAt0, y0 & kAt4};
+                  const uint32_t f1[4] = {x1 & kAt0, x1 & kAt4, y1 & kAt0, y1 & kAt4};
+                  mma(o[r][0], f0, w[k][0], w[k][1]);
+                  mma(o[r][1], f1, w[k][0], w[k][1]);
+                }
               }
             }
           }
@@ -666,31 +739,37 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) attn_kv4_kernel(Kv4
       }
       if (__any_sync(0xffffffffu, poison != 0)) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int r = 0; r < R; ++r)
 #pragma unroll
-          for (int r = 0; r < R; ++r)
+          for (int x = 0; x < 2 * NT; ++x)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              if (poison >> (16 * n + 8 * (e % 2) + r) & 1) o[n][r][0][e] = o[n][r][1][e] = __uint_as_float(0x7fc00000u);
-            }
+            for (int e = 0; e < 4; ++e)
+              if (poison >> (8 * row_of(e) + r) & 1) o[r][x][e] = __uint_as_float(0x7fc00000u);
       }
       // the share's sums into its slot, as with weights that do not go by V's scales
       const float stored = __uint_as_float((uint32_t)(v - (int)kStored + 127) << 23);
+      const float at0 = 0x1p24f * stored, at4 = 0x1p20f * stored;
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int i = 0; i < 2; ++i) {
+        float l = sum[i];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          float l = sum[n][i];
+        for (int k = LANES_0; k <= LANES_1; k <<= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
+        const long long row = slot * (8 * NT) + (WIDE ? 8 * i + g : 2 * t + i);
+        if ((WIDE ? t : g) == 0) p.ml[row] = make_float2(ref[i] - ((float)v - kStored), l * stored);
 #pragma unroll
-          for (int k = 4; k <= 16; k <<= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
-          const long long row = slot * (8 * NT) + 8 * n + 2 * t + i;
-          if (g == 0) p.ml[row] = make_float2(ref[n][i] - ((float)v - kStored), l * stored);
+        for (int r = 0; r < R; ++r) {
+          float* part = p.part + row * D + 32 * r;
+          if constexpr (WIDE) {
 #pragma unroll
-          for (int r = 0; r < R; ++r)
-            *reinterpret_cast<float4*>(p.part + row * D + 32 * r + 4 * g) =
-                make_float4(o[n][r][0][i] * 0x1p24f * stored, o[n][r][0][2 + i] * 0x1p20f * stored,
-                            o[n][r][1][i] * 0x1p24f * stored, o[n][r][1][2 + i] * 0x1p20f * stored);
+            for (int e = 2 * i; e < 2 * i + 2; ++e)
+              *reinterpret_cast<float4*>(part + 8 * t + e % 2 * 4) =
+                  make_float4(o[r][0][e] * at0, o[r][1][e] * at4, o[r][2][e] * at0, o[r][3][e] * at4);
+          } else {
+            *reinterpret_cast<float4*>(part + 4 * g) =
+                make_float4(o[r][0][i] * at0, o[r][0][2 + i] * at4, o[r][1][i] * at0, o[r][1][2 + i] * at4);
+          }
         }
+      }
       if (!ok) break;
       rest -= end - use.s;
       use.s = end;
