@@ -18,8 +18,9 @@
 //   - the 8 by which the stored codes are too large is taken off by the tensor cores: for K as
 //     the value that the sum starts from, for V by a product with a constant (taking it off the
 //     values was eight instructions for every one of those);
-//   - rows (8 at a time: a group's query heads, or several steps' of them) are the products' N,
-//     tokens or channels their M, so few rows waste nothing.
+//   - up to 8 rows (a group's query heads, or several steps' of them) are the products' N, tokens
+//     or channels their M, so few rows waste nothing; 9 to 16 are their M, and the scores' sums
+//     are the next products' operand as they stand.
 // tcgen05 takes its operands from shared memory, where each value would have to be written as
 // 16 bits first, four times what is read: more than the 128 bytes a clock there.  Scales per
 // (token, group) bar its 4-bit kinds, whose scales run along the other dimension for V.
@@ -40,16 +41,16 @@
 // scale of V (ref goes by it), and 30 binary orders below the largest are still in range.
 //
 // Measured, both launches, of the bytes that the cache holds for the tokens: 256 sequences of 100
-// to 8000 tokens (16 query heads, 2 kv heads, d = 256) 120 us, 5.0 TB/s; one of 131072 (32, 8,
-// 128) 41 us, 3.7 TB/s; 64 of 6001 (32, 8, 128) 92 us, 4.8 TB/s, in pages of 16 97 us; 96 of 1 to
-// 2900 (64, 8, 64) 28 us, 2.9 TB/s; 17 of 4 to 6001 with 4 steps (32, 8, 128, pages of 16) 33 us,
-// 1.8 TB/s; one of 833 9 us, latency (the lengths 0.8, first copy asked for 1.3, its rows and the
-// data 1, a stage 1.4, the share written 0.5, join 2).  Per unit of 16 tokens at d = 256: 260
-// clocks of an SM, for 530 instructions (270 of the integer pipe, which starts one every other
-// clock and scheduler: 135) and 48 products (96).  Masks, products and the fp32 arithmetic
-// between them contend for the same issue slots and registers' ports: a timing without the
-// products that take off the 8s was 6 % shorter, one without the multiplications by V's scales
-// 6 %, without V's masks 2 %, with a third more warps none.
+// to 8000 tokens (16 query heads, 2 kv heads, d = 256) 116 us, 5.2 TB/s; one of 131072 (32, 8,
+// 128) 38 us, 4.0 TB/s; 64 of 6001 (32, 8, 128) 87 us, 5.1 TB/s, in pages of 16 92 us; 96 of 1 to
+// 2900 (64, 8, 64) 28 us, 2.9 TB/s; 17 of 4 to 6001 with 4 steps (32, 8, 128, pages of 16) 31 us,
+// 1.9 TB/s; one of 833 8.5 us, latency (the lengths 0.8, first copy asked for 1.3, its rows and the
+// data 1, a stage 1.4, the share written 0.5, join 2).  Per unit of 16 tokens at d = 256: 240
+// clocks of an SM, for 515 instructions (237 of the integer pipe, which starts one every other
+// clock and scheduler: 118) and 40 products (80).  Masks, products and the fp32 arithmetic
+// between them contend for the same issue slots and registers' ports, and their times add up:
+// 12 warps with stages of half the size took 132 us for 114, the next stage's scores between a
+// stage's sums 133, stages of 3 units (registers run out) 129.
 #include <limits.h>
 #include <math.h>
 

@@ -8,8 +8,9 @@ weights by less than 2^-11 together (scores below 2^7 here, sums of 256 products
 all of it.  Codes meet the weights as 0 .. 15 and 8 times the weights are taken off, both in
 fp32: a sum passes through 8 scales (M, the largest magnitude that a group holds) times
 its weights.  A tensor-core product adds 17 terms (16 tokens' and the sum so far), each of
-which may lose what is below a step of the largest, 2^-23 of it; two products a unit make
-2 * 17 * 2^-23 < 2^-17 sum p M."""
+which may lose what is below a step of the largest, 2^-23 of it.  Units come in pairs, with S
+and T = sum p M of their own: their 8s are summed first (products at S, then S + T), then
+their codes are added (at S + T, then T), in all 3 (S + T), so 3 * 17 * 2^-23 < 2^-17 sum p M."""
 import pytest
 import torch
 
