@@ -13,7 +13,7 @@
 // values whatever one does; so everything else is kept from costing any:
 //   - the codes lie as the operands' fragments do, so a lane's words come by 16-byte loads and no
 //     lane hands anything to another;
-//   - four bits masked out of a word are an fp16 number already (see kAt0 below): no
+//   - four bits masked out of a word are an fp16 number already (see kAt3 below): no
 //     conversion, no offset to subtract, at most one shift for two masks;
 //   - the 8 by which the stored codes are too large is taken off by the tensor cores: for K as
 //     the value that the sum starts from, for V by a product with a constant (taking it off the
@@ -145,10 +145,14 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 // are that code times 2^(place - 24), exactly (a subnormal number, which the tensor cores take
 // as it is, or one of the least exponent, whose steps are the same).  The other operand or the
 // end result makes up for the power of two, and a product takes off the 8 that each code is
-// too much.  K's words lie so that two of their four pairs need no shift; V's too.
-constexpr uint32_t kAt0 = 0x000f000fu, kAt4 = 0x00f000f0u, kAt3 = 0x00780078u, kAt7 = 0x07800780u;
-// -8 at those places
-constexpr uint32_t kLess8At0 = 0x80088008u, kLess8At4 = 0x80808080u, kLess8At3 = 0x80408040u, kLess8At7 = 0x84008400u;
+// too much.  The places are the highest two there are: a product's terms are cut off below
+// 2^-25 of the largest, and for a subnormal number that goes by 2^-14, whatever it is.  At places
+// 0 and 4, which would spare V's words a shift, small sums next to a large weight lost what is
+// below 2^-14 of it.  (K's words lie so that one shift is enough.)
+constexpr uint32_t kAt3 = 0x00780078u, kAt7 = 0x07800780u;
+constexpr uint32_t kLess8At3 = 0x80408040u, kLess8At7 = 0x84008400u;   // -8 at those places
+constexpr float kUnit3 = 0x1p-21f, kUnit7 = 0x1p-17f;                   // what 1 is there
+constexpr uint32_t kOnes = 0x3c003c00u;
 
 __device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {   // bf16 pairs; a NaN gives way
   const __nv_bfloat162 m = __hmax2(__habs2(reinterpret_cast<__nv_bfloat162&>(a)), __habs2(reinterpret_cast<__nv_bfloat162&>(b)));
@@ -420,7 +424,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) attn_kv4_kernel(Kv4
         // 2^9 over the power of two in `most`, at most 2^120 (a row of nothing but tiny numbers)
         const uint32_t ex = min(263 - min((int)(__float_as_uint(most) >> 23), 254), 247);
         const uint32_t up = ex << 7 | ex << 23, up16 = (ex + 4) << 7 | (ex + 4) << 23;   // bf16 pairs
-        const float down = p.qscale * 0x1p17f * __uint_as_float((254 - ex) << 23);
+        const float down = p.qscale * (1.0f / kUnit7) * __uint_as_float((254 - ex) << 23);
         if constexpr (WIDE) {
           scale[n] = down;
         } else {
@@ -660,8 +664,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) attn_kv4_kernel(Kv4
         // outputs, over the 16 tokens of each unit: a pair of units' 8s first, a sum for all of a
         // group's channels, then their codes
         constexpr int PAIR = NU < 2 ? NU : 2;
-        const uint32_t less8[4] = {kLess8At0, kLess8At4, kLess8At0, kLess8At4};
-        const uint32_t less8n = g % 2 ? kLess8At4 : kLess8At0;
+        const uint32_t ones[4] = {kOnes, kOnes, kOnes, kOnes};
 #pragma unroll
         for (int k0 = 0; k0 < NU; k0 += PAIR) {
           uint32_t vs[PAIR][TOKS][R / 2];
@@ -691,28 +694,29 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) attn_kv4_kernel(Kv4
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
                       w[k][2 * x + i] = pack_f16x2(y[x][2 * i] * sc[2 * x], y[x][2 * i + 1] * sc[2 * x + 1]);
-                  mma(off, w[k], less8n, less8n);
+                  mma(off, w[k], kOnes, kOnes);
                 } else {
                   w[k][0] = transpose8(pack_f16x2(y[0][0] * sc[0], y[0][1] * sc[0]));
                   w[k][1] = transpose8(pack_f16x2(y[0][2] * sc[1], y[0][3] * sc[1]));
-                  mma(off, less8, w[k][0], w[k][1]);
+                  mma(off, ones, w[k][0], w[k][1]);
                 }
               }
 #pragma unroll
               for (int x = 0; x < 2 * NT; ++x)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o[r][x][e] += off[WIDE ? e / 2 * 2 + x % 2 : e];
+                for (int e = 0; e < 4; ++e)
+                  o[r][x][e] = fmaf(off[e], -8.0f * ((WIDE ? x % 2 : e / 2) ? kUnit7 : kUnit3), o[r][x][e]);
 #pragma unroll
               for (int k = 0; k < PAIR; ++k) {
-                const uint32_t x0 = w0[k][rr], y0 = w1[k][rr], x1 = x0 >> 8, y1 = y0 >> 8;
+                const uint32_t x0 = w0[k][rr] << 3, y0 = w1[k][rr] << 3, x1 = w0[k][rr] >> 5, y1 = w1[k][rr] >> 5;
                 if constexpr (WIDE) {        // rows by channels
-                  mma(o[r][0], w[k], x0 & kAt0, y0 & kAt0);
-                  mma(o[r][1], w[k], x0 & kAt4, y0 & kAt4);
-                  mma(o[r][2], w[k], x1 & kAt0, y1 & kAt0);
-                  mma(o[r][3], w[k], x1 & kAt4, y1 & kAt4);
+                  mma(o[r][0], w[k], x0 & kAt3, y0 & kAt3);
+                  mma(o[r][1], w[k], x0 & kAt7, y0 & kAt7);
+                  mma(o[r][2], w[k], x1 & kAt3, y1 & kAt3);
+                  mma(o[r][3], w[k], x1 & kAt7, y1 & kAt7);
                 } else {                     // channels by rows
-                  const uint32_t f0[4] = {x0 & kAt0, x0 & kAt4, y0 & kAt0, y0 & kAt4};
-                  const uint32_t f1[4] = {x1 & kAt0, x1 & kAt4, y1 & kAt0, y1 & kAt4};
+                  const uint32_t f0[4] = {x0 & kAt3, x0 & kAt7, y0 & kAt3, y0 & kAt7};
+                  const uint32_t f1[4] = {x1 & kAt3, x1 & kAt7, y1 & kAt3, y1 & kAt7};
                   mma(o[r][0], f0, w[k][0], w[k][1]);
                   mma(o[r][1], f1, w[k][0], w[k][1]);
                 }
@@ -749,7 +753,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) attn_kv4_kernel(Kv4
       }
       // the share's sums into its slot, as with weights that do not go by V's scales
       const float stored = __uint_as_float((uint32_t)(v - (int)kStored + 127) << 23);
-      const float at0 = 0x1p24f * stored, at4 = 0x1p20f * stored;
+      const float at3 = stored / kUnit3, at7 = stored / kUnit7;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         float l = sum[i];
@@ -764,10 +768,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) attn_kv4_kernel(Kv4
 #pragma unroll
             for (int e = 2 * i; e < 2 * i + 2; ++e)
               *reinterpret_cast<float4*>(part + 8 * t + e % 2 * 4) =
-                  make_float4(o[r][0][e] * at0, o[r][1][e] * at4, o[r][2][e] * at0, o[r][3][e] * at4);
+                  make_float4(o[r][0][e] * at3, o[r][1][e] * at7, o[r][2][e] * at3, o[r][3][e] * at7);
           } else {
             *reinterpret_cast<float4*>(part + 4 * g) =
-                make_float4(o[r][0][i] * at0, o[r][0][2 + i] * at4, o[r][1][i] * at0, o[r][1][2 + i] * at4);
+                make_float4(o[r][0][i] * at3, o[r][0][2 + i] * at7, o[r][1][i] * at3, o[r][1][2 + i] * at7);
           }
         }
       }

@@ -704,8 +704,9 @@ gdn_status gdn_kv4_load(const gdn_attn_dims* dims, int page, long long n_pages, 
  * reaches such a page are unspecified (nothing outside the cache is read).
  * Each softmax weight times its token's scale is rounded to fp16 (at a power of two that
  * keeps it in range) before it meets the codes, which moves out by at most 2^-11 sum p |v|
- * besides its own rounding; everything else is fp32, with steps of the largest magnitude M
- * in a value's group where values cancel (2^-17 sum p M).  Magnitudes of q are to be below
+ * besides its own rounding; everything else is summed in fp32, with steps of the largest
+ * magnitude M in a value's group where values cancel: at most 2^-16 sum p M of out, and of a
+ * score 2^-16 scale times the sum over its groups of max |q| M.  Magnitudes of q are to be below
  * 2^108.  Equal calls give equal bits; the order
  * of a row's sums, and with it the last bits, depends on the batch, the lengths and the
  * GPU's SM count.

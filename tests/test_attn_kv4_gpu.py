@@ -2,15 +2,19 @@
 cache stands for.
 
 Tolerance, with A = sum p |v|: a weight times its token's scale is rounded to fp16, off by
-at most 2^-11 of itself, so the sum by 2^-11 A; fp32 scores and exponentials move the
-weights by less than 2^-11 together (scores below 2^7 here, sums of 256 products at
-2^-24 each of their sizes' sum); the result is rounded once, 2^-8 |o|.  The gate multiplies
+at most 2^-11 of itself, so the sum by 2^-11 A; scores and exponentials move the
+weights by less than 2^-11 together (a group's two products lose 2^-16 scale max |q| M at most,
+as below: with |q| to 4 and M to 6 under 2^-12 of a weight for d = 256); the result is rounded once, 2^-8 |o|.  The gate multiplies
 all of it.  Codes meet the weights as 0 .. 15 and 8 times the weights are taken off, both in
 fp32: a sum passes through 8 scales (M, the largest magnitude that a group holds) times
-its weights.  A tensor-core product adds 17 terms (16 tokens' and the sum so far), each of
-which may lose what is below a step of the largest, 2^-23 of it.  Units come in pairs, with S
-and T = sum p M of their own: their 8s are summed first (products at S, then S + T), then
-their codes are added (at S + T, then T), in all 3 (S + T), so 3 * 17 * 2^-23 < 2^-17 sum p M."""
+its weights.  A tensor-core product adds 17 terms, 16 tokens' and the sum so far.  It cuts each
+off below a step, 2^-25 of the power of two of the largest; a code below 2^-14 counts as 2^-14
+there, which for the smaller of the two places that codes have is 16 p M, and a step of 2^-21 p M.
+The largest token's term ends above that step, so 16 terms lose at most 2^-17 p M in a product,
+with the largest p: over the units, 2^-17 sum p M.  Where the sum so far is the largest, steps are
+2^-24 of it: units come in pairs, with S and T = sum p M of their own, so twice 17 * 2^-24 (S + T).
+The 8s are whole numbers times the weights themselves, at S, then S + T: as much again at most.
+In all 2^-17 (1 + 0.27 + 0.27) < 2^-16 sum p M."""
 import pytest
 import torch
 
@@ -75,7 +79,7 @@ def reference(x, scale=None):
             p = torch.softmax(torch.einsum("nhd,hd->hn", kk, q[b, i]) * (scale or d ** -0.5), -1)
             out[b, i] = torch.einsum("hn,nhd->hd", p, vv)
             # (in units of the tolerance of a weight, 2^-10 with the scores' share)
-            size[b, i] = torch.einsum("hn,nhd->hd", p, vv.abs() + 2 ** -7 * most[at:at + n].repeat_interleave(G, 1))
+            size[b, i] = torch.einsum("hn,nhd->hd", p, vv.abs() + 2 ** -6 * most[at:at + n].repeat_interleave(G, 1))
         at += n_all
     if x["gate"] is not None:
         f = torch.sigmoid(x["gate"][..., d:].double())
@@ -138,6 +142,11 @@ def test_long_sequences_in_many_shares(d, hk):
     check(build(2, 1, 8 * hk, hk, d, 64, [9001, 5000], seed=3))
 
 
+@pytest.mark.parametrize("d,hk,S", [(256, 2, 2), (128, 1, 4), (64, 2, 3)])
+def test_long_sequences_with_more_than_eight_rows(d, hk, S):
+    check(build(2, S, 16 // S * hk, hk, d, 16, [6003, 2990], seed=13))
+
+
 def test_many_sequences():
     g = torch.Generator().manual_seed(0)
     check(build(300, 1, 8, 1, 128, 16, torch.randint(0, 120, (300,), generator=g).tolist(), seed=4))
@@ -155,6 +164,23 @@ def test_peaked_and_growing_scores():
     n = torch.arange(700)
     k = torch.randn(700, 1, 128, generator=torch.Generator().manual_seed(5)) * (0.02 * n[:, None, None])
     gdn.gdn_kv4_store(x["dims"], k.to(BF).to(DEV), None, x["cache"], slot=x["slot"].to(DEV))
+    check(x)
+
+
+@pytest.mark.parametrize("d,G,S", [(64, 1, 1), (128, 4, 1), (256, 2, 1), (64, 8, 2), (128, 4, 4), (256, 16, 1)])
+@pytest.mark.parametrize("ahead", [4.0, 7.0, 10.0])
+def test_small_sums_next_to_a_large_weight(d, G, S, ahead):
+    # one token takes nearly all the weight and is zero but for a large value in each group:
+    # elsewhere the outputs are the others' small sums
+    n = 48
+    x = build(1, S, G, 1, d, 16, [n], seed=d + G, std=0.5, gate=False)
+    g = torch.Generator().manual_seed(14)
+    u = torch.randn(d, generator=g)
+    x["q"] = (u + 0.02 * torch.randn(1, S, G, d, generator=g)).to(BF).to(DEV)
+    k, v = 0.05 * torch.randn(n, 1, d, generator=g), torch.randn(n, 1, d, generator=g)
+    k[5, 0], v[5] = u * (ahead * d ** 0.5 / u.square().sum()), 0
+    v[5, 0, 3::32] = 8
+    gdn.gdn_kv4_store(x["dims"], k.to(BF).to(DEV), v.to(BF).to(DEV), x["cache"], slot=x["slot"].to(DEV))
     check(x)
 
 
