@@ -14,7 +14,8 @@
 //   - the codes lie as the operands' fragments do, so a lane's words come by 16-byte loads and no
 //     lane hands anything to another;
 //   - four bits masked out of a word are an fp16 number already (see kAt3 below): no
-//     conversion, no offset to subtract, at most one shift for two masks;
+//     conversion, no offset to subtract, at most one shift for two masks (those to the left
+//     go to the fp32 pipe; those to the right cost 4 % more there, as products' upper halves);
 //   - the 8 by which the stored codes are too large is taken off by the tensor cores: for K as
 //     the value that the sum starts from, for V by a product with a constant (taking it off the
 //     values was eight instructions for every one of those);
@@ -42,11 +43,11 @@
 //
 // Measured, both launches, of the bytes that the cache holds for the tokens: 256 sequences of 100
 // to 8000 tokens (16 query heads, 2 kv heads, d = 256) 116 us, 5.2 TB/s; one of 131072 (32, 8,
-// 128) 38 us, 4.0 TB/s; 64 of 6001 (32, 8, 128) 87 us, 5.1 TB/s, in pages of 16 92 us; 96 of 1 to
+// 128) 38 us, 4.0 TB/s; 64 of 6001 (32, 8, 128) 88 us, 5.0 TB/s, in pages of 16 93 us; 96 of 1 to
 // 2900 (64, 8, 64) 28 us, 2.9 TB/s; 17 of 4 to 6001 with 4 steps (32, 8, 128, pages of 16) 31 us,
 // 1.9 TB/s; one of 833 8.5 us, latency (the lengths 0.8, first copy asked for 1.3, its rows and the
 // data 1, a stage 1.4, the share written 0.5, join 2).  Per unit of 16 tokens at d = 256: 240
-// clocks of an SM, for 515 instructions (237 of the integer pipe, which starts one every other
+// clocks of an SM, for 525 instructions (237 of the integer pipe, which starts one every other
 // clock and scheduler: 118) and 40 products (80).  Masks, products and the fp32 arithmetic
 // between them contend for the same issue slots and registers' ports, and their times add up:
 // 12 warps with stages of half the size took 132 us for 114, the next stage's scores between a
