@@ -87,6 +87,32 @@ def test_rows_go_in_and_come_out(d, h, page, T, kind):
     check(dims, special(T, h, d, 1), special(T, h, d, 2), slots(kind, T, pages * page, 3), page, pages, seed=d + T)
 
 
+def test_every_ratio_to_the_extreme():
+    # all significands of the extreme by all of a smaller number, 0 to 8 exponents below it, of
+    # both signs: ties and what lies next to them, at exponents all over the range
+    m = torch.arange(128, 256, dtype=torch.float64)
+    x = (m[:, None] * 2.0 ** -torch.arange(9.0)).flatten()
+    x = torch.cat([x, -x])                                              # [2304], 31 to a group
+    x = torch.cat([x, torch.zeros(-len(x) % 31)]).view(1, -1, 31)
+    big = m[:, None, None].expand(-1, x.shape[1], 1)
+    x = x.expand(128, -1, -1).clamp(-big, big)                          # no larger than the extreme
+    g = torch.Generator().manual_seed(7)
+    by = 2.0 ** torch.randint(-80, 120, (*x.shape[:2], 1), generator=g)
+    for sign in (1, -1):
+        groups = (torch.cat([sign * big, x], -1) * by).view(-1, 32)
+        groups = torch.cat([groups, torch.zeros(-len(groups) % 2, 32)])
+        k = groups.view(-1, 1, 64).to(BF)
+        assert torch.equal(k.double().view(-1, 32), groups)
+        dims = gdn.make_attn_dims(h_q=1, h_kv=1, d=64, rot=0)
+        T = len(k)
+        cache = torch.zeros(-(-T // 256), 1, 16, 18 * 64, dtype=torch.uint8, device=DEV)
+        gdn.gdn_kv4_store(dims, k.to(DEV), k.to(DEV), cache)
+        ko, vo = (torch.empty(T, 1, 64, dtype=torch.float32, device=DEV) for _ in range(2))
+        gdn.gdn_kv4_load(dims, cache, ko, vo)
+        want = kv4.quantise(k)[2]
+        assert torch.equal(ko.cpu().double(), want) and torch.equal(vo.cpu().double(), want)
+
+
 def test_runs_broken_in_the_middle_and_pages_out_of_order():
     dims = gdn.make_attn_dims(h_q=2, h_kv=2, d=128, rot=0)
     T, page = 100, 16
