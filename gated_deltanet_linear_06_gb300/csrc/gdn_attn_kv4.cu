@@ -621,9 +621,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) attn_kv4_kernel(Kv4
             if (!first) m = fmaxf(m, kTop - (float)v);
             const float to = ref[i] + (m - (kTop - (float)v1)), by = ref[i] - to;
             if (by != 0.0f && m != -INFINITY) {
-              const float f = first ? 1.0f : ex2(by);
+              // (two factors: a step of V's scale alone can make `by` -219, past fp32's least power)
+              const float f = first ? 1.0f : ex2(0.5f * by);
               ref[i] = to;
-              sum[i] *= f;
+              sum[i] = sum[i] * f * f;
 #pragma unroll
               for (int e = 0; e < 4; ++e)
                 if (row_of(e) == i) {
@@ -634,7 +635,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) attn_kv4_kernel(Kv4
 #pragma unroll
                   for (int r = 0; r < R; ++r)
 #pragma unroll
-                    for (int x = 0; x < 2 * NT; ++x) o[r][x][e] *= f;
+                    for (int x = 0; x < 2 * NT; ++x) o[r][x][e] = o[r][x][e] * f * f;
                 }
             }
             if (m != -INFINITY) fresh &= ~(1u << i);
