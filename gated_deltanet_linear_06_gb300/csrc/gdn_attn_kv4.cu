@@ -37,12 +37,18 @@
 // Shares follow from the lengths alone, so equal calls add in equal order, and they are found
 // on the device, so a captured call stays valid while the lengths grow.
 //
-// Softmax.  ref moves only when a score passes it by kGrow binary orders or a scale of V by
-// kWide; else a stage costs a vote.  Weights times scales stay below 2^15, fp16's range, at any
-// scale of V (ref goes by it), and 30 binary orders below the largest are still in range.
-//
+// Softmax.  ref moves only when a score passes it by kGrow binary orders; else a stage costs a
+// vote.  Weights times scales of V have to fit fp16, so weights carry a factor 2^-v that suits the
+// scales, those of all groups and tokens of a stage alike, whoever sees them: that they lie near 2^v
+// (13 binary orders, see kNarrow) is looked at in every stage, an add and a maximum for four
+// values of 32.  Where they do not, what is summed goes to the share's slot in memory, in fp32 and
+// free of v, v moves, and scales that still do not fit go by themselves, those near each other at
+// a time: so no scale, seen or not, takes another's bits.  64 sequences of 6001 (32, 8, 128,
+// caches cold) take 98 us; 107 with half of the groups zeros, 100 with every first token's scales
+// 2^-14 of the others', 182 with those of one token in a hundred, 246 with half of the groups'.
+
 // Measured, both launches, of the bytes that the cache holds for the tokens: 256 sequences of 100
-// to 8000 tokens (16 query heads, 2 kv heads, d = 256) 116 us, 5.2 TB/s; one of 131072 (32, 8,
+// to 8000 tokens (16 query heads, 2 kv heads, d = 256) 118 us, 5.1 TB/s; one of 131072 (32, 8,
 // 128) 38 us, 4.0 TB/s; 64 of 6001 (32, 8, 128) 88 us, 5.0 TB/s, in pages of 16 93 us; 96 of 1 to
 // 2900 (64, 8, 64) 28 us, 2.9 TB/s; 17 of 4 to 6001 with 4 steps (32, 8, 128, pages of 16) 31 us,
 // 1.9 TB/s; one of 833 8.5 us, latency (the lengths 0.8, first copy asked for 1.3, its rows and the
@@ -65,14 +71,17 @@ namespace gdn {
 namespace {
 
 constexpr long long kWaitClocks = 2000000000LL;   // a second or so: a copy that has not come by then never will
-// A row's weights are 2^(score - ref); at an update of ref the largest is 2^(kTop - v), with
-// 2^v above the size of every scale of V so far.  Scores may grow by kGrow binary orders and
-// scales by kWide before the next update: a weight times a scale stays below 2^15, in fp16.
+// A row's weights are 2^(score - ref); where ref moves the largest comes to lie above 2^(kTop - 1 - v)
+// and at most at 2^(kTop - v).  Scores may then grow by kGrow binary orders, and V's scales lie from
+// 2^(v - kNarrow) to 2^(v + kWide): a weight times a scale stays below 2^15, in fp16, and what
+// fp16's subnormal numbers round off, 2^-25 at most next to 2^(kTop - 1 - kNarrow), is 2^-22 of the
+// row's largest weight times the least scale there is.  ref moves by whole numbers, so that
+// every factor is a power of two.
 constexpr float kTop = 8.0f, kGrow = 4.0f;
-constexpr int kWide = 3;
+constexpr int kWide = 3, kNarrow = 10;
 constexpr int kLeastV = -93;                       // scales are zero or at least 2^-93
-constexpr int kTinyWeights = 60;                   // with a larger v, weights that count may be subnormal
-constexpr float kStored = 28.0f;                   // shares are stored with weights up to 2^(kTop - kStored)
+constexpr int kMostV = 60;                         // with a larger v, weights that count would be subnormal
+constexpr int kStored = 28;                        // sums are held with weights of 2^(kTop + kGrow - kStored) at the most
 constexpr int kMaxCtas = 160;                      // the workspace has room for
 constexpr int kMaxWarps = 16;
 
@@ -106,19 +115,16 @@ struct Cfg {
   static constexpr int WARPS = D == 64 && NT == 1 ? 12 : 8;   // (registers for 8 or 12; 10 left one scheduler with more)
   static constexpr int UNIT = kv4::unit_bytes(D), STAGE = UNITS * UNIT;
   static constexpr int STAGES = D == 256 && NT == 2 ? 3 : 2;
-  static constexpr int QBYTES = QREG ? 0 : NT * R * 512, BBYTES = BREG ? 0 : R * 64;   // a warp's
-  static constexpr int SMEM = WARPS * (STAGES * STAGE + QBYTES + BBYTES);
+  static constexpr int WORDS = UNITS * R / 4;        // a lane's share of the words of a stage's scales of V,
+  static constexpr int RUN = WORDS < R / 2 ? WORDS : R / 2;   // so many of a token's in a row
+  static constexpr int QBYTES = QREG ? 0 : NT * R * 512, BBYTES = BREG ? 0 : R * 64, SBYTES = WORDS * 128;   // a warp's
+  static constexpr int SMEM = WARPS * (STAGES * STAGE + QBYTES + BBYTES + SBYTES);
   static_assert(SMEM <= 216 * 1024 && UNITS * STAGES <= 32, "shared memory, bits of `bad`");
 };
 
 __device__ __forceinline__ float ex2(float x) {   // results below 2^-126: zero
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float ex2_small(float x) {   // subnormal results too
-  float y;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
@@ -152,13 +158,14 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 // below 2^-14 of it.  (K's words lie so that one shift is enough.)
 constexpr uint32_t kAt3 = 0x00780078u, kAt7 = 0x07800780u;
 constexpr uint32_t kLess8At3 = 0x80408040u, kLess8At7 = 0x84008400u;   // -8 at those places
-constexpr float kUnit3 = 0x1p-21f, kUnit7 = 0x1p-17f;                   // what 1 is there
+constexpr int kUnit3 = -21, kUnit7 = -17;                               // what 1 is there, a power of two
 constexpr uint32_t kOnes = 0x3c003c00u;
 
-__device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {   // bf16 pairs; a NaN gives way
-  const __nv_bfloat162 m = __hmax2(__habs2(reinterpret_cast<__nv_bfloat162&>(a)), __habs2(reinterpret_cast<__nv_bfloat162&>(b)));
-  return reinterpret_cast<const uint32_t&>(m);
-}
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }   // (-126 .. 127)
+// 2^e as the bits of a bf16 number, of an exponent above -127.
+__device__ __forceinline__ uint32_t bf16_pow2(int e) { return (uint32_t)(e + 127) << 7; }
+// The least e with a bf16 magnitude of these bits below 2^e.
+__device__ __forceinline__ int above(uint32_t m) { return (int)(m >> 7) - 126; }
 
 // A bf16 pair times a power of two (exact) as fp16.
 __device__ __forceinline__ uint32_t half_pair(uint32_t x, uint32_t up) {
@@ -275,6 +282,330 @@ __device__ __forceinline__ void next_job(const Kv4Params& p, const long long* be
   } while (it.n < 0 && it.b < p.a.batch);
 }
 
+// Which of a lane's two rows element e of its products is, and which token of a unit (of half x).
+template <int NT>
+__device__ __forceinline__ constexpr int row_of(int e) { return NT == 2 ? e / 2 : e % 2; }
+template <int NT>
+__device__ __forceinline__ int token_of(int lane, int x, int e) {
+  return NT == 2 ? 8 * x + 2 * (lane % 4) + e % 2 : lane / 4 + e / 2 * 8;
+}
+template <int NT>
+constexpr int kTokens = NT == 2 ? 4 : 2;   // of a unit that a lane has
+// The scales of a lane's i-th token of unit k of a stage, K's.
+template <int D, int NT>
+__device__ __forceinline__ uint8_t* scales_of(uint8_t* st, int lane, int k, int i) {
+  return st + k * Cfg<D, NT>::UNIT + 16 * D + (NT == 2 ? 2 * (lane % 4) + i % 2 + i / 2 * 8 : lane / 4 + 8 * i) * (D / 8);
+}
+// A lane's i-th run of words of a stage's scales of V, RUN words of a token's groups.
+template <int D, int NT>
+__device__ __forceinline__ uint32_t* v_scales(uint8_t* st, int lane, int i) {
+  using C = Cfg<D, NT>;
+  constexpr int RUNS = C::R / 2 / C::RUN;    // of a token
+  const int x = lane + 32 * i, token = x / RUNS;
+  return reinterpret_cast<uint32_t*>(st + token / kv4::kUnit * C::UNIT + 16 * D + token % kv4::kUnit * (D / 8) + D / 16 +
+                                     x % RUNS * (C::RUN * 4));
+}
+
+// What a warp has summed of a job.
+template <int D, int NT>
+struct Sums {
+  float o[D / 32][2 * NT][4];   // weights times values, in the codes' units
+  float ref[2], sum[2];         // of weights times 2^(v - kStored): whatever v is
+  int v;
+  uint32_t fresh;               // this lane's rows that have not seen a score
+  bool stands;                  // a part of the outputs' sums is in the share's slot
+};
+
+// The power of two that a stage's scales of V are to be taken relative to, given what it was: the
+// largest is below it, unless they all lie near 2^v as it is.  apart: some are too small for that,
+// or all too large for any; top: above the largest.
+template <int D, int NT>
+__device__ __forceinline__ int range_of(uint8_t* st, int lane, int v, bool& apart, int& top) {
+  using C = Cfg<D, NT>;
+  uint32_t most = 0, least = 0x7f80u;        // of those that are finite
+#pragma unroll 1
+  for (int i = 0; i < C::WORDS; ++i) {
+    const uint32_t w = v_scales<D, NT>(st, lane, i / C::RUN)[i % C::RUN];
+#pragma unroll
+    for (int h = 0; h < 32; h += 16) {
+      const uint32_t m = w >> h & 0x7fffu;
+      if (m < 0x7f80u && m >= bf16_pow2(kLeastV - kNarrow)) most = max(most, m), least = min(least, m);
+    }
+  }
+  most = __reduce_max_sync(0xffffffffu, most);
+  least = __reduce_min_sync(0xffffffffu, least);
+  apart = false;
+  if (most == 0) return v;
+  top = above(most);
+  if (most >= bf16_pow2(v + kWide) || least < bf16_pow2(v - kNarrow)) v = min(max(top, kLeastV), kMostV);
+  apart = least < bf16_pow2(v - kNarrow) || top > v + kWide;
+  return v;
+}
+
+// Moves the rows' references, to the largest of the scores s and to scales relative to 2^v1.
+template <int D, int NT>
+__device__ __forceinline__ void move_refs(Sums<D, NT>& m, float (&s)[Cfg<D, NT>::UNITS][NT][4], int v1) {
+  constexpr int NU = Cfg<D, NT>::UNITS;
+  constexpr int LANES_0 = NT == 2 ? 1 : 4, LANES_1 = NT == 2 ? 2 : 16;   // lane bits that tell tokens, not rows, apart
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    float most = -INFINITY;                  // largest score, less ref
+#pragma unroll
+    for (int k = 0; k < NU; ++k)
+#pragma unroll
+      for (int x = 0; x < NT; ++x)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (row_of<NT>(e) == i) most = fmaxf(most, s[k][x][e]);
+#pragma unroll
+    for (int k = LANES_0; k <= LANES_1; k <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, k));
+    const bool first = m.fresh >> i & 1;
+    if (first && most == -INFINITY) continue;
+    float up = ceilf(most - (kTop - (float)m.v));   // by which it is too large
+    if (!first) up = fmaxf(up, 0.0f);
+    m.fresh &= ~(1u << i);
+    const float by = up + (float)(v1 - m.v);
+    m.ref[i] += by;
+#pragma unroll
+    for (int k = 0; k < NU; ++k)
+#pragma unroll
+      for (int x = 0; x < NT; ++x)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (row_of<NT>(e) == i) s[k][x][e] -= by;
+    if (!first && up != 0.0f) {
+      const float f = up < 127.0f ? pow2(-(int)up) : 0.0f;
+      m.sum[i] *= f;
+#pragma unroll
+      for (int r = 0; r < D / 32; ++r)
+#pragma unroll
+        for (int x = 0; x < 2 * NT; ++x)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (row_of<NT>(e) == i) m.o[r][x][e] *= f;
+    }
+  }
+  m.v = v1;
+}
+
+// Weights s of a stage to the sums.
+template <int D, int NT>
+__device__ __forceinline__ void add_weights(Sums<D, NT>& m, const float (&s)[Cfg<D, NT>::UNITS][NT][4]) {
+  float here[2] = {0.0f, 0.0f};
+#pragma unroll
+  for (int k = 0; k < Cfg<D, NT>::UNITS; ++k)
+#pragma unroll
+    for (int x = 0; x < NT; ++x)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) here[row_of<NT>(e)] += s[k][x][e];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) m.sum[i] = fmaf(here[i], pow2(m.v - kStored), m.sum[i]);
+}
+
+// Weights s times a stage's values to the outputs, over the 16 tokens of each unit: a pair of
+// units' 8s first, a sum for all of a group's channels, then their codes.
+template <int D, int NT>
+__device__ __forceinline__ void add_values(Sums<D, NT>& m, const float (&s)[Cfg<D, NT>::UNITS][NT][4], uint8_t* st, int lane) {
+  constexpr int NU = Cfg<D, NT>::UNITS, R = D / 32, SET = kSet<D>, TOKS = kTokens<NT>;
+  constexpr bool WIDE = NT == 2;
+  constexpr int PAIR = NU < 2 ? NU : 2;
+  const uint32_t ones[4] = {kOnes, kOnes, kOnes, kOnes};
+#pragma unroll
+  for (int k0 = 0; k0 < NU; k0 += PAIR) {
+    uint32_t vs[PAIR][TOKS][R / 2];
+#pragma unroll
+    for (int k = 0; k < PAIR; ++k)
+#pragma unroll
+      for (int i = 0; i < TOKS; ++i) words_at<R / 2>(vs[k][i], scales_of<D, NT>(st, lane, k0 + k, i) + D / 16);
+#pragma unroll
+    for (int set = 0; set < R / SET; ++set) {
+      uint32_t w0[PAIR][SET], w1[PAIR][SET];
+#pragma unroll
+      for (int k = 0; k < PAIR; ++k) codes_at<D>(w0[k], w1[k], st + (k0 + k) * Cfg<D, NT>::UNIT + 8 * D, lane, set);
+#pragma unroll
+      for (int rr = 0; rr < SET; ++rr) {
+        const int r = set * SET + rr;
+        uint32_t w[PAIR][2 * NT];      // weights times scales, as an operand
+        float off[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int k = 0; k < PAIR; ++k) {
+          float sc[TOKS];
+#pragma unroll
+          for (int i = 0; i < TOKS; ++i) sc[i] = r % 2 ? hi_f32(vs[k][i][r / 2]) : lo_f32(vs[k][i][r / 2]);
+          const auto& y = s[k0 + k];
+          if constexpr (WIDE) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                w[k][2 * x + i] = pack_f16x2(y[x][2 * i] * sc[2 * x], y[x][2 * i + 1] * sc[2 * x + 1]);
+            mma(off, w[k], kOnes, kOnes);
+          } else {
+            w[k][0] = transpose8(pack_f16x2(y[0][0] * sc[0], y[0][1] * sc[0]));
+            w[k][1] = transpose8(pack_f16x2(y[0][2] * sc[1], y[0][3] * sc[1]));
+            mma(off, ones, w[k][0], w[k][1]);
+          }
+        }
+#pragma unroll
+        for (int x = 0; x < 2 * NT; ++x)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            m.o[r][x][e] = fmaf(off[e], -8.0f * pow2((WIDE ? x % 2 : e / 2) ? kUnit7 : kUnit3), m.o[r][x][e]);
+#pragma unroll
+        for (int k = 0; k < PAIR; ++k) {
+          const uint32_t x0 = w0[k][rr] << 3, y0 = w1[k][rr] << 3, x1 = w0[k][rr] >> 5, y1 = w1[k][rr] >> 5;
+          if constexpr (WIDE) {        // rows by channels
+            mma(m.o[r][0], w[k], x0 & kAt3, y0 & kAt3);
+            mma(m.o[r][1], w[k], x0 & kAt7, y0 & kAt7);
+            mma(m.o[r][2], w[k], x1 & kAt3, y1 & kAt3);
+            mma(m.o[r][3], w[k], x1 & kAt7, y1 & kAt7);
+          } else {                     // channels by rows
+            const uint32_t f0[4] = {x0 & kAt3, x0 & kAt7, y0 & kAt3, y0 & kAt7};
+            const uint32_t f1[4] = {x1 & kAt3, x1 & kAt7, y1 & kAt3, y1 & kAt7};
+            mma(m.o[r][0], f0, w[k][0], w[k][1]);
+            mma(m.o[r][1], f1, w[k][0], w[k][1]);
+          }
+        }
+      }
+    }
+  }
+}
+
+// The outputs' sums, with weights that carry 2^-vo, to the share's slot, on top of what stands
+// there; the weights' too.
+template <int D, int NT>
+__device__ __forceinline__ void put_sums(const Sums<D, NT>& m, int vo, float* part, float2* ml, int lane) {
+  constexpr bool WIDE = NT == 2;
+  constexpr int LANES_0 = WIDE ? 1 : 4, LANES_1 = WIDE ? 2 : 16;
+  const int g = lane / 4, t = lane % 4;
+  const float at3 = pow2(vo - kStored - kUnit3), at7 = pow2(vo - kStored - kUnit7);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    float l = m.sum[i];
+#pragma unroll
+    for (int k = LANES_0; k <= LANES_1; k <<= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
+    const int row = WIDE ? 8 * i + g : 2 * t + i;
+    const float to = m.ref[i] - (float)(m.v - kStored);
+    float keep = 0.0f;                       // (references never move down)
+    if (m.stands) keep = pow2(max((int)fminf(ml[row].x - to, 0.0f), -127));
+    __syncwarp();
+    if ((WIDE ? t : g) == 0) ml[row] = make_float2(to, l);
+#pragma unroll
+    for (int r = 0; r < D / 32; ++r)
+#pragma unroll
+      for (int e = i; e < (WIDE ? i + 2 : i + 1); ++e) {
+        const int c = WIDE ? i + e : i;      // element of a row's channels 8 t + 4 (e - i) + 0 .. 3 or 4 g + 0 .. 3
+        float4* const at = reinterpret_cast<float4*>(part + row * D + 32 * r + (WIDE ? 8 * t + 4 * (e - i) : 4 * g));
+        float4 x;
+        if constexpr (WIDE) x = make_float4(m.o[r][0][c] * at3, m.o[r][1][c] * at7, m.o[r][2][c] * at3, m.o[r][3][c] * at7);
+        else x = make_float4(m.o[r][0][c] * at3, m.o[r][0][2 + c] * at7, m.o[r][1][c] * at3, m.o[r][1][2 + c] * at7);
+        if (m.stands) {
+          const float4 y = *at;
+          x = make_float4(fmaf(y.x, keep, x.x), fmaf(y.y, keep, x.y), fmaf(y.z, keep, x.z), fmaf(y.w, keep, x.w));
+        }
+        *at = x;
+      }
+  }
+  __syncwarp();
+}
+
+// Of a stage whose scales of V do not fit next to each other: leaves those in [lo, hi) (bits of
+// magnitudes), times 2^up, and those that are not finite, the others zeros; what the stage held
+// stands aside from the first time (save).  Returns the largest below lo.
+template <int D, int NT>
+__device__ __forceinline__ uint32_t leave(uint8_t* st, uint32_t* aside, int lane, uint32_t lo, uint32_t hi, int up, bool save) {
+  using C = Cfg<D, NT>;
+  uint32_t below = 0;
+  __syncwarp();
+#pragma unroll 1
+  for (int i = 0; i < C::WORDS; ++i) {
+    uint32_t* const at = v_scales<D, NT>(st, lane, i / C::RUN) + i % C::RUN;
+    if (save) aside[32 * i + lane] = *at;
+    const uint32_t w = aside[32 * i + lane];
+    uint32_t x = 0;
+#pragma unroll
+    for (int h = 0; h < 32; h += 16) {
+      const uint32_t b = w >> h & 0xffffu, m = b & 0x7fffu;
+      if (m >= 0x7f80u) x |= b << h;
+      else if (m >= lo && m < hi) x |= (b + ((uint32_t)up << 7)) << h;
+      else if (m < lo && m >= bf16_pow2(kLeastV - kNarrow)) below = max(below, m);
+    }
+    *at = x;
+  }
+  __syncwarp();
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // before the stage's next copy
+  return __reduce_max_sync(0xffffffffu, below);
+}
+
+// Weights s times what stands of a stage's values, relative to 2^top, to the share's slot.
+template <int D, int NT>
+__device__ __forceinline__ void add_to_slot(const float (&s)[Cfg<D, NT>::UNITS][NT][4], uint8_t* st, int top, float* part,
+                                            int lane) {
+  constexpr int R = D / 32, TOKS = kTokens<NT>;
+  constexpr bool WIDE = NT == 2;
+  const int g = lane / 4, t = lane % 4;
+  const float at3 = pow2(top - kStored - kUnit3), at7 = pow2(top - kStored - kUnit7);
+  const uint32_t ones[4] = {kOnes, kOnes, kOnes, kOnes};
+#pragma unroll 1
+  for (int r = 0; r < R; ++r) {
+    float o[2 * NT][4], off[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int x = 0; x < 2 * NT; ++x)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[x][e] = 0.0f;
+#pragma unroll
+    for (int k = 0; k < Cfg<D, NT>::UNITS; ++k) {
+      const uint8_t* const codes = st + k * Cfg<D, NT>::UNIT + 8 * D + 16 * lane;
+      const uint32_t w0 = *reinterpret_cast<const uint32_t*>(codes + 512 * (r / 4) + r % 4 * 4);
+      const uint32_t w1 = *reinterpret_cast<const uint32_t*>(codes + 512 * ((R + r) / 4) + (R + r) % 4 * 4);
+      const uint32_t x0 = w0 << 3, y0 = w1 << 3, x1 = w0 >> 5, y1 = w1 >> 5;
+      float sc[TOKS];
+#pragma unroll
+      for (int i = 0; i < TOKS; ++i)
+        sc[i] = __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(scales_of<D, NT>(st, lane, k, i) + D / 16)[r] << 16);
+      const auto& y = s[k];
+      if constexpr (WIDE) {
+        uint32_t w[4];
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            w[2 * x + i] = pack_f16x2(y[x][2 * i] * sc[2 * x], y[x][2 * i + 1] * sc[2 * x + 1]);
+        mma(off, w, kOnes, kOnes);
+        mma(o[0], w, x0 & kAt3, y0 & kAt3);
+        mma(o[1], w, x0 & kAt7, y0 & kAt7);
+        mma(o[2], w, x1 & kAt3, y1 & kAt3);
+        mma(o[3], w, x1 & kAt7, y1 & kAt7);
+      } else {
+        const uint32_t b0 = transpose8(pack_f16x2(y[0][0] * sc[0], y[0][1] * sc[0]));
+        const uint32_t b1 = transpose8(pack_f16x2(y[0][2] * sc[1], y[0][3] * sc[1]));
+        const uint32_t f0[4] = {x0 & kAt3, x0 & kAt7, y0 & kAt3, y0 & kAt7}, f1[4] = {x1 & kAt3, x1 & kAt7, y1 & kAt3, y1 & kAt7};
+        mma(off, ones, b0, b1);
+        mma(o[0], f0, b0, b1);
+        mma(o[1], f1, b0, b1);
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < 2 * NT; ++x)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const bool hi = WIDE ? x % 2 : e / 2;
+        o[x][e] = fmaf(off[e], -8.0f * pow2(hi ? kUnit7 : kUnit3), o[x][e]) * (hi ? at7 : at3);
+      }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int k = 0; k < NT; ++k) {         // four channels of this lane's row i, of each half
+        const int row = WIDE ? 8 * i + g : 2 * t + i, c = WIDE ? 2 * i + k : i;
+        float4* const at = reinterpret_cast<float4*>(part + row * D + 32 * r + (WIDE ? 8 * t + 4 * k : 4 * g));
+        float4 y = *at;
+        if constexpr (WIDE) y.x += o[0][c], y.y += o[1][c], y.z += o[2][c], y.w += o[3][c];
+        else y.x += o[0][c], y.y += o[0][2 + c], y.z += o[1][c], y.w += o[1][2 + c];
+        *at = y;
+      }
+  }
+}
+
 template <int D, int NT>
 __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) attn_kv4_kernel(Kv4Params p) {
   using C = Cfg<D, NT>;
@@ -286,16 +617,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) attn_kv4_kernel(Kv4
   // want them, and the 8s of all of a group's channels take one product instead of two for
   // every 8 rows.
   constexpr bool WIDE = NT == 2;
-  constexpr int LANES_0 = WIDE ? 1 : 4, LANES_1 = WIDE ? 2 : 16;   // lane bits that tell tokens, not rows, apart
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ long long before[GDN_ATTN_MAX_BATCH + 1];
   __shared__ long long warp_sums[kMaxWarps];
   __shared__ uint64_t full[C::WARPS * C::STAGES];
   const AttnKv4Args& a = p.a;
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g = lane / 4, t = lane % 4;
-
-  const auto row_of = [](int e) { return WIDE ? e / 2 : e % 2; };
-  const auto token_of = [&](int x, int e) { return WIDE ? 8 * x + 2 * t + e % 2 : g + e / 2 * 8; };
 
   asm volatile("griddepcontrol.wait;" ::: "memory");
   uint64_t* bar = full + warp * C::STAGES;
@@ -402,8 +729,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) attn_kv4_kernel(Kv4
       // add to this lane's two rows, taken off.
       uint4 q[QREG ? NT : 1][QREG ? R : 1];
       float2 base[BREG ? R : 1];
-      uint8_t* const qs = ring + C::WARPS * C::STAGES * C::STAGE + warp * (C::QBYTES + C::BBYTES);
+      uint8_t* const qs = ring + C::WARPS * C::STAGES * C::STAGE + warp * (C::QBYTES + C::BBYTES + C::SBYTES);
       float2* const bs = reinterpret_cast<float2*>(qs + C::QBYTES) + (WIDE ? g : t);
+      uint32_t* const aside = reinterpret_cast<uint32_t*>(qs + C::QBYTES + C::BBYTES);
       float scale[2];                        // of this lane's rows' scores
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
@@ -425,7 +753,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) attn_kv4_kernel(Kv4
         // 2^9 over the power of two in `most`, at most 2^120 (a row of nothing but tiny numbers)
         const uint32_t ex = min(263 - min((int)(__float_as_uint(most) >> 23), 254), 247);
         const uint32_t up = ex << 7 | ex << 23, up16 = (ex + 4) << 7 | (ex + 4) << 23;   // bf16 pairs
-        const float down = p.qscale * (1.0f / kUnit7) * __uint_as_float((254 - ex) << 23);
+        const float down = p.qscale * pow2(-kUnit7) * __uint_as_float((254 - ex) << 23);
         if constexpr (WIDE) {
           scale[n] = down;
         } else {
@@ -470,16 +798,20 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) attn_kv4_kernel(Kv4
       for (int i = 0; i < 2; ++i)
         last[i] = len - a.steps + min((row0 + (WIDE ? 8 * i + g : 2 * t + i)) / p.pl.G, a.steps - 1);
       const int all_see = len - a.steps;     // tokens up to this one are every row's
-      float o[R][2 * NT][4], ref[2] = {0.0f, 0.0f}, sum[2] = {0.0f, 0.0f};
-      int v = kLeastV;                       // 2^v: above every scale of V at the last update
-      uint32_t fresh = 3;                    // this lane's rows that have not seen a score
-      uint32_t poison = 0;                   // their groups that are NaN, eight bits a row
+      Sums<D, NT> m;
+      m.v = kLeastV;
+      m.fresh = 3;
+      m.stands = false;
+      m.ref[0] = m.ref[1] = m.sum[0] = m.sum[1] = 0.0f;
+      uint32_t poison = 0;                   // this lane's rows' groups that are NaN, eight bits a row
 #pragma unroll
       for (int r = 0; r < R; ++r)
 #pragma unroll
         for (int x = 0; x < 2 * NT; ++x)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o[r][x][e] = 0.0f;
+          for (int e = 0; e < 4; ++e) m.o[r][x][e] = 0.0f;
+      float* const part = p.part + slot * (8 * NT) * D;
+      float2* const ml = p.ml + slot * (8 * NT);
 
       // Where not every row sees all of a stage's tokens: in tokens of no row (past the
       // sequence, of a page that is not there) V's scales become zeros,
@@ -509,20 +841,16 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) attn_kv4_kernel(Kv4
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // before the stage's next copy
       };
 
-      // A stage of units from u on.
-      const auto meet = [&](int u, const uint8_t* st, uint32_t gone, bool edge) {
+      // A stage of units from u on; none: the first, the sums are zero.
+      const auto meet = [&](int u, uint8_t* st, uint32_t gone, bool edge, bool none) {
         constexpr int NU = C::UNITS;
-        constexpr int SET = kSet<D>, TOKS = WIDE ? 4 : 2;   // tokens of a unit that a lane has
-        // the scales of this lane's i-th token of a unit, K's
-        const auto scales = [&](int k, int i) {
-          return st + k * C::UNIT + 16 * D + (WIDE ? 2 * t + i % 2 + i / 2 * 8 : g + 8 * i) * (D / 8);
-        };
-        float s[NU][NT][4];                  // scores: token_of(x, e) of each unit, row row_of(e)
+        constexpr int SET = kSet<D>, TOKS = kTokens<NT>;
+        float s[NU][NT][4];                  // scores: token_of(x, e) of each unit, row row_of<NT>(e)
 #pragma unroll
         for (int k = 0; k < NU; ++k) {
           uint32_t ks[TOKS][R / 2];          // two groups a word
 #pragma unroll
-          for (int i = 0; i < TOKS; ++i) words_at<R / 2>(ks[i], scales(k, i));
+          for (int i = 0; i < TOKS; ++i) words_at<R / 2>(ks[i], scales_of<D, NT>(st, lane, k, i));
 #pragma unroll
           for (int x = 0; x < NT; ++x)
 #pragma unroll
@@ -563,25 +891,28 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) attn_kv4_kernel(Kv4
             }
           }
         }
-        // the widest scale of V: a lane looks at one word of each of two tokens
-        uint32_t widest = 0;
+        // V's scales: twice their magnitudes' bits (a word's first sign falls into its second's last
+        // place, which does not count here) less those of 2^(v - kNarrow), the smaller ones wrapped
+        // around to above all
+        uint32_t far = 0;
+        const uint32_t from = ((0u - 2 * bf16_pow2(m.v - kNarrow)) & 0xffffu) * 0x10001u;
 #pragma unroll
-        for (int k = 0; k < NU; ++k)
+        for (int i = 0; i < C::WORDS / C::RUN; ++i) {
+          uint32_t w[C::RUN];
+          words_at<C::RUN>(w, reinterpret_cast<uint8_t*>(v_scales<D, NT>(st, lane, i)));
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t w = *reinterpret_cast<const uint32_t*>(st + k * C::UNIT + 16 * D + (g + 8 * h) * (D / 8) + D / 16 +
-                                                            t % (R / 2) * 4);
-            widest = max_abs2(widest, w);
-          }
-        const float wide = fmaxf(fmaxf(lo_f32(widest), hi_f32(widest)), 0.0f);   // (0 for NaN)
-        bool over = fresh != 0 || (__float_as_int(wide) >> 23) >= v + kWide + 127;
-        const float room = kTop + kGrow - (float)v;
+          for (int k = 0; k < C::RUN; ++k) far = __viaddmax_u16x2(w[k] + w[k], from, far);
+        }
+        far = max(far & 0xffffu, far >> 16);
+        const bool odd = far >= 2 * 128 * (kWide + kNarrow);   // (or zero)
+        bool over = m.fresh != 0;
+        const float room = kTop + kGrow - (float)m.v;
 #pragma unroll
         for (int k = 0; k < NU; ++k)
 #pragma unroll
           for (int x = 0; x < NT; ++x)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[k][x][e] = fmaf(s[k][x][e], scale[row_of(e)], -ref[row_of(e)]);
+            for (int e = 0; e < 4; ++e) s[k][x][e] = fmaf(s[k][x][e], scale[row_of<NT>(e)], -m.ref[row_of<NT>(e)]);
         if (edge) {
 #pragma unroll
           for (int k = 0; k < NU; ++k) {
@@ -590,7 +921,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) attn_kv4_kernel(Kv4
             for (int x = 0; x < NT; ++x)
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                if (at + token_of(x, e) > last[row_of(e)]) s[k][x][e] = -INFINITY;
+                if (at + token_of<NT>(lane, x, e) > last[row_of<NT>(e)]) s[k][x][e] = -INFINITY;
           }
         }
 #pragma unroll
@@ -599,133 +930,52 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) attn_kv4_kernel(Kv4
           for (int x = 0; x < NT; ++x)
 #pragma unroll
             for (int e = 0; e < 4; ++e) over = over || s[k][x][e] > room;
-        if (__any_sync(0xffffffffu, over)) {
-          float w = wide;
+        if (__any_sync(0xffffffffu, over || odd)) {
+          bool apart;
+          int top = 0;
+          const int v0 = m.v, v1 = range_of<D, NT>(st, lane, v0, apart, top);
+          if (v1 != v0 || __any_sync(0xffffffffu, over)) move_refs(m, s, v1);
+          if (apart || (v1 != v0 && !none)) {
+            // V's scales are far apart, or far from those before: what there is goes to the slot, and
+            // those that do not lie near the largest do too, those near each other at a time
+            put_sums(m, v0, part, ml, lane);
+            m.stands = true;
 #pragma unroll
-          for (int k = 1; k <= 16; k <<= 1) w = fmaxf(w, __shfl_xor_sync(0xffffffffu, w, k));
-          const int v1 = min(max(v, (__float_as_int(w) >> 23) - 126), 126);
+            for (int r = 0; r < R; ++r)
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            // largest score, less ref: of these units and of those before
-            float m = -INFINITY;
+              for (int x = 0; x < 2 * NT; ++x)
 #pragma unroll
-            for (int k = 0; k < NU; ++k)
+                for (int e = 0; e < 4; ++e) m.o[r][x][e] = 0.0f;
+            if (apart) {
+              float y[NU][NT][4];
 #pragma unroll
-              for (int x = 0; x < NT; ++x)
+              for (int k = 0; k < NU; ++k)
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  if (row_of(e) == i) m = fmaxf(m, s[k][x][e]);
+                for (int x = 0; x < NT; ++x)
 #pragma unroll
-            for (int k = LANES_0; k <= LANES_1; k <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
-            const bool first = fresh >> i & 1;
-            if (!first) m = fmaxf(m, kTop - (float)v);
-            const float to = ref[i] + (m - (kTop - (float)v1)), by = ref[i] - to;
-            if (by != 0.0f && m != -INFINITY) {
-              // (two factors: a step of V's scale alone can make `by` -219, past fp32's least power)
-              const float f = first ? 1.0f : ex2(0.5f * by);
-              ref[i] = to;
-              sum[i] = sum[i] * f * f;
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if (row_of(e) == i) {
-#pragma unroll
-                  for (int k = 0; k < NU; ++k)
-#pragma unroll
-                    for (int x = 0; x < NT; ++x) s[k][x][e] += by;
-#pragma unroll
-                  for (int r = 0; r < R; ++r)
-#pragma unroll
-                    for (int x = 0; x < 2 * NT; ++x) o[r][x][e] = o[r][x][e] * f * f;
-                }
+                  for (int e = 0; e < 4; ++e) y[k][x][e] = ex2(s[k][x][e]);
+              // those near 2^v1 stay in the stage
+              const uint32_t lo = bf16_pow2(v1 - kNarrow), hi = top <= v1 + kWide ? 0x7f80u : lo;
+              uint32_t most = leave<D, NT>(st, aside, lane, lo, hi, 0, true);
+              if (hi != lo) top = above(most);
+              else most = lo;                // all that there is goes to the slot
+              while (most != 0) {
+                most = leave<D, NT>(st, aside, lane, bf16_pow2(top - kNarrow), bf16_pow2(top), v1 - top, false);
+                add_to_slot<D, NT>(y, st, top, part, lane);
+                top = above(most);
+              }
+              leave<D, NT>(st, aside, lane, lo, hi, 0, false);
             }
-            if (m != -INFINITY) fresh &= ~(1u << i);
           }
-          v = v1;
-        }
-        if (v > kTinyWeights) {              // V's scales are huge, and weights tiny
-#pragma unroll
-          for (int k = 0; k < NU; ++k)
-#pragma unroll
-            for (int x = 0; x < NT; ++x)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) s[k][x][e] = ex2_small(s[k][x][e]);
-        } else {
-#pragma unroll
-          for (int k = 0; k < NU; ++k)
-#pragma unroll
-            for (int x = 0; x < NT; ++x)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) s[k][x][e] = ex2(s[k][x][e]);
         }
 #pragma unroll
         for (int k = 0; k < NU; ++k)
 #pragma unroll
           for (int x = 0; x < NT; ++x)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sum[row_of(e)] += s[k][x][e];
-        // outputs, over the 16 tokens of each unit: a pair of units' 8s first, a sum for all of a
-        // group's channels, then their codes
-        constexpr int PAIR = NU < 2 ? NU : 2;
-        const uint32_t ones[4] = {kOnes, kOnes, kOnes, kOnes};
-#pragma unroll
-        for (int k0 = 0; k0 < NU; k0 += PAIR) {
-          uint32_t vs[PAIR][TOKS][R / 2];
-#pragma unroll
-          for (int k = 0; k < PAIR; ++k)
-#pragma unroll
-            for (int i = 0; i < TOKS; ++i) words_at<R / 2>(vs[k][i], scales(k0 + k, i) + D / 16);
-#pragma unroll
-          for (int set = 0; set < R / SET; ++set) {
-            uint32_t w0[PAIR][SET], w1[PAIR][SET];
-#pragma unroll
-            for (int k = 0; k < PAIR; ++k) codes_at<D>(w0[k], w1[k], st + (k0 + k) * C::UNIT + 8 * D, lane, set);
-#pragma unroll
-            for (int rr = 0; rr < SET; ++rr) {
-              const int r = set * SET + rr;
-              uint32_t w[PAIR][2 * NT];      // weights times scales, as an operand
-              float off[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-              for (int k = 0; k < PAIR; ++k) {
-                float sc[TOKS];
-#pragma unroll
-                for (int i = 0; i < TOKS; ++i) sc[i] = r % 2 ? hi_f32(vs[k][i][r / 2]) : lo_f32(vs[k][i][r / 2]);
-                const auto& y = s[k0 + k];
-                if constexpr (WIDE) {
-#pragma unroll
-                  for (int x = 0; x < 2; ++x)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                      w[k][2 * x + i] = pack_f16x2(y[x][2 * i] * sc[2 * x], y[x][2 * i + 1] * sc[2 * x + 1]);
-                  mma(off, w[k], kOnes, kOnes);
-                } else {
-                  w[k][0] = transpose8(pack_f16x2(y[0][0] * sc[0], y[0][1] * sc[0]));
-                  w[k][1] = transpose8(pack_f16x2(y[0][2] * sc[1], y[0][3] * sc[1]));
-                  mma(off, ones, w[k][0], w[k][1]);
-                }
-              }
-#pragma unroll
-              for (int x = 0; x < 2 * NT; ++x)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  o[r][x][e] = fmaf(off[e], -8.0f * ((WIDE ? x % 2 : e / 2) ? kUnit7 : kUnit3), o[r][x][e]);
-#pragma unroll
-              for (int k = 0; k < PAIR; ++k) {
-                const uint32_t x0 = w0[k][rr] << 3, y0 = w1[k][rr] << 3, x1 = w0[k][rr] >> 5, y1 = w1[k][rr] >> 5;
-                if constexpr (WIDE) {        // rows by channels
-                  mma(o[r][0], w[k], x0 & kAt3, y0 & kAt3);
-                  mma(o[r][1], w[k], x0 & kAt7, y0 & kAt7);
-                  mma(o[r][2], w[k], x1 & kAt3, y1 & kAt3);
-                  mma(o[r][3], w[k], x1 & kAt7, y1 & kAt7);
-                } else {                     // channels by rows
-                  const uint32_t f0[4] = {x0 & kAt3, x0 & kAt7, y0 & kAt3, y0 & kAt7};
-                  const uint32_t f1[4] = {x1 & kAt3, x1 & kAt7, y1 & kAt3, y1 & kAt7};
-                  mma(o[r][0], f0, w[k][0], w[k][1]);
-                  mma(o[r][1], f1, w[k][0], w[k][1]);
-                }
-              }
-            }
-          }
-        }
+            for (int e = 0; e < 4; ++e) s[k][x][e] = ex2(s[k][x][e]);
+        add_weights(m, s);
+        add_values(m, s, st, lane);
       };
 
 #pragma unroll 1
@@ -738,7 +988,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) attn_kv4_kernel(Kv4
         const uint32_t gone = bad >> (get * C::UNITS) & ((1u << C::UNITS) - 1);
         const bool edge = (u + C::UNITS) * kv4::kUnit - 1 > all_see || gone != 0;
         if (edge) clean(u, st, gone);
-        meet(u, st, gone, edge);
+        meet(u, st, gone, edge, s == use.s);
         __syncwarp();
         get = get + 1 == C::STAGES ? 0 : get + 1;
         parity ^= get == 0;
@@ -751,32 +1001,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::WARPS * 32, 1) attn_kv4_kernel(Kv4
           for (int x = 0; x < 2 * NT; ++x)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              if (poison >> (8 * row_of(e) + r) & 1) o[r][x][e] = __uint_as_float(0x7fc00000u);
+              if (poison >> (8 * row_of<NT>(e) + r) & 1) m.o[r][x][e] = __uint_as_float(0x7fc00000u);
       }
-      // the share's sums into its slot, as with weights that do not go by V's scales
-      const float stored = __uint_as_float((uint32_t)(v - (int)kStored + 127) << 23);
-      const float at3 = stored / kUnit3, at7 = stored / kUnit7;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float l = sum[i];
-#pragma unroll
-        for (int k = LANES_0; k <= LANES_1; k <<= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
-        const long long row = slot * (8 * NT) + (WIDE ? 8 * i + g : 2 * t + i);
-        if ((WIDE ? t : g) == 0) p.ml[row] = make_float2(ref[i] - ((float)v - kStored), l * stored);
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-          float* part = p.part + row * D + 32 * r;
-          if constexpr (WIDE) {
-#pragma unroll
-            for (int e = 2 * i; e < 2 * i + 2; ++e)
-              *reinterpret_cast<float4*>(part + 8 * t + e % 2 * 4) =
-                  make_float4(o[r][0][e] * at3, o[r][1][e] * at7, o[r][2][e] * at3, o[r][3][e] * at7);
-          } else {
-            *reinterpret_cast<float4*>(part + 4 * g) =
-                make_float4(o[r][0][i] * at3, o[r][0][2 + i] * at7, o[r][1][i] * at3, o[r][1][2 + i] * at7);
-          }
-        }
-      }
+      put_sums(m, m.v, part, ml, lane);      // the share's sums into its slot
       if (!ok) break;
       rest -= end - use.s;
       use.s = end;

@@ -702,13 +702,13 @@ gdn_status gdn_kv4_load(const gdn_attn_dims* dims, int page, long long n_pages, 
  * A length outside [0, table_width * page] or a page index outside [0, n_pages) sets
  * GDN_ERR_DEVICE_BOUNDS: the sequence counts as empty, and the outputs of one that
  * reaches such a page are unspecified (nothing outside the cache is read).
- * Each softmax weight times its token's scale is rounded to fp16 (at a power of two that
- * keeps it in range) before it meets the codes, which moves out by at most 2^-11 sum p |v|
- * besides its own rounding; everything else is summed in fp32, with steps of the largest
- * magnitude M in a value's group where values cancel: at most 2^-16 sum p M of out, and of a
- * score 2^-16 scale times the sum over its groups of max |q| M.  Magnitudes of q are to be below
- * 2^108.  Equal calls give equal bits; the order
- * of a row's sums, and with it the last bits, depends on the batch, the lengths and the
+ * Each softmax weight times its token's scale is rounded to fp16.  That moves a weight p by at
+ * most 2^-11 p or, where p is below 2^-11 P, P the query's largest, by at most 2^-22 P (and no
+ * more than p), whatever other queries see and other tokens and groups of channels hold.
+ * Everything else is summed in fp32, with steps of the largest magnitude M in a value's group where
+ * values cancel: at most 2^-16 sum p M of out, and of a score 2^-16 scale times the sum over its
+ * groups of Q M, Q the query's largest magnitude (below 2^108).  Equal calls give equal bits; the
+ * order of a row's sums, and with it the last bits, depends on the batch, the lengths and the
  * GPU's SM count.
  */
 size_t gdn_attn_decode_kv4_workspace_bytes(const gdn_attn_dims* dims, int batch, int steps);
