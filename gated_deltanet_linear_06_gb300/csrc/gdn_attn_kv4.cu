@@ -48,7 +48,7 @@
 // 2^-14 of the others', 182 with those of one token in a hundred, 246 with half of the groups'.
 
 // Measured, both launches, of the bytes that the cache holds for the tokens: 256 sequences of 100
-// to 8000 tokens (16 query heads, 2 kv heads, d = 256) 118 us, 5.1 TB/s; one of 131072 (32, 8,
+// to 8000 tokens (16 query heads, 2 kv heads, d = 256) 119 us, 5.0 TB/s; one of 131072 (32, 8,
 // 128) 38 us, 4.0 TB/s; 64 of 6001 (32, 8, 128) 88 us, 5.0 TB/s, in pages of 16 93 us; 96 of 1 to
 // 2900 (64, 8, 64) 28 us, 2.9 TB/s; 17 of 4 to 6001 with 4 steps (32, 8, 128, pages of 16) 31 us,
 // 1.9 TB/s; one of 833 8.5 us, latency (the lengths 0.8, first copy asked for 1.3, its rows and the
@@ -71,12 +71,12 @@ namespace gdn {
 namespace {
 
 constexpr long long kWaitClocks = 2000000000LL;   // a second or so: a copy that has not come by then never will
-// A row's weights are 2^(score - ref); where ref moves the largest comes to lie above 2^(kTop - 1 - v)
-// and at most at 2^(kTop - v).  Scores may then grow by kGrow binary orders, and V's scales lie from
+// A row's weights are 2^(score - ref); where ref moves the largest comes to 2^(kTop - v), a power of
+// two, so that its products with scales are exact in fp16 (with ref a whole number one output in ten
+// was not the exact one rounded, with this one in thirteen).  Scores may then grow by kGrow binary orders, and V's scales lie from
 // 2^(v - kNarrow) to 2^(v + kWide): a weight times a scale stays below 2^15, in fp16, and what
-// fp16's subnormal numbers round off, 2^-25 at most next to 2^(kTop - 1 - kNarrow), is 2^-22 of the
-// row's largest weight times the least scale there is.  ref moves by whole numbers, so that
-// every factor is a power of two.
+// fp16's subnormal numbers round off, 2^-25 at most next to 2^(kTop - kNarrow), is 2^-23 of the
+// row's largest weight times the least scale there is.
 constexpr float kTop = 8.0f, kGrow = 4.0f;
 constexpr int kWide = 3, kNarrow = 10;
 constexpr int kLeastV = -93;                       // scales are zero or at least 2^-93
@@ -361,11 +361,10 @@ __device__ __forceinline__ void move_refs(Sums<D, NT>& m, float (&s)[Cfg<D, NT>:
     for (int k = LANES_0; k <= LANES_1; k <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, k));
     const bool first = m.fresh >> i & 1;
     if (first && most == -INFINITY) continue;
-    float up = ceilf(most - (kTop - (float)m.v));   // by which it is too large
-    if (!first) up = fmaxf(up, 0.0f);
+    if (!first) most = fmaxf(most, kTop - (float)m.v);
     m.fresh &= ~(1u << i);
-    const float by = up + (float)(v1 - m.v);
-    m.ref[i] += by;
+    const float to = m.ref[i] + (most - (kTop - (float)v1)), by = to - m.ref[i];   // (as rounded)
+    m.ref[i] = to;
 #pragma unroll
     for (int k = 0; k < NU; ++k)
 #pragma unroll
@@ -373,8 +372,8 @@ __device__ __forceinline__ void move_refs(Sums<D, NT>& m, float (&s)[Cfg<D, NT>:
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           if (row_of<NT>(e) == i) s[k][x][e] -= by;
-    if (!first && up != 0.0f) {
-      const float f = up < 127.0f ? pow2(-(int)up) : 0.0f;
+    if (!first && by != (float)(v1 - m.v)) {
+      const float f = ex2((float)(v1 - m.v) - by);
       m.sum[i] *= f;
 #pragma unroll
       for (int r = 0; r < D / 32; ++r)
@@ -487,7 +486,7 @@ __device__ __forceinline__ void put_sums(const Sums<D, NT>& m, int vo, float* pa
     const int row = WIDE ? 8 * i + g : 2 * t + i;
     const float to = m.ref[i] - (float)(m.v - kStored);
     float keep = 0.0f;                       // (references never move down)
-    if (m.stands) keep = pow2(max((int)fminf(ml[row].x - to, 0.0f), -127));
+    if (m.stands) keep = ex2(fminf(ml[row].x - to, 0.0f));
     __syncwarp();
     if ((WIDE ? t : g) == 0) ml[row] = make_float2(to, l);
 #pragma unroll
