@@ -10,9 +10,10 @@ dropped and the pool is drawn together, all between decode steps of the batch:
 
     python examples/paged_decode.py
 
-prints the largest difference between a continuation and the same sequence
-decoded alone, in a pool of its own, without any of that.  Random weights and
-inputs; a model's norms and projections around the layers are plain torch
+prints the largest difference between a continuation's attention outputs and those
+of the same sequence decoded alone, in a pool of its own, without any of that (the
+layers' outputs are mostly their inputs, which would hide one).  Random weights
+and inputs; a model's norms and projections around the layers are plain torch
 operations.
 """
 from __future__ import annotations
@@ -63,8 +64,9 @@ class Cache:
         return torch.tensor(values, dtype=I32, device="cuda")
 
 
-def step(m: Model, c: Cache, seqs, x):
-    """x [n, S, hidden]: S new tokens (at most 8) of the sequences `seqs` -> [n, S, hidden]."""
+def step(m: Model, c: Cache, seqs, x, heads=None):
+    """x [n, S, hidden]: S new tokens (at most 8) of the sequences `seqs` -> [n, S, hidden].  The
+    list `heads` takes each layer's queries, gates and attention outputs, [n, S, h_q, d] all."""
     n, S, H = x.shape
     a, T = m.dims, n * S
     seq = c.i32(seqs)
@@ -83,6 +85,8 @@ def step(m: Model, c: Cache, seqs, x):
         gdn.gdn_kv4_store(a, k, kv[:, 1], cache, slot=slot.view(T), device_status=c.status)
         out = torch.empty_like(q)
         gdn.gdn_attn_decode_kv4(a, q, cache, table, lens, out, ws, gate=qg[..., a.d:], device_status=c.status)
+        if heads is not None:
+            heads.append((q, qg[..., a.d:].view(n, S, a.h_q, a.d), out))
         x = x + out.view(T, a.h_q * a.d) @ w["w_o"].t()
     return x.view(n, S, H)
 
@@ -108,7 +112,8 @@ def main(prompt=77, tokens=6, children=3, verbose=True):
     gdn.gdn_pages_fork(c.pool, c.caches, c.i32([0] * children), c.i32(kids), c.ws, device_status=c.status)
     got = []
     for t in range(tokens):
-        got.append(step(m, c, kids, own[t][:, None]))
+        got.append([])
+        step(m, c, kids, own[t][:, None], got[t])
         before = c.lens[2:].clone()
         step(m, c, kids, drafts)                       # three drafted tokens, none of them kept
         gdn.gdn_pages_trim(c.pool, c.caches, before, c.ws, seq=c.i32(kids), device_status=c.status)
@@ -123,12 +128,14 @@ def main(prompt=77, tokens=6, children=3, verbose=True):
         a = Cache(m, 1, 64)
         read(m, a, 0, first)
         for t in range(tokens):
-            y = step(m, a, [0], own[t, i][None, None])
-            worst = max(worst, float((got[t][i].float() - y[0].float()).abs().max() / y.float().abs().max()))
+            heads = []
+            step(m, a, [0], own[t, i][None, None], heads)
+            for (_, _, y), (_, _, z) in zip(heads, got[t]):
+                worst = max(worst, float((z[i].float() - y[0].float()).abs().max() / y.float().abs().max()))
         assert gdn.gdn_read_device_status(a.status) == 0
     if verbose:
-        print(f"{children} continuations of a prompt of {prompt} tokens, {tokens} steps each: they differ from the same "
-              f"sequences alone by at most {worst:.1e} of the largest output")
+        print(f"{children} continuations of a prompt of {prompt} tokens, {tokens} steps each: their attention differs from "
+              f"the same sequences' alone by at most {worst:.1e} of its largest output")
     return worst
 
 
