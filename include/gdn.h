@@ -758,8 +758,10 @@ gdn_status gdn_attn_decode_kv4(const gdn_attn_dims* dims, int page, long long n_
  * extend, trim, fork and free are done whole or not at all: a sequence out of range or
  * named twice (as dst, of fork), a length or count that may not be, a fork into a sequence
  * that holds tokens, or too few free pages sets GDN_ERR_DEVICE_BOUNDS and changes
- * nothing (extend then gives -1 for all slots).  So does a page index out of range in a
- * table or in copy's lists, but it is only passed over.  copy's pairs run at the same time:
+ * nothing (extend then gives -1 for all slots).  Free is what is free when the call begins, so a trim
+ * that has to copy a shared page can be refused in a full pool, whatever it gives back itself;
+ * one to a whole number of pages never is.  A page index out of range in a table or in copy's
+ * lists sets GDN_ERR_DEVICE_BOUNDS too, but is only passed over.  copy's pairs run at the same time:
  * no destination may be another pair's, source or destination.
  */
 #define GDN_PAGES_MAX_SEQS 65536
