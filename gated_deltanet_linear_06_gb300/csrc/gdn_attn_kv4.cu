@@ -34,8 +34,9 @@
 // many short ones do.  Warps share nothing but the sums of the lengths at the start; each has
 // its own ring of two stages, filled by bulk copies (a page's units of a head are contiguous)
 // while the other is met.  A share ends where it ends; a second launch joins a job's shares.
-// Shares follow from the lengths alone, so equal calls add in equal order, and they are found
-// on the device, so a captured call stays valid while the lengths grow.
+// Shares follow from the lengths alone and are found on the device, so a captured call stays valid
+// while the lengths grow.  Only how many lane groups join a row goes by what the host knows, the
+// table's width: equal calls add in equal order, those of a wider table may join in another.
 //
 // Softmax.  ref moves only when a score passes it by kGrow binary orders; else a stage costs a
 // vote.  Weights times scales of V have to fit fp16, so weights carry a factor 2^-v that suits the

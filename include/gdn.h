@@ -691,7 +691,7 @@ gdn_status gdn_kv4_load(const gdn_attn_dims* dims, int page, long long n_pages, 
  *                 at most GDN_ATTN_MAX_ROWS
  *   q             bf16 [batch][steps][h_q][d]
  *   cache         as above
- *   table         int32 [batch][table_width], entries past a sequence's end unread; null
+ *   table         int32 [batch][table_width], entries past a sequence's end of no account; null
  *                 when table_width is 0; table_width * page at most 2^30
  *   len           int32 [batch], device: a call's launches do not depend on the lengths,
  *                 so a captured step stays valid while they grow
@@ -708,8 +708,8 @@ gdn_status gdn_kv4_load(const gdn_attn_dims* dims, int page, long long n_pages, 
  * Everything else is summed in fp32, with steps of the largest magnitude M in a value's group where
  * values cancel: at most 2^-16 sum p M of out, and of a score 2^-16 scale times the sum over its
  * groups of Q M, Q the query's largest magnitude (below 2^108).  Equal calls give equal bits; the
- * order of a row's sums, and with it the last bits, depends on the batch, the lengths and the
- * GPU's SM count.
+ * order of a row's sums, and with it the last bits, depends on the batch, the lengths,
+ * table_width * page and the GPU's SM count.
  */
 size_t gdn_attn_decode_kv4_workspace_bytes(const gdn_attn_dims* dims, int batch, int steps);
 gdn_status gdn_attn_decode_kv4(const gdn_attn_dims* dims, int page, long long n_pages, int batch,
