@@ -745,7 +745,8 @@ gdn_status gdn_attn_decode_kv4(const gdn_attn_dims* dims, int page, long long n_
  *            to the lowest free one, in order) and every table follows; *n_live, if given, a
  *            device word, is set
  *   copy     page src_page[i] of every cache of one set to page dst_page[i] of another's
- *            (or the same): swapping pages out and in; no pool is involved
+ *            (or the same), both in device memory: moving pages to another set and back; no
+ *            pool is involved
  * Trimmed and freed sequences' entries become -1; a page whose count drops to 0 is free.
  * Pages that calls add are the lowest free ones, in the order of the list.  A page that is
  * not full belongs to one table alone (extend writes into it), which these calls see to.
