@@ -8,7 +8,7 @@
 // so the codes are multiplied as whole numbers, K's scales meet the products' sums in fp32
 // and V's meet the weights before their one rounding, to fp16.
 //
-// What bounds it.  4.5 bits a value: at the memory's rate an SM gets 46 values a clock, and
+// What bounds it.  4.5 bits a value: at the memory's rate an SM gets 38 values a clock, and
 // what it can do for each of them decides.  Taking a nibble out costs an instruction for two
 // values whatever one does; so everything else is kept from costing any:
 //   - the codes lie as the operands' fragments do, so a lane's words come by 16-byte loads and no
@@ -40,25 +40,28 @@
 //
 // Softmax.  ref moves only when a score passes it by kGrow binary orders; else a stage costs a
 // vote.  Weights times scales of V have to fit fp16, so weights carry a factor 2^-v that suits the
-// scales, those of all groups and tokens of a stage alike, whoever sees them: that they lie near 2^v
-// (13 binary orders, see kNarrow) is looked at in every stage, an add and a maximum for four
-// values of 32.  Where they do not, what is summed goes to the share's slot in memory, in fp32 and
-// free of v, v moves, and scales that still do not fit go by themselves, those near each other at
-// a time: so no scale, seen or not, takes another's bits.  64 sequences of 6001 (32, 8, 128,
-// caches cold) take 98 us; 107 with half of the groups zeros, 100 with every first token's scales
-// 2^-14 of the others', 182 with those of one token in a hundred, 246 with half of the groups'.
-
+// scales, those of all groups and tokens of a stage alike, whoever sees them: that they lie near
+// 2^v (13 binary orders, see kNarrow) is looked at in every stage, two instructions for two
+// scales.  Where they do not, what is summed goes to the share's slot in memory, in fp32 and free
+// of v, v moves, and scales that still do not fit go by themselves, those near each other at a
+// time: so no scale, seen or not, takes another's bits.  64 sequences of 6001 (32, 8, 128, caches
+// cold) take 98 us; 107 with half of the groups zeros, 100 with every first token's scales 2^-14
+// of the others', 182 with those of one token in a hundred, 246 with half of the groups'.
+//
 // Measured, both launches, of the bytes that the cache holds for the tokens: 256 sequences of 100
 // to 8000 tokens (16 query heads, 2 kv heads, d = 256) 119 us, 5.0 TB/s; one of 131072 (32, 8,
-// 128) 38 us, 4.0 TB/s; 64 of 6001 (32, 8, 128) 88 us, 5.0 TB/s, in pages of 16 93 us; 96 of 1 to
-// 2900 (64, 8, 64) 28 us, 2.9 TB/s; 17 of 4 to 6001 with 4 steps (32, 8, 128, pages of 16) 31 us,
-// 1.9 TB/s; one of 833 8.5 us, latency (the lengths 0.8, first copy asked for 1.3, its rows and the
-// data 1, a stage 1.4, the share written 0.5, join 2).  Per unit of 16 tokens at d = 256: 240
-// clocks of an SM, for 525 instructions (237 of the integer pipe, which starts one every other
-// clock and scheduler: 118) and 40 products (80).  Masks, products and the fp32 arithmetic
-// between them contend for the same issue slots and registers' ports, and their times add up:
-// 12 warps with stages of half the size took 132 us for 114, the next stage's scores between a
-// stage's sums 133, stages of 3 units (registers run out) 129.
+// 128) 38 us, 4.0 TB/s; 64 of 6001 (32, 8, 128) 86 us, 5.2 TB/s, in pages of 16 90 us; 96 of 1 to
+// 2900 (64, 8, 64) 28 us, 2.9 TB/s; 17 of 4 to 6001 with 4 steps (32, 8, 128, pages of 16) 32 us,
+// 1.9 TB/s; one of 833 8.5 us, latency (the lengths 0.8, first copy asked for 1.3, its rows and
+// the data 1, a stage 1.4, the share written 0.5, join 2).  Per unit of 16 tokens at d = 256, of
+// the full batch: 275 clocks of an SM where the memory's rate gives 217, for 538 instructions (248
+// of the integer pipe, which starts one every other clock and scheduler: 124) and 40 products
+// (80).  Rows above 16 of a kv head meet the same tokens in a job of their own: 64 sequences of
+// 6001 with 1, 2, 4 and 8 steps (16, 2, 256: 8 to 64 rows; caches cold) 61, 104, 180 and 332 us.
+// Masks, products and the fp32 arithmetic between them contend for the same issue slots and
+// registers' ports, and their times add up: 12 warps with stages of half the size took 132 us for
+// 114, the next stage's scores between a stage's sums 133, stages of 3 units (registers run out)
+// 129.
 #include <limits.h>
 #include <math.h>
 

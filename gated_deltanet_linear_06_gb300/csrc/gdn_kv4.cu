@@ -10,10 +10,12 @@
 // units need not begin with one: the tokens are taken in sixteens that end where the first
 // token's unit does.
 //
-// A store is bound by its instructions, some 16 a value (of which 5 for the quotient, its
-// rounding and its place); without divisions and with extremes as packed 16-bit numbers they
-// are less than half of what they were.  Measured, 32768 rows of 2 heads of 256: store 20.7 us
-// (4.2 TB/s of 67 MB read and 19 MB written), load as bf16 15 us (5.8 TB/s).  256 rows of as many
+// A store takes some 16 instructions a value (of which 5 for the quotient, its rounding and its
+// place), less than half of what they were with divisions and without extremes as packed 16-bit
+// numbers.  Nothing that it uses is full (issue slots 68 %, integer pipe 61 %, memory 63 %): a warp
+// loads its vectors, converts them, stores them and ends, so that loads and arithmetic overlap
+// between warps only.  Measured, 32768 rows of 2 heads of 256: store 20.7 us (4.2 TB/s of 67 MB
+// read and 19 MB written), load as bf16 15 us (5.8 TB/s).  256 rows of as many
 // sequences: 5 us each, latency.
 #include "../../include/gdn.h"
 #include "gdn_kv4.cuh"

@@ -16,8 +16,9 @@
 //
 // Measured: 4 tokens more for 256 sequences in a pool of 65536 pages 5.5 us (lists and counts
 // loaded 1.4, sums 0.7, free pages shared out 1.9, rows and tables written 1.3), taking them back
-// 3.8; forking 48 children of 5003 tokens with 12 caches of 36 KB pages 5.8 + 6 us; drawing 2000
-// of 6656 pages of 12 caches together 226 us, 6.2 TB/s read and written, 93 % of a copy's rate.
+// 3.8; forking 48 children of 5003 tokens with 12 caches of 36 KB pages 5.8 + 6 us; drawing
+// 6656 pages of 12 caches together, 3482 of them in use and some 1660 to be moved, 224 us, 6.6 TB/s
+// read and written, 98 % of a copy's rate.
 #include <limits.h>
 
 #include "../../include/gdn.h"
@@ -553,8 +554,8 @@ cudaError_t launch_moves(const PoolParams& a, const MoveParams& v, long long mos
   const cudaError_t e = sm_count(sms);
   if (e != cudaSuccess) return e;
   // Enough warps for every piece there can be, up to sixteen times as many as fit on the GPU:
-  // 2000 pages of 12 caches of 36 KB took 242 us with twice as many, whose shares end far
-  // apart, and 226 so (9700 CTAs without anything to do cost 1 us).
+  // 1660 pages of 12 caches of 36 KB took 242 us with twice as many, whose shares end far
+  // apart, and 224 so (9700 CTAs without anything to do cost 1 us).
   const long long want = (most + kMoveWarps - 1) / kMoveWarps, fit = (long long)sms * 64;
   Launch l((unsigned)(want < 1 ? 1 : want < fit ? want : fit), kMoveWarps * 32, 0, stream);
   return cudaLaunchKernelEx(&l.cfg, pages_move_kernel<ROWS>, a, v);
