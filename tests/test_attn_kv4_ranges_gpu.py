@@ -169,3 +169,67 @@ def test_a_nan_next_to_values_of_many_sizes(d, S, G):
     assert nan[:, :, G:, :32].all() and not nan[:, :, :G].any() and not nan[:, :, G:, 32:].any()
     assert torch.equal(got[:, :, :G], clean[:, :, :G])
     assert errors(x, S, [n])[:, :, 1, :, 32:].max() <= 1
+
+
+def sizes(n, d, seed, span=60):
+    """Values of n tokens, groups of a token up to 2^span apart."""
+    g = torch.Generator().manual_seed(seed)
+    e = span * torch.rand(n, 2, d // 32, 1, generator=g) - span / 2
+    return (torch.randn(n, 2, d // 32, 32, generator=g) * torch.exp2(e)).flatten(-2)
+
+
+@pytest.mark.parametrize("d,S,G", [s for s in SHAPES if s[1] > 1])
+def test_what_is_not_seen_next_to_values_of_many_sizes(d, S, G):
+    lens = [100, 64, 37]
+    v = sizes(sum(lens), d, 37)
+    x = stored(3, S, G, d, lens, None, v, seed=37)
+    clean = call(x)
+    last = x["slot"][[99, 163, 200]].to(DEV)
+    for bad in (float("nan"), 3e38):
+        rows = torch.full((3, 2, d), bad, dtype=BF, device=DEV)
+        gdn.gdn_kv4_store(x["dims"], rows, rows, x["cache"], slot=last)
+        got = call(x)
+        if bad == bad:                         # (other passes, other roundings: held to the formula)
+            assert errors(x, S, lens)[:, :S - 1].max() <= 1
+        else:
+            assert torch.equal(got[:, :S - 1], clean[:, :S - 1]) and torch.isnan(got[:, S - 1]).all()
+
+
+@pytest.mark.parametrize("d,S,G", SHAPES)
+def test_long_sequences_of_many_sizes_in_many_shares(d, S, G):
+    lens = [9001, 5000]
+    v = sizes(sum(lens), d, 38)
+    worst = errors(stored(2, S, G, d, lens, None, v, seed=38), S, lens).max()
+    assert worst <= 1, worst
+
+
+@pytest.mark.parametrize("d,S,G", [(64, 1, 4), (128, 4, 4), (256, 1, 8)])
+def test_equal_and_captured_calls_on_values_of_many_sizes(d, S, G):
+    lens = [700, 33, 0, 260]
+    x = stored(4, S, G, d, lens, None, sizes(sum(lens), d, 39), seed=39)
+    want = call(x)
+    ws = torch.full((gdn.gdn_attn_decode_kv4_workspace_bytes(x["dims"], 4, S),), 255, dtype=torch.uint8, device=DEV)
+    out = torch.empty_like(want)
+    run = lambda: gdn.gdn_attn_decode_kv4(x["dims"], x["q"], x["cache"], x["table"], x["lens"], out, ws)   # noqa: E731
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        run()
+    side.synchronize()
+    assert torch.equal(out, want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for _ in range(3):
+        out.fill_(7)
+        graph.replay()
+        assert torch.equal(out, want)
+
+
+def test_scores_that_grow_over_values_of_many_sizes():
+    # references move between parts of the sums that stand in memory
+    n = 700
+    for d, S, G in SHAPES:
+        g = torch.Generator().manual_seed(d)
+        k = torch.randn(n, 2, d, generator=g) * (0.02 * torch.arange(n)[:, None, None])
+        worst = errors(stored(1, S, G, d, [n], k, sizes(n, d, 40), seed=40), S, [n]).max()
+        assert worst <= 1, (d, S, G, worst)
