@@ -4,7 +4,7 @@ The first layer's keys and values depend on the tokens alone, so a continuation'
 through its table, are the bits of the sequence held alone.  Every layer's attention outputs
 are held to softmax attention in 64 bits, over the rows of the sequence alone (first layer)
 or over the continuation's own (both), with test_attn_kv4_gpu's tolerance.  The same tolerance
-tells a sequence that lacks its last token or has another's page apart."""
+tells a sequence that lacks its last token or has other rows in a page apart."""
 import os
 import sys
 
@@ -72,7 +72,7 @@ def test_rows_and_attention_are_the_sequences(prompt, tokens, children):
             assert worst(m, q, gate, out, k[:n], v[:n]) <= 1
             for layer, x in enumerate(heads):
                 assert worst(m, *(y[i, 0] for y in x), *rows(m, c, s, layer, n)) <= 1
-            # mistakes, in what it is held to: no last token, a page of the other sequence
+            # mistakes, in what it is held to: no last token, other rows in a page
             told.append(worst(m, q, gate, out, k[:n - 1], v[:n - 1]) if n > 1 else 2)
             if n >= 16:
                 k, v = k[:n].clone(), v[:n].clone()
